@@ -9,4 +9,6 @@ from .binding import (  # noqa: F401
     Bf16Pool, Int2Pool, Layout, OscarError, Partials, oscar_bf16_decode_attention, oscar_decode_attention,
     oscar_demote, oscar_get_device_status, oscar_merge, oscar_partials_acc_floats, oscar_partials_ml_floats,
     oscar_quantize_rotated, oscar_rotate_q, oscar_suggest_splits, oscar_version,
+    Int4Pool, oscar_append_kv, oscar_attention_mass_int4, oscar_decode_attention_int4, oscar_demote_int4,
+    oscar_evict_int4, oscar_promote_int4, oscar_suggest_splits_int4,
 )

@@ -19,6 +19,7 @@ LIB_PATH = os.path.join(_PKG, "liboscar.so")
 _lib = None
 
 i32 = ctypes.c_int32
+i64 = ctypes.c_int64
 vp = ctypes.c_void_p
 
 
@@ -41,6 +42,10 @@ class Bf16PoolC(ctypes.Structure):
     _fields_ = [("k", vp), ("v", vp), ("n_pages", i32)]
 
 
+class Int4PoolC(ctypes.Structure):
+    _fields_ = [("codes_k", vp), ("codes_v", vp), ("scale_zero", vp), ("n_pages", i32)]
+
+
 class PartialsC(ctypes.Structure):
     _fields_ = [("m", vp), ("l", vp), ("acc", vp), ("n_splits", i32)]
 
@@ -52,6 +57,8 @@ EXPORTS = [
     "oscar_decode_attention_noalloc", "oscar_decode_attention_history", "oscar_decode_attention_window",
     "oscar_set_launch_overlap", "oscar_get_launch_overlap", "oscar_decode_attention_fused",
     "oscar_demote_range", "oscar_decode_attention_shared_prefix",
+    "oscar_append_kv", "oscar_demote_int4", "oscar_promote_int4", "oscar_suggest_splits_int4",
+    "oscar_decode_attention_int4", "oscar_attention_mass_int4", "oscar_evict_int4",
 ]
 
 
@@ -112,6 +119,24 @@ def lib():
                                                         i32, vp, vp, i32, ctypes.c_float, i32, i32, P(PartialsC),
                                                         vp, vp]
     L.oscar_decode_attention_shared_prefix.restype = st
+    f32 = ctypes.c_float
+    L.oscar_append_kv.argtypes = [P(LayoutC), vp, i64, vp, i64, vp, i64, i32, vp, vp, f32, vp, i32, i32, i32,
+                                  P(Bf16PoolC), vp, i32, i32, vp, vp, vp, vp, vp]
+    L.oscar_append_kv.restype = st
+    L.oscar_demote_int4.argtypes = [P(LayoutC), P(Bf16PoolC), vp, P(Int4PoolC), vp, i32, i32, vp, vp, f32, f32, vp]
+    L.oscar_demote_int4.restype = st
+    L.oscar_promote_int4.argtypes = [P(LayoutC), P(Int4PoolC), vp, P(Bf16PoolC), vp, i32, i32, vp, vp, vp]
+    L.oscar_promote_int4.restype = st
+    L.oscar_suggest_splits_int4.argtypes = [P(LayoutC), i32, i32, i32]
+    L.oscar_suggest_splits_int4.restype = i32
+    attn4 = [P(LayoutC), vp, P(Bf16PoolC), vp, P(Int4PoolC), vp, i32, vp, vp, i32, f32]
+    L.oscar_decode_attention_int4.argtypes = attn4 + [P(PartialsC), vp, vp, vp, vp, vp]
+    L.oscar_decode_attention_int4.restype = st
+    L.oscar_attention_mass_int4.argtypes = attn4 + [vp, vp, vp]
+    L.oscar_attention_mass_int4.restype = st
+    L.oscar_evict_int4.argtypes = [P(LayoutC), P(Int4PoolC), vp, P(Int4PoolC), vp, i32, i32, vp, vp, vp, vp, vp, vp,
+                                   i32, vp]
+    L.oscar_evict_int4.restype = st
     L.oscar_set_launch_overlap.argtypes = [i32]
     L.oscar_set_launch_overlap.restype = st
     L.oscar_get_launch_overlap.argtypes = []
@@ -207,6 +232,28 @@ class Bf16Pool:
 
     def c(self) -> Bf16PoolC:
         return Bf16PoolC(_ptr(self.k), _ptr(self.v), self.n_pages)
+
+
+@dataclasses.dataclass
+class Int4Pool:
+    """Paged INT4 pool of one layer: a page holds one kv head's tokens together."""
+    codes_k: torch.Tensor      # uint8 [n_pages, Hkv, page_size, D / 2]
+    codes_v: torch.Tensor
+    scale_zero: torch.Tensor   # bf16 [n_pages, Hkv, page_size, D / group, 4]: key scale, zero, value scale, zero
+
+    @property
+    def n_pages(self) -> int:
+        return self.codes_k.shape[0]
+
+    @staticmethod
+    def empty(layout: Layout, n_pages: int, device="cuda") -> "Int4Pool":
+        shp = (n_pages, layout.n_kv_heads, layout.page_size)
+        c = lambda: torch.zeros(shp + (layout.head_dim // 2,), dtype=torch.uint8, device=device)
+        return Int4Pool(c(), c(), torch.zeros(shp + (layout.head_dim // layout.group, 4), dtype=torch.bfloat16,
+                                              device=device))
+
+    def c(self) -> Int4PoolC:
+        return Int4PoolC(_ptr(self.codes_k), _ptr(self.codes_v), _ptr(self.scale_zero), self.n_pages)
 
 
 @dataclasses.dataclass
@@ -376,6 +423,180 @@ def oscar_decode_attention_noalloc(layout: Layout, q: torch.Tensor, q_rot: torch
         ctypes.byref(int2_pool.c()), _ptr(int2_page_table), int(int2_page_table.shape[-1]), _ptr(seq_len),
         _ptr(hist_end), int(q.shape[0]), float(sm_scale), int(n_splits), _ptr(R_V), _ptr(out), _ptr(out_f32),
         _ptr(lse), _stream(stream)))
+
+
+def _want(name: str, what: str, t: Optional[torch.Tensor], dtype, shape):
+    """One argument's dtype, shape and place (None: an argument left out)."""
+    if t is None:
+        return
+    if t.dtype != dtype:
+        raise OscarError(f"{name}: {what} must be {dtype}, not {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise OscarError(f"{name}: {what} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise OscarError(f"{name}: {what} is on {t.device}, not on the current CUDA device")
+
+
+def _want_int4(name: str, layout: Layout, pool: Int4Pool):
+    shp = (pool.n_pages, layout.n_kv_heads, layout.page_size)
+    _want(name, "codes_k", pool.codes_k, torch.uint8, shp + (layout.head_dim // 2,))
+    _want(name, "codes_v", pool.codes_v, torch.uint8, shp + (layout.head_dim // 2,))
+    _want(name, "scale_zero", pool.scale_zero, torch.bfloat16, shp + (layout.head_dim // layout.group, 4))
+
+
+def _want_bf16(name: str, layout: Layout, pool: Bf16Pool):
+    shp = (pool.n_pages, layout.page_size, layout.n_kv_heads, layout.head_dim)
+    _want(name, "pool k", pool.k, torch.bfloat16, shp)
+    _want(name, "pool v", pool.v, torch.bfloat16, shp)
+
+
+def _want_tables(name: str, a: torch.Tensor, b: torch.Tensor):
+    if a.dim() != 2:
+        raise OscarError(f"{name}: page tables must be [batch, max_pages]")
+    _want(name, "page table", a, torch.int32, a.shape)
+    _want(name, "page table", b, torch.int32, a.shape)
+    return a.shape
+
+
+def _heads(name: str, what: str, t: torch.Tensor, heads: int, n: int, D: int):
+    """(address, token stride) of [n, heads, D] bf16 whose heads of one token lie together (a slice of a packed row)."""
+    _want(name, what, t, torch.bfloat16, (n, heads, D))
+    if n and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != D)):
+        raise OscarError(f"{name}: the heads of one token of {what} must lie together")
+    return vp(t.data_ptr()), (t.stride(0) if n > 1 else max(t.stride(0), heads * D))
+
+
+def oscar_append_kv(layout: Layout, q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, pool: Bf16Pool,
+                    page_table: torch.Tensor, req_idx: torch.Tensor, positions: torch.Tensor,
+                    q_out: Optional[torch.Tensor] = None, q_weight: Optional[torch.Tensor] = None,
+                    k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, rope: Optional[torch.Tensor] = None,
+                    rot_dim: int = 128, interleaved: bool = False, rope_positions: Optional[torch.Tensor] = None,
+                    stream=None):
+    """New tokens' heads (q [n, Hq, D], k and v [n, Hkv, D] bf16, token rows possibly strided): RMS norm per head,
+    rotary position, q to q_out and k, v to the tokens' slots of the BF16 pool."""
+    name, n, D = "oscar_append_kv", int(k.shape[0]), layout.head_dim
+    _want_bf16(name, layout, pool)
+    batch, max_pages = _want_tables(name, page_table, page_table)
+    for what, t in (("req_idx", req_idx), ("positions", positions), ("rope_positions", rope_positions)):
+        _want(name, what, t, torch.int32, (n,))
+    _want(name, "q_weight", q_weight, torch.bfloat16, (D,))
+    _want(name, "k_weight", k_weight, torch.bfloat16, (D,))
+    _want(name, "q_out", q_out, torch.bfloat16, (n, layout.n_q_heads, D))
+    if rope is not None:
+        _want(name, "rope", rope, torch.float32, (rope.shape[0], 128))
+    qp, qs = _heads(name, "q", q, layout.n_q_heads, n, D) if q is not None else (None, 0)
+    kp, ks = _heads(name, "k", k, layout.n_kv_heads, n, D)
+    vv, vs = _heads(name, "v", v, layout.n_kv_heads, n, D)
+    _check(name, lib().oscar_append_kv(
+        ctypes.byref(layout.c()), qp, qs, kp, ks, vv, vs, n, _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(rope),
+        0 if rope is None else int(rope.shape[0]), int(rot_dim), int(bool(interleaved)), ctypes.byref(pool.c()),
+        _ptr(page_table), max_pages, batch, _ptr(req_idx), _ptr(positions), _ptr(rope_positions), _ptr(q_out),
+        _stream(stream)))
+
+
+def oscar_demote_int4(layout: Layout, src: Bf16Pool, bf16_page_table: torch.Tensor, dst: Int4Pool,
+                      int4_page_table: torch.Tensor, pos_begin: torch.Tensor, pos_end: torch.Tensor, c_K: float = 1.0,
+                      c_V: float = 1.0, stream=None):
+    name = "oscar_demote_int4"
+    _want_bf16(name, layout, src)
+    _want_int4(name, layout, dst)
+    batch, max_pages = _want_tables(name, int4_page_table, bf16_page_table)
+    _want(name, "pos_begin", pos_begin, torch.int32, (batch,))
+    _want(name, "pos_end", pos_end, torch.int32, (batch,))
+    _check(name, lib().oscar_demote_int4(
+        ctypes.byref(layout.c()), ctypes.byref(src.c()), _ptr(bf16_page_table), ctypes.byref(dst.c()),
+        _ptr(int4_page_table), max_pages, batch, _ptr(pos_begin), _ptr(pos_end), float(c_K), float(c_V),
+        _stream(stream)))
+
+
+def oscar_promote_int4(layout: Layout, src: Int4Pool, int4_page_table: torch.Tensor, dst: Bf16Pool,
+                       bf16_page_table: torch.Tensor, pos_begin: torch.Tensor, pos_end: torch.Tensor, stream=None):
+    name = "oscar_promote_int4"
+    _want_int4(name, layout, src)
+    _want_bf16(name, layout, dst)
+    batch, max_pages = _want_tables(name, int4_page_table, bf16_page_table)
+    _want(name, "pos_begin", pos_begin, torch.int32, (batch,))
+    _want(name, "pos_end", pos_end, torch.int32, (batch,))
+    _check(name, lib().oscar_promote_int4(
+        ctypes.byref(layout.c()), ctypes.byref(src.c()), _ptr(int4_page_table), ctypes.byref(dst.c()),
+        _ptr(bf16_page_table), max_pages, batch, _ptr(pos_begin), _ptr(pos_end), _stream(stream)))
+
+
+def oscar_suggest_splits_int4(layout: Layout, batch: int, max_hist_tokens: int, sm_count: int) -> int:
+    return int(lib().oscar_suggest_splits_int4(ctypes.byref(layout.c()), batch, max_hist_tokens, sm_count))
+
+
+def _want_attn4(name: str, layout: Layout, q, bf16_pool, bf16_page_table, int4_pool, int4_page_table, seq_len, hist_end):
+    _want_bf16(name, layout, bf16_pool)
+    _want_int4(name, layout, int4_pool)
+    batch, max_pages = _want_tables(name, int4_page_table, bf16_page_table)
+    _want(name, "q", q, torch.bfloat16, (batch, layout.n_q_heads, layout.head_dim))
+    _want(name, "seq_len", seq_len, torch.int32, (batch,))
+    _want(name, "hist_end", hist_end, torch.int32, (batch,))
+    return batch, max_pages
+
+
+def oscar_decode_attention_int4(layout: Layout, q: torch.Tensor, bf16_pool: Bf16Pool, bf16_page_table: torch.Tensor,
+                                int4_pool: Int4Pool, int4_page_table: torch.Tensor, seq_len: torch.Tensor,
+                                hist_end: torch.Tensor, sm_scale: float, partials: Partials,
+                                out: Optional[torch.Tensor] = None, out_f32: Optional[torch.Tensor] = None,
+                                lse: Optional[torch.Tensor] = None, merge_counters: Optional[torch.Tensor] = None,
+                                stream=None):
+    """Decode attention over [BF16 sink | INT4 history | BF16 recent]; with out or out_f32 also the merge, in the same
+    launch when merge_counters (int32 zeros [batch * n_kv_heads]) is given."""
+    name = "oscar_decode_attention_int4"
+    batch, max_pages = _want_attn4(name, layout, q, bf16_pool, bf16_page_table, int4_pool, int4_page_table, seq_len,
+                                   hist_end)
+    rows = (batch, layout.n_q_heads, partials.n_splits + 1)
+    _want(name, "partials m", partials.m, torch.float32, rows)
+    _want(name, "partials l", partials.l, torch.float32, rows)
+    _want(name, "partials acc", partials.acc, torch.float32, rows + (layout.head_dim,))
+    _want(name, "out", out, torch.bfloat16, q.shape)
+    _want(name, "out_f32", out_f32, torch.float32, q.shape)
+    _want(name, "lse", lse, torch.float32, rows[:2])
+    _want(name, "merge_counters", merge_counters, torch.int32, (batch * layout.n_kv_heads,))
+    _check(name, lib().oscar_decode_attention_int4(
+        ctypes.byref(layout.c()), _ptr(q), ctypes.byref(bf16_pool.c()), _ptr(bf16_page_table),
+        ctypes.byref(int4_pool.c()), _ptr(int4_page_table), max_pages, _ptr(seq_len), _ptr(hist_end), batch,
+        float(sm_scale), ctypes.byref(partials.c()), _ptr(out), _ptr(out_f32), _ptr(lse), _ptr(merge_counters),
+        _stream(stream)))
+
+
+def oscar_attention_mass_int4(layout: Layout, q: torch.Tensor, bf16_pool: Bf16Pool, bf16_page_table: torch.Tensor,
+                              int4_pool: Int4Pool, int4_page_table: torch.Tensor, seq_len: torch.Tensor,
+                              hist_end: torch.Tensor, sm_scale: float, lse: torch.Tensor, mass: torch.Tensor,
+                              stream=None):
+    """Add the attention weight of this step to mass [batch, Hkv, max_pages * page_size] (fp32)."""
+    name = "oscar_attention_mass_int4"
+    batch, max_pages = _want_attn4(name, layout, q, bf16_pool, bf16_page_table, int4_pool, int4_page_table, seq_len,
+                                   hist_end)
+    _want(name, "lse", lse, torch.float32, (batch, layout.n_q_heads))
+    _want(name, "mass", mass, torch.float32, (batch, layout.n_kv_heads, max_pages * layout.page_size))
+    _check(name, lib().oscar_attention_mass_int4(
+        ctypes.byref(layout.c()), _ptr(q), ctypes.byref(bf16_pool.c()), _ptr(bf16_page_table),
+        ctypes.byref(int4_pool.c()), _ptr(int4_page_table), max_pages, _ptr(seq_len), _ptr(hist_end), batch,
+        float(sm_scale), _ptr(lse), _ptr(mass), _stream(stream)))
+
+
+def oscar_evict_int4(layout: Layout, src: Int4Pool, src_page_table: torch.Tensor, dst: Int4Pool,
+                     dst_page_table: torch.Tensor, seq_len: torch.Tensor, hist_end: torch.Tensor, keep: torch.Tensor,
+                     mass: torch.Tensor, mass_out: torch.Tensor, kept: torch.Tensor, stream=None):
+    """Keep the keep[b] history positions of largest mass of each kv head; their rows go to the pages of
+    dst_page_table, their old positions to kept [batch, Hkv, at least max(keep)] (int32)."""
+    name = "oscar_evict_int4"
+    _want_int4(name, layout, src)
+    _want_int4(name, layout, dst)
+    batch, max_pages = _want_tables(name, src_page_table, dst_page_table)
+    for what, t in (("seq_len", seq_len), ("hist_end", hist_end), ("keep", keep)):
+        _want(name, what, t, torch.int32, (batch,))
+    weights = (batch, layout.n_kv_heads, max_pages * layout.page_size)
+    _want(name, "mass", mass, torch.float32, weights)
+    _want(name, "mass_out", mass_out, torch.float32, weights)
+    _want(name, "kept", kept, torch.int32, weights[:2] + (kept.shape[-1],))
+    _check(name, lib().oscar_evict_int4(
+        ctypes.byref(layout.c()), ctypes.byref(src.c()), _ptr(src_page_table), ctypes.byref(dst.c()),
+        _ptr(dst_page_table), max_pages, batch, _ptr(seq_len), _ptr(hist_end), _ptr(keep), _ptr(mass), _ptr(mass_out),
+        _ptr(kept), int(kept.shape[-1]), _stream(stream)))
 
 
 def oscar_get_device_status(stream=None) -> int:

@@ -104,6 +104,26 @@ oscar_status_t check_partials(const oscar_partials_t *p) {
     return OSCAR_OK;
 }
 
+oscar_status_t check_int4_pool(const oscar_layout_t *L, const oscar_int4_pool_t *p) {
+    if (!p) return fail(OSCAR_ERR_INVALID_ARG, "INT4 pool is NULL");
+    if (!p->codes_k || !p->codes_v || !p->scale_zero) return fail(OSCAR_ERR_INVALID_ARG, "INT4 pool has a NULL array");
+    if (!aligned16(p->codes_k) || !aligned16(p->codes_v) || !aligned16(p->scale_zero))
+        return fail(OSCAR_ERR_INVALID_ARG, "INT4 pool array not 16-byte aligned");
+    if (p->n_pages < 1) return fail(OSCAR_ERR_INVALID_ARG, "INT4 pool n_pages %d < 1", p->n_pages);
+    if ((long long)p->n_pages * L->n_kv_heads * L->page_size > 2147483647LL)
+        return fail(OSCAR_ERR_INVALID_ARG, "INT4 pool: n_pages %d times kv heads and page size passes 2^31", p->n_pages);
+    return OSCAR_OK;
+}
+
+// Page tables [batch][max_pages] of the INT4 calls: positions are int32.
+oscar_status_t check_tables(const oscar_layout_t *L, int32_t max_pages, int32_t batch) {
+    if (batch < 0 || batch > 65535) return fail(OSCAR_ERR_INVALID_ARG, "batch %d outside 0..65535", batch);
+    if (max_pages < 1) return fail(OSCAR_ERR_INVALID_ARG, "max_pages_per_req %d < 1", max_pages);
+    if ((long long)max_pages * L->page_size > 2147483647LL - 64)
+        return fail(OSCAR_ERR_INVALID_ARG, "max_pages_per_req %d: positions pass int32", max_pages);
+    return OSCAR_OK;
+}
+
 #define TRY(x)                                \
     do {                                      \
         oscar_status_t s_ = (x);              \
@@ -114,6 +134,9 @@ oscar::Int2PoolView int2_view(const oscar_int2_pool_t *p) {
     return {p->codes_k, p->codes_v, p->scale_k, p->zero_k, p->scale_v, p->zero_v, p->n_pages};
 }
 oscar::Bf16PoolView bf16_view(const oscar_bf16_pool_t *p) { return {p->k, p->v, p->n_pages}; }
+oscar::Int4PoolView int4_view(const oscar_int4_pool_t *p) {
+    return {p->codes_k, p->codes_v, p->scale_zero, p->n_pages};
+}
 oscar::PartialsView part_view(const oscar_partials_t *p) { return {p->m, p->l, p->acc, p->n_splits}; }
 
 }  // namespace
@@ -451,6 +474,151 @@ oscar_status_t oscar_bf16_decode_attention(const oscar_layout_t *layout, const u
                                                     seq_len, nullptr, batch, sm_scale, part_view(partials), 1,
                                                     status_ptr(), (cudaStream_t)stream),
                        "BF16 attention launch");
+}
+
+oscar_status_t oscar_append_kv(const oscar_layout_t *layout, const uint16_t *q, int64_t q_stride, const uint16_t *k,
+                               int64_t k_stride, const uint16_t *v, int64_t v_stride, int32_t n,
+                               const uint16_t *q_weight, const uint16_t *k_weight, float eps, const float *rope,
+                               int32_t rope_rows, int32_t rot_dim, int32_t interleaved, const oscar_bf16_pool_t *pool,
+                               const int32_t *page_table, int32_t max_pages_per_req, int32_t batch,
+                               const int32_t *req_idx, const int32_t *positions, const int32_t *rope_positions,
+                               uint16_t *q_out, void *stream) {
+    TRY(check_layout(layout));
+    TRY(check_bf16_pool(pool));
+    TRY(check_tables(layout, max_pages_per_req, batch));
+    if (n < 0 || n > 65535 * 256) return fail(OSCAR_ERR_INVALID_ARG, "n %d outside 0..%d", n, 65535 * 256);
+    if (n == 0) return OSCAR_OK;
+    if (batch < 1) return fail(OSCAR_ERR_INVALID_ARG, "batch %d < 1", batch);
+    if (!k || !v || !page_table || !req_idx || !positions) return fail(OSCAR_ERR_INVALID_ARG, "NULL argument");
+    if (!q != !q_out) return fail(OSCAR_ERR_INVALID_ARG, "q and q_out: both or neither");
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned16(q_weight) ||
+        !aligned16(k_weight) || !aligned16(rope))
+        return fail(OSCAR_ERR_INVALID_ARG, "q, k, v, q_out, weights and rope must be 16-byte aligned");
+    const int64_t q_row = (int64_t)layout->n_kv_heads * layout->gqa * 128, kv_row = (int64_t)layout->n_kv_heads * 128;
+    if ((q && (q_stride % 8 || q_stride < q_row)) || k_stride % 8 || k_stride < kv_row || v_stride % 8 || v_stride < kv_row)
+        return fail(OSCAR_ERR_INVALID_ARG, "token strides must be multiples of 8 and at least a token's heads");
+    if (q && q == q_out && q_stride != q_row)
+        return fail(OSCAR_ERR_INVALID_ARG, "q_out may be q only where q_stride is a token's heads");
+    if ((q_weight || k_weight) && !(eps >= 0.0f && std::isfinite(eps)))
+        return fail(OSCAR_ERR_INVALID_ARG, "eps must be finite and not negative");
+    if (rope) {
+        if (rot_dim < 16 || rot_dim > 128 || rot_dim % 16)
+            return fail(OSCAR_ERR_INVALID_ARG, "rot_dim %d: a multiple of 16 in 16..128", rot_dim);
+        if (rope_rows < 1) return fail(OSCAR_ERR_INVALID_ARG, "rope_rows %d < 1", rope_rows);
+    }
+    return cuda_status(oscar::launch_append(*layout, {q, k, v, q_stride, k_stride, v_stride}, n, q_weight, k_weight, eps,
+                                            rope, rope_rows, rot_dim, interleaved != 0, bf16_view(pool), page_table,
+                                            max_pages_per_req, batch, req_idx, positions, rope_positions, q_out,
+                                            status_ptr(), (cudaStream_t)stream),
+                       "oscar_append_kv launch");
+}
+
+oscar_status_t oscar_demote_int4(const oscar_layout_t *layout, const oscar_bf16_pool_t *src,
+                                 const int32_t *bf16_page_table, const oscar_int4_pool_t *dst,
+                                 const int32_t *int4_page_table, int32_t max_pages_per_req, int32_t batch,
+                                 const int32_t *pos_begin, const int32_t *pos_end, float c_K, float c_V,
+                                 void *stream) {
+    TRY(check_layout(layout));
+    TRY(check_bf16_pool(src));
+    TRY(check_int4_pool(layout, dst));
+    TRY(check_tables(layout, max_pages_per_req, batch));
+    if (batch == 0) return OSCAR_OK;
+    if (!bf16_page_table || !int4_page_table || !pos_begin || !pos_end)
+        return fail(OSCAR_ERR_INVALID_ARG, "NULL page table or range");
+    if (!(c_K > 0.0f) || !(c_V > 0.0f)) return fail(OSCAR_ERR_INVALID_ARG, "clip ratios must be > 0");
+    return cuda_status(oscar::launch_demote4(*layout, bf16_view(src), bf16_page_table, int4_view(dst), int4_page_table,
+                                             max_pages_per_req, batch, pos_begin, pos_end, c_K, c_V, status_ptr(),
+                                             (cudaStream_t)stream),
+                       "oscar_demote_int4 launch");
+}
+
+oscar_status_t oscar_promote_int4(const oscar_layout_t *layout, const oscar_int4_pool_t *src,
+                                  const int32_t *int4_page_table, const oscar_bf16_pool_t *dst,
+                                  const int32_t *bf16_page_table, int32_t max_pages_per_req, int32_t batch,
+                                  const int32_t *pos_begin, const int32_t *pos_end, void *stream) {
+    TRY(check_layout(layout));
+    TRY(check_int4_pool(layout, src));
+    TRY(check_bf16_pool(dst));
+    TRY(check_tables(layout, max_pages_per_req, batch));
+    if (batch == 0) return OSCAR_OK;
+    if (!bf16_page_table || !int4_page_table || !pos_begin || !pos_end)
+        return fail(OSCAR_ERR_INVALID_ARG, "NULL page table or range");
+    return cuda_status(oscar::launch_promote4(*layout, int4_view(src), int4_page_table, bf16_view(dst), bf16_page_table,
+                                              max_pages_per_req, batch, pos_begin, pos_end, status_ptr(),
+                                              (cudaStream_t)stream),
+                       "oscar_promote_int4 launch");
+}
+
+int32_t oscar_suggest_splits_int4(const oscar_layout_t *L, int32_t batch, int32_t max_hist_tokens, int32_t sm_count) {
+    if (!L || L->n_kv_heads <= 0 || batch <= 0 || max_hist_tokens <= 0 || sm_count <= 0) return 1;
+    return oscar::suggest_splits4(*L, batch, max_hist_tokens, sm_count);
+}
+
+oscar_status_t oscar_decode_attention_int4(const oscar_layout_t *layout, const uint16_t *q,
+                                           const oscar_bf16_pool_t *bf16_pool, const int32_t *bf16_page_table,
+                                           const oscar_int4_pool_t *int4_pool, const int32_t *int4_page_table,
+                                           int32_t max_pages_per_req, const int32_t *seq_len, const int32_t *hist_end,
+                                           int32_t batch, float sm_scale, const oscar_partials_t *partials,
+                                           uint16_t *out, float *out_f32, float *lse, int32_t *merge_counters,
+                                           void *stream) {
+    TRY(check_layout(layout));
+    TRY(check_bf16_pool(bf16_pool));
+    TRY(check_int4_pool(layout, int4_pool));
+    TRY(check_partials(partials));
+    TRY(check_tables(layout, max_pages_per_req, batch));
+    if (batch == 0) return OSCAR_OK;
+    if (!q || !bf16_page_table || !int4_page_table || !seq_len || !hist_end)
+        return fail(OSCAR_ERR_INVALID_ARG, "NULL argument");
+    if (!aligned16(q)) return fail(OSCAR_ERR_INVALID_ARG, "q not 16-byte aligned");
+    if (lse && !out && !out_f32) return fail(OSCAR_ERR_INVALID_ARG, "lse needs out or out_f32");
+    const oscar::Attn4Input in{q, bf16_view(bf16_pool), bf16_page_table, int4_view(int4_pool), int4_page_table,
+                               max_pages_per_req, seq_len, hist_end, sm_scale};
+    return cuda_status(oscar::launch_decode4(*layout, in, batch, part_view(partials), out, out_f32, lse, merge_counters,
+                                             status_ptr(), (cudaStream_t)stream),
+                       "oscar_decode_attention_int4 launch");
+}
+
+oscar_status_t oscar_attention_mass_int4(const oscar_layout_t *layout, const uint16_t *q,
+                                         const oscar_bf16_pool_t *bf16_pool, const int32_t *bf16_page_table,
+                                         const oscar_int4_pool_t *int4_pool, const int32_t *int4_page_table,
+                                         int32_t max_pages_per_req, const int32_t *seq_len, const int32_t *hist_end,
+                                         int32_t batch, float sm_scale, const float *lse, float *mass, void *stream) {
+    TRY(check_layout(layout));
+    TRY(check_bf16_pool(bf16_pool));
+    TRY(check_int4_pool(layout, int4_pool));
+    TRY(check_tables(layout, max_pages_per_req, batch));
+    if (batch == 0) return OSCAR_OK;
+    if (!q || !bf16_page_table || !int4_page_table || !seq_len || !hist_end || !lse || !mass)
+        return fail(OSCAR_ERR_INVALID_ARG, "NULL argument");
+    if (!aligned16(q)) return fail(OSCAR_ERR_INVALID_ARG, "q not 16-byte aligned");
+    const oscar::Attn4Input in{q, bf16_view(bf16_pool), bf16_page_table, int4_view(int4_pool), int4_page_table,
+                               max_pages_per_req, seq_len, hist_end, sm_scale};
+    return cuda_status(oscar::launch_mass4(*layout, in, batch, lse, mass, status_ptr(), (cudaStream_t)stream),
+                       "oscar_attention_mass_int4 launch");
+}
+
+oscar_status_t oscar_evict_int4(const oscar_layout_t *layout, const oscar_int4_pool_t *src,
+                                const int32_t *src_page_table, const oscar_int4_pool_t *dst,
+                                const int32_t *dst_page_table, int32_t max_pages_per_req, int32_t batch,
+                                const int32_t *seq_len, const int32_t *hist_end, const int32_t *keep, const float *mass,
+                                float *mass_out, int32_t *kept, int32_t kept_stride, void *stream) {
+    TRY(check_layout(layout));
+    TRY(check_int4_pool(layout, src));
+    TRY(check_int4_pool(layout, dst));
+    TRY(check_tables(layout, max_pages_per_req, batch));
+    if (batch == 0) return OSCAR_OK;
+    if (!src_page_table || !dst_page_table || !seq_len || !hist_end || !keep || !mass || !mass_out || !kept)
+        return fail(OSCAR_ERR_INVALID_ARG, "NULL argument");
+    if (kept_stride < 1) return fail(OSCAR_ERR_INVALID_ARG, "kept_stride %d < 1", kept_stride);
+    if (src_page_table == dst_page_table && src->codes_k == dst->codes_k)
+        return fail(OSCAR_ERR_INVALID_ARG, "the kept rows need pages of their own: src and dst are the same pages");
+    const size_t floats = (size_t)batch * layout->n_kv_heads * max_pages_per_req * layout->page_size;
+    if (mass < mass_out + floats && mass_out < mass + floats)
+        return fail(OSCAR_ERR_INVALID_ARG, "mass and mass_out overlap");
+    return cuda_status(oscar::launch_evict(*layout, int4_view(src), src_page_table, int4_view(dst), dst_page_table,
+                                           max_pages_per_req, batch, seq_len, hist_end, keep, mass, mass_out, kept,
+                                           kept_stride, status_ptr(), (cudaStream_t)stream),
+                       "oscar_evict_int4 launch");
 }
 
 oscar_status_t oscar_get_device_status(int32_t *status_bits, void *stream) {
