@@ -425,45 +425,84 @@ def oscar_decode_attention_noalloc(layout: Layout, q: torch.Tensor, q_rot: torch
         _ptr(lse), _stream(stream)))
 
 
-def _want(name: str, what: str, t: Optional[torch.Tensor], dtype, shape):
-    """One argument's dtype, shape and place (None: an argument left out)."""
-    if t is None:
-        return
-    if t.dtype != dtype:
+# ---- the 4-bit history.  These calls check every argument's type, shape and device, and are made once per layer and
+# token: a check reads each property once and returns the address, and the layout's descriptor is built once.
+
+_bf16, _f32, _i32, _u8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+
+
+def _refuse(name: str, what: str, t: torch.Tensor, dtype, shape, dev: int):
+    if t.dtype is not dtype:
         raise OscarError(f"{name}: {what} must be {dtype}, not {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise OscarError(f"{name}: {what} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+    if not t.is_cuda or t.get_device() != dev:
         raise OscarError(f"{name}: {what} is on {t.device}, not on the current CUDA device")
+    raise OscarError(f"{name}: {what} must be contiguous")
 
 
-def _want_int4(name: str, layout: Layout, pool: Int4Pool):
-    shp = (pool.n_pages, layout.n_kv_heads, layout.page_size)
-    _want(name, "codes_k", pool.codes_k, torch.uint8, shp + (layout.head_dim // 2,))
-    _want(name, "codes_v", pool.codes_v, torch.uint8, shp + (layout.head_dim // 2,))
-    _want(name, "scale_zero", pool.scale_zero, torch.bfloat16, shp + (layout.head_dim // layout.group, 4))
+def _at(name: str, what: str, t: Optional[torch.Tensor], dtype, shape, dev: int):
+    """The address of a contiguous tensor of this type and shape on device dev (None: an argument left out)."""
+    if t is None:
+        return None
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(name, what, t, dtype, shape, dev)
 
 
-def _want_bf16(name: str, layout: Layout, pool: Bf16Pool):
-    shp = (pool.n_pages, layout.page_size, layout.n_kv_heads, layout.head_dim)
-    _want(name, "pool k", pool.k, torch.bfloat16, shp)
-    _want(name, "pool v", pool.v, torch.bfloat16, shp)
+def _device() -> int:
+    try:
+        return torch.cuda.current_device()
+    except (RuntimeError, AssertionError) as e:
+        raise OscarError("no current CUDA device") from e
 
 
-def _want_tables(name: str, a: torch.Tensor, b: torch.Tensor):
-    if a.dim() != 2:
+def _stream_on(name: str, stream, dev: int) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device.index != dev:
+        raise OscarError(f"{name}: the stream belongs to {stream.device}, not to the current CUDA device")
+    return stream.cuda_stream
+
+
+def _layout_ref(layout: Layout):
+    """The layout's descriptor by reference, built once (a Layout does not change)."""
+    ref = layout.__dict__.get("_ref")
+    if ref is None:
+        ref = ctypes.byref(layout.c())
+        object.__setattr__(layout, "_ref", ref)
+    return ref
+
+
+def _bf16_ref(name: str, layout: Layout, pool: Bf16Pool, dev: int):
+    n = pool.k.shape[0]
+    shape = (n, layout.page_size, layout.n_kv_heads, layout.head_dim)
+    return ctypes.byref(Bf16PoolC(_at(name, "pool k", pool.k, _bf16, shape, dev),
+                                  _at(name, "pool v", pool.v, _bf16, shape, dev), n))
+
+
+def _int4_ref(name: str, layout: Layout, pool: Int4Pool, dev: int):
+    n, H, ps, D = pool.codes_k.shape[0], layout.n_kv_heads, layout.page_size, layout.head_dim
+    shape = (n, H, ps, D // 2)
+    return ctypes.byref(Int4PoolC(_at(name, "codes_k", pool.codes_k, _u8, shape, dev),
+                                  _at(name, "codes_v", pool.codes_v, _u8, shape, dev),
+                                  _at(name, "scale_zero", pool.scale_zero, _bf16, (n, H, ps, D // layout.group, 4), dev), n))
+
+
+def _table_shape(name: str, t: torch.Tensor):
+    if t.dim() != 2:
         raise OscarError(f"{name}: page tables must be [batch, max_pages]")
-    _want(name, "page table", a, torch.int32, a.shape)
-    _want(name, "page table", b, torch.int32, a.shape)
-    return a.shape
+    return t.shape
 
 
-def _heads(name: str, what: str, t: torch.Tensor, heads: int, n: int, D: int):
+def _heads(name: str, what: str, t: torch.Tensor, heads: int, n: int, D: int, dev: int):
     """(address, token stride) of [n, heads, D] bf16 whose heads of one token lie together (a slice of a packed row)."""
-    _want(name, what, t, torch.bfloat16, (n, heads, D))
-    if n and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != D)):
+    if not (t.dtype is _bf16 and t.shape == (n, heads, D) and t.get_device() == dev):
+        _refuse(name, what, t, _bf16, (n, heads, D), dev)
+    s0, s1, s2 = t.stride()
+    if n and (s2 != 1 or (heads > 1 and s1 != D)):
         raise OscarError(f"{name}: the heads of one token of {what} must lie together")
-    return vp(t.data_ptr()), (t.stride(0) if n > 1 else max(t.stride(0), heads * D))
+    return t.data_ptr(), (s0 if n > 1 else heads * D)
 
 
 def oscar_append_kv(layout: Layout, q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, pool: Bf16Pool,
@@ -474,66 +513,61 @@ def oscar_append_kv(layout: Layout, q: Optional[torch.Tensor], k: torch.Tensor, 
                     stream=None):
     """New tokens' heads (q [n, Hq, D], k and v [n, Hkv, D] bf16, token rows possibly strided): RMS norm per head,
     rotary position, q to q_out and k, v to the tokens' slots of the BF16 pool."""
-    name, n, D = "oscar_append_kv", int(k.shape[0]), layout.head_dim
-    _want_bf16(name, layout, pool)
-    batch, max_pages = _want_tables(name, page_table, page_table)
-    for what, t in (("req_idx", req_idx), ("positions", positions), ("rope_positions", rope_positions)):
-        _want(name, what, t, torch.int32, (n,))
-    _want(name, "q_weight", q_weight, torch.bfloat16, (D,))
-    _want(name, "k_weight", k_weight, torch.bfloat16, (D,))
-    _want(name, "q_out", q_out, torch.bfloat16, (n, layout.n_q_heads, D))
-    if rope is not None:
-        _want(name, "rope", rope, torch.float32, (rope.shape[0], 128))
-    qp, qs = _heads(name, "q", q, layout.n_q_heads, n, D) if q is not None else (None, 0)
-    kp, ks = _heads(name, "k", k, layout.n_kv_heads, n, D)
-    vv, vs = _heads(name, "v", v, layout.n_kv_heads, n, D)
+    name, dev, n, D, Hq, H = "oscar_append_kv", _device(), k.shape[0], layout.head_dim, layout.n_q_heads, layout.n_kv_heads
+    pool_ref = _bf16_ref(name, layout, pool, dev)
+    batch, max_pages = shape = _table_shape(name, page_table)
+    rows = 0 if rope is None else rope.shape[0]
+    qp, qs = _heads(name, "q", q, Hq, n, D, dev) if q is not None else (None, 0)
+    kp, ks = _heads(name, "k", k, H, n, D, dev)
+    vv, vs = _heads(name, "v", v, H, n, D, dev)
     _check(name, lib().oscar_append_kv(
-        ctypes.byref(layout.c()), qp, qs, kp, ks, vv, vs, n, _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(rope),
-        0 if rope is None else int(rope.shape[0]), int(rot_dim), int(bool(interleaved)), ctypes.byref(pool.c()),
-        _ptr(page_table), max_pages, batch, _ptr(req_idx), _ptr(positions), _ptr(rope_positions), _ptr(q_out),
-        _stream(stream)))
+        _layout_ref(layout), qp, qs, kp, ks, vv, vs, n, _at(name, "q_weight", q_weight, _bf16, (D,), dev),
+        _at(name, "k_weight", k_weight, _bf16, (D,), dev), eps, _at(name, "rope", rope, _f32, (rows, 128), dev), rows,
+        rot_dim, 1 if interleaved else 0, pool_ref, _at(name, "page_table", page_table, _i32, shape, dev), max_pages,
+        batch, _at(name, "req_idx", req_idx, _i32, (n,), dev), _at(name, "positions", positions, _i32, (n,), dev),
+        _at(name, "rope_positions", rope_positions, _i32, (n,), dev), _at(name, "q_out", q_out, _bf16, (n, Hq, D), dev),
+        _stream_on(name, stream, dev)))
 
 
 def oscar_demote_int4(layout: Layout, src: Bf16Pool, bf16_page_table: torch.Tensor, dst: Int4Pool,
                       int4_page_table: torch.Tensor, pos_begin: torch.Tensor, pos_end: torch.Tensor, c_K: float = 1.0,
                       c_V: float = 1.0, stream=None):
-    name = "oscar_demote_int4"
-    _want_bf16(name, layout, src)
-    _want_int4(name, layout, dst)
-    batch, max_pages = _want_tables(name, int4_page_table, bf16_page_table)
-    _want(name, "pos_begin", pos_begin, torch.int32, (batch,))
-    _want(name, "pos_end", pos_end, torch.int32, (batch,))
+    """BF16 rows at positions [pos_begin[b], pos_end[b]) (int32 [batch]) to 4 bits, as they are stored."""
+    name, dev = "oscar_demote_int4", _device()
+    batch, max_pages = shape = _table_shape(name, int4_page_table)
     _check(name, lib().oscar_demote_int4(
-        ctypes.byref(layout.c()), ctypes.byref(src.c()), _ptr(bf16_page_table), ctypes.byref(dst.c()),
-        _ptr(int4_page_table), max_pages, batch, _ptr(pos_begin), _ptr(pos_end), float(c_K), float(c_V),
-        _stream(stream)))
+        _layout_ref(layout), _bf16_ref(name, layout, src, dev), _at(name, "bf16_page_table", bf16_page_table, _i32, shape, dev),
+        _int4_ref(name, layout, dst, dev), _at(name, "int4_page_table", int4_page_table, _i32, shape, dev), max_pages,
+        batch, _at(name, "pos_begin", pos_begin, _i32, (batch,), dev), _at(name, "pos_end", pos_end, _i32, (batch,), dev),
+        c_K, c_V, _stream_on(name, stream, dev)))
 
 
 def oscar_promote_int4(layout: Layout, src: Int4Pool, int4_page_table: torch.Tensor, dst: Bf16Pool,
                        bf16_page_table: torch.Tensor, pos_begin: torch.Tensor, pos_end: torch.Tensor, stream=None):
-    name = "oscar_promote_int4"
-    _want_int4(name, layout, src)
-    _want_bf16(name, layout, dst)
-    batch, max_pages = _want_tables(name, int4_page_table, bf16_page_table)
-    _want(name, "pos_begin", pos_begin, torch.int32, (batch,))
-    _want(name, "pos_end", pos_end, torch.int32, (batch,))
+    """4-bit rows at positions [pos_begin[b], pos_end[b]) back to BF16."""
+    name, dev = "oscar_promote_int4", _device()
+    batch, max_pages = shape = _table_shape(name, int4_page_table)
     _check(name, lib().oscar_promote_int4(
-        ctypes.byref(layout.c()), ctypes.byref(src.c()), _ptr(int4_page_table), ctypes.byref(dst.c()),
-        _ptr(bf16_page_table), max_pages, batch, _ptr(pos_begin), _ptr(pos_end), _stream(stream)))
+        _layout_ref(layout), _int4_ref(name, layout, src, dev), _at(name, "int4_page_table", int4_page_table, _i32, shape, dev),
+        _bf16_ref(name, layout, dst, dev), _at(name, "bf16_page_table", bf16_page_table, _i32, shape, dev), max_pages,
+        batch, _at(name, "pos_begin", pos_begin, _i32, (batch,), dev), _at(name, "pos_end", pos_end, _i32, (batch,), dev),
+        _stream_on(name, stream, dev)))
 
 
 def oscar_suggest_splits_int4(layout: Layout, batch: int, max_hist_tokens: int, sm_count: int) -> int:
     return int(lib().oscar_suggest_splits_int4(ctypes.byref(layout.c()), batch, max_hist_tokens, sm_count))
 
 
-def _want_attn4(name: str, layout: Layout, q, bf16_pool, bf16_page_table, int4_pool, int4_page_table, seq_len, hist_end):
-    _want_bf16(name, layout, bf16_pool)
-    _want_int4(name, layout, int4_pool)
-    batch, max_pages = _want_tables(name, int4_page_table, bf16_page_table)
-    _want(name, "q", q, torch.bfloat16, (batch, layout.n_q_heads, layout.head_dim))
-    _want(name, "seq_len", seq_len, torch.int32, (batch,))
-    _want(name, "hist_end", hist_end, torch.int32, (batch,))
-    return batch, max_pages
+def _attention4(name: str, layout: Layout, q, bf16_pool, bf16_page_table, int4_pool, int4_page_table, seq_len, hist_end,
+                sm_scale: float, dev: int):
+    """The arguments that decode attention and the attention weights share."""
+    batch, max_pages = shape = _table_shape(name, int4_page_table)
+    return batch, max_pages, (
+        _layout_ref(layout), _at(name, "q", q, _bf16, (batch, layout.n_q_heads, layout.head_dim), dev),
+        _bf16_ref(name, layout, bf16_pool, dev), _at(name, "bf16_page_table", bf16_page_table, _i32, shape, dev),
+        _int4_ref(name, layout, int4_pool, dev), _at(name, "int4_page_table", int4_page_table, _i32, shape, dev), max_pages,
+        _at(name, "seq_len", seq_len, _i32, (batch,), dev), _at(name, "hist_end", hist_end, _i32, (batch,), dev), batch,
+        sm_scale)
 
 
 def oscar_decode_attention_int4(layout: Layout, q: torch.Tensor, bf16_pool: Bf16Pool, bf16_page_table: torch.Tensor,
@@ -544,22 +578,17 @@ def oscar_decode_attention_int4(layout: Layout, q: torch.Tensor, bf16_pool: Bf16
                                 stream=None):
     """Decode attention over [BF16 sink | INT4 history | BF16 recent]; with out or out_f32 also the merge, in the same
     launch when merge_counters (int32 zeros [batch * n_kv_heads]) is given."""
-    name = "oscar_decode_attention_int4"
-    batch, max_pages = _want_attn4(name, layout, q, bf16_pool, bf16_page_table, int4_pool, int4_page_table, seq_len,
-                                   hist_end)
-    rows = (batch, layout.n_q_heads, partials.n_splits + 1)
-    _want(name, "partials m", partials.m, torch.float32, rows)
-    _want(name, "partials l", partials.l, torch.float32, rows)
-    _want(name, "partials acc", partials.acc, torch.float32, rows + (layout.head_dim,))
-    _want(name, "out", out, torch.bfloat16, q.shape)
-    _want(name, "out_f32", out_f32, torch.float32, q.shape)
-    _want(name, "lse", lse, torch.float32, rows[:2])
-    _want(name, "merge_counters", merge_counters, torch.int32, (batch * layout.n_kv_heads,))
+    name, dev = "oscar_decode_attention_int4", _device()
+    batch, _, args = _attention4(name, layout, q, bf16_pool, bf16_page_table, int4_pool, int4_page_table, seq_len,
+                                 hist_end, sm_scale, dev)
+    D, heads, S = layout.head_dim, (batch, layout.n_q_heads), partials.n_splits
+    rows, full = heads + (S + 1,), heads + (D,)
+    part = PartialsC(_at(name, "partials m", partials.m, _f32, rows, dev), _at(name, "partials l", partials.l, _f32, rows, dev),
+                     _at(name, "partials acc", partials.acc, _f32, rows + (D,), dev), S)
     _check(name, lib().oscar_decode_attention_int4(
-        ctypes.byref(layout.c()), _ptr(q), ctypes.byref(bf16_pool.c()), _ptr(bf16_page_table),
-        ctypes.byref(int4_pool.c()), _ptr(int4_page_table), max_pages, _ptr(seq_len), _ptr(hist_end), batch,
-        float(sm_scale), ctypes.byref(partials.c()), _ptr(out), _ptr(out_f32), _ptr(lse), _ptr(merge_counters),
-        _stream(stream)))
+        *args, ctypes.byref(part), _at(name, "out", out, _bf16, full, dev), _at(name, "out_f32", out_f32, _f32, full, dev),
+        _at(name, "lse", lse, _f32, heads, dev),
+        _at(name, "merge_counters", merge_counters, _i32, (batch * layout.n_kv_heads,), dev), _stream_on(name, stream, dev)))
 
 
 def oscar_attention_mass_int4(layout: Layout, q: torch.Tensor, bf16_pool: Bf16Pool, bf16_page_table: torch.Tensor,
@@ -567,15 +596,13 @@ def oscar_attention_mass_int4(layout: Layout, q: torch.Tensor, bf16_pool: Bf16Po
                               hist_end: torch.Tensor, sm_scale: float, lse: torch.Tensor, mass: torch.Tensor,
                               stream=None):
     """Add the attention weight of this step to mass [batch, Hkv, max_pages * page_size] (fp32)."""
-    name = "oscar_attention_mass_int4"
-    batch, max_pages = _want_attn4(name, layout, q, bf16_pool, bf16_page_table, int4_pool, int4_page_table, seq_len,
-                                   hist_end)
-    _want(name, "lse", lse, torch.float32, (batch, layout.n_q_heads))
-    _want(name, "mass", mass, torch.float32, (batch, layout.n_kv_heads, max_pages * layout.page_size))
+    name, dev = "oscar_attention_mass_int4", _device()
+    batch, max_pages, args = _attention4(name, layout, q, bf16_pool, bf16_page_table, int4_pool, int4_page_table, seq_len,
+                                         hist_end, sm_scale, dev)
     _check(name, lib().oscar_attention_mass_int4(
-        ctypes.byref(layout.c()), _ptr(q), ctypes.byref(bf16_pool.c()), _ptr(bf16_page_table),
-        ctypes.byref(int4_pool.c()), _ptr(int4_page_table), max_pages, _ptr(seq_len), _ptr(hist_end), batch,
-        float(sm_scale), _ptr(lse), _ptr(mass), _stream(stream)))
+        *args, _at(name, "lse", lse, _f32, (batch, layout.n_q_heads), dev),
+        _at(name, "mass", mass, _f32, (batch, layout.n_kv_heads, max_pages * layout.page_size), dev),
+        _stream_on(name, stream, dev)))
 
 
 def oscar_evict_int4(layout: Layout, src: Int4Pool, src_page_table: torch.Tensor, dst: Int4Pool,
@@ -583,20 +610,16 @@ def oscar_evict_int4(layout: Layout, src: Int4Pool, src_page_table: torch.Tensor
                      mass: torch.Tensor, mass_out: torch.Tensor, kept: torch.Tensor, stream=None):
     """Keep the keep[b] history positions of largest mass of each kv head; their rows go to the pages of
     dst_page_table, their old positions to kept [batch, Hkv, at least max(keep)] (int32)."""
-    name = "oscar_evict_int4"
-    _want_int4(name, layout, src)
-    _want_int4(name, layout, dst)
-    batch, max_pages = _want_tables(name, src_page_table, dst_page_table)
-    for what, t in (("seq_len", seq_len), ("hist_end", hist_end), ("keep", keep)):
-        _want(name, what, t, torch.int32, (batch,))
-    weights = (batch, layout.n_kv_heads, max_pages * layout.page_size)
-    _want(name, "mass", mass, torch.float32, weights)
-    _want(name, "mass_out", mass_out, torch.float32, weights)
-    _want(name, "kept", kept, torch.int32, weights[:2] + (kept.shape[-1],))
+    name, dev = "oscar_evict_int4", _device()
+    batch, max_pages = shape = _table_shape(name, src_page_table)
+    weights, one, stride = (batch, layout.n_kv_heads, max_pages * layout.page_size), (batch,), kept.shape[-1]
     _check(name, lib().oscar_evict_int4(
-        ctypes.byref(layout.c()), ctypes.byref(src.c()), _ptr(src_page_table), ctypes.byref(dst.c()),
-        _ptr(dst_page_table), max_pages, batch, _ptr(seq_len), _ptr(hist_end), _ptr(keep), _ptr(mass), _ptr(mass_out),
-        _ptr(kept), int(kept.shape[-1]), _stream(stream)))
+        _layout_ref(layout), _int4_ref(name, layout, src, dev), _at(name, "src_page_table", src_page_table, _i32, shape, dev),
+        _int4_ref(name, layout, dst, dev), _at(name, "dst_page_table", dst_page_table, _i32, shape, dev), max_pages, batch,
+        _at(name, "seq_len", seq_len, _i32, one, dev), _at(name, "hist_end", hist_end, _i32, one, dev),
+        _at(name, "keep", keep, _i32, one, dev), _at(name, "mass", mass, _f32, weights, dev),
+        _at(name, "mass_out", mass_out, _f32, weights, dev),
+        _at(name, "kept", kept, _i32, (batch, layout.n_kv_heads, stride), dev), stride, _stream_on(name, stream, dev)))
 
 
 def oscar_get_device_status(stream=None) -> int:

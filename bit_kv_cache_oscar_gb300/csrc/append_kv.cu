@@ -45,10 +45,10 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 template <int U, bool PAIRS>
 __global__ void __launch_bounds__(kWarps * 32) append_kernel(AppendArgs a) {
     const int lane = threadIdx.x & 31, half = lane >> 4, hl = lane & 15;
-    const long long w = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    const int i = (int)(w / a.chunks);
+    const uint32_t w = blockIdx.x * kWarps + (threadIdx.x >> 5);       // below 2^32: n * chunks is (launch_append)
+    const int i = (int)(w / (uint32_t)a.chunks);
     if (i >= a.n) return;
-    const int row0 = (int)(w % a.chunks) * 2 * U + half;
+    const int row0 = (int)(w - (uint32_t)i * a.chunks) * 2 * U + half;
     const int rows = a.n_q + 2 * a.n_kv;
 
     uint4 x[U];
@@ -151,7 +151,11 @@ cudaError_t launch_append(const oscar_layout_t &L, const AppendInput &in, int n,
         kern<<<(unsigned)blocks, kWarps * 32, 0, st>>>(a);
         return cudaGetLastError();
     };
-    return pairs ? run(append_kernel<1, true>, 1) : run(append_kernel<1, false>, 1);
+    // Few tokens: one row a half-warp, so that a step's rows are all in flight on as many warps as there
+    // are.  Once four rows each still fill every SM with 32 warps, fewer warps with more loads each.
+    const bool many = (long long)n * ((rows + 7) / 8) >= 152 * 32;
+    if (pairs) return many ? run(append_kernel<4, true>, 4) : run(append_kernel<1, true>, 1);
+    return many ? run(append_kernel<4, false>, 4) : run(append_kernel<1, false>, 1);
 }
 
 }  // namespace oscar

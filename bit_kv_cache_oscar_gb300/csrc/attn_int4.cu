@@ -688,7 +688,7 @@ cudaError_t launch(const oscar_layout_t &L, const Attn4Input &in, Attn4Args a, i
 // different lengths finish evenly.  At least 8 blocks of 32 tokens (one a warp) for each split.
 int suggest_splits4(const oscar_layout_t &L, int batch, int max_hist, int sm_count) {
     const long long per = (long long)batch * L.n_kv_heads, slots = 2LL * sm_count;
-    long long want = per * 2 <= slots ? slots / per - 1 : (4 * slots + per - 1) / per;
+    long long want = per * 8 <= slots ? slots / per - 1 : (4 * slots + per - 1) / per;
     const long long most = ((long long)max_hist + kWarps * kBlock - 1) / (kWarps * kBlock);
     if (want > most) want = most;
     return (int)(want < 1 ? 1 : want > 1024 ? 1024 : want);

@@ -156,11 +156,14 @@ def test_the_binding_checks_types_shapes_and_places():
     i4 = ob.Int4Pool.empty(lay, 3, "cpu")
     bf = ob.Bf16Pool.empty(lay, 3, "cpu")
     pt, one = f(1, 4, t=torch.int32), f(1, t=torch.int32)
-    with pytest.raises(ob.OscarError, match="current CUDA device"):
+    with pytest.raises(ob.OscarError, match="current CUDA device"):      # CPU tensors, with and without a GPU
         ob.oscar_demote_int4(lay, bf, pt, i4, pt, one, one)
+    at = ob._at
     with pytest.raises(ob.OscarError, match="codes_v must have shape"):
-        ob._want("x", "codes_v", f(3, 2, 16, 32, t=torch.uint8), torch.uint8, (3, 2, 16, 64))
+        at("x", "codes_v", f(3, 2, 16, 32, t=torch.uint8), torch.uint8, (3, 2, 16, 64), 0)
     with pytest.raises(ob.OscarError, match="must be torch.int32"):
-        ob._want("x", "positions", f(4, t=torch.int64), torch.int32, (4,))
+        at("x", "positions", f(4, t=torch.int64), torch.int32, (4,), 0)
     with pytest.raises(ob.OscarError, match="page tables must be"):
-        ob._want_tables("x", one, one)
+        ob._table_shape("x", one)
+    with pytest.raises(ob.OscarError, match="lie together"):
+        ob._heads("x", "k", f(3, 128, 2, t=torch.bfloat16).transpose(1, 2), 2, 3, 128, -1)
