@@ -4,12 +4,17 @@
 // rot_dim channels by the token's angles, (a, b) -> (a cos - b sin, b cos + a sin); fp32 throughout,
 // one rounding to bf16.  Queries go to q_out, keys and values to their slots of the BF16 pool.
 //
-// A head's row is 256 bytes: 16 lanes with 8 channels each (one 16-byte load and store a lane), so
-// the sum of squares is a 4-step shuffle and a rotation partner is either in the lane (channels 2j,
-// 2j+1) or rot_dim/16 lanes away.  A warp takes 2·U rows of one token and loads them all before it
-// needs the first; the token's angles are read once for all of them.
+// Bound by HBM (a row is read and written once).  A head's row is 256 bytes: 16 lanes with 8 channels each
+// (one 16-byte load and store a lane), so the sum of squares is a 4-step shuffle and a rotation partner is
+// either in the lane (channels 2j, 2j+1) or rot_dim/16 lanes away.  A warp takes a run of row pairs of one
+// token, reads the token's angles once, and keeps two rows a half-warp in flight: each row's registers
+// are refilled as soon as it is computed.
 
-#include "oscar_internal.cuh"
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+#include "int4.cuh"
 
 namespace oscar {
 namespace {
@@ -19,143 +24,191 @@ constexpr int kWarps = 8;
 struct AppendArgs {
     const uint16_t *q, *k, *v;
     long long q_stride, k_stride, v_stride;
-    int n, n_q, n_kv, chunks;      // chunks: warps per token
+    int n, n_q, n_kv;
+    int per, runs;                 // row pairs of a warp, warps of a token
     const uint16_t *wq, *wk;
     float eps;
     const float *rope;
     int rope_rows, rot;
     Bf16PoolView pool;
     const int32_t *pt;
-    int max_pages, page_size, batch;
+    int max_pages, page_shift, batch;
     const int32_t *req, *pos, *rope_pos;
     uint16_t *q_out;
     int32_t *status;
 };
 
-__device__ __forceinline__ float lo16(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float hi16(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
-__device__ __forceinline__ void unpack8(uint4 w, float (&x)[8]) {
-    x[0] = lo16(w.x); x[1] = hi16(w.x); x[2] = lo16(w.y); x[3] = hi16(w.y);
-    x[4] = lo16(w.z); x[5] = hi16(w.z); x[6] = lo16(w.w); x[7] = hi16(w.w);
+// packed fp32 pairs
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ void unpair(uint64_t d, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(d)); }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+// the two bf16 of a word as an fp32 pair
+__device__ __forceinline__ uint64_t widen(uint32_t w) { return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)); }
+__device__ __forceinline__ void widen8(uint4 w, uint64_t (&x)[4]) {
+    x[0] = widen(w.x);
+    x[1] = widen(w.y);
+    x[2] = widen(w.z);
+    x[3] = widen(w.w);
 }
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
-    return (uint32_t)f32_to_bf16_rn(a) | ((uint32_t)f32_to_bf16_rn(b) << 16);
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-template <int U, bool PAIRS>
-__global__ void __launch_bounds__(kWarps * 32) append_kernel(AppendArgs a) {
-    const int lane = threadIdx.x & 31, half = lane >> 4, hl = lane & 15;
-    const uint32_t w = blockIdx.x * kWarps + (threadIdx.x >> 5);       // below 2^32: n * chunks is (launch_append)
-    const int i = (int)(w / (uint32_t)a.chunks);
-    if (i >= a.n) return;
-    const int row0 = (int)(w - (uint32_t)i * a.chunks) * 2 * U + half;
-    const int rows = a.n_q + 2 * a.n_kv;
+constexpr int kAhead = 2;
 
-    uint4 x[U];
+template <bool PAIRS>
+__global__ void __launch_bounds__(kWarps * 32, 4) append_kernel(AppendArgs a) {
+    const int lane = threadIdx.x & 31, half = lane >> 4, hl = lane & 15;
+    const uint32_t w = blockIdx.x * kWarps + (threadIdx.x >> 5);       // below 2^32: n * runs is (launch_append)
+    const int i = (int)(w / (uint32_t)a.runs);
+    if (i >= a.n) return;
+    const int rows = a.n_q + 2 * a.n_kv, pair0 = (int)(w - (uint32_t)i * a.runs) * a.per;
+    const int pairs = min(a.per, (rows + 1) / 2 - pair0);
+    const uint16_t *q = a.q + i * a.q_stride + 8 * hl, *k = a.k + i * a.k_stride - (long long)a.n_q * kHeadDim + 8 * hl;
+    const uint16_t *v = a.v + i * a.v_stride - (long long)(a.n_q + a.n_kv) * kHeadDim + 8 * hl;
+    auto load = [&](int j) {                       // row 2 (pair0 + j) + half
+        const int r = 2 * (pair0 + j) + half;
+        if (j >= pairs || r >= rows) return make_uint4(0, 0, 0, 0);
+        return *reinterpret_cast<const uint4 *>((r < a.n_q ? q : r < a.n_q + a.n_kv ? k : v) + (long long)r * kHeadDim);
+    };
+    uint4 x[kAhead];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int r = row0 + 2 * u;
-        const uint16_t *src = r < a.n_q            ? a.q + i * a.q_stride + (long long)r * kHeadDim
-                              : r < a.n_q + a.n_kv ? a.k + i * a.k_stride + (long long)(r - a.n_q) * kHeadDim
-                                                   : a.v + i * a.v_stride + (long long)(r - a.n_q - a.n_kv) * kHeadDim;
-        x[u] = r < rows ? *reinterpret_cast<const uint4 *>(src + 8 * hl) : make_uint4(0, 0, 0, 0);
-    }
+    for (int u = 0; u < kAhead; ++u) x[u] = load(u);
     const int pos = a.pos[i], b = a.req[i];
     if (pos == -1) return;                                        // padding
     const int rp = a.rope_pos ? a.rope_pos[i] : pos;
-    if (b < 0 || b >= a.batch || pos < 0 || pos / a.page_size >= a.max_pages ||
+    if (b < 0 || b >= a.batch || pos < 0 || (pos >> a.page_shift) >= a.max_pages ||
         (a.rope && (rp < 0 || rp >= a.rope_rows))) {
         if (lane == 0) flag_status(a.status, OSCAR_DEV_BAD_LENGTH);
         return;
     }
-    const int page = a.pt[(size_t)b * a.max_pages + pos / a.page_size];
-    const bool page_ok = page >= 0 && page < a.pool.n_pages;
-    if (!page_ok && lane == 0) flag_status(a.status, OSCAR_DEV_BAD_BF16_PAGE);
-    const size_t slot = ((size_t)(page_ok ? page : 0) * a.page_size + pos % a.page_size) * a.n_kv;
+    const int page = a.pt[(size_t)b * a.max_pages + (pos >> a.page_shift)];
 
-    // this lane's angles: pair j0 + e (channels 2j, 2j+1), or channels 8 hl + e of either half
+    // this lane's angles: pair 4 hl + e (channels 2j, 2j + 1), or those of channels 8 hl + e of either half
     const int rl = a.rot >> 4;                                    // lanes per rotated half
     const bool turns = a.rope && 8 * hl < a.rot;
-    float cs[8], sn[8];
-    if (turns) {
-        const float *t = a.rope + (size_t)rp * kHeadDim + (PAIRS ? 4 * hl : 8 * (hl < rl ? hl : hl - rl));
+    // channel pairs (8 hl + 2e, + 1) as fp32 pairs; lanes that do not turn get cos 1, sin 0
+    uint64_t cs[4], sn[4];
+    {
+        float c[8], z[8];
 #pragma unroll
-        for (int e = 0; e < (PAIRS ? 4 : 8); e += 4) {
-            const float4 c = *reinterpret_cast<const float4 *>(t + e), s = *reinterpret_cast<const float4 *>(t + 64 + e);
-            cs[e] = c.x; cs[e + 1] = c.y; cs[e + 2] = c.z; cs[e + 3] = c.w;
-            sn[e] = s.x; sn[e + 1] = s.y; sn[e + 2] = s.z; sn[e + 3] = s.w;
+        for (int e = 0; e < 8; ++e) {
+            c[e] = 1.f;
+            z[e] = 0.f;
+        }
+        if (turns) {
+            const float *t = a.rope + (size_t)rp * kHeadDim + (PAIRS ? 4 * hl : 8 * (hl < rl ? hl : hl - rl));
+#pragma unroll
+            for (int e = 0; e < (PAIRS ? 4 : 8); e += 4) {
+                const float4 cc = *reinterpret_cast<const float4 *>(t + e), ss = *reinterpret_cast<const float4 *>(t + 64 + e);
+                c[e] = cc.x; c[e + 1] = cc.y; c[e + 2] = cc.z; c[e + 3] = cc.w;
+                z[e] = ss.x; z[e + 1] = ss.y; z[e + 2] = ss.z; z[e + 3] = ss.w;
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (PAIRS) {                                          // (a, b)·cos + (b, a)·(-sin, sin)
+                cs[e] = pair(c[e], c[e]);
+                sn[e] = pair(-z[e], z[e]);
+            } else {
+                const float sg = hl < rl ? -1.f : 1.f;
+                cs[e] = pair(c[2 * e], c[2 * e + 1]);
+                sn[e] = pair(sg * z[2 * e], sg * z[2 * e + 1]);
+            }
         }
     }
     const int partner = (lane & 16) | (turns ? (hl < rl ? hl + rl : hl - rl) : hl);
+    const bool page_ok = (uint32_t)page < (uint32_t)a.pool.n_pages;
+    if (!page_ok && lane == 0) flag_status(a.status, OSCAR_DEV_BAD_BF16_PAGE);
+    const long long slot = (((long long)(page_ok ? page : 0) << a.page_shift) + (pos & ((1 << a.page_shift) - 1))) * a.n_kv;
+    uint16_t *qo = a.q_out + (size_t)i * a.n_q * kHeadDim + 8 * hl;
+    uint16_t *ko = const_cast<uint16_t *>(a.pool.k) + (slot - a.n_q) * kHeadDim + 8 * hl;
+    uint16_t *vo = const_cast<uint16_t *>(a.pool.v) + (slot - a.n_q - a.n_kv) * kHeadDim + 8 * hl;
 
+    const uint16_t *held = nullptr;                               // the norm weights now in wv
+    uint64_t wv[4];
+    for (int j0 = 0; j0 < pairs; j0 += kAhead) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int r = row0 + 2 * u;
-        const bool is_q = r < a.n_q, is_v = r >= a.n_q + a.n_kv;
-        float y[8];
-        unpack8(x[u], y);
-        float ss = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
-#pragma unroll
-        for (int o = 8; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        const uint16_t *wt = is_q ? a.wq : a.wk;
-        if (wt && !is_v) {
-            const float inv = rsqrtf(fmaf(ss, 1.f / kHeadDim, a.eps));
-            float wv[8];
-            unpack8(__ldg(reinterpret_cast<const uint4 *>(wt) + hl), wv);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = y[e] * inv * wv[e];
-        }
-        uint4 out = x[u];
-        if constexpr (PAIRS) {
-            if (turns) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float p = y[2 * e], s = y[2 * e + 1];
-                    y[2 * e] = fmaf(p, cs[e], -s * sn[e]);
-                    y[2 * e + 1] = fmaf(s, cs[e], p * sn[e]);
-                }
+        for (int u = 0; u < kAhead; ++u) {
+            const int r = 2 * (pair0 + j0 + u) + half;
+            const uint4 raw = x[u];
+            x[u] = load(j0 + u + kAhead);
+            if (j0 + u >= pairs) continue;                        // the whole warp
+            if (r - half >= a.n_q + a.n_kv) {                     // both rows are values: moved as they are
+                if (page_ok && r < rows) *reinterpret_cast<uint4 *>(vo + (long long)r * kHeadDim) = raw;
+                continue;
             }
-        } else {
-            float z[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) z[e] = __shfl_sync(0xffffffffu, y[e], partner);
-            if (turns) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = fmaf(y[e], cs[e], hl < rl ? -z[e] * sn[e] : z[e] * sn[e]);
+            const bool is_q = r < a.n_q, is_v = r >= a.n_q + a.n_kv;
+            uint64_t y[4];
+            widen8(raw, y);
+            const uint16_t *wt = is_q ? a.wq : a.wk;
+            if (wt != held) {
+                held = wt;
+                if (wt) widen8(__ldg(reinterpret_cast<const uint4 *>(wt) + hl), wv);
             }
+            uint64_t sq = mul2(y[0], y[0]);
+#pragma unroll
+            for (int e = 1; e < 4; ++e) sq = fma2(y[e], y[e], sq);
+            float ss, s1;
+            unpair(sq, ss, s1);
+            ss += s1;
+#pragma unroll
+            for (int o = 8; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            if (wt) {
+                const float inv = rsqrtf(fmaf(ss, 1.f / kHeadDim, a.eps));
+                const uint64_t inv2 = pair(inv, inv);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] = mul2(mul2(y[e], inv2), wv[e]);
+            }
+            uint32_t o[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float p, q2;
+                unpair(y[e], p, q2);
+                const uint64_t z = PAIRS ? pair(q2, p)
+                                         : pair(__shfl_sync(0xffffffffu, p, partner), __shfl_sync(0xffffffffu, q2, partner));
+                unpair(fma2(y[e], cs[e], mul2(z, sn[e])), p, q2);
+                o[e] = pack2(p, q2);
+            }
+            if (r >= rows || (!is_q && !page_ok)) continue;       // a half-warp; nothing below is shared
+            *reinterpret_cast<uint4 *>((is_q ? qo : is_v ? vo : ko) + (long long)r * kHeadDim) =
+                is_v ? raw : make_uint4(o[0], o[1], o[2], o[3]);
         }
-        if (!is_v) out = make_uint4(pack2(y[0], y[1]), pack2(y[2], y[3]), pack2(y[4], y[5]), pack2(y[6], y[7]));
-        if (r >= rows || (!is_q && !page_ok)) continue;
-        uint16_t *dst = is_q ? a.q_out + ((size_t)i * a.n_q + r) * kHeadDim
-                        : is_v ? const_cast<uint16_t *>(a.pool.v) + (slot + r - a.n_q - a.n_kv) * kHeadDim
-                               : const_cast<uint16_t *>(a.pool.k) + (slot + r - a.n_q) * kHeadDim;
-        *reinterpret_cast<uint4 *>(dst + 8 * hl) = out;
     }
 }
 
 }  // namespace
 
 cudaError_t launch_append(const oscar_layout_t &L, const AppendInput &in, int n, const uint16_t *wq, const uint16_t *wk,
-                          float eps, const float *rope, int rope_rows, int rot, bool pairs, Bf16PoolView pool,
+                          float eps, const float *rope, int rope_rows, int rot, bool pairs_interleaved, Bf16PoolView pool,
                           const int32_t *pt, int max_pages, int batch, const int32_t *req, const int32_t *pos,
                           const int32_t *rope_pos, uint16_t *q_out, int32_t *status, cudaStream_t st) {
     const int n_q = in.q ? L.n_kv_heads * L.gqa : 0;
-    AppendArgs a{in.q, in.k, in.v, in.q_stride, in.k_stride, in.v_stride, n, n_q, L.n_kv_heads, 0, wq, wk, eps, rope,
-                 rope_rows, rot, pool, pt, max_pages, L.page_size, batch, req, pos, rope_pos, q_out, status};
-    const int rows = n_q + 2 * L.n_kv_heads;
-    auto run = [&](auto kern, int U) {
-        a.chunks = (rows + 2 * U - 1) / (2 * U);
-        const long long blocks = ((long long)n * a.chunks + kWarps - 1) / kWarps;
-        kern<<<(unsigned)blocks, kWarps * 32, 0, st>>>(a);
-        return cudaGetLastError();
-    };
-    // Few tokens: one row a half-warp, so that a step's rows are all in flight on as many warps as there
-    // are.  Once four rows each still fill every SM with 32 warps, fewer warps with more loads each.
-    const bool many = (long long)n * ((rows + 7) / 8) >= 152 * 32;
-    if (pairs) return many ? run(append_kernel<4, true>, 4) : run(append_kernel<1, true>, 1);
-    return many ? run(append_kernel<4, false>, 4) : run(append_kernel<1, false>, 1);
+    const int pairs = (n_q + 2 * L.n_kv_heads + 1) / 2;
+    // A step's rows go to as many warps as there are row pairs; once whole tokens fill every SM with 32 warps
+    // (4864), a warp takes a whole token; between, runs that give about that many warps.
+    const int per = (int)std::max(1LL, std::min((long long)pairs, (long long)pairs * n / 4864));
+    const int runs = (pairs + per - 1) / per;
+    const AppendArgs a{in.q, in.k, in.v, in.q_stride, in.k_stride, in.v_stride, n, n_q, L.n_kv_heads, per, runs, wq, wk, eps,
+                       rope, rope_rows, rot, pool, pt, max_pages, page_shift(L), batch, req, pos, rope_pos, q_out, status};
+    const unsigned blocks = (unsigned)(((long long)n * runs + kWarps - 1) / kWarps);
+    if (pairs_interleaved) append_kernel<true><<<blocks, kWarps * 32, 0, st>>>(a);
+    else append_kernel<false><<<blocks, kWarps * 32, 0, st>>>(a);
+    return cudaGetLastError();
 }
 
 }  // namespace oscar

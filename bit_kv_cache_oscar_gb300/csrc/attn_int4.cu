@@ -57,7 +57,7 @@ struct Attn4Args {
     const uint16_t *sz;
     int i4_pages;
     const int32_t *ipt;
-    int max_pages, page_size, n_kv, sink;
+    int max_pages, page_shift, n_kv, sink;
     const int32_t *seq_len, *hist_end;
     float scale2;
     PartialsView out;
@@ -67,6 +67,7 @@ struct Attn4Args {
     const float *lse;          // weights only
     float *mass;
     int32_t *status;
+    int smem_bytes;            // from the aligned base on
 };
 
 __device__ __forceinline__ float lo16(uint32_t w) { return __uint_as_float(w << 16); }
@@ -108,7 +109,7 @@ template <int G, int NG, bool MASS>
 __device__ __forceinline__ void history_warp(const Attn4Args &a, const CUtensorMap *tmk, const CUtensorMap *tmv, uint8_t *ring,
                                              uint32_t bars, int b, int h, int split, int he, int warp, int lane, float *res) {
     using R = Ring<NG, MASS>;
-    const int g = lane >> 2, t = lane & 3, ps = a.page_size, S = a.out.S;
+    const int g = lane >> 2, t = lane & 3, sh = a.page_shift, S = a.out.S;
     const int first = a.sink / kBlock, nb = he > a.sink ? (he + kBlock - 1) / kBlock - first : 0;
     const int lo = first + (int)((long long)split * nb / S) + warp, hi = first + (int)((long long)(split + 1) * nb / S);
     const int n = lo < hi ? (hi - lo + kWarps - 1) / kWarps : 0;      // blocks lo, lo + 8, ...
@@ -117,14 +118,13 @@ __device__ __forceinline__ void history_warp(const Attn4Args &a, const CUtensorM
 
     int pg0 = -1, pg1 = -1;        // lane j: pages of the two 16-token halves of block lo + 8 (batch + j)
     uint32_t ok = 0;               // two bits per stage: halves that were loaded
-    auto issue = [&](int i) {
-        const int st = i % R::n;
+    auto issue = [&](int i, int st) {
         if ((i & 31) == 0) {
             const int p = (lo + kWarps * (i + lane)) * kBlock;
             pg0 = pg1 = -1;
             if (i + lane < n) {
-                if (p + 16 > a.sink && p < he) pg0 = pt[p / ps];
-                if (p + kBlock > a.sink && p + 16 < he) pg1 = pt[(p + 16) / ps];
+                if (p + 16 > a.sink && p < he) pg0 = pt[p >> sh];
+                if (p + kBlock > a.sink && p + 16 < he) pg1 = pt[(p + 16) >> sh];
                 if ((p + 16 > a.sink && p < he && (uint32_t)pg0 >= (uint32_t)a.i4_pages) ||
                     (p + kBlock > a.sink && p + 16 < he && (uint32_t)pg1 >= (uint32_t)a.i4_pages))
                     flag_status(a.status, OSCAR_DEV_BAD_INT4_PAGE);
@@ -137,21 +137,21 @@ __device__ __forceinline__ void history_warp(const Attn4Args &a, const CUtensorM
             const int p = (lo + kWarps * i) * kBlock;
             const uint32_t dst = saddr(ring + st * R::stride), bar = bars + 8 * st;
             // pages of 32 or more: one box of 32 rows; pages of 16: a box a half
-            const int rows = ps >= kBlock ? kBlock : 16;
-            const bool l0 = ps >= kBlock ? ok0 || ok1 : ok0, l1 = ps >= kBlock ? false : ok1;
+            const int rows = sh >= 5 ? kBlock : 16;
+            const bool l0 = sh >= 5 ? ok0 || ok1 : ok0, l1 = sh >= 5 ? false : ok1;
             mbar_arrive_expect_tx(bar, (uint32_t)(l0 + l1) * rows * (R::bytes / kBlock));
             const int page[2] = {ok0 ? a0 : a1, a1};
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 if (!(half ? l1 : l0)) continue;
-                const int row = (page[half] * a.n_kv + h) * ps + (p + 16 * half) % ps;
+                const int row = ((page[half] * a.n_kv + h) << sh) + ((p + 16 * half) & ((1 << sh) - 1));
                 tma_rows(dst + half * 1024, tmk, row, bar, pol);
                 if (!MASS) tma_rows(dst + 2048 + half * 1024, tmv, row, bar, pol);
                 tma_load_1d(dst + R::codes + half * 16 * NG * 8, a.sz + (size_t)row * NG * 4, (uint32_t)rows * NG * 8, bar, pol);
             }
         }
     };
-    for (int i = 0; i < R::n && i < n; ++i) issue(i);
+    for (int i = 0; i < R::n && i < n; ++i) issue(i, i);
 
     // B operand of the logits: column g = query head g, channels 32 i + 8 t + e of chunk i; the odd
     // nibbles meet q/16.  fac undoes the scalings, qz is the zero's factor, per column and group.
@@ -217,9 +217,8 @@ __device__ __forceinline__ void history_warp(const Attn4Args &a, const CUtensorM
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.f;
 
-    for (int i = 0; i < n; ++i) {
-        const int st = i % R::n;
-        if (!mbar_wait(bars + 8 * st, (i / R::n) & 1)) {
+    for (int i = 0, st = 0, phase = 0; i < n; ++i) {
+        if (!mbar_wait(bars + 8 * st, phase)) {
             if (lane == 0) flag_status(a.status, OSCAR_DEV_WAIT_TIMEOUT);
             // the copies still under way land before this memory is used again
             for (int k = i + 1; k < i + R::n && k < n; ++k) mbar_wait(bars + 8 * (k % R::n), (k / R::n) & 1);
@@ -293,7 +292,7 @@ __device__ __forceinline__ void history_warp(const Attn4Args &a, const CUtensorM
             }
             const int p = p0 + 8 * t + g;
             if (p >= a.sink && p < he && ((okb >> (t >> 1)) & 1u))
-                atomicAdd(a.mass + ((size_t)b * a.n_kv + h) * a.max_pages * ps + p, add);
+                atomicAdd(a.mass + (((size_t)b * a.n_kv + h) * a.max_pages << sh) + p, add);
         } else {
             // raise the running maximum, or the bound on the value scales, when a block passes it
             float top0 = fmaxf(fmaxf(s[0][0][0], s[0][1][0]), fmaxf(s[1][0][0], s[1][1][0]));
@@ -362,7 +361,11 @@ __device__ __forceinline__ void history_warp(const Attn4Args &a, const CUtensorM
             }
         }
         __syncwarp();
-        if (i + R::n < n) issue(i + R::n);
+        if (i + R::n < n) issue(i + R::n, st);
+        if (++st == R::n) {
+            st = 0;
+            phase ^= 1;
+        }
     }
     if (MASS) return;
 #pragma unroll
@@ -395,7 +398,7 @@ __device__ __forceinline__ void history_warp(const Attn4Args &a, const CUtensorM
 // ---- the BF16 rows: [0, min(sink, T)) and [hist_end, T), 16-token tiles dealt out to the warps -----
 template <int G, bool MASS>
 __device__ __forceinline__ void window_warp(const Attn4Args &a, int b, int h, int T, int he, int warp, int lane, float *res) {
-    const int g = lane >> 2, t = lane & 3, ps = a.page_size;
+    const int g = lane >> 2, t = lane & 3, sh = a.page_shift;
     const int n0 = min(a.sink, T), lo1 = max(he, n0);
     const int sink_tiles = (n0 + 15) / 16, rec0 = lo1 / 16, tiles = sink_tiles + (lo1 < T ? (T + 15) / 16 - rec0 : 0);
     const int32_t *pt = a.bpt + (size_t)b * a.max_pages;
@@ -419,16 +422,33 @@ __device__ __forceinline__ void window_warp(const Attn4Args &a, int b, int h, in
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[hh][e] = 0.f;
 
-    for (int k = warp; k < tiles; k += kWarps) {
+    int pages = -1;                                  // lane j: page of the warp's tile j of this batch of 32
+    for (int k = warp, j = 0; k < tiles; k += kWarps, ++j) {
+        auto tile_pos = [&](int kk) { return (kk < sink_tiles ? kk : rec0 + kk - sink_tiles) * 16; };
+        if ((j & 31) == 0) {
+            const int kk = k + kWarps * lane;
+            pages = kk < tiles ? pt[tile_pos(kk) >> sh] : -1;
+            // the rows of the first few of them start on their way to L2: a 128-byte line a lane, keys then values
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int pg = __shfl_sync(0xffffffffu, pages, u), kk2 = k + kWarps * u;
+                if (kk2 < tiles && (uint32_t)pg < (uint32_t)a.bf.n_pages) {
+                    const size_t row = ((size_t)pg << sh) + (tile_pos(kk2) & ((1 << sh) - 1)) + (lane >> 1);
+                    const size_t at = (row * a.n_kv + h) * kHeadDim + 64 * (lane & 1);
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(a.bf.k + at));
+                    if (!MASS) asm volatile("prefetch.global.L2 [%0];" ::"l"(a.bf.v + at));
+                }
+            }
+        }
         const bool in_sink = k < sink_tiles;
-        const int p0 = (in_sink ? k : rec0 + k - sink_tiles) * 16;
+        const int p0 = tile_pos(k);
         const int lo = in_sink ? 0 : lo1, hi = in_sink ? n0 : T;
-        const int page = pt[p0 / ps];
+        const int page = __shfl_sync(0xffffffffu, pages, j & 31);
         if ((uint32_t)page >= (uint32_t)a.bf.n_pages) {
             if (lane == 0) flag_status(a.status, OSCAR_DEV_BAD_BF16_PAGE);
             continue;
         }
-        const size_t row0 = (size_t)page * ps + p0 % ps;
+        const size_t row0 = ((size_t)page << sh) + (p0 & ((1 << sh) - 1));
         uint4 kx[2][4];
         uint2 vx[16];
 #pragma unroll
@@ -465,7 +485,7 @@ __device__ __forceinline__ void window_warp(const Attn4Args &a, int b, int h, in
                 x += __shfl_xor_sync(0xffffffffu, x, 1);
                 x += __shfl_xor_sync(0xffffffffu, x, 2);
                 const int p = p0 + 8 * r + g;
-                if (t == 0 && p >= lo && p < hi) atomicAdd(a.mass + ((size_t)b * a.n_kv + h) * a.max_pages * ps + p, x);
+                if (t == 0 && p >= lo && p < hi) atomicAdd(a.mass + (((size_t)b * a.n_kv + h) * a.max_pages << sh) + p, x);
             }
             continue;
         }
@@ -511,12 +531,25 @@ __device__ __forceinline__ void window_warp(const Attn4Args &a, int b, int h, in
 }
 
 // The merge of all S + 1 slots of one kv head's G query heads, in oscar_merge's order and arithmetic.
+// The accumulator rows come through shared memory, as many slots at a time as fit, all their 16-byte
+// copies in flight at once and under way while the weights are formed.
 template <int G>
-__device__ __forceinline__ void merge_head(const Attn4Args &a, int b, int h, float *scratch) {
-    const int S1 = a.out.S + 1, S = a.out.S;
+__device__ __forceinline__ void merge_head(const Attn4Args &a, int b, int h, float *scratch, int scratch_bytes) {
+    const int S1 = a.out.S + 1;
     const size_t row0 = ((size_t)b * a.n_kv * G + h * G) * S1;
     float *ws = scratch, *ls = scratch + G * S1, *ms = ls + G * S1;
+    float *rows = scratch + ((2 * G * S1 + G + 3) & ~3);
+    const int chunk = min(S1, (scratch_bytes - (int)((rows - scratch) * 4)) / (G * kHeadDim * 4));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    auto load = [&](int s0) {                          // slots [s0, s0 + chunk) of every head: [head][slot][128]
+        const int n = min(chunk, S1 - s0);
+        for (int e = threadIdx.x; e < G * n * 32; e += kThreads) {
+            const int hh = e / (n * 32), r = e - hh * n * 32;
+            cp_async16(saddr(rows + (size_t)hh * chunk * kHeadDim) + r * 16,
+                       a.out.acc + (row0 + (size_t)hh * S1 + s0) * kHeadDim + r * 4);
+        }
+    };
+    load(0);
     for (int i = threadIdx.x; i < G * S1; i += kThreads) {
         ls[i] = __ldcg(a.out.l + row0 + i);
         ws[i] = __ldcg(a.out.m + row0 + i);
@@ -529,37 +562,44 @@ __device__ __forceinline__ void merge_head(const Attn4Args &a, int b, int h, flo
 #pragma unroll
         for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
         if (lane == 0) ms[warp] = M;
+        for (int i = lane; i < S1; i += 32)
+            ws[warp * S1 + i] = ls[warp * S1 + i] > 0.f ? exp2_taylor(__fsub_rn(ws[warp * S1 + i], M)) : 0.f;
     }
-    __syncthreads();
-    for (int i = threadIdx.x; i < G * S1; i += kThreads) ws[i] = ls[i] > 0.f ? exp2_taylor(__fsub_rn(ws[i], ms[i / S1])) : 0.f;
-    __syncthreads();
-    for (int e = threadIdx.x; e < G * 32; e += kThreads) {
-        const int hh = e >> 5, c4 = e & 31;
-        const float4 *acc = reinterpret_cast<const float4 *>(a.out.acc + (row0 + (size_t)hh * S1) * kHeadDim) + c4;
-        const float *w = ws + hh * S1, *l = ls + hh * S1;
-        float L = 0.f;
-        float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+    constexpr int kPart = G * kHeadDim / kThreads > 0 ? G * kHeadDim / kThreads : 1;
+    float L[kPart], A[kPart];
+#pragma unroll
+    for (int u = 0; u < kPart; ++u) L[u] = A[u] = 0.f;
+    for (int s0 = 0; s0 < S1; s0 += chunk) {
+        if (s0 > 0) {
+            __syncthreads();                           // the previous chunk is consumed
+            load(s0);
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncthreads();
+        const int n = min(chunk, S1 - s0);
+#pragma unroll
+        for (int u = 0; u < kPart; ++u) {
+            const int e = threadIdx.x + u * kThreads, hh = e / kHeadDim, d = e % kHeadDim;
+            if (hh >= G) continue;
+            const float *x = rows + (size_t)hh * chunk * kHeadDim + d, *w = ws + hh * S1 + s0, *l = ls + hh * S1 + s0;
 #pragma unroll 8
-        for (int i = 0; i < S1; ++i) {
-            const float4 x = __ldcg(acc + (size_t)i * 32);
-            if (l[i] > 0.f) {
-                L = __fmaf_rn(l[i], w[i], L);
-                A.x = __fmaf_rn(x.x, w[i], A.x);
-                A.y = __fmaf_rn(x.y, w[i], A.y);
-                A.z = __fmaf_rn(x.z, w[i], A.z);
-                A.w = __fmaf_rn(x.w, w[i], A.w);
+            for (int i = 0; i < n; ++i) {
+                const bool on = l[i] > 0.f;
+                L[u] = on ? __fmaf_rn(l[i], w[i], L[u]) : L[u];
+                A[u] = on ? __fmaf_rn(x[i * kHeadDim], w[i], A[u]) : A[u];
             }
         }
-        const bool on = L > 0.f;
-        const float4 r = make_float4(on ? __fdiv_rn(A.x, L) : 0.f, on ? __fdiv_rn(A.y, L) : 0.f, on ? __fdiv_rn(A.z, L) : 0.f,
-                                     on ? __fdiv_rn(A.w, L) : 0.f);
+    }
+#pragma unroll
+    for (int u = 0; u < kPart; ++u) {
+        const int e = threadIdx.x + u * kThreads, hh = e / kHeadDim, d = e % kHeadDim;
+        if (hh >= G) continue;
+        const bool on = L[u] > 0.f;
+        const float r = on ? __fdiv_rn(A[u], L[u]) : 0.f;
         const size_t orow = (size_t)b * a.n_kv * G + h * G + hh;
-        if (a.of) reinterpret_cast<float4 *>(a.of + orow * kHeadDim)[c4] = r;
-        if (a.o)
-            reinterpret_cast<uint2 *>(a.o + orow * kHeadDim)[c4] =
-                make_uint2((uint32_t)f32_to_bf16_rn(r.x) | ((uint32_t)f32_to_bf16_rn(r.y) << 16),
-                           (uint32_t)f32_to_bf16_rn(r.z) | ((uint32_t)f32_to_bf16_rn(r.w) << 16));
-        if (a.o_lse && c4 == 0) a.o_lse[orow] = on ? (ms[hh] + log2f(L)) * 0.6931471805599453f : -INFINITY;
+        if (a.of) a.of[orow * kHeadDim + d] = r;
+        if (a.o) a.o[orow * kHeadDim + d] = f32_to_bf16_rn(r);
+        if (a.o_lse && d == 0) a.o_lse[orow] = on ? (ms[hh] + log2f(L[u])) * 0.6931471805599453f : -INFINITY;
     }
 }
 
@@ -578,7 +618,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     __syncthreads();
     int T, he;
-    read_lengths(a.seq_len, a.hist_end, b, a.sink, a.max_pages * a.page_size, a.status, T, he);
+    read_lengths(a.seq_len, a.hist_end, b, a.sink, a.max_pages << a.page_shift, a.status, T, he);
     float *res = reinterpret_cast<float *>(smem);
     if (slot == S)
         window_warp<G, MASS>(a, b, h, T, he, warp, lane, res);
@@ -618,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         __threadfence();
     }
     __syncthreads();
-    if (last) merge_head<G>(a, b, h, res);
+    if (last) merge_head<G>(a, b, h, res, a.smem_bytes);
 }
 
 bool rows_tensor_map(CUtensorMap *tm, const uint8_t *base, long long rows, int box_rows) {
@@ -632,11 +672,13 @@ bool rows_tensor_map(CUtensorMap *tm, const uint8_t *base, long long rows, int b
 }
 
 template <int G, int NG, bool MASS>
-cudaError_t launch_one(const Attn4Args &a, const CUtensorMap &tmk, const CUtensorMap &tmv, dim3 grid, cudaStream_t st) {
-    const int merge = (2 * G * (a.out.S + 1) + G) * 4, combine = (2 * kWarps * 8 + kWarps * G * kHeadDim) * 4;
+cudaError_t launch_one(Attn4Args a, const CUtensorMap &tmk, const CUtensorMap &tmv, dim3 grid, cudaStream_t st) {
+    // the merge: weights of every slot, and room for one slot's rows at least
+    const int merge = (((2 * G * (a.out.S + 1) + G + 3) & ~3) + G * kHeadDim) * 4, combine = (2 * kWarps * 8 + kWarps * G * kHeadDim) * 4;
     int smem = Ring<NG, MASS>::total;
     if (!MASS && smem < combine) smem = combine;
     if (!MASS && a.counters && smem < merge) smem = merge;
+    a.smem_bytes = smem;
     smem += 1024;
     auto kern = attn4_kernel<G, NG, MASS>;
     if (cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void *>(kern), smem)) return e;
@@ -662,7 +704,7 @@ cudaError_t launch(const oscar_layout_t &L, const Attn4Input &in, Attn4Args a, i
     a.i4_pages = in.i4.n_pages;
     a.ipt = in.ipt;
     a.max_pages = in.max_pages;
-    a.page_size = L.page_size;
+    a.page_shift = page_shift(L);
     a.n_kv = L.n_kv_heads;
     a.sink = L.sink;
     a.seq_len = in.seq_len;

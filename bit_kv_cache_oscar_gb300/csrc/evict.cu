@@ -15,14 +15,14 @@ namespace oscar {
 namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kBins = 2048;                 // digits of 11, 11 and 10 bits
+constexpr int kBins = 2048;                 // digits of 11, 10 and 11 bits
 constexpr int kCached = 16384;              // keys of a CTA's slice held in shared memory
 constexpr int kCluster = 8;
 
 struct EvictArgs {
     Int4PoolView src, dst;
     const int32_t *spt, *dpt;
-    int max_pages, page_size, n_kv, group, sink;
+    int max_pages, page_shift, n_kv, group, sink;
     const int32_t *seq_len, *hist_end, *keep;
     const float *mass;
     float *mass_out;
@@ -43,7 +43,7 @@ __device__ __forceinline__ uint32_t order_key(float x) {
 __device__ __forceinline__ bool read_request(const EvictArgs &a, int b, int &T, int &he, int &n, int &k, bool flag) {
     k = a.keep[b];
     if (k == -1) return false;
-    read_lengths(a.seq_len, a.hist_end, b, a.sink, a.max_pages * a.page_size, a.status, T, he);
+    read_lengths(a.seq_len, a.hist_end, b, a.sink, a.max_pages << a.page_shift, a.status, T, he);
     n = he > a.sink ? he - a.sink : 0;
     if (k < 0 || k > n || k > a.kept_stride) {
         if (flag) flag_status(a.status, OSCAR_DEV_BAD_LENGTH);
@@ -62,76 +62,119 @@ __device__ __forceinline__ int ld_cluster(const int *p, int rank) {
 
 // One cluster of C CTAs (grid x = C·Hkv) per (request, kv head); CTA r takes the slice [r n / C, (r + 1) n / C)
 // of the history and holds its keys in shared memory (kCached of them; the rest is read again each pass).
-__global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a, int C) {
+// A pass: each CTA counts its slice's digits, sums its share of the bins over the cluster (all C remote
+// reads in flight), and every CTA looks the digit up: share totals first, then that share's bins.
+template <int C>
+__global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a) {
     extern __shared__ uint32_t keys[];
-    __shared__ int hist[kBins], tot[kBins];            // tot: the cluster's counts of this CTA's share of the bins
-    __shared__ int bins[kBins];                        // the counts of the share that holds the digit
+    constexpr int kPer = kBins / C;                    // bins of one CTA's share
+    constexpr int kOwn = (kPer + kThreads - 1) / kThreads;
+    // four counters a bin (lane & 3): weights gather in few bins, and equal bins of a warp are added in turn
+    __shared__ int4 hist[kBins];
+    __shared__ int tot[kPer];                          // the cluster's counts of this CTA's share of the bins
     __shared__ int cnt_gt[kWarps], cnt_eq[kWarps], red[kWarps];
     __shared__ int share, found[2], slice_gt, slice_eq;
     const int rank = blockIdx.x % C, h = blockIdx.x / C, b = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    auto cluster_or_cta_sync = [] {
+        if (C > 1) cluster_sync_all();
+        else __syncthreads();
+    };
+    auto remote = [](const int *p, int r) { return C > 1 ? ld_cluster(p, r) : *p; };
     int T, he, n, k;
     if (!read_request(a, b, T, he, n, k, threadIdx.x == 0 && blockIdx.x == 0) || k == 0) return;     // the whole cluster alike
     const int lo = (int)((long long)rank * n / C), hi = (int)((long long)(rank + 1) * n / C);
-    const float *m = a.mass + ((size_t)b * a.n_kv + h) * a.max_pages * a.page_size + a.sink + lo;
+    const float *m = a.mass + (((size_t)b * a.n_kv + h) * a.max_pages << a.page_shift) + a.sink + lo;
     const int len = hi - lo, cached = min(len, kCached);
     auto key_at = [&](int i) { return i < cached ? keys[i] : order_key(m[i]); };
+#pragma unroll 8
     for (int i = threadIdx.x; i < cached; i += kThreads) keys[i] = order_key(m[i]);
 
+    int *counters = reinterpret_cast<int *>(hist);
     uint32_t prefix = 0;
     int left = k;                                      // still to find among the keys that match the prefix
-    const int per = kBins / C;                         // bins of one CTA's share
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
-        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, nb = pass == 2 ? 1024 : 2048;
-        const uint32_t mask = pass == 0 ? 0u : pass == 1 ? 0xFFE00000u : 0xFFFFFC00u;
-        for (int i = threadIdx.x; i < kBins; i += kThreads) hist[i] = 0;
+        const int shift = pass == 0 ? 21 : pass == 1 ? 11 : 0, nb = pass == 1 ? 1024 : 2048;
+        const uint32_t mask = pass == 0 ? 0u : pass == 1 ? 0xFFE00000u : 0xFFFFF800u;
+        for (int i = threadIdx.x; i < nb; i += kThreads) hist[i] = make_int4(0, 0, 0, 0);
         __syncthreads();
         for (int i = threadIdx.x; i < len; i += kThreads) {
             const uint32_t key = key_at(i);
-            if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & (nb - 1)], 1);
+            if ((key & mask) == prefix) atomicAdd(&counters[4 * ((key >> shift) & (nb - 1)) + (lane & 3)], 1);
         }
-        if (C > 1) cluster_sync_all(); else __syncthreads();
-        int sum = 0;
-        for (int i = threadIdx.x; i < per; i += kThreads) {
-            int v = 0;
-            for (int r = 0; r < C; ++r) v += C > 1 ? ld_cluster(&hist[rank * per + i], r) : hist[i];
-            tot[i] = v;
-            sum += v;
-        }
-        sum = __reduce_add_sync(0xffffffffu, sum);
-        if (lane == 0) red[warp] = sum;
         __syncthreads();
-        if (threadIdx.x == 0) {
-            int s = 0;
-            for (int w = 0; w < kWarps; ++w) s += red[w];
-            share = s;
+        const int per = nb / C;
+        for (int i = threadIdx.x; i < nb; i += kThreads) {
+            const int4 v = hist[i];
+            hist[i].x = v.x + v.y + v.z + v.w;
         }
-        if (C > 1) cluster_sync_all(); else __syncthreads();
-        // every CTA: the share, from the top, in which the count reaches `left`, then its bin
-        int r = C - 1;
-        for (; r > 0; --r) {
-            const int s = C > 1 ? ld_cluster(&share, r) : share;
-            if (left <= s) break;
-            left -= s;
-        }
-        for (int i = threadIdx.x; i < per; i += kThreads) bins[i] = C > 1 ? ld_cluster(&tot[i], r) : tot[i];
-        __syncthreads();
-        if (warp == 0) {
-            const int q = per / 32, top = per - lane * q;            // lane 0: the highest q bins
-            int s = 0;
-            for (int i = 1; i <= q; ++i) s += bins[top - i];
-            int before = s;
+        cluster_or_cta_sync();
+        if (C > 1) {
+            int sum = 0;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, before, o);
-                if (lane >= o) before += v;
+            for (int j = 0; j < kOwn; ++j) {
+                const int i = threadIdx.x + j * kThreads;
+                if (i >= per) break;
+                int v[C], t = 0;
+#pragma unroll
+                for (int r = 0; r < C; ++r) v[r] = remote(&hist[rank * per + i].x, r);
+#pragma unroll
+                for (int r = 0; r < C; ++r) t += v[r];
+                tot[i] = t;
+                sum += t;
             }
-            before -= s;
-            if (before < left && left <= before + s) {
-                int i = 1;
-                while (before + bins[top - i] < left) before += bins[top - i++];
-                found[0] = r * per + top - i;
-                found[1] = left - before;
+            sum = __reduce_add_sync(0xffffffffu, sum);
+            if (lane == 0) red[warp] = sum;
+            __syncthreads();
+            if (warp == 0) {
+                const int t = __reduce_add_sync(0xffffffffu, lane < kWarps ? red[lane] : 0);
+                if (lane == 0) share = t;
+            }
+            cluster_sync_all();
+        }
+        // the share, from the top, in which the count reaches `left`
+        int r = 0;
+        if (C > 1) {
+            int v[C];
+#pragma unroll
+            for (int j = 0; j < C; ++j) v[j] = remote(&share, j);
+            bool looking = true;
+#pragma unroll
+            for (int j = C - 1; j >= 0; --j) {
+                if (looking && left <= v[j]) {
+                    r = j;
+                    looking = false;
+                }
+                left -= looking ? v[j] : 0;
+            }
+        }
+        // its bins from the top, kOwn a thread: thread t has bins [per - kOwn (t + 1), per - kOwn t)
+        int c[kOwn], sum = 0;
+#pragma unroll
+        for (int j = 0; j < kOwn; ++j) {
+            const int i = per - 1 - (int)(threadIdx.x * kOwn + j);
+            c[j] = i < 0 ? 0 : C > 1 ? remote(&tot[i], r) : hist[i].x;
+            sum += c[j];
+        }
+        int upto = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += v;
+        }
+        if (lane == 31) red[warp] = upto;
+        __syncthreads();
+        int before = upto - sum;
+        for (int w = 0; w < warp; ++w) before += red[w];
+        if (before < left && left <= before + sum) {
+#pragma unroll
+            for (int j = 0; j < kOwn; ++j) {
+                if (before < left && left <= before + c[j]) {
+                    found[0] = r * per + per - 1 - (int)(threadIdx.x * kOwn + j);
+                    found[1] = left - before;
+                    break;
+                }
+                before += c[j];
             }
         }
         __syncthreads();
@@ -162,11 +205,20 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a, int
         slice_gt = x;
         slice_eq = y;
     }
-    if (C > 1) cluster_sync_all(); else __syncthreads();
+    cluster_or_cta_sync();
     int gt0 = 0, eq0 = 0;
-    for (int r = 0; r < rank; ++r) {
-        gt0 += ld_cluster(&slice_gt, r);
-        eq0 += ld_cluster(&slice_eq, r);
+    if (C > 1) {
+        int v[C], w[C];
+#pragma unroll
+        for (int r = 0; r < C; ++r) {
+            v[r] = remote(&slice_gt, r);
+            w[r] = remote(&slice_eq, r);
+        }
+#pragma unroll
+        for (int r = 0; r < C; ++r) {
+            gt0 += r < rank ? v[r] : 0;
+            eq0 += r < rank ? w[r] : 0;
+        }
     }
     for (int w = 0; w < warp; ++w) {
         gt0 += cnt_gt[w];
@@ -195,10 +247,10 @@ __global__ void __launch_bounds__(256) evict_move_kernel(EvictArgs a) {
     const int h = blockIdx.y, b = blockIdx.z, hl = threadIdx.x & 7;
     int T, he, n, k;
     if (!read_request(a, b, T, he, n, k, false)) return;
-    const size_t row0 = ((size_t)b * a.n_kv + h) * a.max_pages * a.page_size;
+    const size_t row0 = ((size_t)b * a.n_kv + h) * a.max_pages << a.page_shift;
     const int32_t *kept = a.kept + ((size_t)b * a.n_kv + h) * a.kept_stride;
     const int32_t *spt = a.spt + (size_t)b * a.max_pages, *dpt = a.dpt + (size_t)b * a.max_pages;
-    const int G = kHeadDim / a.group, step = gridDim.x * 32;
+    const int G = kHeadDim / a.group, step = gridDim.x * 32, in_page = (1 << a.page_shift) - 1;
     const uint8_t *sc = hl < 4 ? a.src.codes_k : a.src.codes_v;
     uint8_t *dc = hl < 4 ? a.dst.codes_k : a.dst.codes_v;
     for (long long j0 = blockIdx.x * 32 + (threadIdx.x >> 3); j0 < k; j0 += (long long)kMoveRows * step) {
@@ -212,8 +264,8 @@ __global__ void __launch_bounds__(256) evict_move_kernel(EvictArgs a) {
         for (int u = 0; u < kMoveRows; ++u) {
             if (p[u] < 0) continue;
             const int to = a.sink + (int)(j0 + (long long)u * step);
-            sp[u] = spt[p[u] / a.page_size];
-            dp[u] = dpt[to / a.page_size];
+            sp[u] = spt[p[u] >> a.page_shift];
+            dp[u] = dpt[to >> a.page_shift];
             w[u] = hl == 0 ? a.mass[row0 + p[u]] : 0.f;
         }
 #pragma unroll
@@ -224,7 +276,7 @@ __global__ void __launch_bounds__(256) evict_move_kernel(EvictArgs a) {
                 dp[u] = -1;
                 continue;
             }
-            const size_t from = row4(sp[u], a.n_kv, h, a.page_size, p[u] % a.page_size);
+            const size_t from = row4(sp[u], a.n_kv, h, a.page_shift, p[u] & in_page);
             x[u] = reinterpret_cast<const uint4 *>(sc + from * kRow4)[hl & 3];
             if (hl < G) z[u] = reinterpret_cast<const uint2 *>(a.src.scale_zero)[from * G + hl];
         }
@@ -234,13 +286,13 @@ __global__ void __launch_bounds__(256) evict_move_kernel(EvictArgs a) {
             const int to = a.sink + (int)(j0 + (long long)u * step);
             if (hl == 0) a.mass_out[row0 + to] = w[u];
             if (dp[u] < 0) continue;
-            const size_t at = row4(dp[u], a.n_kv, h, a.page_size, to % a.page_size);
+            const size_t at = row4(dp[u], a.n_kv, h, a.page_shift, to & in_page);
             reinterpret_cast<uint4 *>(dc + at * kRow4)[hl & 3] = x[u];
             if (hl < G) reinterpret_cast<uint2 *>(a.dst.scale_zero)[at * G + hl] = z[u];
         }
     }
     // the weights outside the kept rows: sink, recent rows, nothing behind them
-    const int N = a.max_pages * a.page_size, shift = n - k, lo = min(a.sink, T);
+    const int N = a.max_pages << a.page_shift, shift = n - k, lo = min(a.sink, T);
     for (long long i = blockIdx.x * 256 + threadIdx.x; i < N; i += gridDim.x * 256) {
         if (i < lo) a.mass_out[row0 + i] = a.mass[row0 + i];
         else if (i >= lo + k) a.mass_out[row0 + i] = i + shift < T ? a.mass[row0 + i + shift] : 0.f;
@@ -253,7 +305,7 @@ cudaError_t launch_evict(const oscar_layout_t &L, Int4PoolView src, const int32_
                          const int32_t *dpt, int max_pages, int batch, const int32_t *seq_len, const int32_t *hist_end,
                          const int32_t *keep, const float *mass, float *mass_out, int32_t *kept, int kept_stride,
                          int32_t *status, cudaStream_t st) {
-    const EvictArgs a{src, dst, spt, dpt, max_pages, L.page_size, L.n_kv_heads, L.group, L.sink, seq_len, hist_end, keep,
+    const EvictArgs a{src, dst, spt, dpt, max_pages, page_shift(L), L.n_kv_heads, L.group, L.sink, seq_len, hist_end, keep,
                       mass, mass_out, kept, kept_stride, status};
     // Histories that can pass 8K tokens: eight CTAs a head (a slice each, counts joined across the
     // cluster); below, the passes are shorter than the cluster's barriers.
@@ -261,7 +313,8 @@ cudaError_t launch_evict(const oscar_layout_t &L, Int4PoolView src, const int32_
     const int C = tokens > 8192 ? kCluster : 1;
     const long long slice = (tokens + C - 1) / C;
     const int smem = 4 * (int)(slice < kCached ? slice : kCached);
-    if (cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void *>(evict_select_kernel), smem)) return e;
+    auto kern = C > 1 ? evict_select_kernel<kCluster> : evict_select_kernel<1>;
+    if (cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void *>(kern), smem)) return e;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     cfg.gridDim = dim3(C * L.n_kv_heads, batch);
@@ -275,7 +328,7 @@ cudaError_t launch_evict(const oscar_layout_t &L, Int4PoolView src, const int32_
         cfg.attrs = attr;
         cfg.numAttrs = 1;
     }
-    if (cudaError_t e = cudaLaunchKernelEx(&cfg, evict_select_kernel, a, C)) return e;
+    if (cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a)) return e;
     const long long most = (tokens + 255) / 256;
     const long long want = (8 * 152 + batch * L.n_kv_heads - 1) / (batch * L.n_kv_heads);
     evict_move_kernel<<<dim3((unsigned)(want < most ? want : most), L.n_kv_heads, batch), 256, 0, st>>>(a);

@@ -525,7 +525,7 @@ OSCAR_API oscar_status_t oscar_demote_int4(const oscar_layout_t *layout, const o
 
 /*
  * The way back: every position in [pos_begin[b], pos_end[b]) of the INT4 pool restored (zero +
- * code·scale in fp32, rounded to bf16) into the BF16 pool's page of that position, for a consumer that
+ * code·scale, rounded once to bf16) into the BF16 pool's page of that position, for a consumer that
  * reads BF16 (a prompt's next chunk).  Ranges, pages and errors as for oscar_demote_int4.
  */
 OSCAR_API oscar_status_t oscar_promote_int4(const oscar_layout_t *layout, const oscar_int4_pool_t *src,

@@ -19,6 +19,13 @@ def bf16(a) -> np.ndarray:
     return torch.from_numpy(np.ascontiguousarray(a, dtype=np.float32)).to(torch.bfloat16).double().numpy()
 
 
+def bf16_once(a) -> np.ndarray:
+    """float64 values rounded once to bf16 (nearest, ties to even), as float64; magnitudes of normal bf16 numbers."""
+    a = np.asarray(a, np.float64)
+    step = 2.0 ** (np.floor(np.log2(np.maximum(np.abs(a), 2.0 ** -126))) - 7)
+    return np.rint(a / step) * step
+
+
 def quantize(x: np.ndarray, group: int, clip: float):
     """Rows [..., 128] -> codes [..., 128] and (scale, zero) [..., 128 / group] as stored, float64."""
     g = x.reshape(x.shape[:-1] + (D // group, group))
