@@ -71,7 +71,7 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 constexpr int kAhead = 2;
 
 template <bool PAIRS>
-__global__ void __launch_bounds__(kWarps * 32, 4) append_kernel(AppendArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, 3) append_kernel(AppendArgs a) {
     const int lane = threadIdx.x & 31, half = lane >> 4, hl = lane & 15;
     const uint32_t w = blockIdx.x * kWarps + (threadIdx.x >> 5);       // below 2^32: n * runs is (launch_append)
     const int i = (int)(w / (uint32_t)a.runs);

@@ -1,0 +1,744 @@
+// Decode attention over an INT4 history with BF16 sink and recent rows, and the attention weight each
+// position received, on the tensor cores.
+//
+// With a row's 4-bit codes n_c, scale s and zero z per channel group, a logit is
+//   sm·(s·sum_c q_c n_c + z·sum_c q_c)
+// and an output sum_t p_t v_t = sum_t (p_t s_t) n_t + sum_t p_t z_t: both contractions meet the codes
+// themselves, so the codes are the A operand of mma.sync m16n8k16 (f16 in, fp32 accumulate) and scales
+// and zeros stay outside.  A nibble n in bits 0..3 or 4..7 of an f16 with no exponent bits is the
+// subnormal n·2^-24 or 16n·2^-24, so unpacking eight codes is one shift and four ANDs; the powers of two
+// go into the other operand or the result.  q is bf16 and exact in f16 after a power-of-two scaling of
+// each head; p·s is rounded to f16 (2^-11 relative), scaled by a power of two that follows the value
+// scales.  The contractions have 8 columns: the query heads of one kv head.
+//
+// A CTA takes one kv head of one split; each of its warps takes every W-th block of 32 tokens on its own
+// (2 KB of key codes, 2 KB of value codes, their scale/zero records) through a ring of stages that its
+// lane 0 fills with bulk tensor copies (64-byte swizzle: conflict-free ldmatrix of key rows and
+// ldmatrix.trans of value rows), so no warp waits for another before the end.  p moves from the logits'
+// accumulator layout to the value product's B operand by movmatrix.  The running maximum is only
+// raised when a logit passes it by 2^8: a rescale of the accumulators is rare.
+// The BF16 rows are dealt out in tiles of 16 to the same warps, which work on them while their first
+// blocks are on the way.  With counters, the last CTA of a (request, kv head) to finish merges all its
+// slots, in slot order.
+// W is 16 (one CTA an SM) when the launch has a CTA for each SM at most, else 8 (two an SM, so that one's
+// start and end hide behind the other's stream).
+// Every wait is bounded: one that gives up sets OSCAR_DEV_WAIT_TIMEOUT.
+
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cstring>
+
+#include "attn_int4_args.cuh"
+#include "merge_math.cuh"
+#include "ptx.cuh"
+#include "tma.cuh"
+
+namespace oscar {
+
+namespace {
+
+constexpr uint32_t kM0 = 0x000F000Fu, kM1 = 0x00F000F0u;
+constexpr float kNone = -1e30f;                  // running maximum before the first token
+constexpr float kSlack = 8.f;                    // logits (base 2) may pass the running maximum by this
+constexpr int kPShift = 6;                       // p·s is held at 2^6 below 2^(kSlack + 1): at most 2^15
+
+// One stage of one warp: key codes [32][64 B], value codes, scale/zero records [32][NG][8 B].
+template <int NG, bool MASS, int W>
+struct Ring {
+    static constexpr int codes = MASS ? 2048 : 4096;
+    static constexpr int bytes = codes + kBlock * NG * 8;
+    static constexpr int stride = (bytes + 511) & ~511;          // the swizzle pattern repeats every 512 bytes
+    static constexpr int n = MASS ? 4 : (NG == 4 ? 2 : 3);        // as many as 16 warps an SM leave room for
+    static constexpr int total = W * n * stride;
+};
+
+__device__ __forceinline__ float lo16(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi16(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ uint32_t pack_h2(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ uint32_t pack_b2(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
+    uint32_t d;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    return d;
+}
+__device__ __forceinline__ void tma_rows(uint32_t dst, const void *tmap, int row, uint32_t bar, uint64_t pol) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint "
+        "[%0], [%1, {%2, %3}], [%4], %5;"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(0), "r"(row), "r"(bar), "l"(pol)
+        : "memory");
+}
+__device__ __forceinline__ float col_sum(float x) {       // over the 8 lanes of a column
+    x += __shfl_xor_sync(0xffffffffu, x, 4);
+    x += __shfl_xor_sync(0xffffffffu, x, 8);
+    return x + __shfl_xor_sync(0xffffffffu, x, 16);
+}
+__device__ __forceinline__ float col_max(float x) {
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+    return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+}
+
+// What a warp holds of the G heads' partials when it is done: column c = 2 t + j is head c.
+struct ColState {
+    float m[2], l[2];
+};
+
+// Bound and scaling of the value scales from the bits of the largest (positive): 2^e <= it < 2^(e + 1).
+__device__ __forceinline__ void set_value_bound(uint32_t bits, float &vmax, float &vinv) {
+    const int e = max((int)(bits >> 23) - 127, -100);
+    vinv = __uint_as_float((uint32_t)(kPShift - e + 127) << 23);
+    vmax = e >= 126 ? INFINITY : __uint_as_float((uint32_t)(e + 1 + 127) << 23);
+}
+
+// ---- the BF16 rows: [0, min(sink, T)) and [hist_end, T), 16-token tiles dealt out to the warps ----------
+struct Window {
+    int n0, lo1, T, sink_tiles, rec0, tiles;
+    __device__ __forceinline__ Window(int sink, int T_, int he) {
+        T = T_;
+        n0 = min(sink, T);
+        lo1 = max(he, n0);
+        sink_tiles = (n0 + 15) / 16;
+        rec0 = lo1 / 16;
+        tiles = sink_tiles + (lo1 < T ? (T + 15) / 16 - rec0 : 0);
+    }
+};
+
+// The rows of tile k on their way to shared memory: 16 key rows of 256 bytes, then 16 value rows; value rows
+// outside the tile's positions are zeroed.  False (and no copy) for a bad page.
+struct WindowTile {
+    int p0, lo, hi;
+};
+template <bool MASS>
+__device__ __forceinline__ bool issue_tile(const Attn4Args &a, const Window &w, int k, int b, int h, int lane, uint8_t *dst, uint32_t bar,
+                                           WindowTile &x) {
+    const bool in_sink = k < w.sink_tiles;
+    x.p0 = (in_sink ? k : w.rec0 + k - w.sink_tiles) * 16;
+    x.lo = in_sink ? 0 : w.lo1;
+    x.hi = in_sink ? w.n0 : w.T;
+    const int page = a.bpt[(size_t)b * a.max_pages + (x.p0 >> a.page_shift)];
+    if ((uint32_t)page >= (uint32_t)a.bf.n_pages) {
+        if (lane == 0) flag_status(a.status, OSCAR_DEV_BAD_BF16_PAGE);
+        return false;
+    }
+    const int rows = min(x.hi, x.p0 + 16) - max(x.lo, x.p0), r = lane & 15;
+    if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)rows * 256 * (MASS ? 1 : 2));
+    __syncwarp();
+    if (!MASS || lane < 16) {
+        uint8_t *to = dst + lane * 256;
+        if (x.p0 + r >= x.lo && x.p0 + r < x.hi) {
+            const size_t row = ((size_t)page << a.page_shift) + (x.p0 & ((1 << a.page_shift) - 1)) + r;
+            tma_load_1d(saddr(to), (lane < 16 ? a.bf.k : a.bf.v) + (row * a.n_kv + h) * kHeadDim, 256, bar);
+        } else if (lane >= 16) {
+            for (int i = 0; i < 16; ++i) reinterpret_cast<uint4 *>(to)[i] = make_uint4(0, 0, 0, 0);
+        }
+    }
+    return true;
+}
+
+// Fold the warp's tiles first, first + every, ... (the first is under way in buf, `ok` unless its page is bad).
+// Leaves the running maxima and sums in cs, and the accumulators in the layout, scaling and bound (vmax,
+// vinv) that the history's loop goes on with.  Lane (g, t) reads channels 32 i + 8 t .. + 7 of tokens g and
+// g + 8; value rows become the A operand through movmatrix (channels 32 c + 4 n + 2 j of eight tokens are
+// an 8 x 8 matrix), p the B operand in two bf16 parts.
+template <int G, bool MASS>
+__device__ __forceinline__ void window_tiles(const Attn4Args &a, const Window &w, int b, int h, int first, int every, int lane,
+                                             uint8_t *buf, uint32_t bar, bool ok, WindowTile &x, ColState &cs, float (&out)[4][2][4],
+                                             float &vmax, float &vinv) {
+    const int g = lane >> 2, t = lane & 3, sh = a.page_shift;
+    uint4 bq[4];
+    const uint16_t *qr = a.q + ((size_t)b * a.n_kv * G + h * G + (g < G ? g : 0)) * kHeadDim + 8 * t;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) bq[i] = g < G ? *reinterpret_cast<const uint4 *>(qr + 32 * i) : make_uint4(0, 0, 0, 0);
+    uint32_t phase = 0;
+#pragma unroll 1
+    for (int k = first; k < w.tiles; k += every) {
+        if (k != first) {
+            fence_proxy_async_smem();                          // the tile before is read, its zeros are written
+            __syncwarp();
+            ok = issue_tile<MASS>(a, w, k, b, h, lane, buf, bar, x);
+        }
+        if (!ok) continue;
+        if (!mbar_wait(bar, phase)) {
+            if (lane == 0) flag_status(a.status, OSCAR_DEV_WAIT_TIMEOUT);
+            mbar_wait(bar, phase);                             // its copies land before this memory is used again
+            break;
+        }
+        phase ^= 1;
+        __syncwarp();
+        const uint4 *rows = reinterpret_cast<const uint4 *>(buf) + g * 16 + t;
+        float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint4 k0 = rows[4 * i], k1 = rows[4 * i + 128];
+            mma16816_bf16(d, k0.x, k1.x, k0.y, k1.y, bq[i].x, bq[i].y);
+            mma16816_bf16(d, k0.z, k1.z, k0.w, k1.w, bq[i].z, bq[i].w);
+        }
+        float s[2][2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const bool in = x.p0 + 8 * r + g >= x.lo && x.p0 + 8 * r + g < x.hi;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) s[r][j] = in ? d[2 * r + j] * a.scale2 : -INFINITY;
+        }
+        if (MASS) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                float y = ex2_approx(s[r][0] - cs.m[0]) + ex2_approx(s[r][1] - cs.m[1]);
+                y += __shfl_xor_sync(0xffffffffu, y, 1);
+                y += __shfl_xor_sync(0xffffffffu, y, 2);
+                const int p = x.p0 + 8 * r + g;
+                if (t == 0 && p >= x.lo && p < x.hi) atomicAdd(a.mass + (((size_t)b * a.n_kv + h) * a.max_pages << sh) + p, y);
+            }
+            continue;
+        }
+        float al[2], pr[2][2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float m = fmaxf(cs.m[j], col_max(fmaxf(s[0][j], s[1][j])));
+            al[j] = ex2_approx(cs.m[j] - m);
+            cs.m[j] = m;
+            pr[0][j] = ex2_approx(s[0][j] - m);
+            pr[1][j] = ex2_approx(s[1][j] - m);
+            cs.l[j] = fmaf(cs.l[j], al[j], pr[0][j] + pr[1][j]);
+        }
+        uint32_t bh[2], bl[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const uint32_t hi = pack_b2(pr[r][0], pr[r][1]);
+            bh[r] = movmatrix_trans(hi);
+            bl[r] = movmatrix_trans(pack_b2(pr[r][0] - lo16(hi), pr[r][1] - hi16(hi)));
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const uint4 v0 = rows[4 * c + 256], v1 = rows[4 * c + 384];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint32_t m0 = movmatrix_trans(__byte_perm(j ? v0.y : v0.x, j ? v0.w : v0.z, 0x5410));
+                const uint32_t m1 = movmatrix_trans(__byte_perm(j ? v0.y : v0.x, j ? v0.w : v0.z, 0x7632));
+                const uint32_t m2 = movmatrix_trans(__byte_perm(j ? v1.y : v1.x, j ? v1.w : v1.z, 0x5410));
+                const uint32_t m3 = movmatrix_trans(__byte_perm(j ? v1.y : v1.x, j ? v1.w : v1.z, 0x7632));
+#pragma unroll
+                for (int e = 0; e < 4; ++e) out[c][j][e] *= al[e & 1];
+                mma16816_bf16(out[c][j], m0, m1, m2, m3, bh[0], bh[1]);
+                mma16816_bf16(out[c][j], m0, m1, m2, m3, bl[0], bl[1]);
+            }
+        }
+    }
+    if (MASS) return;
+    float top = 0.f;
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top = fmaxf(top, fabsf(out[c][j][e]));
+    top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+    if (top > 0.f) set_value_bound(__float_as_uint(top), vmax, vinv);
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) out[c][j][e] *= vinv * (e >> 1 ? 0x1p-20f : 0x1p-24f);
+}
+
+// ---- the history -------------------------------------------------------------------------------
+template <int G, int NG, bool MASS, int W>
+__device__ __forceinline__ void history_warp(const Attn4Args &a, const CUtensorMap *tmk, const CUtensorMap *tmv, uint8_t *ring,
+                                             uint32_t bars, int b, int h, int split, int T, int he, int warp, int lane, float *res) {
+    using R = Ring<NG, MASS, W>;
+    const int g = lane >> 2, t = lane & 3, sh = a.page_shift, S = a.out.S;
+    const int first = a.sink / kBlock, nb = he > a.sink ? (he + kBlock - 1) / kBlock - first : 0;
+    const int lo = first + (int)((long long)split * nb / S) + warp, hi = first + (int)((long long)(split + 1) * nb / S);
+    const int n = lo < hi ? (hi - lo + W - 1) / W : 0;      // blocks lo, lo + W, ...
+    const int32_t *pt = a.ipt + (size_t)b * a.max_pages;
+    const uint64_t pol = l2_evict_first_policy();
+
+    int pg0 = -1, pg1 = -1;        // lane j: pages of the two 16-token halves of block lo + W (batch + j)
+    uint32_t ok = 0;               // two bits per stage: halves that were loaded
+    auto issue = [&](int i, int st) {
+        if ((i & 31) == 0) {
+            const int p = (lo + W * (i + lane)) * kBlock;
+            pg0 = pg1 = -1;
+            if (i + lane < n) {
+                if (p + 16 > a.sink && p < he) pg0 = pt[p >> sh];
+                if (p + kBlock > a.sink && p + 16 < he) pg1 = pt[(p + 16) >> sh];
+                if ((p + 16 > a.sink && p < he && (uint32_t)pg0 >= (uint32_t)a.i4_pages) ||
+                    (p + kBlock > a.sink && p + 16 < he && (uint32_t)pg1 >= (uint32_t)a.i4_pages))
+                    flag_status(a.status, OSCAR_DEV_BAD_INT4_PAGE);
+            }
+        }
+        const int a0 = __shfl_sync(0xffffffffu, pg0, i & 31), a1 = __shfl_sync(0xffffffffu, pg1, i & 31);
+        const bool ok0 = (uint32_t)a0 < (uint32_t)a.i4_pages, ok1 = (uint32_t)a1 < (uint32_t)a.i4_pages;
+        ok = (ok & ~(3u << (2 * st))) | ((ok0 ? 1u : 0u) | (ok1 ? 2u : 0u)) << (2 * st);
+        if (lane == 0) {
+            const int p = (lo + W * i) * kBlock;
+            const uint32_t dst = saddr(ring + st * R::stride), bar = bars + 8 * st;
+            // pages of 32 or more: one box of 32 rows; pages of 16: a box a half
+            const int rows = sh >= 5 ? kBlock : 16;
+            const bool l0 = sh >= 5 ? ok0 || ok1 : ok0, l1 = sh >= 5 ? false : ok1;
+            mbar_arrive_expect_tx(bar, (uint32_t)(l0 + l1) * rows * (R::bytes / kBlock));
+            const int page[2] = {ok0 ? a0 : a1, a1};
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                if (!(half ? l1 : l0)) continue;
+                const int row = ((page[half] * a.n_kv + h) << sh) + ((p + 16 * half) & ((1 << sh) - 1));
+                tma_rows(dst + half * 1024, tmk, row, bar, pol);
+                if (!MASS) tma_rows(dst + 2048 + half * 1024, tmv, row, bar, pol);
+                tma_load_1d(dst + R::codes + half * 16 * NG * 8, a.sz + (size_t)row * NG * 4, (uint32_t)rows * NG * 8, bar, pol);
+            }
+        }
+    };
+    // The warp's first tile of BF16 rows, ahead of its blocks in the memory queues: it takes the first two
+    // stages, so the blocks start in the third (in a ring of two: when the tiles are done).
+    const Window win(a.sink, T, he);
+    const int tile0 = warp * S + split, wbar = R::n;
+    const bool has_tile = tile0 < win.tiles;
+    WindowTile wt;
+    bool tile_ok = false;
+    if (has_tile) tile_ok = issue_tile<MASS>(a, win, tile0, b, h, lane, ring, bars + 8 * wbar, wt);
+    const int st0 = has_tile ? 2 % R::n : 0, ahead = has_tile ? R::n - 2 : R::n;
+    for (int i = 0; i < ahead && i < n; ++i) issue(i, (st0 + i) % R::n);
+
+    ColState cs;
+    float zs[NG][2], acc[4][2][4];
+    float vmax = 0.f, vinv = 1.f;                  // value scales seen are at most vmax = 2^(e + 1); vinv = 2^(kPShift - e)
+#pragma unroll
+    for (int i = 0; i < NG; ++i) zs[i][0] = zs[i][1] = 0.f;
+    cs.m[0] = cs.m[1] = kNone;
+    cs.l[0] = cs.l[1] = 0.f;
+    if (MASS) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float l = 2 * t + j < G ? a.lse[(size_t)b * a.n_kv * G + h * G + 2 * t + j] : -INFINITY;
+            cs.m[j] = l == -INFINITY ? INFINITY : l * kLog2e;
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[c][j][e] = 0.f;
+    if (has_tile) {
+        window_tiles<G, MASS>(a, win, b, h, tile0, S * W, lane, ring, bars + 8 * wbar, tile_ok, wt, cs, acc, vmax, vinv);
+        fence_proxy_async_smem();
+        __syncwarp();
+        for (int i = ahead; i < R::n && i < n; ++i) issue(i, (st0 + i) % R::n);
+    }
+
+    // B operand of the logits: column g = query head g, channels 32 i + 8 t + e of chunk i; the odd
+    // nibbles meet q/16.  fac undoes the scalings, qz is the zero's factor, per column and group.
+    uint32_t bq[4][4];
+    float fac[2], qz[NG][2];
+    {
+        uint4 w[4];
+        const uint16_t *qr = a.q + ((size_t)b * a.n_kv * G + h * G + (g < G ? g : 0)) * kHeadDim + 8 * t;
+        float mx = 0.f, qs[NG];
+#pragma unroll
+        for (int j = 0; j < NG; ++j) qs[j] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            w[i] = g < G ? *reinterpret_cast<const uint4 *>(qr + 32 * i) : make_uint4(0, 0, 0, 0);
+            const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                mx = fmaxf(mx, fmaxf(fabsf(lo16(x[e])), fabsf(hi16(x[e]))));
+                qs[i * NG / 4] += lo16(x[e]) + hi16(x[e]);
+            }
+        }
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const int ex = min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 117);   // |q| < 2^(ex + 1)
+        const float mul = __uint_as_float((uint32_t)(14 - ex + 127) << 23), mul16 = mul * 0.0625f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            bq[i][0] = pack_h2(lo16(w[i].x) * mul, lo16(w[i].z) * mul);
+            bq[i][1] = pack_h2(hi16(w[i].x) * mul16, hi16(w[i].z) * mul16);
+            bq[i][2] = pack_h2(lo16(w[i].y) * mul, lo16(w[i].w) * mul);
+            bq[i][3] = pack_h2(hi16(w[i].y) * mul16, hi16(w[i].w) * mul16);
+        }
+        const float f = a.scale2 * __uint_as_float((uint32_t)(10 + ex + 127) << 23);   // 2^24 / mul
+#pragma unroll
+        for (int j = 0; j < 2; ++j) fac[j] = __shfl_sync(0xffffffffu, f, 4 * (2 * t + j));
+#pragma unroll
+        for (int k = 0; k < NG; ++k) {
+            qs[k] += __shfl_xor_sync(0xffffffffu, qs[k], 1);
+            qs[k] += __shfl_xor_sync(0xffffffffu, qs[k], 2);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) qz[k][j] = __shfl_sync(0xffffffffu, qs[k] * a.scale2, 4 * (2 * t + j));
+        }
+    }
+    for (int i = 0, st = st0, round = 0, phase = 0; i < n; ++i) {
+        if (!mbar_wait(bars + 8 * st, phase)) {
+            if (lane == 0) flag_status(a.status, OSCAR_DEV_WAIT_TIMEOUT);
+            // the copies still under way land before this memory is used again
+            for (int k = i + 1; k < i + R::n && k < n; ++k) mbar_wait(bars + 8 * ((st0 + k) % R::n), (k / R::n) & 1);
+            break;
+        }
+        const uint8_t *stage = ring + st * R::stride;
+        const uint32_t sb = saddr(stage);
+        const int p0 = (lo + W * i) * kBlock;
+        const uint32_t okb = (ok >> (2 * st)) & 3u;
+        const bool full = okb == 3u && p0 >= a.sink && p0 + kBlock <= he;
+
+        float s[2][2][2];                            // [tile][row g, g + 8][column]
+        uint32_t vw[2][2][NG];                       // value scale | zero of those rows
+#pragma unroll
+        for (int tl = 0; tl < 2; ++tl) {
+            uint32_t w[2][4];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int row = tl * 16 + r * 8 + (lane & 7);
+                ldmatrix_x4(sb + row * 64 + (((lane >> 3) ^ ((row >> 1) & 3)) << 4), w[r][0], w[r][1], w[r][2], w[r][3]);
+            }
+            float d[NG][4];
+#pragma unroll
+            for (int k = 0; k < NG; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) d[k][e] = 0.f;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const uint32_t x = w[0][c], y = w[1][c], x8 = x >> 8, y8 = y >> 8;
+                mma16816_nv(d[c * NG / 4], x & kM0, y & kM0, x & kM1, y & kM1, bq[c][0], bq[c][1]);
+                mma16816_nv(d[c * NG / 4], x8 & kM0, y8 & kM0, x8 & kM1, y8 & kM1, bq[c][2], bq[c][3]);
+            }
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int row = tl * 16 + r * 8 + g;
+                const uint2 *rec = reinterpret_cast<const uint2 *>(stage + R::codes) + row * NG;
+                float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+                for (int k = 0; k < NG; ++k) {
+                    const uint2 z = rec[k];
+                    const float ks = lo16(z.x), kz = hi16(z.x);
+                    s0 += fmaf(ks, d[k][2 * r] * fac[0], kz * qz[k][0]);
+                    s1 += fmaf(ks, d[k][2 * r + 1] * fac[1], kz * qz[k][1]);
+                    vw[tl][r][k] = z.y;
+                }
+                s[tl][r][0] = s0;
+                s[tl][r][1] = s1;
+            }
+        }
+        if (!full) {
+#pragma unroll
+            for (int tl = 0; tl < 2; ++tl)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const int p = p0 + tl * 16 + r * 8 + g;
+                    if (p < a.sink || p >= he || !((okb >> tl) & 1u)) {
+                        s[tl][r][0] = s[tl][r][1] = -INFINITY;
+#pragma unroll
+                        for (int k = 0; k < NG; ++k) vw[tl][r][k] = 0u;
+                    }
+                }
+        }
+        if (MASS) {
+            float add = 0.f;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                float x = ex2_approx(s[u >> 1][u & 1][0] - cs.m[0]) + ex2_approx(s[u >> 1][u & 1][1] - cs.m[1]);
+                x += __shfl_xor_sync(0xffffffffu, x, 1);
+                x += __shfl_xor_sync(0xffffffffu, x, 2);
+                if (t == u) add = x;
+            }
+            const int p = p0 + 8 * t + g;
+            if (p >= a.sink && p < he && ((okb >> (t >> 1)) & 1u))
+                atomicAdd(a.mass + (((size_t)b * a.n_kv + h) * a.max_pages << sh) + p, add);
+        } else {
+            // raise the running maximum, or the bound on the value scales, when a block passes it
+            float top0 = fmaxf(fmaxf(s[0][0][0], s[0][1][0]), fmaxf(s[1][0][0], s[1][1][0]));
+            float top1 = fmaxf(fmaxf(s[0][0][1], s[0][1][1]), fmaxf(s[1][0][1], s[1][1][1]));
+            float vs = 0.f;
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int k = 0; k < NG; ++k) vs = fmaxf(vs, fabsf(lo16(vw[u >> 1][u & 1][k])));
+            if (__any_sync(0xffffffffu, top0 > cs.m[0] + kSlack || top1 > cs.m[1] + kSlack || vs > vmax)) {
+                const float m0 = fmaxf(cs.m[0], col_max(top0)), m1 = fmaxf(cs.m[1], col_max(top1));
+                const float al0 = ex2_approx(cs.m[0] - m0), al1 = ex2_approx(cs.m[1] - m1);
+                cs.m[0] = m0;
+                cs.m[1] = m1;
+                cs.l[0] *= al0;
+                cs.l[1] *= al1;
+#pragma unroll
+                for (int k = 0; k < NG; ++k) {
+                    zs[k][0] *= al0;
+                    zs[k][1] *= al1;
+                }
+                const uint32_t vb = __reduce_max_sync(0xffffffffu, __float_as_uint(vs));
+                float down = 1.f;
+                if (__uint_as_float(vb) > vmax) {
+                    const float old = vmax > 0.f ? vinv : INFINITY;      // nothing but zeros was summed before
+                    set_value_bound(vb, vmax, vinv);
+                    down = vinv / old;                                   // a power of two
+                }
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[c][j][e] *= (e & 1 ? al1 : al0) * down;
+            }
+#pragma unroll
+            for (int tl = 0; tl < 2; ++tl) {
+                uint32_t bp[NG][2];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float q0 = ex2_approx(s[tl][r][0] - cs.m[0]), q1 = ex2_approx(s[tl][r][1] - cs.m[1]);
+                    cs.l[0] += q0;
+                    cs.l[1] += q1;
+#pragma unroll
+                    for (int k = 0; k < NG; ++k) {
+                        const float v = lo16(vw[tl][r][k]) * vinv, z = hi16(vw[tl][r][k]);
+                        zs[k][0] = fmaf(q0, z, zs[k][0]);
+                        zs[k][1] = fmaf(q1, z, zs[k][1]);
+                        bp[k][r] = movmatrix_trans(pack_h2(q0 * v, q1 * v));
+                    }
+                }
+                const int row = tl * 16 + (lane & 15);
+#pragma unroll
+                for (int c = 0; c < 4; c += 2) {
+                    uint32_t r0, r1, r2, r3;
+                    ldmatrix_x4_trans(sb + 2048 + row * 64 + (((c + (lane >> 4)) ^ ((row >> 1) & 3)) << 4), r0, r1, r2, r3);
+                    const int k0 = c * NG / 4, k1 = (c + 1) * NG / 4;
+                    mma16816_nv(acc[c][0], r0 & kM0, r0 & kM1, r1 & kM0, r1 & kM1, bp[k0][0], bp[k0][1]);
+                    mma16816_nv(acc[c + 1][0], r2 & kM0, r2 & kM1, r3 & kM0, r3 & kM1, bp[k1][0], bp[k1][1]);
+                    r0 >>= 8; r1 >>= 8; r2 >>= 8; r3 >>= 8;
+                    mma16816_nv(acc[c][1], r0 & kM0, r0 & kM1, r1 & kM0, r1 & kM1, bp[k0][0], bp[k0][1]);
+                    mma16816_nv(acc[c + 1][1], r2 & kM0, r2 & kM1, r3 & kM0, r3 & kM1, bp[k1][0], bp[k1][1]);
+                }
+            }
+        }
+        __syncwarp();
+        if (i + R::n < n) issue(i + R::n, st);
+        if (++st == R::n) st = 0;
+        if (++round == R::n) {                           // every stage once more
+            round = 0;
+            phase ^= 1;
+        }
+    }
+    if (MASS) return;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        cs.l[j] = col_sum(cs.l[j]);
+#pragma unroll
+        for (int k = 0; k < NG; ++k) zs[k][j] = col_sum(zs[k][j]);
+    }
+    __syncthreads();                                 // every warp is done with its ring: results take its place
+    float *wm = res, *wl = res + W * 8, *wa = res + 2 * W * 8 + warp * G * kHeadDim;
+    if (g == 0) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            wm[warp * 8 + 2 * t + j] = cs.l[j] > 0.f ? cs.m[j] : -INFINITY;
+            wl[warp * 8 + 2 * t + j] = cs.l[j];
+        }
+    }
+    const float up = 1.f / vinv;                     // a power of two
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int head = 2 * t + (e & 1), ch = 32 * c + 4 * g + 2 * j + (e >> 1);
+                if (head < G) wa[head * kHeadDim + ch] = acc[c][j][e] * (e >> 1 ? 1048576.f : 16777216.f) * up + zs[c * NG / 4][e & 1];
+            }
+}
+
+// One channel of a merged row: sum A over weight L, maximum M (oscar_merge's last steps).
+__device__ __forceinline__ void write_out(const Attn4Args &a, size_t orow, int d, float A, float L, float M) {
+    const bool on = L > 0.f;
+    const float r = on ? __fdiv_rn(A, L) : 0.f;
+    if (a.of) a.of[orow * kHeadDim + d] = r;
+    if (a.o) a.o[orow * kHeadDim + d] = f32_to_bf16_rn(r);
+    if (a.o_lse && d == 0) a.o_lse[orow] = on ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+}
+
+// The merge of all S + 1 slots of one kv head's G query heads, in oscar_merge's order and arithmetic.
+// The accumulator rows come through shared memory, as many slots at a time as fit, all their 16-byte
+// copies in flight at once and under way while the weights are formed.
+template <int G, int W>
+__device__ __forceinline__ void merge_head(const Attn4Args &a, int b, int h, float *scratch, int scratch_bytes) {
+    const int S1 = a.out.S + 1;
+    const size_t row0 = ((size_t)b * a.n_kv * G + h * G) * S1;
+    float *ws = scratch, *ls = scratch + G * S1, *ms = ls + G * S1;
+    float *rows = scratch + ((2 * G * S1 + G + 3) & ~3);
+    const int chunk = min(S1, (scratch_bytes - (int)((rows - scratch) * 4)) / (G * kHeadDim * 4));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int kThreads = W * 32;
+    auto load = [&](int s0) {                          // slots [s0, s0 + chunk) of every head: [head][slot][128]
+        const int n = min(chunk, S1 - s0) * 32;
+#pragma unroll
+        for (int hh = 0; hh < G; ++hh) {
+            const float *src = a.out.acc + (row0 + (size_t)hh * S1 + s0) * kHeadDim;
+            const uint32_t dst = saddr(rows + (size_t)hh * chunk * kHeadDim);
+            for (int r = threadIdx.x; r < n; r += kThreads) cp_async16(dst + r * 16, src + r * 4);
+        }
+    };
+    load(0);
+    for (int i = threadIdx.x; i < G * S1; i += kThreads) {
+        ls[i] = __ldcg(a.out.l + row0 + i);
+        ws[i] = __ldcg(a.out.m + row0 + i);
+    }
+    __syncthreads();
+    if (warp < G) {
+        float M = -INFINITY;
+        for (int i = lane; i < S1; i += 32)
+            if (ls[warp * S1 + i] > 0.f) M = fmaxf(M, ws[warp * S1 + i]);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        if (lane == 0) ms[warp] = M;
+        for (int i = lane; i < S1; i += 32)
+            ws[warp * S1 + i] = ls[warp * S1 + i] > 0.f ? exp2_taylor(__fsub_rn(ws[warp * S1 + i], M)) : 0.f;
+    }
+    constexpr int kPart = G * kHeadDim / kThreads > 0 ? G * kHeadDim / kThreads : 1;
+    float L[kPart], A[kPart];
+#pragma unroll
+    for (int u = 0; u < kPart; ++u) L[u] = A[u] = 0.f;
+    for (int s0 = 0; s0 < S1; s0 += chunk) {
+        if (s0 > 0) {
+            __syncthreads();                           // the previous chunk is consumed
+            load(s0);
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncthreads();
+        const int n = min(chunk, S1 - s0);
+#pragma unroll
+        for (int u = 0; u < kPart; ++u) {
+            const int e = threadIdx.x + u * kThreads, hh = e / kHeadDim, d = e % kHeadDim;
+            if (hh >= G) continue;
+            const float *x = rows + (size_t)hh * chunk * kHeadDim + d, *w = ws + hh * S1 + s0, *l = ls + hh * S1 + s0;
+#pragma unroll 8
+            for (int i = 0; i < n; ++i) {
+                const bool on = l[i] > 0.f;
+                L[u] = on ? __fmaf_rn(l[i], w[i], L[u]) : L[u];
+                A[u] = on ? __fmaf_rn(x[i * kHeadDim], w[i], A[u]) : A[u];
+            }
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < kPart; ++u) {
+        const int e = threadIdx.x + u * kThreads, hh = e / kHeadDim, d = e % kHeadDim;
+        if (hh >= G) continue;
+        write_out(a, ((size_t)b * a.n_kv + h) * G + hh, d, A[u], L[u], ms[hh]);
+    }
+}
+
+// grid (S, Hkv, batch): CTA x takes split x; the first of each (request, kv head) also writes slot S, empty.
+template <int G, int NG, bool MASS, int W>
+__global__ void __launch_bounds__(W * 32, 16 / W)
+    attn4_kernel(Attn4Args a, const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
+    using R = Ring<NG, MASS, W>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t bars[W * (R::n + 1)];           // a warp's stages, then its tile of BF16 rows
+    __shared__ int last;
+    __shared__ float wf[W * 8], wM[8];
+    uint8_t *smem = smem_raw + ((1024u - (saddr(smem_raw) & 1023u)) & 1023u);
+    const int h = blockIdx.y, b = blockIdx.z, S = a.out.S, slot = blockIdx.x;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (lane == 0)
+        for (int i = 0; i <= R::n; ++i) mbar_init(saddr(&bars[warp * (R::n + 1) + i]), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    __syncwarp();
+    int T, he;
+    read_lengths(a.seq_len, a.hist_end, b, a.sink, a.max_pages << a.page_shift, a.status, T, he);
+    float *res = reinterpret_cast<float *>(smem);
+    history_warp<G, NG, MASS, W>(a, &tmk, &tmv, smem + warp * R::n * R::stride, saddr(&bars[warp * (R::n + 1)]), b, h, slot, T, he, warp,
+                                 lane, res);
+    if (MASS) return;
+    __syncthreads();
+    const size_t S1 = (size_t)S + 1, row0 = ((size_t)b * a.n_kv * G + h * G) * S1;
+    // every warp's weight 2^(m - M) once, then the sums
+    const float *wm = res, *wl = res + W * 8, *wa = res + 2 * W * 8;
+    if (threadIdx.x < W * 8) {
+        const int hh = threadIdx.x & 7;
+        float M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < W; ++w) M = fmaxf(M, wm[w * 8 + hh]);
+        wf[threadIdx.x] = M != -INFINITY ? exp2f(wm[threadIdx.x] - M) : 0.f;
+        if (threadIdx.x < 8) wM[hh] = M;
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < G * kHeadDim; e += W * 32) {
+        const int hh = e / kHeadDim, d = e % kHeadDim;
+        const float M = wM[hh];
+        float L = 0.f, A = 0.f;
+#pragma unroll 4
+        for (int w = 0; w < W; ++w) {
+            const float f = wf[w * 8 + hh], x = wa[(w * G + hh) * kHeadDim + d];
+            L = fmaf(wl[w * 8 + hh], f, L);
+            A = fmaf(f > 0.f ? x : 0.f, f, A);
+        }
+        const size_t row = row0 + hh * S1 + slot;
+        a.out.acc[row * kHeadDim + d] = A;
+        if (d == 0) {
+            a.out.m[row] = M;
+            a.out.l[row] = L;
+        }
+        if (slot == 0) {
+            a.out.acc[(row + S) * kHeadDim + d] = 0.f;
+            if (d == 0) {
+                a.out.m[row + S] = -INFINITY;
+                a.out.l[row + S] = 0.f;
+            }
+        }
+        if (S == 1 && a.counters) write_out(a, ((size_t)b * a.n_kv + h) * G + hh, d, A, L, M);   // weight 2^0: merged
+    }
+    if (!a.counters || S == 1) return;
+    __syncthreads();                                  // the slot is written; the count releases it
+    if (threadIdx.x == 0) {
+        int32_t *c = a.counters + (size_t)b * a.n_kv + h;
+        int32_t n;
+        asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(n) : "l"(c) : "memory");
+        last = n == S - 1;
+        if (last) *c = 0;
+    }
+    __syncthreads();
+    if (last) merge_head<G, W>(a, b, h, res, a.smem_bytes);
+}
+
+template <int G, int NG, bool MASS, int W>
+cudaError_t launch_one(Attn4Args a, const CUtensorMap &tmk, const CUtensorMap &tmv, int batch, cudaStream_t st) {
+    // the merge: weights of every slot, and room for one slot's rows at least
+    const int merge = (((2 * G * (a.out.S + 1) + G + 3) & ~3) + G * kHeadDim) * 4, combine = (2 * W * 8 + W * G * kHeadDim) * 4;
+    int smem = Ring<NG, MASS, W>::total;
+    if (!MASS && smem < combine) smem = combine;
+    if (!MASS && a.counters && smem < merge) smem = merge;
+    a.smem_bytes = smem;
+    smem += 1024;
+    auto kern = attn4_kernel<G, NG, MASS, W>;
+    if (cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void *>(kern), smem)) return e;
+    kern<<<dim3(a.out.S, a.n_kv, batch), W * 32, smem, st>>>(a, tmk, tmv);
+    return cudaGetLastError();
+}
+
+template <int G, bool MASS, int W>
+cudaError_t launch_group(const Attn4Args &a, int group, const CUtensorMap &tmk, const CUtensorMap &tmv, int batch, cudaStream_t st) {
+    switch (group) {
+        case 32: return launch_one<G, 4, MASS, W>(a, tmk, tmv, batch, st);
+        case 64: return launch_one<G, 2, MASS, W>(a, tmk, tmv, batch, st);
+        default: return launch_one<G, 1, MASS, W>(a, tmk, tmv, batch, st);
+    }
+}
+
+}  // namespace
+
+template <int G>
+cudaError_t launch_attn4(const Attn4Args &a, int group, bool mass, const CUtensorMap &tmk, const CUtensorMap &tmv, int batch,
+                         cudaStream_t st) {
+    const bool wide = (long long)a.out.S * a.n_kv * batch <= kSms;       // a CTA for each SM at most: 16 warps each
+    if (mass) return wide ? launch_group<G, true, 16>(a, group, tmk, tmv, batch, st) : launch_group<G, true, 8>(a, group, tmk, tmv, batch, st);
+    return wide ? launch_group<G, false, 16>(a, group, tmk, tmv, batch, st) : launch_group<G, false, 8>(a, group, tmk, tmv, batch, st);
+}
+
+}  // namespace oscar

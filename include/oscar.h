@@ -541,9 +541,9 @@ OSCAR_API int32_t oscar_suggest_splits_int4(const oscar_layout_t *layout, int32_
  * Decode attention over [BF16 sink | INT4 history | BF16 recent]: arguments as for
  * oscar_decode_attention, with the unrotated bf16 q (16-byte aligned) against both pools and an INT4
  * pool as the history.  Any n_kv_heads; the layout's codebook levels are not used.
- * Writes every slot of `partials` (history slots 0..S-1 of whole 32-token blocks at absolute positions
- * 32 i, in ascending order, slot S the BF16 rows); with out or out_f32 non-NULL also their merge, as
- * oscar_merge(R_V = NULL) defines it, lse optional.  Query products and softmax sums are fp32 or finer;
+ * Writes every slot of `partials`: the history is cut into S splits of whole 32-token blocks (at absolute
+ * positions 32 i), the BF16 rows are dealt out to the same splits, slot S is written empty.  With out or
+ * out_f32 non-NULL also their merge, as oscar_merge(R_V = NULL) defines it, lse optional.  Query products and softmax sums are fp32 or finer;
  * a probability times its value scale is rounded to fp16 (2^-11 relative) for the value product.
  *   merge_counters  NULL: the merge is a second launch.  Else int32 [batch·n_kv_heads], all zero, left
  *                   zero: the last CTA of a request's kv head to finish merges it, in the same launch
