@@ -1,4 +1,4 @@
-"""Thin ctypes binding of liboscar.so (include/oscar.h): argument marshalling only.
+"""Thin binding of liboscar.so (include/oscar.h): argument marshalling only, by ctypes or, for the INT4 calls, natively.
 
 Every function here has the name of the C entry point it calls, takes torch
 tensors (device memory, caller-owned) and passes their addresses, sizes and the
@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import importlib.util
 import os
 from typing import Optional
 
@@ -425,84 +426,35 @@ def oscar_decode_attention_noalloc(layout: Layout, q: torch.Tensor, q_rot: torch
         _ptr(lse), _stream(stream)))
 
 
-# ---- the 4-bit history.  These calls check every argument's type, shape and device, and are made once per layer and
-# token: a check reads each property once and returns the address, and the layout's descriptor is built once.
+# ---- the 4-bit history.  These calls are made once per layer and token, and check every argument's type, shape and
+# device; the checks and the call are native (csrc/marshal.cpp), the functions here give them names and defaults.
 
-_bf16, _f32, _i32, _u8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
-
-
-def _refuse(name: str, what: str, t: torch.Tensor, dtype, shape, dev: int):
-    if t.dtype is not dtype:
-        raise OscarError(f"{name}: {what} must be {dtype}, not {t.dtype}")
-    if t.shape != shape:
-        raise OscarError(f"{name}: {what} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if not t.is_cuda or t.get_device() != dev:
-        raise OscarError(f"{name}: {what} is on {t.device}, not on the current CUDA device")
-    raise OscarError(f"{name}: {what} must be contiguous")
+_marshal = None
 
 
-def _at(name: str, what: str, t: Optional[torch.Tensor], dtype, shape, dev: int):
-    """The address of a contiguous tensor of this type and shape on device dev (None: an argument left out)."""
-    if t is None:
-        return None
-    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
-        return t.data_ptr()
-    _refuse(name, what, t, dtype, shape, dev)
+def _native():
+    global _marshal
+    if _marshal is None:
+        path = os.path.join(_PKG, "_marshal.so")
+        if not os.path.exists(path):
+            raise OscarError(f"{path} is missing: build it with __graft_entry__.build()")
+        lib()                                          # the library that the extension calls
+        spec = importlib.util.spec_from_file_location("_marshal", path)
+        _marshal = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(_marshal)
+        _marshal.set_error(OscarError)
+    return _marshal
 
 
-def _device() -> int:
-    try:
-        return torch.cuda.current_device()
-    except (RuntimeError, AssertionError) as e:
-        raise OscarError("no current CUDA device") from e
-
-
-def _stream_on(name: str, stream, dev: int) -> int:
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)
-    if stream.device.index != dev:
-        raise OscarError(f"{name}: the stream belongs to {stream.device}, not to the current CUDA device")
-    return stream.cuda_stream
-
-
-def _layout_ref(layout: Layout):
-    """The layout's descriptor by reference, built once (a Layout does not change)."""
-    ref = layout.__dict__.get("_ref")
-    if ref is None:
-        ref = ctypes.byref(layout.c())
-        object.__setattr__(layout, "_ref", ref)
-    return ref
-
-
-def _bf16_ref(name: str, layout: Layout, pool: Bf16Pool, dev: int):
-    n = pool.k.shape[0]
-    shape = (n, layout.page_size, layout.n_kv_heads, layout.head_dim)
-    return ctypes.byref(Bf16PoolC(_at(name, "pool k", pool.k, _bf16, shape, dev),
-                                  _at(name, "pool v", pool.v, _bf16, shape, dev), n))
-
-
-def _int4_ref(name: str, layout: Layout, pool: Int4Pool, dev: int):
-    n, H, ps, D = pool.codes_k.shape[0], layout.n_kv_heads, layout.page_size, layout.head_dim
-    shape = (n, H, ps, D // 2)
-    return ctypes.byref(Int4PoolC(_at(name, "codes_k", pool.codes_k, _u8, shape, dev),
-                                  _at(name, "codes_v", pool.codes_v, _u8, shape, dev),
-                                  _at(name, "scale_zero", pool.scale_zero, _bf16, (n, H, ps, D // layout.group, 4), dev), n))
-
-
-def _table_shape(name: str, t: torch.Tensor):
-    if t.dim() != 2:
-        raise OscarError(f"{name}: page tables must be [batch, max_pages]")
-    return t.shape
-
-
-def _heads(name: str, what: str, t: torch.Tensor, heads: int, n: int, D: int, dev: int):
-    """(address, token stride) of [n, heads, D] bf16 whose heads of one token lie together (a slice of a packed row)."""
-    if not (t.dtype is _bf16 and t.shape == (n, heads, D) and t.get_device() == dev):
-        _refuse(name, what, t, _bf16, (n, heads, D), dev)
-    s0, s1, s2 = t.stride()
-    if n and (s2 != 1 or (heads > 1 and s1 != D)):
-        raise OscarError(f"{name}: the heads of one token of {what} must lie together")
-    return t.data_ptr(), (s0 if n > 1 else heads * D)
+def _layout_at(layout: Layout) -> int:
+    """The address of the layout's descriptor, built once (a Layout does not change)."""
+    at = layout.__dict__.get("_at")
+    if at is None:
+        c = layout.c()
+        object.__setattr__(layout, "_c", c)
+        at = ctypes.addressof(c)
+        object.__setattr__(layout, "_at", at)
+    return at
 
 
 def oscar_append_kv(layout: Layout, q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, pool: Bf16Pool,
@@ -513,61 +465,26 @@ def oscar_append_kv(layout: Layout, q: Optional[torch.Tensor], k: torch.Tensor, 
                     stream=None):
     """New tokens' heads (q [n, Hq, D], k and v [n, Hkv, D] bf16, token rows possibly strided): RMS norm per head,
     rotary position, q to q_out and k, v to the tokens' slots of the BF16 pool."""
-    name, dev, n, D, Hq, H = "oscar_append_kv", _device(), k.shape[0], layout.head_dim, layout.n_q_heads, layout.n_kv_heads
-    pool_ref = _bf16_ref(name, layout, pool, dev)
-    batch, max_pages = shape = _table_shape(name, page_table)
-    rows = 0 if rope is None else rope.shape[0]
-    qp, qs = _heads(name, "q", q, Hq, n, D, dev) if q is not None else (None, 0)
-    kp, ks = _heads(name, "k", k, H, n, D, dev)
-    vv, vs = _heads(name, "v", v, H, n, D, dev)
-    _check(name, lib().oscar_append_kv(
-        _layout_ref(layout), qp, qs, kp, ks, vv, vs, n, _at(name, "q_weight", q_weight, _bf16, (D,), dev),
-        _at(name, "k_weight", k_weight, _bf16, (D,), dev), eps, _at(name, "rope", rope, _f32, (rows, 128), dev), rows,
-        rot_dim, 1 if interleaved else 0, pool_ref, _at(name, "page_table", page_table, _i32, shape, dev), max_pages,
-        batch, _at(name, "req_idx", req_idx, _i32, (n,), dev), _at(name, "positions", positions, _i32, (n,), dev),
-        _at(name, "rope_positions", rope_positions, _i32, (n,), dev), _at(name, "q_out", q_out, _bf16, (n, Hq, D), dev),
-        _stream_on(name, stream, dev)))
+    _native().append_kv(_layout_at(layout), q, k, v, pool, page_table, req_idx, positions, q_out, q_weight, k_weight, eps,
+                        rope, rot_dim, interleaved, rope_positions, stream)
 
 
 def oscar_demote_int4(layout: Layout, src: Bf16Pool, bf16_page_table: torch.Tensor, dst: Int4Pool,
                       int4_page_table: torch.Tensor, pos_begin: torch.Tensor, pos_end: torch.Tensor, c_K: float = 1.0,
                       c_V: float = 1.0, stream=None):
     """BF16 rows at positions [pos_begin[b], pos_end[b]) (int32 [batch]) to 4 bits, as they are stored."""
-    name, dev = "oscar_demote_int4", _device()
-    batch, max_pages = shape = _table_shape(name, int4_page_table)
-    _check(name, lib().oscar_demote_int4(
-        _layout_ref(layout), _bf16_ref(name, layout, src, dev), _at(name, "bf16_page_table", bf16_page_table, _i32, shape, dev),
-        _int4_ref(name, layout, dst, dev), _at(name, "int4_page_table", int4_page_table, _i32, shape, dev), max_pages,
-        batch, _at(name, "pos_begin", pos_begin, _i32, (batch,), dev), _at(name, "pos_end", pos_end, _i32, (batch,), dev),
-        c_K, c_V, _stream_on(name, stream, dev)))
+    _native().demote_int4(_layout_at(layout), src, bf16_page_table, dst, int4_page_table, pos_begin, pos_end, c_K, c_V,
+                          stream)
 
 
 def oscar_promote_int4(layout: Layout, src: Int4Pool, int4_page_table: torch.Tensor, dst: Bf16Pool,
                        bf16_page_table: torch.Tensor, pos_begin: torch.Tensor, pos_end: torch.Tensor, stream=None):
     """4-bit rows at positions [pos_begin[b], pos_end[b]) back to BF16."""
-    name, dev = "oscar_promote_int4", _device()
-    batch, max_pages = shape = _table_shape(name, int4_page_table)
-    _check(name, lib().oscar_promote_int4(
-        _layout_ref(layout), _int4_ref(name, layout, src, dev), _at(name, "int4_page_table", int4_page_table, _i32, shape, dev),
-        _bf16_ref(name, layout, dst, dev), _at(name, "bf16_page_table", bf16_page_table, _i32, shape, dev), max_pages,
-        batch, _at(name, "pos_begin", pos_begin, _i32, (batch,), dev), _at(name, "pos_end", pos_end, _i32, (batch,), dev),
-        _stream_on(name, stream, dev)))
+    _native().promote_int4(_layout_at(layout), src, int4_page_table, dst, bf16_page_table, pos_begin, pos_end, stream)
 
 
 def oscar_suggest_splits_int4(layout: Layout, batch: int, max_hist_tokens: int, sm_count: int) -> int:
     return int(lib().oscar_suggest_splits_int4(ctypes.byref(layout.c()), batch, max_hist_tokens, sm_count))
-
-
-def _attention4(name: str, layout: Layout, q, bf16_pool, bf16_page_table, int4_pool, int4_page_table, seq_len, hist_end,
-                sm_scale: float, dev: int):
-    """The arguments that decode attention and the attention weights share."""
-    batch, max_pages = shape = _table_shape(name, int4_page_table)
-    return batch, max_pages, (
-        _layout_ref(layout), _at(name, "q", q, _bf16, (batch, layout.n_q_heads, layout.head_dim), dev),
-        _bf16_ref(name, layout, bf16_pool, dev), _at(name, "bf16_page_table", bf16_page_table, _i32, shape, dev),
-        _int4_ref(name, layout, int4_pool, dev), _at(name, "int4_page_table", int4_page_table, _i32, shape, dev), max_pages,
-        _at(name, "seq_len", seq_len, _i32, (batch,), dev), _at(name, "hist_end", hist_end, _i32, (batch,), dev), batch,
-        sm_scale)
 
 
 def oscar_decode_attention_int4(layout: Layout, q: torch.Tensor, bf16_pool: Bf16Pool, bf16_page_table: torch.Tensor,
@@ -578,17 +495,8 @@ def oscar_decode_attention_int4(layout: Layout, q: torch.Tensor, bf16_pool: Bf16
                                 stream=None):
     """Decode attention over [BF16 sink | INT4 history | BF16 recent]; with out or out_f32 also the merge, in the same
     launch when merge_counters (int32 zeros [batch * n_kv_heads]) is given."""
-    name, dev = "oscar_decode_attention_int4", _device()
-    batch, _, args = _attention4(name, layout, q, bf16_pool, bf16_page_table, int4_pool, int4_page_table, seq_len,
-                                 hist_end, sm_scale, dev)
-    D, heads, S = layout.head_dim, (batch, layout.n_q_heads), partials.n_splits
-    rows, full = heads + (S + 1,), heads + (D,)
-    part = PartialsC(_at(name, "partials m", partials.m, _f32, rows, dev), _at(name, "partials l", partials.l, _f32, rows, dev),
-                     _at(name, "partials acc", partials.acc, _f32, rows + (D,), dev), S)
-    _check(name, lib().oscar_decode_attention_int4(
-        *args, ctypes.byref(part), _at(name, "out", out, _bf16, full, dev), _at(name, "out_f32", out_f32, _f32, full, dev),
-        _at(name, "lse", lse, _f32, heads, dev),
-        _at(name, "merge_counters", merge_counters, _i32, (batch * layout.n_kv_heads,), dev), _stream_on(name, stream, dev)))
+    _native().decode_attention_int4(_layout_at(layout), q, bf16_pool, bf16_page_table, int4_pool, int4_page_table, seq_len,
+                                    hist_end, sm_scale, partials, out, out_f32, lse, merge_counters, stream)
 
 
 def oscar_attention_mass_int4(layout: Layout, q: torch.Tensor, bf16_pool: Bf16Pool, bf16_page_table: torch.Tensor,
@@ -596,13 +504,8 @@ def oscar_attention_mass_int4(layout: Layout, q: torch.Tensor, bf16_pool: Bf16Po
                               hist_end: torch.Tensor, sm_scale: float, lse: torch.Tensor, mass: torch.Tensor,
                               stream=None):
     """Add the attention weight of this step to mass [batch, Hkv, max_pages * page_size] (fp32)."""
-    name, dev = "oscar_attention_mass_int4", _device()
-    batch, max_pages, args = _attention4(name, layout, q, bf16_pool, bf16_page_table, int4_pool, int4_page_table, seq_len,
-                                         hist_end, sm_scale, dev)
-    _check(name, lib().oscar_attention_mass_int4(
-        *args, _at(name, "lse", lse, _f32, (batch, layout.n_q_heads), dev),
-        _at(name, "mass", mass, _f32, (batch, layout.n_kv_heads, max_pages * layout.page_size), dev),
-        _stream_on(name, stream, dev)))
+    _native().attention_mass_int4(_layout_at(layout), q, bf16_pool, bf16_page_table, int4_pool, int4_page_table, seq_len,
+                                  hist_end, sm_scale, lse, mass, stream)
 
 
 def oscar_evict_int4(layout: Layout, src: Int4Pool, src_page_table: torch.Tensor, dst: Int4Pool,
@@ -610,16 +513,8 @@ def oscar_evict_int4(layout: Layout, src: Int4Pool, src_page_table: torch.Tensor
                      mass: torch.Tensor, mass_out: torch.Tensor, kept: torch.Tensor, stream=None):
     """Keep the keep[b] history positions of largest mass of each kv head; their rows go to the pages of
     dst_page_table, their old positions to kept [batch, Hkv, at least max(keep)] (int32)."""
-    name, dev = "oscar_evict_int4", _device()
-    batch, max_pages = shape = _table_shape(name, src_page_table)
-    weights, one, stride = (batch, layout.n_kv_heads, max_pages * layout.page_size), (batch,), kept.shape[-1]
-    _check(name, lib().oscar_evict_int4(
-        _layout_ref(layout), _int4_ref(name, layout, src, dev), _at(name, "src_page_table", src_page_table, _i32, shape, dev),
-        _int4_ref(name, layout, dst, dev), _at(name, "dst_page_table", dst_page_table, _i32, shape, dev), max_pages, batch,
-        _at(name, "seq_len", seq_len, _i32, one, dev), _at(name, "hist_end", hist_end, _i32, one, dev),
-        _at(name, "keep", keep, _i32, one, dev), _at(name, "mass", mass, _f32, weights, dev),
-        _at(name, "mass_out", mass_out, _f32, weights, dev),
-        _at(name, "kept", kept, _i32, (batch, layout.n_kv_heads, stride), dev), stride, _stream_on(name, stream, dev)))
+    _native().evict_int4(_layout_at(layout), src, src_page_table, dst, dst_page_table, seq_len, hist_end, keep, mass,
+                         mass_out, kept, stream)
 
 
 def oscar_get_device_status(stream=None) -> int:

@@ -529,6 +529,41 @@ def test_evict_flags_and_shared_pages():
     assert np.array_equal(kept[0, 1, :280], np.arange(64, 344))
 
 
+# ----------------------------------------------------------------- binding --
+def test_the_binding_refuses_types_shapes_strides_and_places():
+    c = ic.Cache([400], seed=1).upload()
+    L, cpu = c.L, lambda t: t.cpu()
+    lo, hi = i32([64]), i32([144])
+    demote = lambda **k: ob.oscar_demote_int4(L, k.get("src", c.bfp), k.get("bt", c.db), k.get("dst", c.int4), k.get("it", c.d4),
+                                              k.get("lo", lo), k.get("hi", hi))
+    cases = [(dict(lo=lo.long()), "pos_begin must be torch.int32, not Long"), (dict(hi=i32([1, 2])), "pos_end must have shape .1,., not .2,."),
+             (dict(lo=cpu(lo)), "pos_begin is on cpu, not on the current CUDA device"), (dict(it=c.d4[0]), "page tables must be"),
+             (dict(bt=c.db[:, :5]), "bf16_page_table must have shape"), (dict(src=ob.Bf16Pool(c.bfp.k.float(), c.bfp.v)), "pool k must be torch.bfloat16"),
+             (dict(src=ob.Bf16Pool(c.bfp.k, c.bfp.v[:1])), "pool v must have shape"), (dict(lo=7), "pos_begin must be a tensor"),
+             (dict(bt=c.db.t().contiguous().t()), "bf16_page_table must be contiguous" if c.db.shape[0] > 1 else None),
+             (dict(dst=ob.Int4Pool(c.int4.codes_k, c.int4.codes_v.view(torch.int8), c.int4.scale_zero)), "codes_v must be torch.uint8"),
+             (dict(dst=ob.Int4Pool(c.int4.codes_k, c.int4.codes_v, c.int4.scale_zero[..., :2])), "scale_zero must have shape")]
+    before = c.int4.codes_k.clone()
+    for kw, text in cases:
+        if text:
+            with pytest.raises(ob.OscarError, match=text):
+                demote(**kw)
+    x = torch.zeros((2, 2, D), dtype=torch.bfloat16, device="cuda")
+    for bad in (x.transpose(0, 1).contiguous().transpose(0, 1), torch.zeros((2, 2, 2 * D), dtype=torch.bfloat16, device="cuda")[..., ::2]):
+        with pytest.raises(ob.OscarError, match="lie together"):
+            ob.oscar_append_kv(L, None, bad, x, c.bfp, c.db, i32([0, 0]), i32([0, 1]))
+    with pytest.raises(ob.OscarError, match="failed .1.: .*both or neither"):
+        ob.oscar_append_kv(L, None, x, x, c.bfp, c.db, i32([0, 0]), i32([0, 1]), q_out=torch.zeros((2, 8, D), dtype=torch.bfloat16, device="cuda"))
+    with pytest.raises(ob.OscarError, match="clip"):
+        ob.oscar_demote_int4(L, c.bfp, c.db, c.int4, c.d4, lo, hi, 0.0)
+    with pytest.raises(AttributeError):
+        demote(src=None)
+    with pytest.raises(TypeError):
+        ob.oscar_demote_int4(L, c.bfp, c.db, c.int4, c.d4, lo, hi, "1")
+    torch.cuda.synchronize()
+    assert torch.equal(before, c.int4.codes_k) and ob.oscar_get_device_status() == 0
+
+
 # ---------------------------------------------------------------- together --
 @pytest.mark.parametrize("n_kv,gqa,page,group", [(2, 4, 16, 128), (1, 8, 32, 32)])
 def test_a_conversation(n_kv, gqa, page, group):

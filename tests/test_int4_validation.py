@@ -150,20 +150,9 @@ def test_suggested_splits(L):
     assert ob.oscar_suggest_splits_int4(lay, 0, 100, 152) == 1 and ob.oscar_suggest_splits_int4(lay, 1, 0, 152) == 1
 
 
-def test_the_binding_checks_types_shapes_and_places():
+def test_the_binding_needs_a_device():
     lay = ob.Layout(2, 4, 16)
-    f = lambda *s, t=torch.float32: torch.zeros(s, dtype=t)
-    i4 = ob.Int4Pool.empty(lay, 3, "cpu")
-    bf = ob.Bf16Pool.empty(lay, 3, "cpu")
-    pt, one = f(1, 4, t=torch.int32), f(1, t=torch.int32)
+    i4, bf = ob.Int4Pool.empty(lay, 3, "cpu"), ob.Bf16Pool.empty(lay, 3, "cpu")
+    pt, one = torch.zeros(1, 4, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
     with pytest.raises(ob.OscarError, match="current CUDA device"):      # CPU tensors, with and without a GPU
         ob.oscar_demote_int4(lay, bf, pt, i4, pt, one, one)
-    at = ob._at
-    with pytest.raises(ob.OscarError, match="codes_v must have shape"):
-        at("x", "codes_v", f(3, 2, 16, 32, t=torch.uint8), torch.uint8, (3, 2, 16, 64), 0)
-    with pytest.raises(ob.OscarError, match="must be torch.int32"):
-        at("x", "positions", f(4, t=torch.int64), torch.int32, (4,), 0)
-    with pytest.raises(ob.OscarError, match="page tables must be"):
-        ob._table_shape("x", one)
-    with pytest.raises(ob.OscarError, match="lie together"):
-        ob._heads("x", "k", f(3, 128, 2, t=torch.bfloat16).transpose(1, 2), 2, 3, 128, -1)
