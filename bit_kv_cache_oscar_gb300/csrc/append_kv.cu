@@ -7,7 +7,7 @@
 // Bound by HBM (a row is read and written once).  A head's row is 256 bytes: 16 lanes with 8 channels each
 // (one 16-byte load and store a lane), so the sum of squares is a 4-step shuffle and a rotation partner is
 // either in the lane (channels 2j, 2j+1) or rot_dim/16 lanes away.  A warp takes a run of row pairs of one
-// token, reads the token's angles once, and keeps two rows a half-warp in flight: each row's registers
+// token, reads the token's angles once, and keeps four rows a half-warp in flight: each row's registers
 // are refilled as soon as it is computed.
 
 #include <cuda_bf16.h>
@@ -68,7 +68,7 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-constexpr int kAhead = 2;
+constexpr int kAhead = 4;
 
 template <bool PAIRS>
 __global__ void __launch_bounds__(kWarps * 32, 3) append_kernel(AppendArgs a) {

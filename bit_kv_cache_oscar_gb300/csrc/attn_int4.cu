@@ -1,5 +1,7 @@
 // Decode attention and attention weights over an INT4 history: the host side of attn_int4.cuh.
 
+#include <algorithm>
+
 #include "attn_int4_args.cuh"
 #include "tma.cuh"
 
@@ -45,15 +47,16 @@ cudaError_t launch(const oscar_layout_t &L, const Attn4Input &in, Attn4Args a, b
 
 }  // namespace
 
-// One split up to 2048 tokens: it needs no merge, which takes longer than four rounds of blocks (3 and 0.8 us
-// each).  Above: one CTA an SM when the batch's heads are few enough for each to get several, else about four
-// waves of two an SM, so that requests of different lengths finish evenly.  At least 16 blocks of 32 tokens
-// (one a warp) for each split.
+// Splits of at least 256 tokens (8 blocks): shorter ones cost more in the merge than they save.  Up to that
+// bound one CTA of 16 warps an SM where that fills nine SMs in ten; else, while the heads leave each four
+// splits, one wave of CTAs of 8 warps, two an SM; else about six waves of those, so that requests of
+// different lengths finish evenly.  (100K tokens, 8 heads: 31.5 us with 19 splits of 16 warps, 36.8 with 37 of
+// 8; 4 x 131K: 145 us with 9 splits in one wave, 152 with 4 of 16 warps, 182 with 38 in four waves; ragged
+// batch of 32: 649, 523, 507, 497 and 507 us with 1, 3, 5, 7 and 10.)
 int suggest_splits4(const oscar_layout_t &L, int batch, int max_hist, int sm_count) {
-    if (max_hist <= 2048) return 1;
-    const long long per = (long long)batch * L.n_kv_heads;
-    long long want = per * 4 <= sm_count ? sm_count / per : (8LL * sm_count + per - 1) / per;
-    const long long most = ((long long)max_hist + 16 * kBlock - 1) / (16 * kBlock);
+    const long long per = (long long)batch * L.n_kv_heads, wide = sm_count / per, slots = 2LL * sm_count;
+    long long want = wide * per * 10 >= sm_count * 9LL ? wide : per * 4 <= slots ? slots / per : 6 * slots / per;
+    const long long most = ((long long)max_hist + 255) / 256;
     if (want > most) want = most;
     return (int)(want < 1 ? 1 : want > 1024 ? 1024 : want);
 }
@@ -75,7 +78,11 @@ cudaError_t launch_decode4(const oscar_layout_t &L, const Attn4Input &in, int ba
 cudaError_t launch_mass4(const oscar_layout_t &L, const Attn4Input &in, int batch, const float *lse, float *mass,
                          int32_t *status, cudaStream_t st) {
     Attn4Args a{};
-    a.out.S = suggest_splits4(L, batch, in.max_pages * L.page_size, kSms);
+    // no merge to pay for: about three waves of CTAs even where one would hold the splits (a ragged batch of
+    // 8: 100, 86, 84 and 90 us with 4, 9, 14 and 28)
+    const long long per = (long long)batch * L.n_kv_heads;
+    const int S = suggest_splits4(L, batch, in.max_pages * L.page_size, kSms), waves = (int)std::min(1024LL, 6LL * kSms / per);
+    a.out.S = per > kSms / 4 && S < waves ? (int)std::min<long long>(waves, (in.max_pages * (long long)L.page_size + 255) / 256) : S;
     a.lse = lse;
     a.mass = mass;
     a.status = status;

@@ -56,6 +56,8 @@ struct Ring {
 
 __device__ __forceinline__ float lo16(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi16(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ __nv_bfloat162 as_bf2(uint32_t w) { return *reinterpret_cast<const __nv_bfloat162 *>(&w); }
+__device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 v) { return *reinterpret_cast<const uint32_t *>(&v); }
 __device__ __forceinline__ uint32_t pack_h2(float a, float b) {
     const __half2 h = __floats2half2_rn(a, b);
     return *reinterpret_cast<const uint32_t *>(&h);
@@ -416,17 +418,19 @@ __device__ __forceinline__ void history_warp(const Attn4Args &a, const CUtensorM
             for (int r = 0; r < 2; ++r) {
                 const int row = tl * 16 + r * 8 + g;
                 const uint2 *rec = reinterpret_cast<const uint2 *>(stage + R::codes) + row * NG;
-                float s0 = 0.f, s1 = 0.f;
+                float s0, s1, z0, z1;
 #pragma unroll
                 for (int k = 0; k < NG; ++k) {
                     const uint2 z = rec[k];
                     const float ks = lo16(z.x), kz = hi16(z.x);
-                    s0 += fmaf(ks, d[k][2 * r] * fac[0], kz * qz[k][0]);
-                    s1 += fmaf(ks, d[k][2 * r + 1] * fac[1], kz * qz[k][1]);
+                    s0 = k ? fmaf(ks, d[k][2 * r], s0) : ks * d[k][2 * r];
+                    s1 = k ? fmaf(ks, d[k][2 * r + 1], s1) : ks * d[k][2 * r + 1];
+                    z0 = k ? fmaf(kz, qz[k][0], z0) : kz * qz[k][0];
+                    z1 = k ? fmaf(kz, qz[k][1], z1) : kz * qz[k][1];
                     vw[tl][r][k] = z.y;
                 }
-                s[tl][r][0] = s0;
-                s[tl][r][1] = s1;
+                s[tl][r][0] = fmaf(s0, fac[0], z0);
+                s[tl][r][1] = fmaf(s1, fac[1], z1);
             }
         }
         if (!full) {
@@ -458,11 +462,12 @@ __device__ __forceinline__ void history_warp(const Attn4Args &a, const CUtensorM
             // raise the running maximum, or the bound on the value scales, when a block passes it
             float top0 = fmaxf(fmaxf(s[0][0][0], s[0][1][0]), fmaxf(s[1][0][0], s[1][1][0]));
             float top1 = fmaxf(fmaxf(s[0][0][1], s[0][1][1]), fmaxf(s[1][0][1], s[1][1][1]));
-            float vs = 0.f;
+            __nv_bfloat162 vs2 = as_bf2(vw[0][0][0]);        // scales in the low halves (never negative)
 #pragma unroll
             for (int u = 0; u < 4; ++u)
 #pragma unroll
-                for (int k = 0; k < NG; ++k) vs = fmaxf(vs, fabsf(lo16(vw[u >> 1][u & 1][k])));
+                for (int k = 0; k < NG; ++k) vs2 = __hmax2(vs2, as_bf2(vw[u >> 1][u & 1][k]));
+            const float vs = fmaxf(lo16(as_u32(vs2)), 0.f);
             if (__any_sync(0xffffffffu, top0 > cs.m[0] + kSlack || top1 > cs.m[1] + kSlack || vs > vmax)) {
                 const float m0 = fmaxf(cs.m[0], col_max(top0)), m1 = fmaxf(cs.m[1], col_max(top1));
                 const float al0 = ex2_approx(cs.m[0] - m0), al1 = ex2_approx(cs.m[1] - m1);
@@ -495,14 +500,15 @@ __device__ __forceinline__ void history_warp(const Attn4Args &a, const CUtensorM
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     const float q0 = ex2_approx(s[tl][r][0] - cs.m[0]), q1 = ex2_approx(s[tl][r][1] - cs.m[1]);
+                    const float w0 = q0 * vinv, w1 = q1 * vinv;
                     cs.l[0] += q0;
                     cs.l[1] += q1;
 #pragma unroll
                     for (int k = 0; k < NG; ++k) {
-                        const float v = lo16(vw[tl][r][k]) * vinv, z = hi16(vw[tl][r][k]);
+                        const float v = lo16(vw[tl][r][k]), z = hi16(vw[tl][r][k]);
                         zs[k][0] = fmaf(q0, z, zs[k][0]);
                         zs[k][1] = fmaf(q1, z, zs[k][1]);
-                        bp[k][r] = movmatrix_trans(pack_h2(q0 * v, q1 * v));
+                        bp[k][r] = movmatrix_trans(pack_h2(w0 * v, w1 * v));
                     }
                 }
                 const int row = tl * 16 + (lane & 15);

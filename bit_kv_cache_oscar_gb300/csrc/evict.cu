@@ -42,8 +42,14 @@ __device__ __forceinline__ uint32_t order_key(float x) {
 // kernels decides alike.
 __device__ __forceinline__ bool read_request(const EvictArgs &a, int b, int &T, int &he, int &n, int &k, bool flag) {
     k = a.keep[b];
+    const int t0 = a.seq_len[b], h0 = a.hist_end[b];           // all three on their way at once
     if (k == -1) return false;
-    read_lengths(a.seq_len, a.hist_end, b, a.sink, a.max_pages << a.page_shift, a.status, T, he);
+    if (t0 < 0 || h0 < 0 || h0 > t0 || t0 > (a.max_pages << a.page_shift) || (h0 < a.sink && t0 >= a.sink)) {
+        read_lengths(a.seq_len, a.hist_end, b, a.sink, a.max_pages << a.page_shift, a.status, T, he);
+    } else {
+        T = t0;
+        he = max(h0, min(a.sink, t0));
+    }
     n = he > a.sink ? he - a.sink : 0;
     if (k < 0 || k > n || k > a.kept_stride) {
         if (flag) flag_status(a.status, OSCAR_DEV_BAD_LENGTH);
@@ -60,26 +66,31 @@ __device__ __forceinline__ int ld_cluster(const int *p, int rank) {
     return v;
 }
 
+__device__ __forceinline__ void st_cluster(int *p, int rank, int v) {
+    uint32_t ra;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(saddr(p)), "r"(rank));
+    asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(ra), "r"(v) : "memory");
+}
+
 // One cluster of C CTAs (grid x = C·Hkv) per (request, kv head); CTA r takes the slice [r n / C, (r + 1) n / C)
 // of the history and holds its keys in shared memory (kCached of them; the rest is read again each pass).
 // A pass: each CTA counts its slice's digits, sums its share of the bins over the cluster (all C remote
-// reads in flight), and every CTA looks the digit up: share totals first, then that share's bins.
+// reads in flight), sends the sums to every CTA, and each finds the digit among all the bins by itself.
 template <int C>
 __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a) {
     extern __shared__ uint32_t keys[];
-    constexpr int kPer = kBins / C;                    // bins of one CTA's share
-    constexpr int kOwn = (kPer + kThreads - 1) / kThreads;
+    constexpr int kOwn = kBins / kThreads;             // bins of one thread in the search
     // four counters a bin (lane & 3): weights gather in few bins, and equal bins of a warp are added in turn
     __shared__ int4 hist[kBins];
-    __shared__ int tot[kPer];                          // the cluster's counts of this CTA's share of the bins
+    __shared__ int tot[C > 1 ? kBins : 1];             // the cluster's counts
     __shared__ int cnt_gt[kWarps], cnt_eq[kWarps], red[kWarps];
-    __shared__ int share, found[2], slice_gt, slice_eq;
+    __shared__ int found[2], slice_gt, slice_eq;
     const int rank = blockIdx.x % C, h = blockIdx.x / C, b = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     auto cluster_or_cta_sync = [] {
         if (C > 1) cluster_sync_all();
         else __syncthreads();
     };
-    auto remote = [](const int *p, int r) { return C > 1 ? ld_cluster(p, r) : *p; };
+    pdl_trigger();                                     // the move may be set up meanwhile; it waits for this grid
     int T, he, n, k;
     if (!read_request(a, b, T, he, n, k, threadIdx.x == 0 && blockIdx.x == 0) || k == 0) return;     // the whole cluster alike
     const int lo = (int)((long long)rank * n / C), hi = (int)((long long)(rank + 1) * n / C);
@@ -110,50 +121,23 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a) {
         }
         cluster_or_cta_sync();
         if (C > 1) {
-            int sum = 0;
-#pragma unroll
-            for (int j = 0; j < kOwn; ++j) {
-                const int i = threadIdx.x + j * kThreads;
-                if (i >= per) break;
+            for (int i = threadIdx.x; i < per; i += kThreads) {
                 int v[C], t = 0;
 #pragma unroll
-                for (int r = 0; r < C; ++r) v[r] = remote(&hist[rank * per + i].x, r);
+                for (int r = 0; r < C; ++r) v[r] = ld_cluster(&hist[rank * per + i].x, r);
 #pragma unroll
                 for (int r = 0; r < C; ++r) t += v[r];
-                tot[i] = t;
-                sum += t;
-            }
-            sum = __reduce_add_sync(0xffffffffu, sum);
-            if (lane == 0) red[warp] = sum;
-            __syncthreads();
-            if (warp == 0) {
-                const int t = __reduce_add_sync(0xffffffffu, lane < kWarps ? red[lane] : 0);
-                if (lane == 0) share = t;
+#pragma unroll
+                for (int r = 0; r < C; ++r) st_cluster(&tot[rank * per + i], r, t);
             }
             cluster_sync_all();
         }
-        // the share, from the top, in which the count reaches `left`
-        int r = 0;
-        if (C > 1) {
-            int v[C];
-#pragma unroll
-            for (int j = 0; j < C; ++j) v[j] = remote(&share, j);
-            bool looking = true;
-#pragma unroll
-            for (int j = C - 1; j >= 0; --j) {
-                if (looking && left <= v[j]) {
-                    r = j;
-                    looking = false;
-                }
-                left -= looking ? v[j] : 0;
-            }
-        }
-        // its bins from the top, kOwn a thread: thread t has bins [per - kOwn (t + 1), per - kOwn t)
+        // the digit: bins from the top, kOwn a thread
         int c[kOwn], sum = 0;
 #pragma unroll
         for (int j = 0; j < kOwn; ++j) {
-            const int i = per - 1 - (int)(threadIdx.x * kOwn + j);
-            c[j] = i < 0 ? 0 : C > 1 ? remote(&tot[i], r) : hist[i].x;
+            const int i = nb - 1 - (int)(threadIdx.x * kOwn + j);
+            c[j] = i < 0 ? 0 : C > 1 ? tot[i] : hist[i].x;
             sum += c[j];
         }
         int upto = sum;
@@ -164,13 +148,13 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a) {
         }
         if (lane == 31) red[warp] = upto;
         __syncthreads();
-        int before = upto - sum;
-        for (int w = 0; w < warp; ++w) before += red[w];
+        const int before0 = __reduce_add_sync(0xffffffffu, lane < warp ? red[lane & (kWarps - 1)] : 0);
+        int before = upto - sum + before0;
         if (before < left && left <= before + sum) {
 #pragma unroll
             for (int j = 0; j < kOwn; ++j) {
                 if (before < left && left <= before + c[j]) {
-                    found[0] = r * per + per - 1 - (int)(threadIdx.x * kOwn + j);
+                    found[0] = nb - 1 - (int)(threadIdx.x * kOwn + j);
                     found[1] = left - before;
                     break;
                 }
@@ -196,14 +180,13 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a) {
         cnt_eq[warp] = eq;
     }
     __syncthreads();
-    if (threadIdx.x == 0) {
-        int x = 0, y = 0;
-        for (int w = 0; w < kWarps; ++w) {
-            x += cnt_gt[w];
-            y += cnt_eq[w];
+    if (warp == 0) {
+        const int x = __reduce_add_sync(0xffffffffu, lane < kWarps ? cnt_gt[lane & (kWarps - 1)] : 0);
+        const int y = __reduce_add_sync(0xffffffffu, lane < kWarps ? cnt_eq[lane & (kWarps - 1)] : 0);
+        if (lane == 0) {
+            slice_gt = x;
+            slice_eq = y;
         }
-        slice_gt = x;
-        slice_eq = y;
     }
     cluster_or_cta_sync();
     int gt0 = 0, eq0 = 0;
@@ -211,8 +194,8 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a) {
         int v[C], w[C];
 #pragma unroll
         for (int r = 0; r < C; ++r) {
-            v[r] = remote(&slice_gt, r);
-            w[r] = remote(&slice_eq, r);
+            v[r] = ld_cluster(&slice_gt, r);
+            w[r] = ld_cluster(&slice_eq, r);
         }
 #pragma unroll
         for (int r = 0; r < C; ++r) {
@@ -220,10 +203,8 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a) {
             eq0 += r < rank ? w[r] : 0;
         }
     }
-    for (int w = 0; w < warp; ++w) {
-        gt0 += cnt_gt[w];
-        eq0 += cnt_eq[w];
-    }
+    gt0 += __reduce_add_sync(0xffffffffu, lane < warp ? cnt_gt[lane & (kWarps - 1)] : 0);
+    eq0 += __reduce_add_sync(0xffffffffu, lane < warp ? cnt_eq[lane & (kWarps - 1)] : 0);
     int32_t *out = a.kept + ((size_t)b * a.n_kv + h) * a.kept_stride;
     const uint32_t below = (1u << lane) - 1;
     for (int i = w0; i < w1; i += 32) {
@@ -239,57 +220,36 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a) {
     if (C > 1) cluster_sync_all();                     // no CTA leaves while another reads its memory
 }
 
-// grid (X, Hkv, batch).  A row is 8 lanes: 4 with the key's 64 bytes, 4 with the value's; a thread has
-// kMoveRows rows in flight (list entry, page table, data: three dependent loads each).
-constexpr int kMoveRows = 4;
-
+// grid (X, Hkv, batch).  A row is 8 lanes: 4 with the key's 64 bytes, 4 with the value's.  List entry, page
+// ids and data depend on each other, and what hides that is many warps with few registers each: one row a
+// thread at a time and sixteen CTAs an SM (2 x 100K to half, read back: 149 us; four rows a thread, eight
+// CTAs: 153; the next rows' entries and pages loaded ahead, four CTAs: 191).
 __global__ void __launch_bounds__(256) evict_move_kernel(EvictArgs a) {
     const int h = blockIdx.y, b = blockIdx.z, hl = threadIdx.x & 7;
     int T, he, n, k;
-    if (!read_request(a, b, T, he, n, k, false)) return;
+    const bool on = read_request(a, b, T, he, n, k, false);
+    pdl_wait();                                        // the selection is complete; every CTA waits, for what follows too
+    if (!on) return;
     const size_t row0 = ((size_t)b * a.n_kv + h) * a.max_pages << a.page_shift;
     const int32_t *kept = a.kept + ((size_t)b * a.n_kv + h) * a.kept_stride;
     const int32_t *spt = a.spt + (size_t)b * a.max_pages, *dpt = a.dpt + (size_t)b * a.max_pages;
     const int G = kHeadDim / a.group, step = gridDim.x * 32, in_page = (1 << a.page_shift) - 1;
     const uint8_t *sc = hl < 4 ? a.src.codes_k : a.src.codes_v;
     uint8_t *dc = hl < 4 ? a.dst.codes_k : a.dst.codes_v;
-    for (long long j0 = blockIdx.x * 32 + (threadIdx.x >> 3); j0 < k; j0 += (long long)kMoveRows * step) {
-        int p[kMoveRows], sp[kMoveRows], dp[kMoveRows];
-        uint4 x[kMoveRows];
-        uint2 z[kMoveRows];
-        float w[kMoveRows];
-#pragma unroll
-        for (int u = 0; u < kMoveRows; ++u) p[u] = j0 + (long long)u * step < k ? kept[j0 + (long long)u * step] : -1;
-#pragma unroll
-        for (int u = 0; u < kMoveRows; ++u) {
-            if (p[u] < 0) continue;
-            const int to = a.sink + (int)(j0 + (long long)u * step);
-            sp[u] = spt[p[u] >> a.page_shift];
-            dp[u] = dpt[to >> a.page_shift];
-            w[u] = hl == 0 ? a.mass[row0 + p[u]] : 0.f;
+    for (long long j = blockIdx.x * 32 + (threadIdx.x >> 3); j < k; j += step) {
+        const int p = kept[j], to = a.sink + (int)j;
+        const int sp = spt[p >> a.page_shift], dp = dpt[to >> a.page_shift];
+        if (hl == 0) a.mass_out[row0 + to] = a.mass[row0 + p];
+        if ((uint32_t)sp >= (uint32_t)a.src.n_pages || (uint32_t)dp >= (uint32_t)a.dst.n_pages) {
+            if (hl == 0) flag_status(a.status, OSCAR_DEV_BAD_INT4_PAGE);
+            continue;
         }
-#pragma unroll
-        for (int u = 0; u < kMoveRows; ++u) {
-            if (p[u] < 0) continue;
-            if ((uint32_t)sp[u] >= (uint32_t)a.src.n_pages || (uint32_t)dp[u] >= (uint32_t)a.dst.n_pages) {
-                if (hl == 0) flag_status(a.status, OSCAR_DEV_BAD_INT4_PAGE);
-                dp[u] = -1;
-                continue;
-            }
-            const size_t from = row4(sp[u], a.n_kv, h, a.page_shift, p[u] & in_page);
-            x[u] = reinterpret_cast<const uint4 *>(sc + from * kRow4)[hl & 3];
-            if (hl < G) z[u] = reinterpret_cast<const uint2 *>(a.src.scale_zero)[from * G + hl];
-        }
-#pragma unroll
-        for (int u = 0; u < kMoveRows; ++u) {
-            if (p[u] < 0) continue;
-            const int to = a.sink + (int)(j0 + (long long)u * step);
-            if (hl == 0) a.mass_out[row0 + to] = w[u];
-            if (dp[u] < 0) continue;
-            const size_t at = row4(dp[u], a.n_kv, h, a.page_shift, to & in_page);
-            reinterpret_cast<uint4 *>(dc + at * kRow4)[hl & 3] = x[u];
-            if (hl < G) reinterpret_cast<uint2 *>(a.dst.scale_zero)[at * G + hl] = z[u];
-        }
+        const size_t from = row4(sp, a.n_kv, h, a.page_shift, p & in_page), at = row4(dp, a.n_kv, h, a.page_shift, to & in_page);
+        const uint4 x = reinterpret_cast<const uint4 *>(sc + from * kRow4)[hl & 3];
+        uint2 z = make_uint2(0, 0);
+        if (hl < G) z = reinterpret_cast<const uint2 *>(a.src.scale_zero)[from * G + hl];
+        reinterpret_cast<uint4 *>(dc + at * kRow4)[hl & 3] = x;
+        if (hl < G) reinterpret_cast<uint2 *>(a.dst.scale_zero)[at * G + hl] = z;
     }
     // the weights outside the kept rows: sink, recent rows, nothing behind them
     const int N = a.max_pages << a.page_shift, shift = n - k, lo = min(a.sink, T);
@@ -329,10 +289,18 @@ cudaError_t launch_evict(const oscar_layout_t &L, Int4PoolView src, const int32_
         cfg.numAttrs = 1;
     }
     if (cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a)) return e;
-    const long long most = (tokens + 255) / 256;
-    const long long want = (8 * 152 + batch * L.n_kv_heads - 1) / (batch * L.n_kv_heads);
-    evict_move_kernel<<<dim3((unsigned)(want < most ? want : most), L.n_kv_heads, batch), 256, 0, st>>>(a);
-    return cudaGetLastError();
+    // CTAs: about sixteen an SM, no more than there are runs of 32 rows
+    const long long most = (tokens + 31) / 32, pairs = (long long)batch * L.n_kv_heads, want = (16 * 152 + pairs - 1) / pairs;
+    cudaLaunchConfig_t mv = {};
+    cudaLaunchAttribute overlap[1];
+    mv.gridDim = dim3((unsigned)(want < most ? want : most), L.n_kv_heads, batch);
+    mv.blockDim = dim3(256);
+    mv.stream = st;
+    overlap[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;      // set up while the selection runs
+    overlap[0].val.programmaticStreamSerializationAllowed = 1;
+    mv.attrs = overlap;
+    mv.numAttrs = 1;
+    return cudaLaunchKernelEx(&mv, evict_move_kernel, a);
 }
 
 }  // namespace oscar
