@@ -15,6 +15,7 @@
 #include <algorithm>
 
 #include "int4.cuh"
+#include "ptx.cuh"
 
 namespace oscar {
 namespace {
@@ -75,6 +76,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) append_kernel(AppendArgs a) {
     const int lane = threadIdx.x & 31, half = lane >> 4, hl = lane & 15;
     const uint32_t w = blockIdx.x * kWarps + (threadIdx.x >> 5);       // below 2^32: n * runs is (launch_append)
     const int i = (int)(w / (uint32_t)a.runs);
+    pdl_wait();
     if (i >= a.n) return;
     const int rows = a.n_q + 2 * a.n_kv, pair0 = (int)(w - (uint32_t)i * a.runs) * a.per;
     const int pairs = min(a.per, (rows + 1) / 2 - pair0);
@@ -206,9 +208,7 @@ cudaError_t launch_append(const oscar_layout_t &L, const AppendInput &in, int n,
     const AppendArgs a{in.q, in.k, in.v, in.q_stride, in.k_stride, in.v_stride, n, n_q, L.n_kv_heads, per, runs, wq, wk, eps,
                        rope, rope_rows, rot, pool, pt, max_pages, page_shift(L), batch, req, pos, rope_pos, q_out, status};
     const unsigned blocks = (unsigned)(((long long)n * runs + kWarps - 1) / kWarps);
-    if (pairs_interleaved) append_kernel<true><<<blocks, kWarps * 32, 0, st>>>(a);
-    else append_kernel<false><<<blocks, kWarps * 32, 0, st>>>(a);
-    return cudaGetLastError();
+    return launch_ahead(pairs_interleaved ? append_kernel<true> : append_kernel<false>, dim3(blocks), kWarps * 32, 0, st, a);
 }
 
 }  // namespace oscar

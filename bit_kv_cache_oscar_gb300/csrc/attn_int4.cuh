@@ -656,6 +656,7 @@ __global__ void __launch_bounds__(W * 32, 16 / W)
         for (int i = 0; i <= R::n; ++i) mbar_init(saddr(&bars[warp * (R::n + 1) + i]), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     __syncwarp();
+    pdl_wait();
     int T, he;
     read_lengths(a.seq_len, a.hist_end, b, a.sink, a.max_pages << a.page_shift, a.status, T, he);
     float *res = reinterpret_cast<float *>(smem);
@@ -724,8 +725,7 @@ cudaError_t launch_one(Attn4Args a, const CUtensorMap &tmk, const CUtensorMap &t
     smem += 1024;
     auto kern = attn4_kernel<G, NG, MASS, W>;
     if (cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void *>(kern), smem)) return e;
-    kern<<<dim3(a.out.S, a.n_kv, batch), W * 32, smem, st>>>(a, tmk, tmv);
-    return cudaGetLastError();
+    return launch_ahead(kern, dim3(a.out.S, a.n_kv, batch), W * 32, smem, st, a, tmk, tmv);
 }
 
 template <int G, bool MASS, int W>

@@ -90,6 +90,7 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a) {
         if (C > 1) cluster_sync_all();
         else __syncthreads();
     };
+    pdl_wait();
     pdl_trigger();                                     // the move may be set up meanwhile; it waits for this grid
     int T, he, n, k;
     if (!read_request(a, b, T, he, n, k, threadIdx.x == 0 && blockIdx.x == 0) || k == 0) return;     // the whole cluster alike
@@ -227,9 +228,8 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a) {
 __global__ void __launch_bounds__(256) evict_move_kernel(EvictArgs a) {
     const int h = blockIdx.y, b = blockIdx.z, hl = threadIdx.x & 7;
     int T, he, n, k;
-    const bool on = read_request(a, b, T, he, n, k, false);
-    pdl_wait();                                        // the selection is complete; every CTA waits, for what follows too
-    if (!on) return;
+    pdl_wait();                                        // the selection is complete
+    if (!read_request(a, b, T, he, n, k, false)) return;
     const size_t row0 = ((size_t)b * a.n_kv + h) * a.max_pages << a.page_shift;
     const int32_t *kept = a.kept + ((size_t)b * a.n_kv + h) * a.kept_stride;
     const int32_t *spt = a.spt + (size_t)b * a.max_pages, *dpt = a.dpt + (size_t)b * a.max_pages;
@@ -276,31 +276,22 @@ cudaError_t launch_evict(const oscar_layout_t &L, Int4PoolView src, const int32_
     auto kern = C > 1 ? evict_select_kernel<kCluster> : evict_select_kernel<1>;
     if (cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void *>(kern), smem)) return e;
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     cfg.gridDim = dim3(C * L.n_kv_heads, batch);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    if (C > 1) {
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = C;
-        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-    }
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = C;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = C > 1 ? 2 : 1;
     if (cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a)) return e;
     // CTAs: about sixteen an SM, no more than there are runs of 32 rows
     const long long most = (tokens + 31) / 32, pairs = (long long)batch * L.n_kv_heads, want = (16 * 152 + pairs - 1) / pairs;
-    cudaLaunchConfig_t mv = {};
-    cudaLaunchAttribute overlap[1];
-    mv.gridDim = dim3((unsigned)(want < most ? want : most), L.n_kv_heads, batch);
-    mv.blockDim = dim3(256);
-    mv.stream = st;
-    overlap[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;      // set up while the selection runs
-    overlap[0].val.programmaticStreamSerializationAllowed = 1;
-    mv.attrs = overlap;
-    mv.numAttrs = 1;
-    return cudaLaunchKernelEx(&mv, evict_move_kernel, a);
+    return launch_ahead(evict_move_kernel, dim3((unsigned)(want < most ? want : most), L.n_kv_heads, batch), 256, 0, st, a);
 }
 
 }  // namespace oscar

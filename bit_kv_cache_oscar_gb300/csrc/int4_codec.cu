@@ -14,6 +14,7 @@
 #include <cuda_bf16.h>
 
 #include "int4.cuh"
+#include "ptx.cuh"
 
 namespace oscar {
 namespace {
@@ -165,6 +166,7 @@ template <int GROUP, bool DEMOTE>
 __global__ void __launch_bounds__(kThreads) codec4_kernel(RangeArgs a) {
     const int h = blockIdx.y, b = blockIdx.z, hl = threadIdx.x & 7, row = threadIdx.x >> 4;
     const bool value = threadIdx.x & 8;
+    pdl_wait();
     const int lo = a.begin[b], hi = a.end[b];
     if (lo < 0 || hi < lo || (long long)hi > ((long long)a.max_pages << a.page_shift)) {
         if (threadIdx.x == 0 && blockIdx.x == 0) flag_status(a.status, OSCAR_DEV_BAD_LENGTH);
@@ -243,11 +245,10 @@ cudaError_t launch(const oscar_layout_t &L, const RangeArgs &a, int batch, cudaS
     const long long want = (8 * 152 + pairs - 1) / pairs;
     const dim3 grid((unsigned)(want < most ? want : most), L.n_kv_heads, batch);
     switch (L.group) {
-        case 32: codec4_kernel<32, DEMOTE><<<grid, kThreads, 0, st>>>(a); break;
-        case 64: codec4_kernel<64, DEMOTE><<<grid, kThreads, 0, st>>>(a); break;
-        default: codec4_kernel<128, DEMOTE><<<grid, kThreads, 0, st>>>(a);
+        case 32: return launch_ahead(codec4_kernel<32, DEMOTE>, grid, kThreads, 0, st, a);
+        case 64: return launch_ahead(codec4_kernel<64, DEMOTE>, grid, kThreads, 0, st, a);
+        default: return launch_ahead(codec4_kernel<128, DEMOTE>, grid, kThreads, 0, st, a);
     }
-    return cudaGetLastError();
 }
 
 }  // namespace

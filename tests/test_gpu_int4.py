@@ -529,6 +529,105 @@ def test_evict_flags_and_shared_pages():
     assert np.array_equal(kept[0, 1, :280], np.arange(64, 344))
 
 
+def test_evict_within_one_pool_and_a_kept_view():
+    """Source and destination pages of the same pool, apart; kept a larger array than any keep."""
+    c = ic.Cache([900], n_kv=2, gqa=1, page=16, seed=3, extra_pages=0)
+    n = c.ck.shape[0]
+    grow = lambda a: np.concatenate([a, np.zeros((40,) + a.shape[1:], a.dtype)])
+    c.ck, c.cv, c.sz = grow(c.ck), grow(c.cv), grow(c.sz)
+    c.upload()
+    L, mass = c.L, weights(c.rng, (1, 2, c.max_pages * 16), "plain")
+    tn = np.full_like(c.t4, -1)
+    tn[0, 4:4 + 20] = n + c.rng.permutation(40)[:20]
+    dm = torch.from_numpy(mass).cuda()
+    out, kept = torch.empty_like(dm), torch.full((1, 2, 500), -7, dtype=torch.int32, device="cuda")
+    before = c.int4.codes_k[:n].clone()
+    ob.oscar_evict_int4(L, c.int4, c.d4, c.int4, i32(tn), c.dT, c.dh, i32([313]), dm, out, kept)
+    assert torch.equal(before, c.int4.codes_k[:n])
+    for h in range(2):
+        want = evict_reference(mass[0, h], 64, 644, 313)
+        assert np.array_equal(kept[0, h, :313].cpu().numpy(), want) and torch.all(kept[0, h, 313:] == -7)
+        to = 64 + np.arange(313)
+        assert np.array_equal(c.int4.codes_v.cpu().numpy()[tn[0, to // 16], h, to % 16], c.cv[c.t4[0, want // 16], h, want % 16])
+    assert ob.oscar_get_device_status() == 0
+
+
+# ------------------------------------------------------------ order of work --
+def test_calls_follow_the_kernels_copies_and_fills_before_them():
+    """Each call is launched ahead of its predecessor's end: it still sees what that one wrote, in a stream and in a graph,
+    after kernels, copies and fills, and what follows sees what it wrote."""
+    c = ic.Cache([900, 340], n_kv=2, gqa=4, page=16, seed=12, rubbish=False).upload()
+    L, B = c.L, c.B
+    want, want_lse, _ = decode(c, 3)
+    N = c.max_pages * 16
+    src = [t.clone() for t in (c.int4.codes_k, c.int4.codes_v, c.int4.scale_zero, c.dq)]
+    dst = (c.int4.codes_k, c.int4.codes_v, c.int4.scale_zero, c.dq)
+    part, counters = ob.Partials.empty(L, B, 3), torch.zeros(B * 2, dtype=torch.int32, device="cuda")
+    out, lse, mass, copy = torch.empty_like(want), torch.empty_like(want_lse), torch.zeros((B, 2, N), device="cuda"), torch.empty_like(want)
+    big = torch.empty(1 << 26, device="cuda")
+
+    def step():
+        for t in dst:                                   # fills, then late copies of the real inputs
+            t.zero_()
+        big.normal_()
+        for t, s in zip(dst, src):
+            t.copy_(s)
+        mass.zero_()
+        ob.oscar_decode_attention_int4(*c.attention_args(), part, None, out, lse, counters)
+        ob.oscar_attention_mass_int4(*c.attention_args(), lse, mass)
+        copy.copy_(out)
+
+    ref_mass = torch.zeros_like(mass)
+    ob.oscar_attention_mass_int4(*c.attention_args(), want_lse, ref_mass)
+    for _ in range(5):
+        step()
+        torch.cuda.synchronize()
+        assert torch.equal(copy, want) and torch.equal(lse, want_lse) and torch.equal(mass, ref_mass)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for _ in range(3):
+        copy.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(copy, want) and torch.equal(lse, want_lse) and torch.equal(mass, ref_mass)
+
+
+def test_a_chain_of_calls_many_times_over():
+    """append -> demote -> promote -> append ... back to back on the same pages: every call reads the one before."""
+    L = ob.Layout(2, 4, 16)
+    a, b, q4 = ob.Bf16Pool.empty(L, 4), ob.Bf16Pool.empty(L, 4), ob.Int4Pool.empty(L, 4)
+    t, lo, hi, req, pos = i32([[2, 0, 3, 1]]), i32([0]), i32([64]), i32([0] * 64), i32(np.arange(64))
+    x = torch.randn((64, 4, D), device="cuda").to(torch.bfloat16)
+    ob.oscar_append_kv(L, None, x[:, :2], x[:, 2:], a, t, req, pos)
+    ob.oscar_demote_int4(L, a, t, q4, t, lo, hi)
+    ob.oscar_promote_int4(L, q4, t, b, t, lo, hi)
+    torch.cuda.synchronize()
+    want = b.k.clone(), b.v.clone(), q4.codes_k.clone()
+    for _ in range(300):
+        a.k.zero_(), q4.codes_k.zero_(), b.k.zero_()
+        ob.oscar_append_kv(L, None, x[:, :2], x[:, 2:], a, t, req, pos)
+        ob.oscar_demote_int4(L, a, t, q4, t, lo, hi)
+        ob.oscar_promote_int4(L, q4, t, b, t, lo, hi)
+        assert bool((b.k == want[0]).all() & (b.v == want[1]).all() & (q4.codes_k == want[2]).all())
+
+
+def test_two_calls_at_once_on_two_streams():
+    cs = [ic.Cache([2000, 700], n_kv=2, gqa=4, page=16, seed=s).upload() for s in (1, 2)]
+    want = [decode(c, 5) for c in cs]
+    streams = [torch.cuda.Stream() for _ in cs]
+    torch.cuda.synchronize()
+    work = [(ob.Partials.empty(c.L, c.B, 5), torch.zeros(4, dtype=torch.int32, device="cuda"), torch.empty_like(w[0]), torch.empty_like(w[1]))
+            for c, w in zip(cs, want)]
+    torch.cuda.synchronize()
+    for _ in range(50):
+        for c, s, (p, n, o, l) in zip(cs, streams, work):
+            ob.oscar_decode_attention_int4(*c.attention_args(), p, None, o, l, n, s)
+    torch.cuda.synchronize()
+    for (p, n, o, l), w in zip(work, want):
+        assert torch.equal(o, w[0]) and torch.equal(l, w[1]) and not n.any()
+
+
 # ----------------------------------------------------------------- binding --
 def test_the_binding_refuses_types_shapes_strides_and_places():
     c = ic.Cache([400], seed=1).upload()
