@@ -78,11 +78,11 @@ cudaError_t launch_decode4(const oscar_layout_t &L, const Attn4Input &in, int ba
 cudaError_t launch_mass4(const oscar_layout_t &L, const Attn4Input &in, int batch, const float *lse, float *mass,
                          int32_t *status, cudaStream_t st) {
     Attn4Args a{};
-    // no merge to pay for: about three waves of CTAs even where one would hold the splits (a ragged batch of
-    // 8: 100, 86, 84 and 90 us with 4, 9, 14 and 28)
-    const long long per = (long long)batch * L.n_kv_heads;
-    const int S = suggest_splits4(L, batch, in.max_pages * L.page_size, kSms), waves = (int)std::min(1024LL, 6LL * kSms / per);
-    a.out.S = per > kSms / 4 && S < waves ? (int)std::min<long long>(waves, (in.max_pages * (long long)L.page_size + 255) / 256) : S;
+    // no merge to pay for: about two waves of CTAs of 4 warps even where one would hold the splits (a ragged
+    // batch of 8: 135, 89, 80 and 80 us with 4, 9, 19 and 28; of 8 warps: 100, 86, 85 and 90)
+    const long long per = (long long)batch * L.n_kv_heads, tokens = in.max_pages * (long long)L.page_size;
+    const int S = suggest_splits4(L, batch, (int)tokens, kSms);
+    a.out.S = per > kSms / 4 ? (int)std::max<long long>(1, std::min({1024LL, 8LL * kSms / per, (tokens + 255) / 256})) : S;
     a.lse = lse;
     a.mass = mass;
     a.status = status;

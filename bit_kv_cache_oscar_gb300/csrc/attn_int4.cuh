@@ -20,8 +20,8 @@
 // The BF16 rows are dealt out in tiles of 16 to the same warps, which work on them while their first
 // blocks are on the way.  With counters, the last CTA of a (request, kv head) to finish merges all its
 // slots, in slot order.
-// W is 16 (one CTA an SM) when the launch has a CTA for each SM at most, else 8 (two an SM, so that one's
-// start and end hide behind the other's stream).
+// W is 16 (one CTA an SM) when the launch has a CTA for each SM at most, else 8, or 4 for the weights, whose
+// CTAs have no results to join: several CTAs an SM, so that one's start and end hide behind another's stream.
 // Every wait is bounded: one that gives up sets OSCAR_DEV_WAIT_TIMEOUT.
 
 #pragma once
@@ -743,7 +743,7 @@ template <int G>
 cudaError_t launch_attn4(const Attn4Args &a, int group, bool mass, const CUtensorMap &tmk, const CUtensorMap &tmv, int batch,
                          cudaStream_t st) {
     const bool wide = (long long)a.out.S * a.n_kv * batch <= kSms;       // a CTA for each SM at most: 16 warps each
-    if (mass) return wide ? launch_group<G, true, 16>(a, group, tmk, tmv, batch, st) : launch_group<G, true, 8>(a, group, tmk, tmv, batch, st);
+    if (mass) return wide ? launch_group<G, true, 16>(a, group, tmk, tmv, batch, st) : launch_group<G, true, 4>(a, group, tmk, tmv, batch, st);
     return wide ? launch_group<G, false, 16>(a, group, tmk, tmv, batch, st) : launch_group<G, false, 8>(a, group, tmk, tmv, batch, st);
 }
 

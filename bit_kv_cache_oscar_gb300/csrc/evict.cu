@@ -110,10 +110,12 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a) {
         const uint32_t mask = pass == 0 ? 0u : pass == 1 ? 0xFFE00000u : 0xFFFFF800u;
         for (int i = threadIdx.x; i < nb; i += kThreads) hist[i] = make_int4(0, 0, 0, 0);
         __syncthreads();
-        for (int i = threadIdx.x; i < len; i += kThreads) {
-            const uint32_t key = key_at(i);
+        auto count = [&](uint32_t key) {
             if ((key & mask) == prefix) atomicAdd(&counters[4 * ((key >> shift) & (nb - 1)) + (lane & 3)], 1);
-        }
+        };
+#pragma unroll 4
+        for (int i = threadIdx.x; i < cached; i += kThreads) count(keys[i]);
+        for (int i = cached + threadIdx.x; i < len; i += kThreads) count(order_key(m[i]));
         __syncthreads();
         const int per = nb / C;
         for (int i = threadIdx.x; i < nb; i += kThreads) {
@@ -170,6 +172,7 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a) {
     // places: warp w takes [w len / W, (w + 1) len / W) of the slice; counts first, then positions in order
     const int w0 = (int)((long long)warp * len / kWarps), w1 = (int)((long long)(warp + 1) * len / kWarps);
     int gt = 0, eq = 0;
+#pragma unroll 4
     for (int i = w0; i < w1; i += 32) {
         const bool in = i + lane < w1;
         const uint32_t key = in ? key_at(i + lane) : 0u;
@@ -208,6 +211,7 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a) {
     eq0 += __reduce_add_sync(0xffffffffu, lane < warp ? cnt_eq[lane & (kWarps - 1)] : 0);
     int32_t *out = a.kept + ((size_t)b * a.n_kv + h) * a.kept_stride;
     const uint32_t below = (1u << lane) - 1;
+#pragma unroll 4
     for (int i = w0; i < w1; i += 32) {
         const bool in = i + lane < w1;
         const uint32_t key = in ? key_at(i + lane) : 0u;
