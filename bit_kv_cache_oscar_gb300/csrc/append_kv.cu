@@ -72,7 +72,7 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 constexpr int kAhead = 4;
 
 template <bool PAIRS>
-__global__ void __launch_bounds__(kWarps * 32, 3) append_kernel(AppendArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, 2) append_kernel(AppendArgs a) {
     const int lane = threadIdx.x & 31, half = lane >> 4, hl = lane & 15;
     const uint32_t w = blockIdx.x * kWarps + (threadIdx.x >> 5);       // below 2^32: n * runs is (launch_append)
     const int i = (int)(w / (uint32_t)a.runs);
@@ -141,54 +141,76 @@ __global__ void __launch_bounds__(kWarps * 32, 3) append_kernel(AppendArgs a) {
     uint16_t *ko = const_cast<uint16_t *>(a.pool.k) + (slot - a.n_q) * kHeadDim + 8 * hl;
     uint16_t *vo = const_cast<uint16_t *>(a.pool.v) + (slot - a.n_q - a.n_kv) * kHeadDim + 8 * hl;
 
+    // Two row pairs at a time: their reductions, roots and shuffles overlap.
     const uint16_t *held = nullptr;                               // the norm weights now in wv
     uint64_t wv[4];
     for (int j0 = 0; j0 < pairs; j0 += kAhead) {
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            const int r = 2 * (pair0 + j0 + u) + half;
-            const uint4 raw = x[u];
+        for (int u = 0; u < kAhead; u += 2) {
+            const int r0 = 2 * (pair0 + j0 + u) + half;
+            const uint4 raw[2] = {x[u], x[u + 1]};
             x[u] = load(j0 + u + kAhead);
+            x[u + 1] = load(j0 + u + 1 + kAhead);
             if (j0 + u >= pairs) continue;                        // the whole warp
-            if (r - half >= a.n_q + a.n_kv) {                     // both rows are values: moved as they are
-                if (page_ok && r < rows) *reinterpret_cast<uint4 *>(vo + (long long)r * kHeadDim) = raw;
+            const int in_warp = min(rows, 2 * (pair0 + pairs));   // rows from here on are another warp's, or none
+            if (r0 - half >= a.n_q + a.n_kv) {                    // values: moved as they are
+#pragma unroll
+                for (int v2 = 0; v2 < 2; ++v2)
+                    if (page_ok && r0 + 2 * v2 < in_warp) *reinterpret_cast<uint4 *>(vo + (long long)(r0 + 2 * v2) * kHeadDim) = raw[v2];
                 continue;
             }
-            const bool is_q = r < a.n_q, is_v = r >= a.n_q + a.n_kv;
-            uint64_t y[4];
-            widen8(raw, y);
-            const uint16_t *wt = is_q ? a.wq : a.wk;
-            if (wt != held) {
-                held = wt;
-                if (wt) widen8(__ldg(reinterpret_cast<const uint4 *>(wt) + hl), wv);
+            uint64_t y[2][4];
+            float ss[2];
+#pragma unroll
+            for (int v2 = 0; v2 < 2; ++v2) {
+                widen8(raw[v2], y[v2]);
+                uint64_t sq = mul2(y[v2][0], y[v2][0]);
+#pragma unroll
+                for (int e = 1; e < 4; ++e) sq = fma2(y[v2][e], y[v2][e], sq);
+                float s0, s1;
+                unpair(sq, s0, s1);
+                ss[v2] = s0 + s1;
             }
-            uint64_t sq = mul2(y[0], y[0]);
 #pragma unroll
-            for (int e = 1; e < 4; ++e) sq = fma2(y[e], y[e], sq);
-            float ss, s1;
-            unpair(sq, ss, s1);
-            ss += s1;
-#pragma unroll
-            for (int o = 8; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            if (wt) {
-                const float inv = rsqrtf(fmaf(ss, 1.f / kHeadDim, a.eps));
-                const uint64_t inv2 = pair(inv, inv);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) y[e] = mul2(mul2(y[e], inv2), wv[e]);
+            for (int o = 8; o; o >>= 1) {
+                const float t0 = __shfl_xor_sync(0xffffffffu, ss[0], o), t1 = __shfl_xor_sync(0xffffffffu, ss[1], o);
+                ss[0] += t0;
+                ss[1] += t1;
             }
-            uint32_t o[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float p, q2;
-                unpair(y[e], p, q2);
-                const uint64_t z = PAIRS ? pair(q2, p)
-                                         : pair(__shfl_sync(0xffffffffu, p, partner), __shfl_sync(0xffffffffu, q2, partner));
-                unpair(fma2(y[e], cs[e], mul2(z, sn[e])), p, q2);
-                o[e] = pack2(p, q2);
+            for (int v2 = 0; v2 < 2; ++v2) {
+                const uint16_t *wt = r0 + 2 * v2 < a.n_q ? a.wq : a.wk;
+                if (wt != held) {
+                    held = wt;
+                    if (wt) widen8(__ldg(reinterpret_cast<const uint4 *>(wt) + hl), wv);
+                }
+                if (wt) {
+                    const float inv = rsqrtf(fmaf(ss[v2], 1.f / kHeadDim, a.eps));
+                    const uint64_t inv2 = pair(inv, inv);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) y[v2][e] = mul2(mul2(y[v2][e], inv2), wv[e]);
+                }
             }
-            if (r >= rows || (!is_q && !page_ok)) continue;       // a half-warp; nothing below is shared
-            *reinterpret_cast<uint4 *>((is_q ? qo : is_v ? vo : ko) + (long long)r * kHeadDim) =
-                is_v ? raw : make_uint4(o[0], o[1], o[2], o[3]);
+            uint32_t o[2][4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int v2 = 0; v2 < 2; ++v2) {
+                    float p, q2;
+                    unpair(y[v2][e], p, q2);
+                    const uint64_t z = PAIRS ? pair(q2, p)
+                                             : pair(__shfl_sync(0xffffffffu, p, partner), __shfl_sync(0xffffffffu, q2, partner));
+                    unpair(fma2(y[v2][e], cs[e], mul2(z, sn[e])), p, q2);
+                    o[v2][e] = pack2(p, q2);
+                }
+#pragma unroll
+            for (int v2 = 0; v2 < 2; ++v2) {
+                const int r = r0 + 2 * v2;
+                const bool is_q = r < a.n_q, is_v = r >= a.n_q + a.n_kv;
+                if (r < in_warp && (is_q || page_ok))
+                    *reinterpret_cast<uint4 *>((is_q ? qo : is_v ? vo : ko) + (long long)r * kHeadDim) =
+                        is_v ? raw[v2] : make_uint4(o[v2][0], o[v2][1], o[v2][2], o[v2][3]);
+            }
         }
     }
 }

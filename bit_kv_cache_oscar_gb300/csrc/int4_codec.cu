@@ -60,17 +60,17 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 // (the saturating product is the clamp, and 0 for NaN) is the code or one below it whatever the error, and
 // d - k·scale, which is exact, against scale/2 tells which: above it k + 1, below it k, on it the even one
 // (its last bit is set where k is odd, which only then lifts it above scale/2).  d = x - zero is exact in
-// fp32 unless one of the two is below 2^-15 of the other: a lane that may hold such a value (one in some
-// hundred) adds the error of d, by a two-sum, to the comparison.
+// fp32 unless one of the two is below 2^-15 of the other.  A zero that small shows in the group's range.  A
+// value x that small lies within 2^-10 codes of -zero/scale, so it matters only where that is that near a
+// border, which one group in 200 is.  Such groups add the error of d, by a two-sum, to the comparison.
 template <int GROUP>
 __device__ __forceinline__ uint2 quantize16(const uint32_t (&w)[8], float clip, uint32_t *sz) {
     // (min, -max) of the lane's values as one bf16 pair, then the least of both over the group's lanes
-    __nv_bfloat162 mn2 = as_bf2(w[0]), mx2 = as_bf2(w[0]), ab2 = __habs2(as_bf2(w[0]));
+    __nv_bfloat162 mn2 = as_bf2(w[0]), mx2 = as_bf2(w[0]);
 #pragma unroll
     for (int i = 1; i < 8; ++i) {
         mn2 = __hmin2(mn2, as_bf2(w[i]));
         mx2 = __hmax2(mx2, as_bf2(w[i]));
-        ab2 = __hmin2(ab2, __habs2(as_bf2(w[i])));
     }
     __nv_bfloat162 r = __halves2bfloat162(__hmin(mn2.x, mn2.y), __hneg(__hmax(mx2.x, mx2.y)));
 #pragma unroll
@@ -85,10 +85,11 @@ __device__ __forceinline__ uint2 quantize16(const uint32_t (&w)[8], float clip, 
     // the arithmetic below leaves fp32's range for ranges near its ends: those are moved by 2^64
     const float up = s < 1e-30f ? 0x1p64f : (s > 1e36f ? 0x1p-64f : 1.0f);
     const float top = fmaxf(fabsf(mn), fabsf(mx)), az = fabsf(z);
-    const float least = fminf(lo16(as_u32(ab2)), hi16(as_u32(ab2)));
+    const float ss = s * up, iv = __fdividef(1.0f, ss * 14.0f), at0 = -z * up * (iv * 14.0f);     // the code position of x = 0
+    const bool near0 = fabsf(at0 - floorf(at0) - 0.5f) < 0x1p-9f;
     uint32_t code[2] = {0u, 0u};
-    if (up != 1.0f || least < az * 0x1p-15f || (az < top * 0x1p-15f && az > 0.0f)) {
-        const float zz = z * up, ss = s * up, iv = __fdividef(1.0f, ss * 14.0f);
+    if (up != 1.0f || near0 || (az < top * 0x1p-15f && az > 0.0f)) {
+        const float zz = z * up;
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
             const float x = (e & 1 ? hi16(w[e >> 1]) : lo16(w[e >> 1])) * up;
@@ -102,7 +103,7 @@ __device__ __forceinline__ uint2 quantize16(const uint32_t (&w)[8], float clip, 
         return make_uint2(code[0], code[1]);
     }
     constexpr float kMagic = 12582912.0f;                               // 1.5·2^23: adding it rounds to an integer
-    const float inv = __fdividef(1.0f, s * 14.0f), half = 0.5f * s;
+    const float inv = iv, half = 0.5f * s;
     const uint64_t nz = pair(-z, -z), ns = pair(-s, -s), f14 = pair(14.0f, 14.0f), magic = pair(kMagic, kMagic),
                    down = pair(-kMagic, -kMagic);
 #pragma unroll
