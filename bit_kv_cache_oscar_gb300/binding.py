@@ -1,4 +1,4 @@
-"""Thin binding of liboscar.so (include/oscar.h): argument marshalling only, by ctypes or, for the INT4 calls, natively.
+"""Thin binding of liboscar.so (include/oscar.h, oscar_int4.h): argument marshalling only, by ctypes or, for the INT4 calls, natively.
 
 Every function here has the name of the C entry point it calls, takes torch
 tensors (device memory, caller-owned) and passes their addresses, sizes and the
@@ -58,6 +58,8 @@ EXPORTS = [
     "oscar_decode_attention_noalloc", "oscar_decode_attention_history", "oscar_decode_attention_window",
     "oscar_set_launch_overlap", "oscar_get_launch_overlap", "oscar_decode_attention_fused",
     "oscar_demote_range", "oscar_decode_attention_shared_prefix",
+]
+EXPORTS_INT4 = [                    # include/oscar_int4.h
     "oscar_append_kv", "oscar_demote_int4", "oscar_promote_int4", "oscar_suggest_splits_int4",
     "oscar_decode_attention_int4", "oscar_attention_mass_int4", "oscar_evict_int4",
 ]

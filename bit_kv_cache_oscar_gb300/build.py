@@ -49,7 +49,8 @@ def _marshal_flags() -> tuple:
 def build(verbose: bool = False, extra: list | None = None) -> str:
     os.makedirs(BUILD, exist_ok=True)
     headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
-    headers.append(os.path.join(ROOT, "include", "oscar.h"))
+    public = [os.path.join(ROOT, "include", f) for f in ("oscar.h", "oscar_int4.h")]
+    headers += public
     flags = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden",
                     "-I", os.path.join(ROOT, "include"), "--expt-relaxed-constexpr",
                     "-Xptxas", "-warn-spills"] + (extra or [])
@@ -64,7 +65,7 @@ def build(verbose: bool = False, extra: list | None = None) -> str:
             procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     msrc, mobj = os.path.join(CSRC, "marshal.cpp"), os.path.join(BUILD, "marshal.o")
     mflags = _marshal_flags()
-    if _stale(mobj, [msrc, os.path.join(ROOT, "include", "oscar.h")]):
+    if _stale(mobj, [msrc, *public]):
         cmd = ["g++", *mflags[0], "-c", msrc, "-o", mobj]
         if verbose:
             print(" ".join(cmd), flush=True)

@@ -1,5 +1,5 @@
 // C ABI of liboscar.so: argument validation, the device status word, dispatch
-// to the kernels.  Declarations and contracts: include/oscar.h.
+// to the kernels.  Declarations and contracts: include/oscar.h, include/oscar_int4.h.
 
 #include <atomic>
 #include <cmath>
@@ -9,6 +9,7 @@
 #include <mutex>
 #include <string>
 
+#include "int4.cuh"
 #include "oscar_internal.cuh"
 
 namespace {

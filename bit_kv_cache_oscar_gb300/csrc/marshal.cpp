@@ -15,7 +15,7 @@
 #include <initializer_list>
 #include <string>
 
-#include "oscar.h"
+#include "oscar_int4.h"
 
 namespace {
 

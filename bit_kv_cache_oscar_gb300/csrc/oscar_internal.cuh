@@ -227,52 +227,4 @@ cudaError_t launch_merge(const oscar_layout_t &L, PartialsView p, const float *R
                          float *out_f32, float *lse, cudaStream_t st, int32_t *counters = nullptr,
                          int expected = 0, int32_t *status = nullptr);
 
-// ------------------------------------------------------- the 4-bit history --
-
-struct Int4PoolView {
-    uint8_t *codes_k, *codes_v;
-    uint16_t *scale_zero;
-    int n_pages;
-};
-
-// New tokens' heads: token i at q + i * q_stride elements (q NULL: keys and values only).
-struct AppendInput {
-    const uint16_t *q, *k, *v;
-    long long q_stride, k_stride, v_stride;
-};
-cudaError_t launch_append(const oscar_layout_t &L, const AppendInput &in, int n, const uint16_t *wq, const uint16_t *wk,
-                          float eps, const float *rope, int rope_rows, int rot, bool pairs, Bf16PoolView pool,
-                          const int32_t *pt, int max_pages, int batch, const int32_t *req, const int32_t *pos,
-                          const int32_t *rope_pos, uint16_t *q_out, int32_t *status, cudaStream_t st);
-
-cudaError_t launch_demote4(const oscar_layout_t &L, Bf16PoolView src, const int32_t *bpt, Int4PoolView dst,
-                           const int32_t *ipt, int max_pages, int batch, const int32_t *begin, const int32_t *end,
-                           float cK, float cV, int32_t *status, cudaStream_t st);
-cudaError_t launch_promote4(const oscar_layout_t &L, Int4PoolView src, const int32_t *ipt, Bf16PoolView dst,
-                            const int32_t *bpt, int max_pages, int batch, const int32_t *begin, const int32_t *end,
-                            int32_t *status, cudaStream_t st);
-
-// What decode attention and the attention weights read: one query per request, both pools.
-struct Attn4Input {
-    const uint16_t *q;
-    Bf16PoolView bf;
-    const int32_t *bpt;
-    Int4PoolView i4;
-    const int32_t *ipt;
-    int max_pages;
-    const int32_t *seq_len, *hist_end;
-    float sm_scale;
-};
-int suggest_splits4(const oscar_layout_t &L, int batch, int max_hist, int sm_count);
-// counters: NULL (the merge, if any, is a second launch) or int32 [batch * n_kv_heads], zero and left zero
-cudaError_t launch_decode4(const oscar_layout_t &L, const Attn4Input &in, int batch, PartialsView out, uint16_t *o,
-                           float *of, float *lse, int32_t *counters, int32_t *status, cudaStream_t st);
-cudaError_t launch_mass4(const oscar_layout_t &L, const Attn4Input &in, int batch, const float *lse, float *mass,
-                         int32_t *status, cudaStream_t st);
-
-cudaError_t launch_evict(const oscar_layout_t &L, Int4PoolView src, const int32_t *spt, Int4PoolView dst,
-                         const int32_t *dpt, int max_pages, int batch, const int32_t *seq_len, const int32_t *hist_end,
-                         const int32_t *keep, const float *mass, float *mass_out, int32_t *kept, int kept_stride,
-                         int32_t *status, cudaStream_t st);
-
 }  // namespace oscar

@@ -1,6 +1,6 @@
 """A batch's cache [BF16 sink | INT4 history | BF16 recent] with the 64-bit arithmetic its tests compare with.
 
-Host plumbing and plain numpy in float64, written from the definitions in include/oscar.h.
+Host plumbing and plain numpy in float64, written from the definitions in include/oscar_int4.h.
 """
 from __future__ import annotations
 

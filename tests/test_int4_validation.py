@@ -1,6 +1,8 @@
 """Host-side argument checks of the INT4 entry points, without a GPU: every call here is refused (or, with no work,
 accepted) before the library makes a CUDA call."""
 import ctypes
+import os
+import re
 
 import pytest
 import torch
@@ -19,6 +21,13 @@ no_gpu = pytest.mark.skipif(torch.cuda.is_available(), reason="placeholder addre
 def L():
     build.build()
     return ob.lib()
+
+
+def test_the_header_is_exported_and_bound(L):
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    text = open(os.path.join(root, "include", "oscar_int4.h")).read()
+    names = sorted(set(re.findall(r"OSCAR_API\s+[\w\s\*]*?\b(oscar_\w+)\s*\(", text)))
+    assert names == sorted(ob.EXPORTS_INT4) and all(hasattr(L, n) and hasattr(ob, n) for n in names)
 
 
 def layout(**kw):
