@@ -23,6 +23,12 @@
 // W is 16 (one CTA an SM) when the launch has a CTA for each SM at most, else 8, or 4 for the weights, whose
 // CTAs have no results to join: several CTAs an SM, so that one's start and end hide behind another's stream.
 // Every wait is bounded: one that gives up sets OSCAR_DEV_WAIT_TIMEOUT.
+//
+// Measured (passes back to back, 32 query and 8 kv heads, group 128): 100K tokens 28.3 us, of which about 14
+// stream 110 MB after a start of 7 to 10 us (lengths, page ids and the first copies of all warps at once) and
+// 5 join warps and splits; a ragged batch of 32, 64K to 100K, 494 us = 5.9 TB/s (0.87 of a copy's rate): HBM.
+// 64 query heads and groups of 32, 4 x 131K: 141 us = 4.8 TB/s: issue slots, 710 instructions a block, whose
+// largest part is the unpacking on the ALU pipe.  Weights, ragged batch of 8: 78 us = 5.2 TB/s.
 
 #pragma once
 

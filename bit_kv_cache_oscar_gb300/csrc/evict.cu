@@ -7,6 +7,10 @@
 // value is above that threshold, or equal to it and among the first `keep - above` equal ones.  The
 // positions come out in order because each warp takes a run of them and knows the counts before its run.
 // A second kernel copies the kept rows to their new pages, 8 lanes a row.
+//
+// Measured, two requests of 67K to 100K tokens, 8 kv heads, half kept: selection 31 us (latency: three passes
+// of a histogram in shared memory, a cluster's barriers and remote reads; 7 MB are read), move 47 us = 4.0 TB/s
+// (latency: list entry, page ids and data depend on each other).
 
 #include "int4.cuh"
 #include "ptx.cuh"

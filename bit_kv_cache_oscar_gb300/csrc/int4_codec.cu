@@ -9,7 +9,9 @@
 // quantizer's steps run on packed fp32 pairs.  A CTA takes one kv head and 16-token tiles of the range at
 // absolute positions 16 i (inside one page, so no division by the number of heads; a tile's codes are
 // 1 KB in a row) and loads a tile ahead.  The number of CTAs does not depend on the ranges, which are
-// device data: one token a step and a whole prompt are the same launch.
+// device data: one token a step and a whole prompt are the same launch.  Measured, 100K tokens of 8 kv
+// heads at g = 128: demotion 144 us = 3.6 TB/s (the ALU pipe: 310 instructions a warp and two rows),
+// promotion 85 us = 6.1 TB/s.
 
 #include <cuda_bf16.h>
 
