@@ -12,6 +12,8 @@
 // of a histogram in shared memory, a cluster's barriers and remote reads; 7 MB are read), move 47 us = 4.0 TB/s
 // (latency: list entry, page ids and data depend on each other).
 
+#include <algorithm>
+
 #include "int4.cuh"
 #include "ptx.cuh"
 
@@ -275,10 +277,12 @@ cudaError_t launch_evict(const oscar_layout_t &L, Int4PoolView src, const int32_
                          int32_t *status, cudaStream_t st) {
     const EvictArgs a{src, dst, spt, dpt, max_pages, page_shift(L), L.n_kv_heads, L.group, L.sink, seq_len, hist_end, keep,
                       mass, mass_out, kept, kept_stride, status};
-    // Histories that can pass 8K tokens: eight CTAs a head (a slice each, counts joined across the
-    // cluster); below, the passes are shorter than the cluster's barriers.
-    const long long tokens = (long long)max_pages * L.page_size;
-    const int C = tokens > 8192 ? kCluster : 1;
+    // Long histories of few heads: eight CTAs a head, a slice each, counts joined across the cluster.  Short ones
+    // are done before a cluster's barriers are, and many heads fill the SMs by themselves: one CTA a head.  Whole
+    // call, 8 heads, one and eight CTAs: 6K tokens 20.8 and 22.2 us, 9K 23.0 and 23.6, 16K 29.0 and 24.9; 64
+    // heads, 16K 37 and 46, 40K 95 and 66; 128 heads, 40K 106 and 107; 256 heads, 40K 142 and 197.
+    const long long tokens = (long long)max_pages * L.page_size, pairs = (long long)batch * L.n_kv_heads;
+    const int C = tokens > 256 * std::max(32LL, pairs) ? kCluster : 1;
     const long long slice = (tokens + C - 1) / C;
     const int smem = 4 * (int)(slice < kCached ? slice : kCached);
     auto kern = C > 1 ? evict_select_kernel<kCluster> : evict_select_kernel<1>;
@@ -298,7 +302,7 @@ cudaError_t launch_evict(const oscar_layout_t &L, Int4PoolView src, const int32_
     cfg.numAttrs = C > 1 ? 2 : 1;
     if (cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a)) return e;
     // CTAs: about sixteen an SM, no more than there are runs of 32 rows
-    const long long most = (tokens + 31) / 32, pairs = (long long)batch * L.n_kv_heads, want = (16 * 152 + pairs - 1) / pairs;
+    const long long most = (tokens + 31) / 32, want = (16 * 152 + pairs - 1) / pairs;
     return launch_ahead(evict_move_kernel, dim3((unsigned)(want < most ? want : most), L.n_kv_heads, batch), 256, 0, st, a);
 }
 

@@ -452,7 +452,7 @@ def check_evict(c, keep, mass, stride=None):
     written = np.zeros((new.n_pages, L.n_kv_heads, ps), bool)
     for b in range(c.B):
         T, he, k = int(c.seq[b]), int(c.hist[b]), int(keep[b])
-        if k < 0:
+        if k < 0 or k > max(0, he - L.sink):                         # left alone, or refused
             assert np.all(kept[b] == -7) and np.all(out[b] == 11)
             continue
         for h in range(L.n_kv_heads):
@@ -507,6 +507,14 @@ def test_evict_long_histories(T):
         mass = weights(c.rng, (1, 2, c.max_pages * 64), kind)
         for k in (1, T // 3, int(c.hist[0]) - 64 - 1):
             check_evict(c, [k], mass)
+
+
+def test_evict_many_heads_with_long_histories():
+    """One CTA a head, with more keys than it holds in shared memory; a request without a history to keep 3 of."""
+    c = ic.Cache([20000, 300, 18000], n_kv=64, gqa=1, page=64, seed=1, rubbish=False).upload()
+    mass = weights(c.rng, (3, 64, c.max_pages * 64), "ties")
+    check_evict(c, [700, 3, 17680], mass)
+    assert ob.oscar_get_device_status() == BAD_LENGTH
 
 
 def test_evict_flags_and_shared_pages():
