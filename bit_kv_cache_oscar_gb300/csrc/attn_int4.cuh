@@ -46,6 +46,7 @@ namespace oscar {
 namespace {
 
 constexpr uint32_t kM0 = 0x000F000Fu, kM1 = 0x00F000F0u;
+constexpr int kResRow = kHeadDim + 4;           // floats of a result row: heads 2 t, t = 0..3, in different banks
 constexpr float kNone = -1e30f;                  // running maximum before the first token
 constexpr float kSlack = 8.f;                    // logits (base 2) may pass the running maximum by this
 constexpr int kPShift = 6;                       // p·s is held at 2^6 below 2^(kSlack + 1): at most 2^15
@@ -547,7 +548,7 @@ __device__ __forceinline__ void history_warp(const Attn4Args &a, const CUtensorM
         for (int k = 0; k < NG; ++k) zs[k][j] = col_sum(zs[k][j]);
     }
     __syncthreads();                                 // every warp is done with its ring: results take its place
-    float *wm = res, *wl = res + W * 8, *wa = res + 2 * W * 8 + warp * G * kHeadDim;
+    float *wm = res, *wl = res + W * 8, *wa = res + 2 * W * 8 + warp * G * kResRow;
     if (g == 0) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
@@ -559,11 +560,12 @@ __device__ __forceinline__ void history_warp(const Attn4Args &a, const CUtensorM
 #pragma unroll
     for (int c = 0; c < 4; ++c)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int head = 2 * t + (e & 1), ch = 32 * c + 4 * g + 2 * j + (e >> 1);
-                if (head < G) wa[head * kHeadDim + ch] = acc[c][j][e] * (e >> 1 ? 1048576.f : 16777216.f) * up + zs[c * NG / 4][e & 1];
+        for (int e = 0; e < 2; ++e)                  // head 2 t + e, channels 32 c + 4 g .. + 3
+            if (2 * t + e < G) {
+                const float z = zs[c * NG / 4][e];
+                *reinterpret_cast<float4 *>(wa + (2 * t + e) * kResRow + 32 * c + 4 * g) =
+                    make_float4(acc[c][0][e] * 0x1p24f * up + z, acc[c][0][2 + e] * 0x1p20f * up + z, acc[c][1][e] * 0x1p24f * up + z,
+                                acc[c][1][2 + e] * 0x1p20f * up + z);
             }
 }
 
@@ -576,73 +578,51 @@ __device__ __forceinline__ void write_out(const Attn4Args &a, size_t orow, int d
     if (a.o_lse && d == 0) a.o_lse[orow] = on ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
 }
 
-// The merge of all S + 1 slots of one kv head's G query heads, in oscar_merge's order and arithmetic.
-// The accumulator rows come through shared memory, as many slots at a time as fit, all their 16-byte
-// copies in flight at once and under way while the weights are formed.
+// The merge of one kv head's G query heads over the S splits (slot S is empty), in oscar_merge's order and
+// arithmetic.  A warp takes 32 channels of a head, 32 splits at a time: their rows are on their way while
+// the lanes form the weights, a split each, and half of them always is while the other half is added up.
 template <int G, int W>
-__device__ __forceinline__ void merge_head(const Attn4Args &a, int b, int h, float *scratch, int scratch_bytes) {
-    const int S1 = a.out.S + 1;
-    const size_t row0 = ((size_t)b * a.n_kv * G + h * G) * S1;
-    float *ws = scratch, *ls = scratch + G * S1, *ms = ls + G * S1;
-    float *rows = scratch + ((2 * G * S1 + G + 3) & ~3);
-    const int chunk = min(S1, (scratch_bytes - (int)((rows - scratch) * 4)) / (G * kHeadDim * 4));
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    constexpr int kThreads = W * 32;
-    auto load = [&](int s0) {                          // slots [s0, s0 + chunk) of every head: [head][slot][128]
-        const int n = min(chunk, S1 - s0) * 32;
+__device__ __forceinline__ void merge_head(const Attn4Args &a, int b, int h) {
+    constexpr int kHalf = 16;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, S = a.out.S;
+    for (int item = warp; item < 4 * G; item += W) {
+        const int hh = item >> 2, d = (item & 3) * 32 + lane;
+        const size_t orow = ((size_t)b * a.n_kv + h) * G + hh, row0 = orow * (S + 1);
+        const float *m = a.out.m + row0, *l = a.out.l + row0, *acc = a.out.acc + row0 * kHeadDim + d;
+        float x[2][kHalf];
+        auto load = [&](float (&r)[kHalf], int s0) {
 #pragma unroll
-        for (int hh = 0; hh < G; ++hh) {
-            const float *src = a.out.acc + (row0 + (size_t)hh * S1 + s0) * kHeadDim;
-            const uint32_t dst = saddr(rows + (size_t)hh * chunk * kHeadDim);
-            for (int r = threadIdx.x; r < n; r += kThreads) cp_async16(dst + r * 16, src + r * 4);
+            for (int i = 0; i < kHalf; ++i) r[i] = s0 + i < S ? __ldcg(acc + (size_t)(s0 + i) * kHeadDim) : 0.f;
+        };
+        load(x[0], 0);
+        load(x[1], kHalf);
+        float l1 = lane < S ? __ldcg(l + lane) : 0.f, m1 = lane < S ? __ldcg(m + lane) : 0.f;
+        float M = l1 > 0.f ? m1 : -INFINITY;
+        for (int i = 32 + lane; i < S; i += 32) {
+            const float li = __ldcg(l + i), mi = __ldcg(m + i);
+            if (li > 0.f) M = fmaxf(M, mi);
         }
-    };
-    load(0);
-    for (int i = threadIdx.x; i < G * S1; i += kThreads) {
-        ls[i] = __ldcg(a.out.l + row0 + i);
-        ws[i] = __ldcg(a.out.m + row0 + i);
-    }
-    __syncthreads();
-    if (warp < G) {
-        float M = -INFINITY;
-        for (int i = lane; i < S1; i += 32)
-            if (ls[warp * S1 + i] > 0.f) M = fmaxf(M, ws[warp * S1 + i]);
 #pragma unroll
         for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        if (lane == 0) ms[warp] = M;
-        for (int i = lane; i < S1; i += 32)
-            ws[warp * S1 + i] = ls[warp * S1 + i] > 0.f ? exp2_taylor(__fsub_rn(ws[warp * S1 + i], M)) : 0.f;
-    }
-    constexpr int kPart = G * kHeadDim / kThreads > 0 ? G * kHeadDim / kThreads : 1;
-    float L[kPart], A[kPart];
+        float L = 0.f, A = 0.f;
+        for (int s0 = 0; s0 < S; s0 += 32) {
+            const float li = l1, wi = li > 0.f ? exp2_taylor(__fsub_rn(m1, M)) : 0.f;
+            const bool more = s0 + 32 + lane < S;
+            l1 = more ? __ldcg(l + s0 + 32 + lane) : 0.f;
+            m1 = more ? __ldcg(m + s0 + 32 + lane) : 0.f;
 #pragma unroll
-    for (int u = 0; u < kPart; ++u) L[u] = A[u] = 0.f;
-    for (int s0 = 0; s0 < S1; s0 += chunk) {
-        if (s0 > 0) {
-            __syncthreads();                           // the previous chunk is consumed
-            load(s0);
-        }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        __syncthreads();
-        const int n = min(chunk, S1 - s0);
+            for (int p = 0; p < 2; ++p) {
 #pragma unroll
-        for (int u = 0; u < kPart; ++u) {
-            const int e = threadIdx.x + u * kThreads, hh = e / kHeadDim, d = e % kHeadDim;
-            if (hh >= G) continue;
-            const float *x = rows + (size_t)hh * chunk * kHeadDim + d, *w = ws + hh * S1 + s0, *l = ls + hh * S1 + s0;
-#pragma unroll 8
-            for (int i = 0; i < n; ++i) {
-                const bool on = l[i] > 0.f;
-                L[u] = on ? __fmaf_rn(l[i], w[i], L[u]) : L[u];
-                A[u] = on ? __fmaf_rn(x[i * kHeadDim], w[i], A[u]) : A[u];
+                for (int i = 0; i < kHalf; ++i) {
+                    if (s0 + p * kHalf + i >= S) break;
+                    const float lw = __shfl_sync(0xffffffffu, li, p * kHalf + i), w = __shfl_sync(0xffffffffu, wi, p * kHalf + i);
+                    L = lw > 0.f ? __fmaf_rn(lw, w, L) : L;
+                    A = lw > 0.f ? __fmaf_rn(x[p][i], w, A) : A;
+                }
+                load(x[p], s0 + 32 + p * kHalf);
             }
         }
-    }
-#pragma unroll
-    for (int u = 0; u < kPart; ++u) {
-        const int e = threadIdx.x + u * kThreads, hh = e / kHeadDim, d = e % kHeadDim;
-        if (hh >= G) continue;
-        write_out(a, ((size_t)b * a.n_kv + h) * G + hh, d, A[u], L[u], ms[hh]);
+        write_out(a, orow, d, A, L, M);
     }
 }
 
@@ -688,7 +668,7 @@ __global__ void __launch_bounds__(W * 32, 16 / W)
         float L = 0.f, A = 0.f;
 #pragma unroll 4
         for (int w = 0; w < W; ++w) {
-            const float f = wf[w * 8 + hh], x = wa[(w * G + hh) * kHeadDim + d];
+            const float f = wf[w * 8 + hh], x = wa[(w * G + hh) * kResRow + d];
             L = fmaf(wl[w * 8 + hh], f, L);
             A = fmaf(f > 0.f ? x : 0.f, f, A);
         }
@@ -717,17 +697,14 @@ __global__ void __launch_bounds__(W * 32, 16 / W)
         if (last) *c = 0;
     }
     __syncthreads();
-    if (last) merge_head<G, W>(a, b, h, res, a.smem_bytes);
+    if (last) merge_head<G, W>(a, b, h);
 }
 
 template <int G, int NG, bool MASS, int W>
-cudaError_t launch_one(Attn4Args a, const CUtensorMap &tmk, const CUtensorMap &tmv, int batch, cudaStream_t st) {
-    // the merge: weights of every slot, and room for one slot's rows at least
-    const int merge = (((2 * G * (a.out.S + 1) + G + 3) & ~3) + G * kHeadDim) * 4, combine = (2 * W * 8 + W * G * kHeadDim) * 4;
+cudaError_t launch_one(const Attn4Args &a, const CUtensorMap &tmk, const CUtensorMap &tmv, int batch, cudaStream_t st) {
+    const int combine = (2 * W * 8 + W * G * kResRow) * 4;
     int smem = Ring<NG, MASS, W>::total;
     if (!MASS && smem < combine) smem = combine;
-    if (!MASS && a.counters && smem < merge) smem = merge;
-    a.smem_bytes = smem;
     smem += 1024;
     auto kern = attn4_kernel<G, NG, MASS, W>;
     if (cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void *>(kern), smem)) return e;

@@ -27,7 +27,6 @@ struct Attn4Args {
     const float *lse;          // weights only
     float *mass;
     int32_t *status;
-    int smem_bytes;            // from the aligned base on
 };
 
 // One instantiation per number of query heads a kv head (G), each in a file of its own.

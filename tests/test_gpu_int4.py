@@ -305,6 +305,16 @@ def test_decode_many_splits_and_long_history():
     check_decode(c, ob.oscar_suggest_splits_int4(c.L, 2, 30000, 152))
 
 
+@pytest.mark.parametrize("splits", [15, 16, 31, 32, 33, 48, 65, 100, 1024])
+@pytest.mark.parametrize("gqa", [1, 8])
+def test_decode_merge_of_any_number_of_splits(splits, gqa):
+    """The merge inside the launch has the separate merge's bits: full ones, part ones, empty ones, none."""
+    c = ic.Cache([3300, 0, 500, 70], n_kv=2, gqa=gqa, page=16, seed=splits).upload()
+    out, lse, _ = check_decode(c, splits)
+    two = decode(c, splits, fused=False)
+    assert torch.equal(out, two[0]) and torch.equal(lse, two[1])
+
+
 def test_decode_bad_pages_and_lengths_are_flagged():
     c = ic.Cache([600, 600], seed=4).upload()
     good = decode(c, 3)[0]
