@@ -50,9 +50,9 @@ cudaError_t launch(const oscar_layout_t &L, const Attn4Input &in, Attn4Args a, b
 // Splits of at least 256 tokens (8 blocks): shorter ones cost more in the merge than they save.  Up to that
 // bound one CTA of 16 warps an SM where that fills nine SMs in ten; else, while the heads leave each four
 // splits, one wave of CTAs of 8 warps, two an SM; else about six waves of those, so that requests of
-// different lengths finish evenly.  (100K tokens, 8 heads: 31.5 us with 19 splits of 16 warps, 36.8 with 37 of
-// 8; 4 x 131K: 145 us with 9 splits in one wave, 152 with 4 of 16 warps, 182 with 38 in four waves; ragged
-// batch of 32: 649, 523, 507, 497 and 507 us with 1, 3, 5, 7 and 10.)
+// different lengths finish evenly.  (100K tokens, 8 heads: 30.8 us with 19 splits of 16 warps, 35.1 with 37 of
+// 8; 4 x 131K: 145 us with 9 splits in one wave, 152 with 4 of 16 warps, 196 with 10; ragged batch of 32:
+// 497, 494, 488, 493 and 497 us with 5, 6, 7, 8 and 10.)
 int suggest_splits4(const oscar_layout_t &L, int batch, int max_hist, int sm_count) {
     const long long per = (long long)batch * L.n_kv_heads, wide = sm_count / per, slots = 2LL * sm_count;
     long long want = wide * per * 10 >= sm_count * 9LL ? wide : per * 4 <= slots ? slots / per : 6 * slots / per;

@@ -191,6 +191,12 @@ def test_demote_and_promote_bit_exact(n_kv, page, group, ranges, clip):
     assert np.array_equal(back.v.double().cpu().numpy(), want_back[1])
 
 
+@pytest.mark.parametrize("n_kv,page,group", [(2, 16, 128), (8, 32, 64), (1, 64, 32)])
+@pytest.mark.parametrize("ranges", [[(75, 309), (1, 319), (66, 303)], [(7, 318)]])
+def test_demote_long_ranges_that_begin_and_end_anywhere(n_kv, page, group, ranges):
+    test_demote_and_promote_bit_exact(n_kv, page, group, ranges, (1.0, 0.96))
+
+
 def test_demote_and_promote_flag_bad_ranges_and_pages():
     L = ob.Layout(2, 1, 16)
     src, dst = ob.Bf16Pool.empty(L, 4), ob.Int4Pool.empty(L, 4)
