@@ -224,10 +224,11 @@ cudaError_t launch_append(const oscar_layout_t &L, const AppendInput &in, int n,
                           const int32_t *rope_pos, uint16_t *q_out, int32_t *status, cudaStream_t st) {
     const int n_q = in.q ? L.n_kv_heads * L.gqa : 0;
     const int pairs = (n_q + 2 * L.n_kv_heads + 1) / 2;
-    // A step's rows go to as many warps as there are row pairs; once whole tokens fill every SM with 32 warps
-    // (4864), a warp takes a whole token; between, runs that give about that many warps.
-    const int per = (int)std::max(1LL, std::min((long long)pairs, (long long)pairs * n / 4864));
-    const int runs = (pairs + per - 1) / per;
+    // A token's row pairs go to equal runs of as many warps as the SMs hold at once (16 each), one pair a warp at
+    // least, and to one warp where there are more tokens than that.  (32 query and 8 kv heads: 300 tokens 6.3 us,
+    // 1,024 10.0, 2,048 15.4, 4,000 26.0; twice the warps: 8.3, 10.4, 17.5, 26.0; half: 6.2, 11.6, 15.4, 26.0.)
+    const int most = (int)std::max(1LL, std::min((long long)pairs, 16LL * 152 / n));
+    const int per = (pairs + most - 1) / most, runs = (pairs + per - 1) / per;
     const AppendArgs a{in.q, in.k, in.v, in.q_stride, in.k_stride, in.v_stride, n, n_q, L.n_kv_heads, per, runs, wq, wk, eps,
                        rope, rope_rows, rot, pool, pt, max_pages, page_shift(L), batch, req, pos, rope_pos, q_out, status};
     const unsigned blocks = (unsigned)(((long long)n * runs + kWarps - 1) / kWarps);
