@@ -47,18 +47,22 @@ cudaError_t launch(const oscar_layout_t &L, const Attn4Input &in, Attn4Args a, b
 
 }  // namespace
 
-// Splits of at least 256 tokens (8 blocks): shorter ones cost more in the merge than they save.  Up to that
-// bound one CTA of 16 warps an SM where that fills nine SMs in ten; else, while the heads leave each four
-// splits, one wave of CTAs of 8 warps, two an SM; else about six waves of those, so that requests of
-// different lengths finish evenly.  (100K tokens, 8 heads: 30.8 us with 19 splits of 16 warps, 35.1 with 37 of
-// 8; 4 x 131K: 145 us with 9 splits in one wave, 152 with 4 of 16 warps, 196 with 10; ragged batch of 32:
-// 497, 494, 488, 493 and 497 us with 5, 6, 7, 8 and 10.)
+// One wave of CTAs at first: of 16 warps, one an SM, or of 8, two an SM, by the tokens an SM gets (the
+// latter takes 2.1 times as long a token of its split, and 500 tokens more).  A wave costs about 4.5 us, so
+// only splits that are long in that wave (32K tokens, or 16K with 8 warps) are cut into more waves, which finish
+// evenly: 8K tokens each, six waves at most.  Splits of at least 256 tokens (8 blocks): shorter ones cost more in the
+// merge than they save.  8 heads, us: 1 x 100K 30.8 with 19 splits of 16 warps, 35.1 with 37 of 8; 4 x 131K 105
+// with 9 splits (8 warps), 110 with 4 (16); 4 x 8K 16.9 and 15.9; 16 x 8K 34.8, 39, 44, 49 and 68 with 1, 2, 4, 7 and
+// 14; 32 x 8K 64, 73, 75 and 89 with 1, 2, 4 and 7; lengths 22K to 32K, 32 requests: 213, 198, 182 and 187; 32 of
+// 64K to 100K: 497, 494, 488, 493 and 497 with 5, 6, 7, 8 and 10.
 int suggest_splits4(const oscar_layout_t &L, int batch, int max_hist, int sm_count) {
-    const long long per = (long long)batch * L.n_kv_heads, wide = sm_count / per, slots = 2LL * sm_count;
-    long long want = wide * per * 10 >= sm_count * 9LL ? wide : per * 4 <= slots ? slots / per : 6 * slots / per;
-    const long long most = ((long long)max_hist + 255) / 256;
-    if (want > most) want = most;
-    return (int)(want < 1 ? 1 : want > 1024 ? 1024 : want);
+    const long long heads = (long long)batch * L.n_kv_heads, h = max_hist;
+    const long long wide = sm_count / heads, narrow = std::max(1LL, 2LL * sm_count / heads);
+    const bool is_wide = wide > 0 && 10 * h / wide <= 21 * h / narrow + 5000;
+    long long want = is_wide ? wide : narrow;
+    if (h > want * (is_wide ? 32768 : 16384)) want = std::max(want, std::min(h / 8192, 12LL * sm_count / heads));
+    want = std::min(want, (h + 255) / 256);
+    return (int)std::max(1LL, std::min(want, 1024LL));
 }
 
 cudaError_t launch_decode4(const oscar_layout_t &L, const Attn4Input &in, int batch, PartialsView out, uint16_t *o,
@@ -78,11 +82,14 @@ cudaError_t launch_decode4(const oscar_layout_t &L, const Attn4Input &in, int ba
 cudaError_t launch_mass4(const oscar_layout_t &L, const Attn4Input &in, int batch, const float *lse, float *mass,
                          int32_t *status, cudaStream_t st) {
     Attn4Args a{};
-    // no merge to pay for: about two waves of CTAs of 4 warps even where one would hold the splits (a ragged
-    // batch of 8: 135, 89, 80 and 80 us with 4, 9, 19 and 28; of 8 warps: 100, 86, 85 and 90)
-    const long long per = (long long)batch * L.n_kv_heads, tokens = in.max_pages * (long long)L.page_size;
-    const int S = suggest_splits4(L, batch, (int)tokens, kSms);
-    a.out.S = per > kSms / 4 ? (int)std::max<long long>(1, std::min({1024LL, 8LL * kSms / per, (tokens + 255) / 256})) : S;
+    // no merge to pay for: CTAs of 16 warps, one an SM, where they fill nine SMs in ten; else of 4 warps, four an
+    // SM, one wave, or two where that leaves splits of 1,200 tokens (8 heads, one and two waves: 4 x 32K 20.0 and
+    // 23.3 us, 8 x 8K 12.8 and 15.9, 8 x 100K 97.6 and 90.0, 64 x 8K 78.9 and 68.6; 4 x 100K 49.5, of 8 warps 64.8)
+    const long long heads = (long long)batch * L.n_kv_heads, tokens = in.max_pages * (long long)L.page_size;
+    const long long wide = kSms / heads, wave = 4LL * kSms;
+    long long want = 10 * wide * heads >= 9 * kSms ? wide : tokens * heads >= 2 * wave * 1200 ? 2 * wave / heads : wave / heads;
+    want = std::min(want, (tokens + 255) / 256);
+    a.out.S = (int)std::max(1LL, std::min(want, 1024LL));
     a.lse = lse;
     a.mass = mass;
     a.status = status;
