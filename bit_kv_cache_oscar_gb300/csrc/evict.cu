@@ -233,8 +233,9 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a) {
 
 // grid (X, Hkv, batch).  A row is 8 lanes: 4 with the key's 64 bytes, 4 with the value's.  List entry, page
 // ids and data depend on each other, and what hides that is many warps with few registers each: one row a
-// thread at a time and sixteen CTAs an SM (2 x 100K to half, read back: 149 us; four rows a thread, eight
-// CTAs: 153; the next rows' entries and pages loaded ahead, four CTAs: 191).
+// thread at a time and sixteen CTAs an SM, the next entry asked into L1 meanwhile (8 x 100K to half, read back:
+// 588 us; without that 596; the next entry held in a register, 40 of them: 607.  2 x 100K: 149; four rows a thread,
+// eight CTAs: 153; the next rows' entries and pages loaded ahead, four CTAs: 191).
 __global__ void __launch_bounds__(256) evict_move_kernel(EvictArgs a) {
     const int h = blockIdx.y, b = blockIdx.z, hl = threadIdx.x & 7;
     int T, he, n, k;
@@ -248,6 +249,7 @@ __global__ void __launch_bounds__(256) evict_move_kernel(EvictArgs a) {
     uint8_t *dc = hl < 4 ? a.dst.codes_k : a.dst.codes_v;
     for (long long j = blockIdx.x * 32 + (threadIdx.x >> 3); j < k; j += step) {
         const int p = kept[j], to = a.sink + (int)j;
+        if (j + step < k) asm volatile("prefetch.global.L1 [%0];" ::"l"(kept + j + step));
         const int sp = spt[p >> a.page_shift], dp = dpt[to >> a.page_shift];
         if (hl == 0) a.mass_out[row0 + to] = a.mass[row0 + p];
         if ((uint32_t)sp >= (uint32_t)a.src.n_pages || (uint32_t)dp >= (uint32_t)a.dst.n_pages) {
