@@ -8,8 +8,12 @@
 // and zeros stay outside.  A nibble n in bits 0..3 or 4..7 of an f16 with no exponent bits is the
 // subnormal n·2^-24 or 16n·2^-24, so unpacking eight codes is one shift and four ANDs; the powers of two
 // go into the other operand or the result.  q is bf16 and exact in f16 after a power-of-two scaling of
-// each head; p·s is rounded to f16 (2^-11 relative), scaled by a power of two that follows the value
-// scales.  The contractions have 8 columns: the query heads of one kv head.
+// each head.  p·s goes in as two f16 parts, 22 bits together: codes are not centred, so the zero points
+// cancel most of the sum, and with one part the output was off by up to 1e-3 of its size, half a bf16 step.
+// The parts are scaled by a power of two that follows the largest p·s met so far, not the largest s: a row
+// whose scale is far above the others' and whose weight is far below must not push them out of f16's range.
+// The contractions have 8 columns: the query heads of one kv head, twice for up to four heads, whose second
+// four columns take the lower parts of p·s (and of the BF16 rows' p) in the same instructions.
 //
 // A CTA takes one kv head of one split; each of its warps takes every W-th block of 32 tokens on its own
 // (2 KB of key codes, 2 KB of value codes, their scale/zero records) through a ring of stages that its
@@ -24,11 +28,11 @@
 // CTAs have no results to join: several CTAs an SM, so that one's start and end hide behind another's stream.
 // Every wait is bounded: one that gives up sets OSCAR_DEV_WAIT_TIMEOUT.
 //
-// Measured (passes back to back, 32 query and 8 kv heads, group 128): 100K tokens 28.3 us, of which about 14
+// Measured (passes back to back, 32 query and 8 kv heads, group 128): 100K tokens 28.5 us, of which about 14
 // stream 110 MB after a start of 7 to 10 us (lengths, page ids and the first copies of all warps at once) and
-// 5 join warps and splits; a ragged batch of 32, 64K to 100K, 494 us = 5.9 TB/s (0.87 of a copy's rate): HBM.
-// 64 query heads and groups of 32, 4 x 131K: 141 us = 4.8 TB/s: issue slots, 710 instructions a block, whose
-// largest part is the unpacking on the ALU pipe.  Weights, ragged batch of 8: 78 us = 5.2 TB/s.
+// 5 join warps and splits; a ragged batch of 32, 64K to 100K, 504 us = 5.8 TB/s (0.85 of a copy's rate): HBM and
+// issue slots.  64 query heads and groups of 32, 4 x 131K: 168 us = 4.0 TB/s: issue slots.  With p·s in one part
+// these were 27.4, 487 and 141 us.  Weights, ragged batch of 8: 78 us = 5.2 TB/s.
 
 #pragma once
 
@@ -49,7 +53,9 @@ constexpr uint32_t kM0 = 0x000F000Fu, kM1 = 0x00F000F0u;
 constexpr int kResRow = kHeadDim + 4;           // floats of a result row: heads 2 t, t = 0..3, in different banks
 constexpr float kNone = -1e30f;                  // running maximum before the first token
 constexpr float kSlack = 8.f;                    // logits (base 2) may pass the running maximum by this
-constexpr int kPShift = 6;                       // p·s is held at 2^6 below 2^(kSlack + 1): at most 2^15
+constexpr int kPShift = 11;                      // a new scaling brings the largest p·s into [2^11, 2^12); near 2^15 another is due
+constexpr float kPMost = 0x1p110f;               // the largest scaling: that of sums that are still all zero
+constexpr uint32_t kHighPart = 0xFFFFE000u;      // fp32 bits that f16 holds
 
 // One stage of one warp: key codes [32][64 B], value codes, scale/zero records [32][NG][8 B].
 template <int NG, bool MASS, int W>
@@ -73,6 +79,10 @@ __device__ __forceinline__ uint32_t pack_b2(float a, float b) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t *>(&h);
 }
+// Heads of column c: up to four heads have their columns twice, for the two parts of p·s.
+template <int G>
+__device__ __forceinline__ int column_head(int c) { return G <= 4 ? c & 3 : c; }
+__device__ __forceinline__ float high_part(float x) { return __uint_as_float(__float_as_uint(x) & kHighPart); }
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
     uint32_t d;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
@@ -101,11 +111,16 @@ struct ColState {
     float m[2], l[2];
 };
 
-// Bound and scaling of the value scales from the bits of the largest (positive): 2^e <= it < 2^(e + 1).
-__device__ __forceinline__ void set_value_bound(uint32_t bits, float &vmax, float &vinv) {
-    const int e = max((int)(bits >> 23) - 127, -100);
-    vinv = __uint_as_float((uint32_t)(kPShift - e + 127) << 23);
-    vmax = e >= 126 ? INFINITY : __uint_as_float((uint32_t)(e + 1 + 127) << 23);
+// The power of two that brings x > 0, 2^e <= x < 2^(e + 1), to 2^kPShift.
+__device__ __forceinline__ float scaling(float x) {
+    const int e = max((int)(__float_as_uint(x) >> 23) - 127, kPShift - 110);
+    return __uint_as_float((uint32_t)(kPShift - e + 127) << 23);
+}
+
+// Limit of logit + log2 s, as the history's loop forms it, under maximum m and this scaling: 2^15 for p·s·vinv, with 2^-7 for
+// the sum's own rounding far below f16's end.
+__device__ __forceinline__ float logit_limit(float m, float vinv) {
+    return m + (65536.f + 127.f + 15.f - (float)((int)(__float_as_uint(vinv) >> 23) - 127));
 }
 
 // ---- the BF16 rows: [0, min(sink, T)) and [hist_end, T), 16-token tiles dealt out to the warps ----------
@@ -154,19 +169,20 @@ __device__ __forceinline__ bool issue_tile(const Attn4Args &a, const Window &w, 
 }
 
 // Fold the warp's tiles first, first + every, ... (the first is under way in buf, `ok` unless its page is bad).
-// Leaves the running maxima and sums in cs, and the accumulators in the layout, scaling and bound (vmax,
-// vinv) that the history's loop goes on with.  Lane (g, t) reads channels 32 i + 8 t .. + 7 of tokens g and
-// g + 8; value rows become the A operand through movmatrix (channels 32 c + 4 n + 2 j of eight tokens are
-// an 8 x 8 matrix), p the B operand in two bf16 parts.
+// Leaves the running maxima and sums in cs, and the accumulators in the layout and scaling (vinv) that the
+// history's loop goes on with.  Lane (g, t) reads channels 32 i + 8 t .. + 7 of tokens g and g + 8; value rows
+// become the A operand through movmatrix (channels 32 c + 4 n + 2 j of eight tokens are an 8 x 8 matrix), p
+// the B operand in two bf16 parts.
 template <int G, bool MASS>
 __device__ __forceinline__ void window_tiles(const Attn4Args &a, const Window &w, int b, int h, int first, int every, int lane,
                                              uint8_t *buf, uint32_t bar, bool ok, WindowTile &x, ColState &cs, float (&out)[4][2][4],
-                                             float &vmax, float &vinv) {
-    const int g = lane >> 2, t = lane & 3, sh = a.page_shift;
+                                             float (&vinv)[2]) {
+    const int g = lane >> 2, t = lane & 3, sh = a.page_shift, head = MASS ? g : column_head<G>(g);
+    const bool lower = G <= 4 && t >= 2;                       // this lane's columns take the lower parts
     uint4 bq[4];
-    const uint16_t *qr = a.q + ((size_t)b * a.n_kv * G + h * G + (g < G ? g : 0)) * kHeadDim + 8 * t;
+    const uint16_t *qr = a.q + ((size_t)b * a.n_kv * G + h * G + (head < G ? head : 0)) * kHeadDim + 8 * t;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) bq[i] = g < G ? *reinterpret_cast<const uint4 *>(qr + 32 * i) : make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < 4; ++i) bq[i] = head < G ? *reinterpret_cast<const uint4 *>(qr + 32 * i) : make_uint4(0, 0, 0, 0);
     uint32_t phase = 0;
 #pragma unroll 1
     for (int k = first; k < w.tiles; k += every) {
@@ -222,9 +238,9 @@ __device__ __forceinline__ void window_tiles(const Attn4Args &a, const Window &w
         uint32_t bh[2], bl[2];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-            const uint32_t hi = pack_b2(pr[r][0], pr[r][1]);
-            bh[r] = movmatrix_trans(hi);
-            bl[r] = movmatrix_trans(pack_b2(pr[r][0] - lo16(hi), pr[r][1] - hi16(hi)));
+            const uint32_t hi = pack_b2(pr[r][0], pr[r][1]), lo = pack_b2(pr[r][0] - lo16(hi), pr[r][1] - hi16(hi));
+            bh[r] = movmatrix_trans(lower ? lo : hi);
+            if (G > 4) bl[r] = movmatrix_trans(lo);
         }
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -238,26 +254,30 @@ __device__ __forceinline__ void window_tiles(const Attn4Args &a, const Window &w
 #pragma unroll
                 for (int e = 0; e < 4; ++e) out[c][j][e] *= al[e & 1];
                 mma16816_bf16(out[c][j], m0, m1, m2, m3, bh[0], bh[1]);
-                mma16816_bf16(out[c][j], m0, m1, m2, m3, bl[0], bl[1]);
+                if (G > 4) mma16816_bf16(out[c][j], m0, m1, m2, m3, bl[0], bl[1]);
             }
         }
     }
     if (MASS) return;
-    float top = 0.f;
+    float top[2] = {0.f, 0.f};
 #pragma unroll
     for (int c = 0; c < 4; ++c)
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) top = fmaxf(top, fabsf(out[c][j][e]));
-    top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
-    if (top > 0.f) set_value_bound(__float_as_uint(top), vmax, vinv);
+            for (int e = 0; e < 4; ++e) top[e & 1] = fmaxf(top[e & 1], fabsf(out[c][j][e]));
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        top[j] = col_max(top[j]);
+        if (G <= 4) top[j] = fmaxf(top[j], __shfl_xor_sync(0xffffffffu, top[j], 2));     // both parts of a head alike
+        vinv[j] = scaling(top[j]);
+    }
 #pragma unroll
     for (int c = 0; c < 4; ++c)
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) out[c][j][e] *= vinv * (e >> 1 ? 0x1p-20f : 0x1p-24f);
+            for (int e = 0; e < 4; ++e) out[c][j][e] *= vinv[e & 1] * (e >> 1 ? 0x1p-20f : 0x1p-24f);
 }
 
 // ---- the history -------------------------------------------------------------------------------
@@ -265,7 +285,8 @@ template <int G, int NG, bool MASS, int W>
 __device__ __forceinline__ void history_warp(const Attn4Args &a, const CUtensorMap *tmk, const CUtensorMap *tmv, uint8_t *ring,
                                              uint32_t bars, int b, int h, int split, int T, int he, int warp, int lane, float *res) {
     using R = Ring<NG, MASS, W>;
-    const int g = lane >> 2, t = lane & 3, sh = a.page_shift, S = a.out.S;
+    const int g = lane >> 2, t = lane & 3, sh = a.page_shift, S = a.out.S, head = MASS ? g : column_head<G>(g);
+    const bool lower = G <= 4 && t >= 2;           // this lane's columns take the lower parts of p·s
     const int first = a.sink / kBlock, nb = he > a.sink ? (he + kBlock - 1) / kBlock - first : 0;
     const int lo = first + (int)((long long)split * nb / S) + warp, hi = first + (int)((long long)(split + 1) * nb / S);
     const int n = lo < hi ? (hi - lo + W - 1) / W : 0;      // blocks lo, lo + W, ...
@@ -320,7 +341,7 @@ __device__ __forceinline__ void history_warp(const Attn4Args &a, const CUtensorM
 
     ColState cs;
     float zs[NG][2], acc[4][2][4];
-    float vmax = 0.f, vinv = 1.f;                  // value scales seen are at most vmax = 2^(e + 1); vinv = 2^(kPShift - e)
+    float vinv[2] = {kPMost, kPMost};              // what this lane's columns' p·s are multiplied by, powers of two
 #pragma unroll
     for (int i = 0; i < NG; ++i) zs[i][0] = zs[i][1] = 0.f;
     cs.m[0] = cs.m[1] = kNone;
@@ -339,25 +360,25 @@ __device__ __forceinline__ void history_warp(const Attn4Args &a, const CUtensorM
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[c][j][e] = 0.f;
     if (has_tile) {
-        window_tiles<G, MASS>(a, win, b, h, tile0, S * W, lane, ring, bars + 8 * wbar, tile_ok, wt, cs, acc, vmax, vinv);
+        window_tiles<G, MASS>(a, win, b, h, tile0, S * W, lane, ring, bars + 8 * wbar, tile_ok, wt, cs, acc, vinv);
         fence_proxy_async_smem();
         __syncwarp();
         for (int i = ahead; i < R::n && i < n; ++i) issue(i, (st0 + i) % R::n);
     }
 
-    // B operand of the logits: column g = query head g, channels 32 i + 8 t + e of chunk i; the odd
+    // B operand of the logits: column g = its query head, channels 32 i + 8 t + e of chunk i; the odd
     // nibbles meet q/16.  fac undoes the scalings, qz is the zero's factor, per column and group.
     uint32_t bq[4][4];
     float fac[2], qz[NG][2];
     {
         uint4 w[4];
-        const uint16_t *qr = a.q + ((size_t)b * a.n_kv * G + h * G + (g < G ? g : 0)) * kHeadDim + 8 * t;
+        const uint16_t *qr = a.q + ((size_t)b * a.n_kv * G + h * G + (head < G ? head : 0)) * kHeadDim + 8 * t;
         float mx = 0.f, qs[NG];
 #pragma unroll
         for (int j = 0; j < NG; ++j) qs[j] = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            w[i] = g < G ? *reinterpret_cast<const uint4 *>(qr + 32 * i) : make_uint4(0, 0, 0, 0);
+            w[i] = head < G ? *reinterpret_cast<const uint4 *>(qr + 32 * i) : make_uint4(0, 0, 0, 0);
             const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -387,6 +408,7 @@ __device__ __forceinline__ void history_warp(const Attn4Args &a, const CUtensorM
             for (int j = 0; j < 2; ++j) qz[k][j] = __shfl_sync(0xffffffffu, qs[k] * a.scale2, 4 * (2 * t + j));
         }
     }
+    float most[2] = {logit_limit(cs.m[0], vinv[0]), logit_limit(cs.m[1], vinv[1])};
     for (int i = 0, st = st0, round = 0, phase = 0; i < n; ++i) {
         if (!mbar_wait(bars + 8 * st, phase)) {
             if (lane == 0) flag_status(a.status, OSCAR_DEV_WAIT_TIMEOUT);
@@ -466,69 +488,97 @@ __device__ __forceinline__ void history_warp(const Attn4Args &a, const CUtensorM
             if (p >= a.sink && p < he && ((okb >> (t >> 1)) & 1u))
                 atomicAdd(a.mass + (((size_t)b * a.n_kv + h) * a.max_pages << sh) + p, add);
         } else {
-            // raise the running maximum, or the bound on the value scales, when a block passes it
-            float top0 = fmaxf(fmaxf(s[0][0][0], s[0][1][0]), fmaxf(s[1][0][0], s[1][1][0]));
-            float top1 = fmaxf(fmaxf(s[0][0][1], s[0][1][1]), fmaxf(s[1][0][1], s[1][1][1]));
-            __nv_bfloat162 vs2 = as_bf2(vw[0][0][0]);        // scales in the low halves (never negative)
+            // Raise the running maximum when a block passes it, change the scaling when a p·s might pass f16's range:
+            // looked at only where the lane's largest logit with its largest scale would, rows apart or not.  log2 s
+            // is at most 0.09 above its exponent and fraction read as one number, bits/128 - 127.
+            float top[2], far[2];
+            __nv_bfloat162 v2 = as_bf2(vw[0][0][0]);                     // scales in the low halves (never negative)
 #pragma unroll
             for (int u = 0; u < 4; ++u)
 #pragma unroll
-                for (int k = 0; k < NG; ++k) vs2 = __hmax2(vs2, as_bf2(vw[u >> 1][u & 1][k]));
-            const float vs = fmaxf(lo16(as_u32(vs2)), 0.f);
-            if (__any_sync(0xffffffffu, top0 > cs.m[0] + kSlack || top1 > cs.m[1] + kSlack || vs > vmax)) {
-                const float m0 = fmaxf(cs.m[0], col_max(top0)), m1 = fmaxf(cs.m[1], col_max(top1));
-                const float al0 = ex2_approx(cs.m[0] - m0), al1 = ex2_approx(cs.m[1] - m1);
-                cs.m[0] = m0;
-                cs.m[1] = m1;
-                cs.l[0] *= al0;
-                cs.l[1] *= al1;
+                for (int k = 0; k < NG; ++k) v2 = __hmax2(v2, as_bf2(vw[u >> 1][u & 1][k]));
+            const float bits = __uint_as_float(__byte_perm(as_u32(v2), 0x4B000000u, 0x7610));       // 2^23 + the scale's 16 bits
 #pragma unroll
-                for (int k = 0; k < NG; ++k) {
-                    zs[k][0] *= al0;
-                    zs[k][1] *= al1;
-                }
-                const uint32_t vb = __reduce_max_sync(0xffffffffu, __float_as_uint(vs));
-                float down = 1.f;
-                if (__uint_as_float(vb) > vmax) {
-                    const float old = vmax > 0.f ? vinv : INFINITY;      // nothing but zeros was summed before
-                    set_value_bound(vb, vmax, vinv);
-                    down = vinv / old;                                   // a power of two
+            for (int j = 0; j < 2; ++j) {
+                top[j] = fmaxf(fmaxf(s[0][0][j], s[0][1][j]), fmaxf(s[1][0][j], s[1][1][j]));
+                far[j] = fmaf(bits, 0x1p-7f, top[j]);                    // 2^16 + 127 + log2(scale) + logit
+            }
+            if (__any_sync(0xffffffffu, top[0] > cs.m[0] + kSlack || top[1] > cs.m[1] + kSlack || far[0] > most[0] || far[1] > most[1])) {
+                float f[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const float m = fmaxf(cs.m[j], col_max(top[j])), al = ex2_approx(cs.m[j] - m);
+                    // what was summed shrinks by al, so the scaling may grow by as much (by 2^100 at most)
+                    const float up = __uint_as_float((uint32_t)(__float2int_rn(fminf(m - cs.m[j], 100.f)) + 127) << 23), old = vinv[j];
+                    cs.m[j] = m;
+                    cs.l[j] *= al;
+#pragma unroll
+                    for (int k = 0; k < NG; ++k) zs[k][j] *= al;
+                    float x = 0.f;
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+#pragma unroll
+                        for (int k = 0; k < NG; ++k) x = fmaxf(x, ex2_approx(s[u >> 1][u & 1][j] - m) * lo16(vw[u >> 1][u & 1][k]));
+                    x = col_max(x);
+                    vinv[j] = fminf(old * up, kPMost);
+                    if (x * vinv[j] > 0x1p14f) vinv[j] = scaling(x);
+                    f[j] = al * (vinv[j] / old);                         // both powers of two
+                    most[j] = logit_limit(m, vinv[j]);
                 }
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[c][j][e] *= (e & 1 ? al1 : al0) * down;
+                        for (int e = 0; e < 4; ++e) acc[c][j][e] *= f[e & 1];
             }
 #pragma unroll
             for (int tl = 0; tl < 2; ++tl) {
-                uint32_t bp[NG][2];
+                float w[2][2];                               // p·vinv of rows g and g + 8
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const float q0 = ex2_approx(s[tl][r][0] - cs.m[0]), q1 = ex2_approx(s[tl][r][1] - cs.m[1]);
-                    const float w0 = q0 * vinv, w1 = q1 * vinv;
-                    cs.l[0] += q0;
-                    cs.l[1] += q1;
+                for (int r = 0; r < 2; ++r)
 #pragma unroll
-                    for (int k = 0; k < NG; ++k) {
-                        const float v = lo16(vw[tl][r][k]), z = hi16(vw[tl][r][k]);
-                        zs[k][0] = fmaf(q0, z, zs[k][0]);
-                        zs[k][1] = fmaf(q1, z, zs[k][1]);
-                        bp[k][r] = movmatrix_trans(pack_h2(w0 * v, w1 * v));
+                    for (int j = 0; j < 2; ++j) {
+                        const float p = ex2_approx(s[tl][r][j] - cs.m[j]);
+                        cs.l[j] += p;
+#pragma unroll
+                        for (int k = 0; k < NG; ++k) zs[k][j] = fmaf(p, hi16(vw[tl][r][k]), zs[k][j]);
+                        w[r][j] = p * vinv[j];
                     }
-                }
+                uint32_t bp[2][2], bl[2][2];                 // B operands of channels 32 c .. and 32 (c + 1) ..
                 const int row = tl * 16 + (lane & 15);
 #pragma unroll
                 for (int c = 0; c < 4; c += 2) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int k = (c + i) * NG / 4;
+                        if ((c + i) * NG % 4) {                  // the group of the 32 channels before
+                            if (i) for (int r = 0; r < 2; ++r) bp[1][r] = bp[0][r], bl[1][r] = bl[0][r];
+                            continue;
+                        }
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            const float v = lo16(vw[tl][r][k]), y0 = w[r][0] * v, y1 = w[r][1] * v, h0 = high_part(y0), h1 = high_part(y1);
+                            if (G <= 4) {
+                                bp[i][r] = movmatrix_trans(pack_h2(lower ? y0 - h0 : h0, lower ? y1 - h1 : h1));
+                            } else {
+                                bp[i][r] = movmatrix_trans(pack_h2(h0, h1));
+                                bl[i][r] = movmatrix_trans(pack_h2(y0 - h0, y1 - h1));
+                            }
+                        }
+                    }
                     uint32_t r0, r1, r2, r3;
                     ldmatrix_x4_trans(sb + 2048 + row * 64 + (((c + (lane >> 4)) ^ ((row >> 1) & 3)) << 4), r0, r1, r2, r3);
-                    const int k0 = c * NG / 4, k1 = (c + 1) * NG / 4;
-                    mma16816_nv(acc[c][0], r0 & kM0, r0 & kM1, r1 & kM0, r1 & kM1, bp[k0][0], bp[k0][1]);
-                    mma16816_nv(acc[c + 1][0], r2 & kM0, r2 & kM1, r3 & kM0, r3 & kM1, bp[k1][0], bp[k1][1]);
-                    r0 >>= 8; r1 >>= 8; r2 >>= 8; r3 >>= 8;
-                    mma16816_nv(acc[c][1], r0 & kM0, r0 & kM1, r1 & kM0, r1 & kM1, bp[k0][0], bp[k0][1]);
-                    mma16816_nv(acc[c + 1][1], r2 & kM0, r2 & kM1, r3 & kM0, r3 & kM1, bp[k1][0], bp[k1][1]);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        mma16816_nv(acc[c][j], r0 & kM0, r0 & kM1, r1 & kM0, r1 & kM1, bp[0][0], bp[0][1]);
+                        mma16816_nv(acc[c + 1][j], r2 & kM0, r2 & kM1, r3 & kM0, r3 & kM1, bp[1][0], bp[1][1]);
+                        if (G > 4) {
+                            mma16816_nv(acc[c][j], r0 & kM0, r0 & kM1, r1 & kM0, r1 & kM1, bl[0][0], bl[0][1]);
+                            mma16816_nv(acc[c + 1][j], r2 & kM0, r2 & kM1, r3 & kM0, r3 & kM1, bl[1][0], bl[1][1]);
+                        }
+                        r0 >>= 8; r1 >>= 8; r2 >>= 8; r3 >>= 8;
+                    }
                 }
             }
         }
@@ -556,17 +606,20 @@ __device__ __forceinline__ void history_warp(const Attn4Args &a, const CUtensorM
             wl[warp * 8 + 2 * t + j] = cs.l[j];
         }
     }
-    const float up = 1.f / vinv;                     // a power of two
 #pragma unroll
     for (int c = 0; c < 4; ++c)
 #pragma unroll
-        for (int e = 0; e < 2; ++e)                  // head 2 t + e, channels 32 c + 4 g .. + 3
-            if (2 * t + e < G) {
-                const float z = zs[c * NG / 4][e];
-                *reinterpret_cast<float4 *>(wa + (2 * t + e) * kResRow + 32 * c + 4 * g) =
-                    make_float4(acc[c][0][e] * 0x1p24f * up + z, acc[c][0][2 + e] * 0x1p20f * up + z, acc[c][1][e] * 0x1p24f * up + z,
-                                acc[c][1][2 + e] * 0x1p20f * up + z);
+        for (int e = 0; e < 2; ++e) {                // head 2 t + e, channels 32 c + 4 g .. + 3
+            const float up = 1.f / vinv[e], z = zs[c * NG / 4][e];
+            float x[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[i] = acc[c][i >> 1][2 * (i & 1) + e] * (i & 1 ? 0x1p20f : 0x1p24f) * up;
+                if (G <= 4) x[i] += __shfl_xor_sync(0xffffffffu, x[i], 2);       // the upper parts' sum and the lower ones'
             }
+            if (2 * t + e < G)
+                *reinterpret_cast<float4 *>(wa + (2 * t + e) * kResRow + 32 * c + 4 * g) = make_float4(x[0] + z, x[1] + z, x[2] + z, x[3] + z);
+        }
 }
 
 // One channel of a merged row: sum A over weight L, maximum M (oscar_merge's last steps).

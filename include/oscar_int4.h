@@ -115,7 +115,8 @@ OSCAR_API int32_t oscar_suggest_splits_int4(const oscar_layout_t *layout, int32_
  * Writes every slot of `partials`: the history is cut into S splits of whole 32-token blocks (at absolute
  * positions 32 i), the BF16 rows are dealt out to the same splits, slot S is written empty.  With out or
  * out_f32 non-NULL also their merge, as oscar_merge(R_V = NULL) defines it, lse optional.  Query products and softmax sums are fp32 or finer;
- * a probability times its value scale is rounded to fp16 (2^-11 relative) for the value product.
+ * a probability times its value scale enters the value product in two fp16 parts: 2^-21 relative, or 2^-30 of the
+ * largest such product.
  *   merge_counters  NULL: the merge is a second launch.  Else int32 [batch·n_kv_heads], all zero, left
  *                   zero: the last CTA of a request's kv head to finish merges it, in the same launch
  *                   and in slot order whichever CTA that is.  Calls that may run concurrently must
