@@ -448,17 +448,6 @@ def _native():
     return _marshal
 
 
-def _layout_at(layout: Layout) -> int:
-    """The address of the layout's descriptor, built once (a Layout does not change)."""
-    at = layout.__dict__.get("_at")
-    if at is None:
-        c = layout.c()
-        object.__setattr__(layout, "_c", c)
-        at = ctypes.addressof(c)
-        object.__setattr__(layout, "_at", at)
-    return at
-
-
 def oscar_append_kv(layout: Layout, q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, pool: Bf16Pool,
                     page_table: torch.Tensor, req_idx: torch.Tensor, positions: torch.Tensor,
                     q_out: Optional[torch.Tensor] = None, q_weight: Optional[torch.Tensor] = None,
@@ -467,7 +456,7 @@ def oscar_append_kv(layout: Layout, q: Optional[torch.Tensor], k: torch.Tensor, 
                     stream=None):
     """New tokens' heads (q [n, Hq, D], k and v [n, Hkv, D] bf16, token rows possibly strided): RMS norm per head,
     rotary position, q to q_out and k, v to the tokens' slots of the BF16 pool."""
-    _native().append_kv(_layout_at(layout), q, k, v, pool, page_table, req_idx, positions, q_out, q_weight, k_weight, eps,
+    _native().append_kv(layout, q, k, v, pool, page_table, req_idx, positions, q_out, q_weight, k_weight, eps,
                         rope, rot_dim, interleaved, rope_positions, stream)
 
 
@@ -475,14 +464,14 @@ def oscar_demote_int4(layout: Layout, src: Bf16Pool, bf16_page_table: torch.Tens
                       int4_page_table: torch.Tensor, pos_begin: torch.Tensor, pos_end: torch.Tensor, c_K: float = 1.0,
                       c_V: float = 1.0, stream=None):
     """BF16 rows at positions [pos_begin[b], pos_end[b]) (int32 [batch]) to 4 bits, as they are stored."""
-    _native().demote_int4(_layout_at(layout), src, bf16_page_table, dst, int4_page_table, pos_begin, pos_end, c_K, c_V,
+    _native().demote_int4(layout, src, bf16_page_table, dst, int4_page_table, pos_begin, pos_end, c_K, c_V,
                           stream)
 
 
 def oscar_promote_int4(layout: Layout, src: Int4Pool, int4_page_table: torch.Tensor, dst: Bf16Pool,
                        bf16_page_table: torch.Tensor, pos_begin: torch.Tensor, pos_end: torch.Tensor, stream=None):
     """4-bit rows at positions [pos_begin[b], pos_end[b]) back to BF16."""
-    _native().promote_int4(_layout_at(layout), src, int4_page_table, dst, bf16_page_table, pos_begin, pos_end, stream)
+    _native().promote_int4(layout, src, int4_page_table, dst, bf16_page_table, pos_begin, pos_end, stream)
 
 
 def oscar_suggest_splits_int4(layout: Layout, batch: int, max_hist_tokens: int, sm_count: int) -> int:
@@ -497,7 +486,7 @@ def oscar_decode_attention_int4(layout: Layout, q: torch.Tensor, bf16_pool: Bf16
                                 stream=None):
     """Decode attention over [BF16 sink | INT4 history | BF16 recent]; with out or out_f32 also the merge, in the same
     launch when merge_counters (int32 zeros [batch * n_kv_heads]) is given."""
-    _native().decode_attention_int4(_layout_at(layout), q, bf16_pool, bf16_page_table, int4_pool, int4_page_table, seq_len,
+    _native().decode_attention_int4(layout, q, bf16_pool, bf16_page_table, int4_pool, int4_page_table, seq_len,
                                     hist_end, sm_scale, partials, out, out_f32, lse, merge_counters, stream)
 
 
@@ -506,7 +495,7 @@ def oscar_attention_mass_int4(layout: Layout, q: torch.Tensor, bf16_pool: Bf16Po
                               hist_end: torch.Tensor, sm_scale: float, lse: torch.Tensor, mass: torch.Tensor,
                               stream=None):
     """Add the attention weight of this step to mass [batch, Hkv, max_pages * page_size] (fp32)."""
-    _native().attention_mass_int4(_layout_at(layout), q, bf16_pool, bf16_page_table, int4_pool, int4_page_table, seq_len,
+    _native().attention_mass_int4(layout, q, bf16_pool, bf16_page_table, int4_pool, int4_page_table, seq_len,
                                   hist_end, sm_scale, lse, mass, stream)
 
 
@@ -515,7 +504,7 @@ def oscar_evict_int4(layout: Layout, src: Int4Pool, src_page_table: torch.Tensor
                      mass: torch.Tensor, mass_out: torch.Tensor, kept: torch.Tensor, stream=None):
     """Keep the keep[b] history positions of largest mass of each kv head; their rows go to the pages of
     dst_page_table, their old positions to kept [batch, Hkv, at least max(keep)] (int32)."""
-    _native().evict_int4(_layout_at(layout), src, src_page_table, dst, dst_page_table, seq_len, hist_end, keep, mass,
+    _native().evict_int4(layout, src, src_page_table, dst, dst_page_table, seq_len, hist_end, keep, mass,
                          mass_out, kept, stream)
 
 

@@ -21,6 +21,7 @@ namespace {
 
 PyObject *g_error = nullptr;                 // OscarError
 PyObject *s_k, *s_v, *s_codes_k, *s_codes_v, *s_scale_zero, *s_m, *s_l, *s_acc, *s_n_splits, *s_device, *s_index, *s_cuda_stream;
+PyObject *s_head_dim, *s_n_kv_heads, *s_gqa, *s_page_size, *s_group, *s_sink, *s_recent, *s_levels_k, *s_levels_v;
 
 struct Refused : std::exception {};          // a Python error is set
 
@@ -45,6 +46,56 @@ const char *dtype_text(at::ScalarType t) {
 }
 
 using Shape = std::initializer_list<int64_t>;
+
+struct Attr {                                // an attribute, held while its address is used
+    PyObject *o;
+    Attr(PyObject *from, PyObject *name) : o(PyObject_GetAttr(from, name)) {
+        if (!o) throw Refused();
+    }
+    ~Attr() { Py_DECREF(o); }
+    Attr(const Attr &) = delete;
+};
+double real(PyObject *o) {
+    const double x = PyFloat_AsDouble(o);
+    if (x == -1.0 && PyErr_Occurred()) throw Refused();
+    return x;
+}
+int32_t whole(PyObject *o) {
+    const long x = PyLong_AsLong(o);
+    if (x == -1 && PyErr_Occurred()) throw Refused();
+    if (x != (int32_t)x) refuse("an integer argument passes 32 bits");
+    return (int32_t)x;
+}
+
+// The fields of a Layout, read on every call: an object that is copied, sent to another process or used by
+// several threads holds nothing of this extension.
+oscar_layout_t layout(PyObject *o) {
+    oscar_layout_t L = {};
+    const auto field = [&](PyObject *name) { return whole(Attr(o, name).o); };
+    L.head_dim = field(s_head_dim);
+    L.n_kv_heads = field(s_n_kv_heads);
+    L.gqa = field(s_gqa);
+    L.page_size = field(s_page_size);
+    L.group = field(s_group);
+    L.sink = field(s_sink);
+    L.recent = field(s_recent);
+    const Attr k(o, s_levels_k), v(o, s_levels_v);
+    if (k.o == Py_None && v.o == Py_None) return L;
+    const auto levels = [](PyObject *from, float *to) {
+        if (!PySequence_Check(from) || PySequence_Size(from) != 4) refuse("a layout's levels are 4 numbers for keys and 4 for values, or None");
+        for (int i = 0; i < 4; ++i) {
+            PyObject *x = PySequence_GetItem(from, i);
+            if (!x) throw Refused();
+            const double d = PyFloat_AsDouble(x);
+            Py_DECREF(x);
+            if (d == -1.0 && PyErr_Occurred()) throw Refused();
+            to[i] = (float)d;
+        }
+    };
+    levels(k.o, L.levels_k);
+    levels(v.o, L.levels_v);
+    return L;
+}
 
 struct Call {
     std::string name;
@@ -85,14 +136,6 @@ struct Call {
         *stride = n > 1 ? t.stride(0) : heads * 128;
         return static_cast<const uint16_t *>(t.data_ptr());
     }
-    struct Attr {                            // an attribute, held while its address is used
-        PyObject *o;
-        Attr(PyObject *from, PyObject *name) : o(PyObject_GetAttr(from, name)) {
-            if (!o) throw Refused();
-        }
-        ~Attr() { Py_DECREF(o); }
-        Attr(const Attr &) = delete;
-    };
     oscar_bf16_pool_t bf16(const oscar_layout_t *L, PyObject *pool) const {
         const Attr k(pool, s_k), v(pool, s_v);
         const at::Tensor &t = tensor("pool k", k.o);
@@ -126,22 +169,6 @@ struct Call {
         if (PyErr_Occurred()) throw Refused();
         return p;
     }
-    static double real(PyObject *o) {
-        const double x = PyFloat_AsDouble(o);
-        if (x == -1.0 && PyErr_Occurred()) throw Refused();
-        return x;
-    }
-    static int32_t whole(PyObject *o) {
-        const long x = PyLong_AsLong(o);
-        if (x == -1 && PyErr_Occurred()) throw Refused();
-        if (x != (int32_t)x) refuse("an integer argument passes 32 bits");
-        return (int32_t)x;
-    }
-    static const oscar_layout_t *layout(PyObject *o) {
-        void *p = PyLong_AsVoidPtr(o);
-        if (!p) throw Refused();
-        return static_cast<const oscar_layout_t *>(p);
-    }
     int32_t pages32(int64_t n) const {
         if (n > 2147483647) refuse(name + ": more than 2^31 - 1 pages or requests");
         return (int32_t)n;
@@ -163,8 +190,8 @@ struct Call {
 // layout, q, k, v, pool, page_table, req_idx, positions, q_out, q_weight, k_weight, eps, rope, rot_dim, interleaved,
 // rope_positions, stream
 void append_kv(PyObject *const *a) {
+    const oscar_layout_t layout_ = layout(a[0]), *L = &layout_;
     const Call c("oscar_append_kv");
-    const oscar_layout_t *L = Call::layout(a[0]);
     const int64_t H = L->n_kv_heads, Hq = H * L->gqa;
     const at::Tensor &k = c.tensor("k", a[2]);
     const int64_t n = k.dim() ? k.size(0) : 0;
@@ -184,8 +211,8 @@ void append_kv(PyObject *const *a) {
     const float *rope = c.at<float>("rope", a[12], at::kFloat, {rows, 128});
     const int turn = PyObject_IsTrue(a[14]);
     if (turn < 0) throw Refused();
-    const int32_t *rp = c.ints("rope_positions", a[15], n), rot = Call::whole(a[13]);
-    const float eps = (float)Call::real(a[11]);
+    const int32_t *rp = c.ints("rope_positions", a[15], n), rot = whole(a[13]);
+    const float eps = (float)real(a[11]);
     void *st = c.stream(a[16]);
     c.done(OFF_GIL(oscar_append_kv(L, qp, qs, kp, ks, vp, vs, c.pages32(n), wq, wk, eps, rope, (int32_t)std::min<int64_t>(rows, 2147483647),
                                    rot, turn, &pool, pt, c.pages32(max_pages), c.pages32(batch), req, pos, rp, qo, st)));
@@ -193,23 +220,23 @@ void append_kv(PyObject *const *a) {
 
 // layout, src, bf16_page_table, dst, int4_page_table, pos_begin, pos_end, c_K, c_V, stream
 void demote_int4(PyObject *const *a) {
+    const oscar_layout_t layout_ = layout(a[0]), *L = &layout_;
     const Call c("oscar_demote_int4");
-    const oscar_layout_t *L = Call::layout(a[0]);
     int64_t batch, max_pages;
     c.table(a[4], &batch, &max_pages);
     const oscar_bf16_pool_t src = c.bf16(L, a[1]);
     const oscar_int4_pool_t dst = c.int4(L, a[3]);
     const int32_t *bpt = c.pages("bf16_page_table", a[2], batch, max_pages), *ipt = c.pages("int4_page_table", a[4], batch, max_pages);
     const int32_t *lo = c.ints("pos_begin", a[5], batch), *hi = c.ints("pos_end", a[6], batch);
-    const float ck = (float)Call::real(a[7]), cv = (float)Call::real(a[8]);
+    const float ck = (float)real(a[7]), cv = (float)real(a[8]);
     void *st = c.stream(a[9]);
     c.done(OFF_GIL(oscar_demote_int4(L, &src, bpt, &dst, ipt, c.pages32(max_pages), c.pages32(batch), lo, hi, ck, cv, st)));
 }
 
 // layout, src, int4_page_table, dst, bf16_page_table, pos_begin, pos_end, stream
 void promote_int4(PyObject *const *a) {
+    const oscar_layout_t layout_ = layout(a[0]), *L = &layout_;
     const Call c("oscar_promote_int4");
-    const oscar_layout_t *L = Call::layout(a[0]);
     int64_t batch, max_pages;
     c.table(a[2], &batch, &max_pages);
     const oscar_int4_pool_t src = c.int4(L, a[1]);
@@ -223,14 +250,18 @@ void promote_int4(PyObject *const *a) {
 // what decode attention and the attention weights share: layout, q, bf16_pool, bf16_page_table, int4_pool,
 // int4_page_table, seq_len, hist_end, sm_scale
 struct Attention {
-    const oscar_layout_t *L;
+    oscar_layout_t layout_;
+    const oscar_layout_t *L = &layout_;
     int64_t batch, max_pages, Hq;
     const uint16_t *q;
     oscar_bf16_pool_t bf;
     oscar_int4_pool_t i4;
     const int32_t *bpt, *ipt, *T, *he;
     float scale;
-    Attention(const Call &c, PyObject *const *a) : L(Call::layout(a[0])) {
+    const Call call;
+    Attention(const Attention &) = delete;
+    Attention(const char *name, PyObject *const *a) : layout_(layout(a[0])), call(name) {
+        const Call &c = call;
         c.table(a[5], &batch, &max_pages);
         Hq = (int64_t)L->n_kv_heads * L->gqa;
         q = c.at<uint16_t>("q", a[1], at::kBFloat16, {batch, Hq, 128});
@@ -240,16 +271,16 @@ struct Attention {
         ipt = c.pages("int4_page_table", a[5], batch, max_pages);
         T = c.ints("seq_len", a[6], batch);
         he = c.ints("hist_end", a[7], batch);
-        scale = (float)Call::real(a[8]);
+        scale = (float)real(a[8]);
     }
 };
 
 // ..., partials, out, out_f32, lse, merge_counters, stream
 void decode_attention_int4(PyObject *const *a) {
-    const Call c("oscar_decode_attention_int4");
-    const Attention x(c, a);
-    const Call::Attr m(a[9], s_m), l(a[9], s_l), acc(a[9], s_acc), ns(a[9], s_n_splits);
-    const int32_t S = Call::whole(ns.o);
+    const Attention x("oscar_decode_attention_int4", a);
+    const Call &c = x.call;
+    const Attr m(a[9], s_m), l(a[9], s_l), acc(a[9], s_acc), ns(a[9], s_n_splits);
+    const int32_t S = whole(ns.o);
     const int64_t S1 = (int64_t)S + 1;
     const oscar_partials_t part{c.at<float>("partials m", m.o, at::kFloat, {x.batch, x.Hq, S1}), c.at<float>("partials l", l.o, at::kFloat, {x.batch, x.Hq, S1}),
                                 c.at<float>("partials acc", acc.o, at::kFloat, {x.batch, x.Hq, S1, 128}), S};
@@ -263,8 +294,8 @@ void decode_attention_int4(PyObject *const *a) {
 
 // ..., lse, mass, stream
 void attention_mass_int4(PyObject *const *a) {
-    const Call c("oscar_attention_mass_int4");
-    const Attention x(c, a);
+    const Attention x("oscar_attention_mass_int4", a);
+    const Call &c = x.call;
     const float *lse = c.at<float>("lse", a[9], at::kFloat, {x.batch, x.Hq});
     float *mass = c.at<float>("mass", a[10], at::kFloat, {x.batch, x.L->n_kv_heads, x.max_pages * x.L->page_size});
     void *st = c.stream(a[11]);
@@ -274,8 +305,8 @@ void attention_mass_int4(PyObject *const *a) {
 
 // layout, src, src_page_table, dst, dst_page_table, seq_len, hist_end, keep, mass, mass_out, kept, stream
 void evict_int4(PyObject *const *a) {
+    const oscar_layout_t layout_ = layout(a[0]), *L = &layout_;
     const Call c("oscar_evict_int4");
-    const oscar_layout_t *L = Call::layout(a[0]);
     int64_t batch, max_pages;
     c.table(a[2], &batch, &max_pages);
     const oscar_int4_pool_t src = c.int4(L, a[1]), dst = c.int4(L, a[3]);
@@ -322,7 +353,9 @@ PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_marshal", "Argument checks of t
 PyMODINIT_FUNC PyInit__marshal(void) {
     struct { PyObject **to; const char *text; } names[] = {
         {&s_k, "k"}, {&s_v, "v"}, {&s_codes_k, "codes_k"}, {&s_codes_v, "codes_v"}, {&s_scale_zero, "scale_zero"}, {&s_m, "m"}, {&s_l, "l"},
-        {&s_acc, "acc"}, {&s_n_splits, "n_splits"}, {&s_device, "device"}, {&s_index, "index"}, {&s_cuda_stream, "cuda_stream"}};
+        {&s_acc, "acc"}, {&s_n_splits, "n_splits"}, {&s_device, "device"}, {&s_index, "index"}, {&s_cuda_stream, "cuda_stream"},
+        {&s_head_dim, "head_dim"}, {&s_n_kv_heads, "n_kv_heads"}, {&s_gqa, "gqa"}, {&s_page_size, "page_size"}, {&s_group, "group"},
+        {&s_sink, "sink"}, {&s_recent, "recent"}, {&s_levels_k, "levels_k"}, {&s_levels_v, "levels_v"}};
     for (auto &n : names)
         if (!(*n.to = PyUnicode_InternFromString(n.text))) return nullptr;
     PyObject *m = PyModule_Create(&g_module);
