@@ -440,11 +440,11 @@ def _native():
         path = os.path.join(_PKG, "_marshal.so")
         if not os.path.exists(path):
             raise OscarError(f"{path} is missing: build it with __graft_entry__.build()")
-        lib()                                          # the library that the extension calls
         spec = importlib.util.spec_from_file_location("_marshal", path)
-        _marshal = importlib.util.module_from_spec(spec)
-        spec.loader.exec_module(_marshal)
-        _marshal.set_error(OscarError)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.connect(lib()._handle, OscarError)
+        _marshal = module                              # other threads see it once it is complete
     return _marshal
 
 

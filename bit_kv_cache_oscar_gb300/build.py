@@ -43,7 +43,15 @@ def _marshal_flags() -> tuple:
            os.path.join(root, "include", "torch", "csrc", "api", "include"), os.path.join(CUDA_HOME, "include")]
     libs = os.path.join(root, "lib")
     return (["-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={abi}"] + [f"-I{i}" for i in inc],
-            [f"-L{libs}", "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10", f"-Wl,-rpath,{libs}", LIB, "-Wl,-rpath,$ORIGIN"])
+            [f"-L{libs}", "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10", f"-Wl,-rpath,{libs}", "-ldl"])
+
+
+def _stamp(path: str, text: str) -> str:
+    """A file that holds `text` and is as old as that."""
+    if not os.path.exists(path) or open(path).read() != text:
+        with open(path, "w") as f:
+            f.write(text)
+    return path
 
 
 def build(verbose: bool = False, extra: list | None = None) -> str:
@@ -65,7 +73,9 @@ def build(verbose: bool = False, extra: list | None = None) -> str:
             procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     msrc, mobj = os.path.join(CSRC, "marshal.cpp"), os.path.join(BUILD, "marshal.o")
     mflags = _marshal_flags()
-    if _stale(mobj, [msrc, *public]):
+    import torch
+    made_with = _stamp(os.path.join(BUILD, "marshal.made_with"), repr((mflags, torch.__version__, sys.version)))
+    if _stale(mobj, [msrc, made_with, *public]):
         cmd = ["g++", *mflags[0], "-c", msrc, "-o", mobj]
         if verbose:
             print(" ".join(cmd), flush=True)
@@ -90,7 +100,7 @@ def build(verbose: bool = False, extra: list | None = None) -> str:
             print(" ".join(cmd), flush=True)
         subprocess.check_call(cmd)
         os.replace(tmp, LIB)
-    if _stale(MARSHAL, [mobj, LIB]):
+    if _stale(MARSHAL, [mobj]):
         tmp = MARSHAL + f".tmp{os.getpid()}"
         cmd = ["g++", "-shared", "-o", tmp, mobj, *mflags[1]]
         if verbose:

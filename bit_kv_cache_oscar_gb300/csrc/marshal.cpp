@@ -1,10 +1,13 @@
 // The Python side of the INT4 entry points: every argument's type, shape and device checked, addresses,
-// strides and the current stream passed on to liboscar.so.
+// strides and the current stream passed on to liboscar.so: the one that the binding loaded, whose entry points
+// connect() looks up, since a library found by name or path could be another copy of the package.
 //
 // These calls are made once per layer and token.  Checked in Python one costs 12 to 20 us of host time, more
 // than most of the kernels it starts take at batch 1; here it costs about 1 us.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
+
+#include <dlfcn.h>
 
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
@@ -20,6 +23,16 @@
 namespace {
 
 PyObject *g_error = nullptr;                 // OscarError
+
+// liboscar.so's entry points (connect)
+#define ENTRY_POINTS(X) \
+    X(oscar_append_kv) X(oscar_demote_int4) X(oscar_promote_int4) X(oscar_decode_attention_int4) X(oscar_attention_mass_int4) X(oscar_evict_int4) \
+    X(oscar_last_error_string)
+struct {
+#define X(f) decltype(&::f) f;
+    ENTRY_POINTS(X)
+#undef X
+} g_lib;
 PyObject *s_k, *s_v, *s_codes_k, *s_codes_v, *s_scale_zero, *s_m, *s_l, *s_acc, *s_n_splits, *s_device, *s_index, *s_cuda_stream;
 PyObject *s_head_dim, *s_n_kv_heads, *s_gqa, *s_page_size, *s_group, *s_sink, *s_recent, *s_levels_k, *s_levels_v;
 
@@ -174,7 +187,7 @@ struct Call {
         return (int32_t)n;
     }
     void done(oscar_status_t st) const {
-        if (st != OSCAR_OK) refuse(name + " failed (" + std::to_string((int)st) + "): " + oscar_last_error_string());
+        if (st != OSCAR_OK) refuse(name + " failed (" + std::to_string((int)st) + "): " + g_lib.oscar_last_error_string());
     }
 };
 
@@ -214,7 +227,7 @@ void append_kv(PyObject *const *a) {
     const int32_t *rp = c.ints("rope_positions", a[15], n), rot = whole(a[13]);
     const float eps = (float)real(a[11]);
     void *st = c.stream(a[16]);
-    c.done(OFF_GIL(oscar_append_kv(L, qp, qs, kp, ks, vp, vs, c.pages32(n), wq, wk, eps, rope, (int32_t)std::min<int64_t>(rows, 2147483647),
+    c.done(OFF_GIL(g_lib.oscar_append_kv(L, qp, qs, kp, ks, vp, vs, c.pages32(n), wq, wk, eps, rope, (int32_t)std::min<int64_t>(rows, 2147483647),
                                    rot, turn, &pool, pt, c.pages32(max_pages), c.pages32(batch), req, pos, rp, qo, st)));
 }
 
@@ -230,7 +243,7 @@ void demote_int4(PyObject *const *a) {
     const int32_t *lo = c.ints("pos_begin", a[5], batch), *hi = c.ints("pos_end", a[6], batch);
     const float ck = (float)real(a[7]), cv = (float)real(a[8]);
     void *st = c.stream(a[9]);
-    c.done(OFF_GIL(oscar_demote_int4(L, &src, bpt, &dst, ipt, c.pages32(max_pages), c.pages32(batch), lo, hi, ck, cv, st)));
+    c.done(OFF_GIL(g_lib.oscar_demote_int4(L, &src, bpt, &dst, ipt, c.pages32(max_pages), c.pages32(batch), lo, hi, ck, cv, st)));
 }
 
 // layout, src, int4_page_table, dst, bf16_page_table, pos_begin, pos_end, stream
@@ -244,7 +257,7 @@ void promote_int4(PyObject *const *a) {
     const int32_t *ipt = c.pages("int4_page_table", a[2], batch, max_pages), *bpt = c.pages("bf16_page_table", a[4], batch, max_pages);
     const int32_t *lo = c.ints("pos_begin", a[5], batch), *hi = c.ints("pos_end", a[6], batch);
     void *st = c.stream(a[7]);
-    c.done(OFF_GIL(oscar_promote_int4(L, &src, ipt, &dst, bpt, c.pages32(max_pages), c.pages32(batch), lo, hi, st)));
+    c.done(OFF_GIL(g_lib.oscar_promote_int4(L, &src, ipt, &dst, bpt, c.pages32(max_pages), c.pages32(batch), lo, hi, st)));
 }
 
 // what decode attention and the attention weights share: layout, q, bf16_pool, bf16_page_table, int4_pool,
@@ -288,7 +301,7 @@ void decode_attention_int4(PyObject *const *a) {
     float *of = c.at<float>("out_f32", a[11], at::kFloat, {x.batch, x.Hq, 128}), *lse = c.at<float>("lse", a[12], at::kFloat, {x.batch, x.Hq});
     int32_t *counters = c.at<int32_t>("merge_counters", a[13], at::kInt, {x.batch * x.L->n_kv_heads});
     void *st = c.stream(a[14]);
-    c.done(OFF_GIL(oscar_decode_attention_int4(x.L, x.q, &x.bf, x.bpt, &x.i4, x.ipt, c.pages32(x.max_pages), x.T, x.he, c.pages32(x.batch), x.scale,
+    c.done(OFF_GIL(g_lib.oscar_decode_attention_int4(x.L, x.q, &x.bf, x.bpt, &x.i4, x.ipt, c.pages32(x.max_pages), x.T, x.he, c.pages32(x.batch), x.scale,
                                                &part, out, of, lse, counters, st)));
 }
 
@@ -299,7 +312,7 @@ void attention_mass_int4(PyObject *const *a) {
     const float *lse = c.at<float>("lse", a[9], at::kFloat, {x.batch, x.Hq});
     float *mass = c.at<float>("mass", a[10], at::kFloat, {x.batch, x.L->n_kv_heads, x.max_pages * x.L->page_size});
     void *st = c.stream(a[11]);
-    c.done(OFF_GIL(oscar_attention_mass_int4(x.L, x.q, &x.bf, x.bpt, &x.i4, x.ipt, c.pages32(x.max_pages), x.T, x.he, c.pages32(x.batch), x.scale, lse,
+    c.done(OFF_GIL(g_lib.oscar_attention_mass_int4(x.L, x.q, &x.bf, x.bpt, &x.i4, x.ipt, c.pages32(x.max_pages), x.T, x.he, c.pages32(x.batch), x.scale, lse,
                                              mass, st)));
 }
 
@@ -319,7 +332,7 @@ void evict_int4(PyObject *const *a) {
     const int64_t stride = k.dim() ? k.size(k.dim() - 1) : 0;
     int32_t *kept = c.at<int32_t>("kept", a[10], at::kInt, {batch, H, stride});
     void *st = c.stream(a[11]);
-    c.done(OFF_GIL(oscar_evict_int4(L, &src, spt, &dst, dpt, c.pages32(max_pages), c.pages32(batch), T, he, keep, mass, out, kept, c.pages32(stride), st)));
+    c.done(OFF_GIL(g_lib.oscar_evict_int4(L, &src, spt, &dst, dpt, c.pages32(max_pages), c.pages32(batch), T, he, keep, mass, out, kept, c.pages32(stride), st)));
 }
 
 // Python entry: a fixed number of positional arguments; no C++ exception leaves it.
@@ -337,15 +350,24 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
     Py_RETURN_NONE;
 }
 
-// the exception class that refusals raise
-PyObject *set_error(PyObject *, PyObject *cls) {
-    Py_XSETREF(g_error, Py_NewRef(cls));
+// connect(handle of the loaded liboscar.so, the exception class that refusals raise): before any other call
+PyObject *connect(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    if (n != 2) return PyErr_Format(PyExc_TypeError, "2 arguments, not %zd", n);
+    void *lib = PyLong_AsVoidPtr(args[0]);
+    if (PyErr_Occurred()) return nullptr;
+#define X(f)                                                                                     \
+    g_lib.f = lib ? reinterpret_cast<decltype(&::f)>(dlsym(lib, #f)) : nullptr;                  \
+    if (!g_lib.f) return PyErr_Format(PyExc_ImportError, "liboscar.so has no " #f);
+    ENTRY_POINTS(X)
+#undef X
+    Py_XSETREF(g_error, Py_NewRef(args[1]));
     Py_RETURN_NONE;
 }
 
 #define ENTRY(f, n) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<f, n>)), METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {ENTRY(append_kv, 17), ENTRY(demote_int4, 10), ENTRY(promote_int4, 8), ENTRY(decode_attention_int4, 15),
-                           ENTRY(attention_mass_int4, 12), ENTRY(evict_int4, 12), {"set_error", set_error, METH_O, nullptr}, {nullptr, nullptr, 0, nullptr}};
+                           ENTRY(attention_mass_int4, 12), ENTRY(evict_int4, 12), 
+                           {"connect", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&connect)), METH_FASTCALL, nullptr}, {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_marshal", "Argument checks of the INT4 entry points.", -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
