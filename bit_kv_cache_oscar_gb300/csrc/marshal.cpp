@@ -154,7 +154,7 @@ struct Call {
         const at::Tensor &t = tensor("pool k", k.o);
         const int64_t n = t.dim() ? t.size(0) : 0;
         return {at<uint16_t>("pool k", k.o, at::kBFloat16, {n, L->page_size, L->n_kv_heads, 128}),
-                at<uint16_t>("pool v", v.o, at::kBFloat16, {n, L->page_size, L->n_kv_heads, 128}), (int32_t)n};
+                at<uint16_t>("pool v", v.o, at::kBFloat16, {n, L->page_size, L->n_kv_heads, 128}), pages32(n)};
     }
     oscar_int4_pool_t int4(const oscar_layout_t *L, PyObject *pool) const {
         const Attr k(pool, s_codes_k), v(pool, s_codes_v), z(pool, s_scale_zero);
@@ -162,7 +162,7 @@ struct Call {
         const int64_t n = t.dim() ? t.size(0) : 0, H = L->n_kv_heads, ps = L->page_size;
         if (L->group < 1) refuse(name + ": group " + std::to_string(L->group));
         return {at<uint8_t>("codes_k", k.o, at::kByte, {n, H, ps, 64}), at<uint8_t>("codes_v", v.o, at::kByte, {n, H, ps, 64}),
-                at<uint16_t>("scale_zero", z.o, at::kBFloat16, {n, H, ps, 128 / L->group, 4}), (int32_t)n};
+                at<uint16_t>("scale_zero", z.o, at::kBFloat16, {n, H, ps, 128 / L->group, 4}), pages32(n)};
     }
     // [batch, max_pages] of a page table
     void table(PyObject *o, int64_t *batch, int64_t *max_pages) const {
@@ -191,14 +191,16 @@ struct Call {
     }
 };
 
-#define OFF_GIL(x)                 \
-    [&] {                          \
-        oscar_status_t s_;         \
-        Py_BEGIN_ALLOW_THREADS     \
-        s_ = (x);                  \
-        Py_END_ALLOW_THREADS       \
-        return s_;                 \
-    }()
+// The interpreter's lock is given up for a call into the library; every argument is formed before.
+struct Unlocked {
+    PyThreadState *state = PyEval_SaveThread();
+    ~Unlocked() { PyEval_RestoreThread(state); }
+};
+template <typename F, typename... A>
+oscar_status_t unlocked(F f, A... args) {
+    const Unlocked u;
+    return f(args...);
+}
 
 // layout, q, k, v, pool, page_table, req_idx, positions, q_out, q_weight, k_weight, eps, rope, rot_dim, interleaved,
 // rope_positions, stream
@@ -227,8 +229,8 @@ void append_kv(PyObject *const *a) {
     const int32_t *rp = c.ints("rope_positions", a[15], n), rot = whole(a[13]);
     const float eps = (float)real(a[11]);
     void *st = c.stream(a[16]);
-    c.done(OFF_GIL(g_lib.oscar_append_kv(L, qp, qs, kp, ks, vp, vs, c.pages32(n), wq, wk, eps, rope, (int32_t)std::min<int64_t>(rows, 2147483647),
-                                   rot, turn, &pool, pt, c.pages32(max_pages), c.pages32(batch), req, pos, rp, qo, st)));
+    c.done(unlocked(g_lib.oscar_append_kv, L, qp, qs, kp, ks, vp, vs, c.pages32(n), wq, wk, eps, rope, (int32_t)std::min<int64_t>(rows, 2147483647),
+                                   rot, turn, &pool, pt, c.pages32(max_pages), c.pages32(batch), req, pos, rp, qo, st));
 }
 
 // layout, src, bf16_page_table, dst, int4_page_table, pos_begin, pos_end, c_K, c_V, stream
@@ -243,7 +245,7 @@ void demote_int4(PyObject *const *a) {
     const int32_t *lo = c.ints("pos_begin", a[5], batch), *hi = c.ints("pos_end", a[6], batch);
     const float ck = (float)real(a[7]), cv = (float)real(a[8]);
     void *st = c.stream(a[9]);
-    c.done(OFF_GIL(g_lib.oscar_demote_int4(L, &src, bpt, &dst, ipt, c.pages32(max_pages), c.pages32(batch), lo, hi, ck, cv, st)));
+    c.done(unlocked(g_lib.oscar_demote_int4, L, &src, bpt, &dst, ipt, c.pages32(max_pages), c.pages32(batch), lo, hi, ck, cv, st));
 }
 
 // layout, src, int4_page_table, dst, bf16_page_table, pos_begin, pos_end, stream
@@ -257,7 +259,7 @@ void promote_int4(PyObject *const *a) {
     const int32_t *ipt = c.pages("int4_page_table", a[2], batch, max_pages), *bpt = c.pages("bf16_page_table", a[4], batch, max_pages);
     const int32_t *lo = c.ints("pos_begin", a[5], batch), *hi = c.ints("pos_end", a[6], batch);
     void *st = c.stream(a[7]);
-    c.done(OFF_GIL(g_lib.oscar_promote_int4(L, &src, ipt, &dst, bpt, c.pages32(max_pages), c.pages32(batch), lo, hi, st)));
+    c.done(unlocked(g_lib.oscar_promote_int4, L, &src, ipt, &dst, bpt, c.pages32(max_pages), c.pages32(batch), lo, hi, st));
 }
 
 // what decode attention and the attention weights share: layout, q, bf16_pool, bf16_page_table, int4_pool,
@@ -301,8 +303,8 @@ void decode_attention_int4(PyObject *const *a) {
     float *of = c.at<float>("out_f32", a[11], at::kFloat, {x.batch, x.Hq, 128}), *lse = c.at<float>("lse", a[12], at::kFloat, {x.batch, x.Hq});
     int32_t *counters = c.at<int32_t>("merge_counters", a[13], at::kInt, {x.batch * x.L->n_kv_heads});
     void *st = c.stream(a[14]);
-    c.done(OFF_GIL(g_lib.oscar_decode_attention_int4(x.L, x.q, &x.bf, x.bpt, &x.i4, x.ipt, c.pages32(x.max_pages), x.T, x.he, c.pages32(x.batch), x.scale,
-                                               &part, out, of, lse, counters, st)));
+    c.done(unlocked(g_lib.oscar_decode_attention_int4, x.L, x.q, &x.bf, x.bpt, &x.i4, x.ipt, c.pages32(x.max_pages), x.T, x.he, c.pages32(x.batch), x.scale,
+                                               &part, out, of, lse, counters, st));
 }
 
 // ..., lse, mass, stream
@@ -312,8 +314,8 @@ void attention_mass_int4(PyObject *const *a) {
     const float *lse = c.at<float>("lse", a[9], at::kFloat, {x.batch, x.Hq});
     float *mass = c.at<float>("mass", a[10], at::kFloat, {x.batch, x.L->n_kv_heads, x.max_pages * x.L->page_size});
     void *st = c.stream(a[11]);
-    c.done(OFF_GIL(g_lib.oscar_attention_mass_int4(x.L, x.q, &x.bf, x.bpt, &x.i4, x.ipt, c.pages32(x.max_pages), x.T, x.he, c.pages32(x.batch), x.scale, lse,
-                                             mass, st)));
+    c.done(unlocked(g_lib.oscar_attention_mass_int4, x.L, x.q, &x.bf, x.bpt, &x.i4, x.ipt, c.pages32(x.max_pages), x.T, x.he, c.pages32(x.batch), x.scale, lse,
+                                             mass, st));
 }
 
 // layout, src, src_page_table, dst, dst_page_table, seq_len, hist_end, keep, mass, mass_out, kept, stream
@@ -332,7 +334,7 @@ void evict_int4(PyObject *const *a) {
     const int64_t stride = k.dim() ? k.size(k.dim() - 1) : 0;
     int32_t *kept = c.at<int32_t>("kept", a[10], at::kInt, {batch, H, stride});
     void *st = c.stream(a[11]);
-    c.done(OFF_GIL(g_lib.oscar_evict_int4(L, &src, spt, &dst, dpt, c.pages32(max_pages), c.pages32(batch), T, he, keep, mass, out, kept, c.pages32(stride), st)));
+    c.done(unlocked(g_lib.oscar_evict_int4, L, &src, spt, &dst, dpt, c.pages32(max_pages), c.pages32(batch), T, he, keep, mass, out, kept, c.pages32(stride), st));
 }
 
 // Python entry: a fixed number of positional arguments; no C++ exception leaves it.
