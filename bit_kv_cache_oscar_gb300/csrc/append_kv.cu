@@ -8,7 +8,7 @@
 // (one 16-byte load and store a lane), so the sum of squares is a 4-step shuffle and a rotation partner is
 // either in the lane (channels 2j, 2j+1) or rot_dim/16 lanes away.  A warp takes a run of row pairs of one
 // token, reads the token's angles once, and keeps four rows a half-warp in flight: each row's registers
-// are refilled as soon as it is computed.  Measured: 8,115 tokens of 32 query and 8 kv heads 42.9 us = 4.7 TB/s
+// are refilled as soon as it is computed.  Measured: 8,115 tokens of 32 query and 8 kv heads 43.1 us = 4.7 TB/s
 // (latency: half the issue slots are used, 16 warps an SM); one token 2.7 us a call in a stream.
 
 #include <cuda_bf16.h>
@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) append_kernel(AppendArgs a) {
     // this lane's angles: pair 4 hl + e (channels 2j, 2j + 1), or those of channels 8 hl + e of either half
     const int rl = a.rot >> 4;                                    // lanes per rotated half
     const bool turns = a.rope && 8 * hl < a.rot;
-    // channel pairs (8 hl + 2e, + 1) as fp32 pairs; lanes that do not turn get cos 1, sin 0
+    // channel pairs (8 hl + 2e, + 1) as fp32 pairs; what lanes that do not turn get of them is not used
     uint64_t cs[4], sn[4];
     {
         float c[8], z[8];
@@ -204,6 +204,19 @@ __global__ void __launch_bounds__(kWarps * 32, 2) append_kernel(AppendArgs a) {
                     unpair(fma2(y[v2][e], cs[e], mul2(z, sn[e])), p, q2);
                     o[v2][e] = pack2(p, q2);
                 }
+            if (!turns) {                                         // normalised at most, else moved as they are
+#pragma unroll
+                for (int v2 = 0; v2 < 2; ++v2) {
+                    const bool normed = (r0 + 2 * v2 < a.n_q ? a.wq : a.wk) != nullptr;
+                    const uint32_t as_read[4] = {raw[v2].x, raw[v2].y, raw[v2].z, raw[v2].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float p, q2;
+                        unpair(y[v2][e], p, q2);
+                        o[v2][e] = normed ? pack2(p, q2) : as_read[e];
+                    }
+                }
+            }
 #pragma unroll
             for (int v2 = 0; v2 < 2; ++v2) {
                 const int r = r0 + 2 * v2;
