@@ -5,11 +5,12 @@
 //   sm·(s·sum_c q_c n_c + z·sum_c q_c)
 // and an output sum_t p_t v_t = sum_t (p_t s_t) n_t + sum_t p_t z_t: both contractions meet the codes
 // themselves, so the codes are the A operand of mma.sync m16n8k16 (f16 in, fp32 accumulate) and scales
-// and zeros stay outside.  A nibble n in bits 0..3 or 4..7 of an f16 with no exponent bits is the
-// subnormal n·2^-24 or 16n·2^-24, so unpacking eight codes is one shift and four ANDs; the powers of two
+// and zeros stay outside.  A nibble n in bits 0..3, 2..5, 4..7 or 6..9 of an f16 with no exponent bits is the
+// subnormal n·2^-24 to n·2^-18, so unpacking eight codes is one or two shifts and four ANDs; the powers of two
 // go into the other operand or the result.  q is bf16 and exact in f16 after a power-of-two scaling of
-// each head.  p·s goes in as two f16 parts, 22 bits together: codes are not centred, so the zero points
-// cancel most of the sum, and with one part the output was off by up to 1e-3 of its size, half a bf16 step.
+// each head (elements down to 2^-25 of its largest).  p·s goes in as two f16 parts, 22 bits together: codes are
+// not centred, so the zero points cancel most of the sum, and what is lost of it counts hundreds of times over
+// in the output of a long history.
 // The parts are scaled by a power of two that follows the largest p·s met so far, not the largest s: a row
 // whose scale is far above the others' and whose weight is far below must not push them out of f16's range.
 // The contractions have 8 columns: the query heads of one kv head, twice for up to four heads, whose second
@@ -28,11 +29,15 @@
 // CTAs have no results to join: several CTAs an SM, so that one's start and end hide behind another's stream.
 // Every wait is bounded: one that gives up sets OSCAR_DEV_WAIT_TIMEOUT.
 //
-// Measured (passes back to back, 32 query and 8 kv heads, group 128): 100K tokens 28.5 us, of which about 14
+// Measured (passes back to back, 32 query and 8 kv heads, group 128): 100K tokens 29.3 us, of which about 14
 // stream 110 MB after a start of 7 to 10 us (lengths, page ids and the first copies of all warps at once) and
-// 5 join warps and splits; a ragged batch of 32, 64K to 100K, 504 us = 5.8 TB/s (0.85 of a copy's rate): HBM and
-// issue slots.  64 query heads and groups of 32, 4 x 131K: 168 us = 4.0 TB/s: issue slots.  With p·s in one part
-// these were 27.4, 487 and 141 us.  Weights, ragged batch of 8: 78 us = 5.2 TB/s.
+// 5 join warps and splits; a ragged batch of 32, 64K to 100K, 531 us = 5.5 TB/s (0.81 of a copy's rate): issue
+// slots and HBM.  64 query heads and groups of 32, 4 x 131K: 177 us = 3.8 TB/s: issue slots.  What the value
+// product's precision costs of that, with the bf16 outputs' distance from fp32 arithmetic: p·s in one part and
+// one running sum 27.4, 486 and 141 us, 2.0, 2.1 and 2.1e-3 of their size; two parts and one running sum 28.4, 497
+// and 168 us, 1.6, 2.0 and 3.5e-3 (the sum's truncation, twice as often for eight heads); as it is 0.56, 0.53 and
+// 0.61e-3.  Codes centred by one more operation each: 0.01, 0.17 and 0.08e-3, in 32, 605 and 192 us.  Weights, ragged
+// batch of 8: 78 us = 5.2 TB/s.
 
 #pragma once
 
@@ -49,7 +54,9 @@ namespace oscar {
 
 namespace {
 
-constexpr uint32_t kM0 = 0x000F000Fu, kM1 = 0x00F000F0u;
+constexpr uint32_t kM0 = 0x000F000Fu, kM1 = 0x00F000F0u;                         // keys: codes n as n·2^-24 and 16n·2^-24
+constexpr uint32_t kV0 = 0x003C003Cu, kV1 = 0x03C003C0u;                         // values: n·2^-22 and n·2^-18
+constexpr float kVScale0 = 0x1p-22f, kVScale1 = 0x1p-18f;
 constexpr int kResRow = kHeadDim + 4;           // floats of a result row: heads 2 t, t = 0..3, in different banks
 constexpr float kNone = -1e30f;                  // running maximum before the first token
 constexpr float kSlack = 8.f;                    // logits (base 2) may pass the running maximum by this
@@ -83,6 +90,13 @@ __device__ __forceinline__ uint32_t pack_b2(float a, float b) {
 template <int G>
 __device__ __forceinline__ int column_head(int c) { return G <= 4 ? c & 3 : c; }
 __device__ __forceinline__ float high_part(float x) { return __uint_as_float(__float_as_uint(x) & kHighPart); }
+__device__ __forceinline__ void add4(float (&a)[4], const float (&d)[4]) {       // in packed pairs
+#pragma unroll
+    for (int i = 0; i < 4; i += 2)
+        asm("{\n.reg .b64 x, y;\nmov.b64 x, {%0, %1};\nmov.b64 y, {%2, %3};\nadd.rn.f32x2 x, x, y;\nmov.b64 {%0, %1}, x;\n}"
+            : "+f"(a[i]), "+f"(a[i + 1])
+            : "f"(d[i]), "f"(d[i + 1]));
+}
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
     uint32_t d;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
@@ -277,7 +291,7 @@ __device__ __forceinline__ void window_tiles(const Attn4Args &a, const Window &w
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) out[c][j][e] *= vinv[e & 1] * (e >> 1 ? 0x1p-20f : 0x1p-24f);
+            for (int e = 0; e < 4; ++e) out[c][j][e] *= vinv[e & 1] * (e >> 1 ? kVScale1 : kVScale0);
 }
 
 // ---- the history -------------------------------------------------------------------------------
@@ -532,53 +546,60 @@ __device__ __forceinline__ void history_warp(const Attn4Args &a, const CUtensorM
 #pragma unroll
                         for (int e = 0; e < 4; ++e) acc[c][j][e] *= f[e & 1];
             }
+            float w[4][2], z4[NG][2];                            // p·vinv of rows g, g + 8 of both tiles; the zeros' part of the block
 #pragma unroll
-            for (int tl = 0; tl < 2; ++tl) {
-                float w[2][2];                               // p·vinv of rows g and g + 8
+            for (int u = 0; u < 4; ++u)
 #pragma unroll
-                for (int r = 0; r < 2; ++r)
+                for (int j = 0; j < 2; ++j) {
+                    const float p = ex2_approx(s[u >> 1][u & 1][j] - cs.m[j]);
+                    cs.l[j] += p;
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const float p = ex2_approx(s[tl][r][j] - cs.m[j]);
-                        cs.l[j] += p;
-#pragma unroll
-                        for (int k = 0; k < NG; ++k) zs[k][j] = fmaf(p, hi16(vw[tl][r][k]), zs[k][j]);
-                        w[r][j] = p * vinv[j];
+                    for (int k = 0; k < NG; ++k) {
+                        const float z = hi16(vw[u >> 1][u & 1][k]);
+                        z4[k][j] = u ? fmaf(p, z, z4[k][j]) : p * z;
                     }
-                uint32_t bp[2][2], bl[2][2];                 // B operands of channels 32 c .. and 32 (c + 1) ..
-                const int row = tl * 16 + (lane & 15);
+                    w[u][j] = p * vinv[j];
+                }
 #pragma unroll
-                for (int c = 0; c < 4; c += 2) {
+            for (int k = 0; k < NG; ++k)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int k = (c + i) * NG / 4;
-                        if ((c + i) * NG % 4) {                  // the group of the 32 channels before
-                            if (i) for (int r = 0; r < 2; ++r) bp[1][r] = bp[0][r], bl[1][r] = bl[0][r];
-                            continue;
-                        }
+                for (int j = 0; j < 2; ++j) zs[k][j] += z4[k][j];
+            // 32 channels at a time.  A block's products are summed on their own, then added: the tensor cores truncate
+            // their sums, and a running one of codes that are never negative would drift by a bit each time.  Products
+            // keep 25 bits below the largest one's exponents, for which a subnormal's is 2^-14: codes are moved up, to
+            // 2^-22 and 2^-18 a unit, so that weights 2^-7 and 2^-11 of their tile's largest still lose nothing.
+            uint32_t bp[4], bl[4], vc[2][4];
 #pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            const float v = lo16(vw[tl][r][k]), y0 = w[r][0] * v, y1 = w[r][1] * v, h0 = high_part(y0), h1 = high_part(y1);
-                            if (G <= 4) {
-                                bp[i][r] = movmatrix_trans(pack_h2(lower ? y0 - h0 : h0, lower ? y1 - h1 : h1));
-                            } else {
-                                bp[i][r] = movmatrix_trans(pack_h2(h0, h1));
-                                bl[i][r] = movmatrix_trans(pack_h2(y0 - h0, y1 - h1));
-                            }
+            for (int c = 0; c < 4; ++c) {
+                if (c % 2 == 0)
+#pragma unroll
+                    for (int tl = 0; tl < 2; ++tl) {
+                        const int row = tl * 16 + (lane & 15);
+                        ldmatrix_x4_trans(sb + 2048 + row * 64 + (((c + (lane >> 4)) ^ ((row >> 1) & 3)) << 4), vc[tl][0], vc[tl][1], vc[tl][2],
+                                          vc[tl][3]);
+                    }
+                const int k = c * NG / 4;
+                if (c * NG % 4 == 0)                             // a new group
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const float v = lo16(vw[u >> 1][u & 1][k]), y0 = w[u][0] * v, y1 = w[u][1] * v, h0 = high_part(y0), h1 = high_part(y1);
+                        if (G <= 4) {
+                            bp[u] = movmatrix_trans(pack_h2(lower ? y0 - h0 : h0, lower ? y1 - h1 : h1));
+                        } else {
+                            bp[u] = movmatrix_trans(pack_h2(h0, h1));
+                            bl[u] = movmatrix_trans(pack_h2(y0 - h0, y1 - h1));
                         }
                     }
-                    uint32_t r0, r1, r2, r3;
-                    ldmatrix_x4_trans(sb + 2048 + row * 64 + (((c + (lane >> 4)) ^ ((row >> 1) & 3)) << 4), r0, r1, r2, r3);
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        mma16816_nv(acc[c][j], r0 & kM0, r0 & kM1, r1 & kM0, r1 & kM1, bp[0][0], bp[0][1]);
-                        mma16816_nv(acc[c + 1][j], r2 & kM0, r2 & kM1, r3 & kM0, r3 & kM1, bp[1][0], bp[1][1]);
-                        if (G > 4) {
-                            mma16816_nv(acc[c][j], r0 & kM0, r0 & kM1, r1 & kM0, r1 & kM1, bl[0][0], bl[0][1]);
-                            mma16816_nv(acc[c + 1][j], r2 & kM0, r2 & kM1, r3 & kM0, r3 & kM1, bl[1][0], bl[1][1]);
-                        }
-                        r0 >>= 8; r1 >>= 8; r2 >>= 8; r3 >>= 8;
+                for (int j = 0; j < 2; ++j) {
+                    float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int tl = 0; tl < 2; ++tl) {
+                        const uint32_t a0 = vc[tl][2 * (c & 1)], a1 = vc[tl][2 * (c & 1) + 1], x = j ? a0 >> 6 : a0 << 2, y = j ? a1 >> 6 : a1 << 2;
+                        if (G > 4) mma16816_nv(d, x & kV0, x & kV1, y & kV0, y & kV1, bl[2 * tl], bl[2 * tl + 1]);
+                        mma16816_nv(d, x & kV0, x & kV1, y & kV0, y & kV1, bp[2 * tl], bp[2 * tl + 1]);
                     }
+                    add4(acc[c][j], d);
                 }
             }
         }
@@ -614,7 +635,7 @@ __device__ __forceinline__ void history_warp(const Attn4Args &a, const CUtensorM
             float x[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                x[i] = acc[c][i >> 1][2 * (i & 1) + e] * (i & 1 ? 0x1p20f : 0x1p24f) * up;
+                x[i] = acc[c][i >> 1][2 * (i & 1) + e] * (i & 1 ? 1.f / kVScale1 : 1.f / kVScale0) * up;
                 if (G <= 4) x[i] += __shfl_xor_sync(0xffffffffu, x[i], 2);       // the upper parts' sum and the lower ones'
             }
             if (2 * t + e < G)

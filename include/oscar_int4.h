@@ -115,8 +115,9 @@ OSCAR_API int32_t oscar_suggest_splits_int4(const oscar_layout_t *layout, int32_
  * Writes every slot of `partials`: the history is cut into S splits of whole 32-token blocks (at absolute
  * positions 32 i), the BF16 rows are dealt out to the same splits, slot S is written empty.  With out or
  * out_f32 non-NULL also their merge, as oscar_merge(R_V = NULL) defines it, lse optional.  Query products and softmax sums are fp32 or finer;
- * a probability times its value scale enters the value product in two fp16 parts: 2^-21 relative, or 2^-30 of the
- * largest such product.
+ * a probability times its value scale enters the value product in two fp16 parts (2^-21 relative, or 2^-30 of the
+ * largest one so far); of 16 tokens' products with their codes, what lies 2^-17 below a unit of the largest is cut off.
+ * Query elements below 2^-25 of their head's largest lose low bits.
  *   merge_counters  NULL: the merge is a second launch.  Else int32 [batch·n_kv_heads], all zero, left
  *                   zero: the last CTA of a request's kv head to finish merges it, in the same launch
  *                   and in slot order whichever CTA that is.  Calls that may run concurrently must

@@ -133,3 +133,62 @@ def test_weights_that_rise_along_the_history_while_scales_run_over_the_range(gqa
         c.sz[row][:, 1] = ic.bf16(np.float32(60 * x))
         c.sz[row][:, 2:] = ic.bf16(c.sz[row][:, 2:] * 2.0 ** (order * (100 * x - 50)))
     check(c.upload(), 1)
+
+
+@pytest.mark.parametrize("gqa,group", [(4, 128), (8, 128), (8, 32), (4, 32), (2, 64)])
+@pytest.mark.parametrize("splits", [1, 3])
+def test_long_sums_are_not_biased(gqa, group, splits):
+    """40,001 rows of codes 0 .. 15, zero 0, scale 1: sums that only grow.  The mean relative error over all heads and channels
+    is what does not average out.  A sum in the tensor cores may be truncated (2^-23 each); four in a row at most are, one lower
+    and one upper part of two tiles, before a rounded addition.  Rounded operations leave 2^-24 sqrt(n) an output for n below
+    2^9 additions a lane, over more than 2^6 lanes and outputs together: 2^-24 sqrt(2^9 / 2^6) < 2^-22, and 2^-23 for the
+    exponentials."""
+    T = 40001
+    c = cache(T, gqa=gqa, group=group, n_kv=2, page=64, seed=splits)
+    c.sz[..., 2], c.sz[..., 3] = 1.0, 0.0
+    c.upload()
+    out = decode(c, splits)[0].double().cpu().numpy()
+    for_all = []
+    for h in range(2):
+        v = c.rows(0, h, 1)
+        for hq in range(h * gqa, (h + 1) * gqa):
+            z = c.logits(0, hq)
+            w = np.exp(z - z.max())
+            for_all.append(out[0, hq] / (w @ v / w.sum()) - 1)
+    assert np.abs(np.mean(for_all)) <= 4 * 2.0 ** -23 + 2.0 ** -22 + 2.0 ** -23, np.mean(for_all)
+
+
+@pytest.mark.parametrize("gqa,group", [(4, 128), (8, 32)])
+@pytest.mark.parametrize("splits", [1, 9])
+def test_a_long_history_of_values_around_zero(gqa, group, splits):
+    """131,072 rows whose values are random around zero: the output is the small rest of two sums, codes and zero points, each
+    hundreds of times as large.  Their relative error of at most 2^-21 (see above, with 2^-24 sqrt(2^10 / 2^7) for 2^10 additions
+    a lane) meets 7.5, the mean code."""
+    c = cache(131072, gqa=gqa, group=group, n_kv=1, page=64, seed=9)
+    c.sz[..., 2], c.sz[..., 3] = 1.0, -7.5
+    c.upload()
+    out = decode(c, splits)[0].double().cpu().numpy()
+    k, v = c.rows(0, 0, 0), c.rows(0, 0, 1)
+    for hq in range(gqa):
+        w = np.exp(k @ c.q[0, hq])
+        assert np.sqrt(np.mean((out[0, hq] - w @ v / w.sum()) ** 2)) <= 2.0 ** -21 * 7.5
+
+
+@pytest.mark.parametrize("gqa,group", SHAPES)
+@pytest.mark.parametrize("large", [3, 20])
+def test_weights_far_below_their_tile_s_largest(gqa, group, large):
+    """One row of weight 1 whose codes are 0 and 31 of about 2^-10 with codes 15: the output is theirs.  The tensor cores cut a
+    sum's terms off 25 bits below the largest one's exponents, 2^-17 of the largest p·scale for a unit of code at 2^-22 (half of
+    the channels; 2^-21 for the others): once for each of the 15 rows of the same tile, and the sum before it."""
+    c = cache(32, gqa=gqa, group=group, page=16, seed=large)
+    c.q[..., CH] = 1.0
+    c.sz[..., 0], c.sz[..., 2], c.sz[..., 3] = ic.bf16(np.float32(0.47)), 1.0, 0.0
+    c.ck[:], c.cv[:] = 0, 0xFF
+    c.ck[at(c, large)], c.cv[at(c, large)] = 0xFF, 0
+    c.upload()
+    out = decode(c, 1)[0].double().cpu().numpy()
+    z = c.logits(0, 0)
+    w = np.exp(z - z.max())
+    ref = (w @ c.rows(0, 0, 1) / w.sum())[None]
+    cut = np.where(np.arange(D) % 2 == 0, 2.0 ** -17, 2.0 ** -21) * 16 / w.sum()
+    assert np.all(np.abs(out[0] - ref) <= cut + 2.0 ** -18 * ref)
