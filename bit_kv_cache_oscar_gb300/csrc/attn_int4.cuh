@@ -131,11 +131,9 @@ __device__ __forceinline__ float scaling(float x) {
     return __uint_as_float((uint32_t)(kPShift - e + 127) << 23);
 }
 
-// Limit of logit + log2 s, as the history's loop forms it, under maximum m and this scaling: 2^15 for p·s·vinv, with 2^-7 for
-// the sum's own rounding far below f16's end.
-__device__ __forceinline__ float logit_limit(float m, float vinv) {
-    return m + (65536.f + 127.f + 15.f - (float)((int)(__float_as_uint(vinv) >> 23) - 127));
-}
+// Limit of (logit - maximum) + log2 s, as the history's loop forms it, under this scaling: 2^15 for p·s·vinv, the 2^-7 of the
+// sum's own rounding far below f16's end.
+__device__ __forceinline__ float product_limit(float vinv) { return 65536.f + 127.f + 15.f - (float)((int)(__float_as_uint(vinv) >> 23) - 127); }
 
 // ---- the BF16 rows: [0, min(sink, T)) and [hist_end, T), 16-token tiles dealt out to the warps ----------
 struct Window {
@@ -422,7 +420,7 @@ __device__ __forceinline__ void history_warp(const Attn4Args &a, const CUtensorM
             for (int j = 0; j < 2; ++j) qz[k][j] = __shfl_sync(0xffffffffu, qs[k] * a.scale2, 4 * (2 * t + j));
         }
     }
-    float most[2] = {logit_limit(cs.m[0], vinv[0]), logit_limit(cs.m[1], vinv[1])};
+    float most[2] = {product_limit(vinv[0]), product_limit(vinv[1])};
     for (int i = 0, st = st0, round = 0, phase = 0; i < n; ++i) {
         if (!mbar_wait(bars + 8 * st, phase)) {
             if (lane == 0) flag_status(a.status, OSCAR_DEV_WAIT_TIMEOUT);
@@ -505,7 +503,7 @@ __device__ __forceinline__ void history_warp(const Attn4Args &a, const CUtensorM
             // Raise the running maximum when a block passes it, change the scaling when a p·s might pass f16's range:
             // looked at only where the lane's largest logit with its largest scale would, rows apart or not.  log2 s
             // is at most 0.09 above its exponent and fraction read as one number, bits/128 - 127.
-            float top[2], far[2];
+            float top[2], over[2], far[2];                               // largest logit, that less the maximum, that with log2 s
             __nv_bfloat162 v2 = as_bf2(vw[0][0][0]);                     // scales in the low halves (never negative)
 #pragma unroll
             for (int u = 0; u < 4; ++u)
@@ -515,9 +513,10 @@ __device__ __forceinline__ void history_warp(const Attn4Args &a, const CUtensorM
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 top[j] = fmaxf(fmaxf(s[0][0][j], s[0][1][j]), fmaxf(s[1][0][j], s[1][1][j]));
-                far[j] = fmaf(bits, 0x1p-7f, top[j]);                    // 2^16 + 127 + log2(scale) + logit
+                over[j] = top[j] - cs.m[j];                              // as for p: exact where it matters
+                far[j] = fmaf(bits, 0x1p-7f, over[j]);                   // 2^16 + 127 + log2(p·s)
             }
-            if (__any_sync(0xffffffffu, top[0] > cs.m[0] + kSlack || top[1] > cs.m[1] + kSlack || far[0] > most[0] || far[1] > most[1])) {
+            if (__any_sync(0xffffffffu, fmaxf(over[0], over[1]) > kSlack || far[0] > most[0] || far[1] > most[1])) {
                 float f[2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
@@ -537,7 +536,7 @@ __device__ __forceinline__ void history_warp(const Attn4Args &a, const CUtensorM
                     vinv[j] = fminf(old * up, kPMost);
                     if (x * vinv[j] > 0x1p14f) vinv[j] = scaling(x);
                     f[j] = al * (vinv[j] / old);                         // both powers of two
-                    most[j] = logit_limit(m, vinv[j]);
+                    most[j] = product_limit(vinv[j]);
                 }
 #pragma unroll
                 for (int c = 0; c < 4; ++c)

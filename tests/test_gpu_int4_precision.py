@@ -192,3 +192,24 @@ def test_weights_far_below_their_tile_s_largest(gqa, group, large):
     ref = (w @ c.rows(0, 0, 1) / w.sum())[None]
     cut = np.where(np.arange(D) % 2 == 0, 2.0 ** -17, 2.0 ** -21) * 16 / w.sum()
     assert np.all(np.abs(out[0] - ref) <= cut + 2.0 ** -18 * ref)
+
+
+@pytest.mark.parametrize("gqa,group", SHAPES)
+@pytest.mark.parametrize("scale", [1.0, 2.0, 4.0, 8.0, 16.0, 64.0])
+def test_logits_whose_last_bit_is_8(gqa, group, scale):
+    """Logits of 2^26 and, from every warp's second block on, 2^26 + 8 in base 2, each an fp32 number: weights of 1 and 2^8, which
+    the running maximum need not follow but the scaling of p·scale must."""
+    T = 32 * 16 * 3
+    c = cache(T, gqa=gqa, group=group, page=16, seed=1)
+    c.sm_scale = float(np.log(2))
+    assert np.float32(c.sm_scale) * np.float32(1.4426950408889634) == 1
+    c.q[..., CH] = 2.0 ** 16
+    c.ck[:] = 0
+    c.sz[..., 0], c.sz[..., 1], c.sz[..., 2], c.sz[..., 3] = 2.0 ** -13, 2.0 ** 10, scale, -7.5 * scale
+    late = np.arange(512, T)
+    c.ck[c.t4[0, late // 16], 0, late % 16, CH // 2] = 0x11
+    c.upload()
+    out = decode(c, 1)[0].double().cpu().numpy()
+    w, v = np.where(np.arange(T) < 512, 1.0, 256.0), c.rows(0, 0, 1)
+    ref = w @ v / w.sum()
+    assert np.all(np.abs(out[0] - ref[None]) <= 2.0 ** -18 * 15 * scale)
