@@ -255,9 +255,6 @@ class Int4Pool:
         return Int4Pool(c(), c(), torch.zeros(shp + (layout.head_dim // layout.group, 4), dtype=torch.bfloat16,
                                               device=device))
 
-    def c(self) -> Int4PoolC:
-        return Int4PoolC(_ptr(self.codes_k), _ptr(self.codes_v), _ptr(self.scale_zero), self.n_pages)
-
 
 @dataclasses.dataclass
 class Partials:
