@@ -29,15 +29,15 @@
 // CTAs have no results to join: several CTAs an SM, so that one's start and end hide behind another's stream.
 // Every wait is bounded: one that gives up sets OSCAR_DEV_WAIT_TIMEOUT.
 //
-// Measured (passes back to back, 32 query and 8 kv heads, group 128): 100K tokens 29.3 us, of which about 14
-// stream 110 MB after a start of 7 to 10 us (lengths, page ids and the first copies of all warps at once) and
-// 5 join warps and splits; a ragged batch of 32, 64K to 100K, 531 us = 5.5 TB/s (0.81 of a copy's rate): issue
-// slots and HBM.  64 query heads and groups of 32, 4 x 131K: 177 us = 3.8 TB/s: issue slots.  What the value
-// product's precision costs of that, with the bf16 outputs' distance from fp32 arithmetic: p·s in one part and
-// one running sum 27.4, 486 and 141 us, 2.0, 2.1 and 2.1e-3 of their size; two parts and one running sum 28.4, 497
-// and 168 us, 1.6, 2.0 and 3.5e-3 (the sum's truncation, twice as often for eight heads); as it is 0.56, 0.53 and
-// 0.61e-3.  Codes centred by one more operation each: 0.01, 0.17 and 0.08e-3, in 32, 605 and 192 us.  Weights, ragged
-// batch of 8: 78 us = 5.2 TB/s.
+// Measured (passes back to back, 32 query and 8 kv heads, group 128): 100K tokens 29.4 us: 8 us to the first
+// block (lengths, page ids and the first copies of all warps at once), 16 to the loop's end (110 MB in all), 5 to
+// join warps and splits; a ragged batch of 32, 64K to 100K, 528 us = 5.5 TB/s (0.82 of a copy's rate): issue slots
+// (661 instructions a block) and HBM.  64 query heads and groups of 32, 4 x 131K: 176 us = 3.8 TB/s: issue slots, 928
+// instructions a block.  What the value product's precision costs of that, with the bf16 outputs' distance from
+// fp32 arithmetic: p·s in one part and one running sum 27.4, 486 and 141 us, 2.0, 2.1 and 2.1e-3 of their size; two
+// parts and one running sum 28.4, 497 and 168 us, 1.6, 2.0 and 3.5e-3 (the sum's truncation, twice as often for eight
+// heads); as it is 0.44, 0.50 and 0.54e-3.  Codes centred by one more operation each: 0.01, 0.17 and 0.08e-3, in 32,
+// 605 and 192 us.  Weights, ragged batch of 8: 76 us = 5.4 TB/s.
 
 #pragma once
 
