@@ -339,8 +339,6 @@ def _handles(case, s):
             splits = ob.oscar_suggest_splits_tree_int4(L, case["batch"], case["nodes"], case["context"],
                                                        torch.cuda.get_device_properties(0).multi_processor_count)
             h["partials"] = ob.Partials.empty(L, s["q"].shape[0], splits)
-        if case["op"] == "sample":
-            h["workspace"] = torch.zeros(ob.oscar_sample_workspace_bytes(case["rows"], case["vocab"]), dtype=torch.uint8, device=DEV)
         if case["op"] == "accept":
             h["pools"] = [ob.Bf16Pool(k, v) for k, v in zip(s["k"], s["v"])]
         s["lib"] = h
@@ -355,7 +353,7 @@ def _run_own(case, s):
                                      s["sm_scale"], h["partials"], out=s["out"], lse=s["lse"])
         return s["out"], s["lse"]
     if op == "sample":
-        ob.oscar_sample(s["logits"], s["temperature"], s["u"], s["tokens"], h["workspace"], top_k=s["top_k"], top_p=s["top_p"], min_p=s["min_p"])
+        ob.oscar_sample(s["logits"], s["temperature"], s["u"], s["tokens"], top_k=s["top_k"], top_p=s["top_p"], min_p=s["min_p"])
         return s["tokens"]
     ob.oscar_tree_accept(h["L"], s["target"], s["draft"], s["parents"], s["begin"], s["T"], s["accepted"], s["path"], s["tokens"], s["new_len"],
                          pools=h["pools"], page_table=s["tb"])
