@@ -355,7 +355,7 @@ def _run_own(case, s):
     if op == "sample":
         ob.oscar_sample(s["logits"], s["temperature"], s["u"], s["tokens"], top_k=s["top_k"], top_p=s["top_p"], min_p=s["min_p"])
         return s["tokens"]
-    ob.oscar_tree_accept(h["L"], s["target"], s["draft"], s["parents"], s["begin"], s["T"], s["accepted"], s["path"], s["tokens"], s["new_len"],
+    ob.oscar_tree_accept(h["L"], s["target"], s["draft"], s["parents"], s["begin"], case["nodes"], s["T"], s["accepted"], s["path"], s["tokens"], s["new_len"],
                          pools=h["pools"], page_table=s["tb"])
     return s["accepted"], s["path"], s["tokens"], s["new_len"], s["k"], s["v"]
 
