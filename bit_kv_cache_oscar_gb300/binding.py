@@ -1,4 +1,4 @@
-"""Thin binding of liboscar.so (include/oscar.h, oscar_int4.h): argument marshalling only, by ctypes or, for the INT4 calls, natively.
+"""Thin binding of liboscar.so (include/oscar.h, oscar_int4.h, oscar_tree.h): argument marshalling only, by ctypes or, for the INT4 and speculative decoding calls, natively.
 
 Every function here has the name of the C entry point it calls, takes torch
 tensors (device memory, caller-owned) and passes their addresses, sizes and the
@@ -62,6 +62,9 @@ EXPORTS = [
 EXPORTS_INT4 = [                    # include/oscar_int4.h
     "oscar_append_kv", "oscar_demote_int4", "oscar_promote_int4", "oscar_suggest_splits_int4",
     "oscar_decode_attention_int4", "oscar_attention_mass_int4", "oscar_evict_int4",
+]
+EXPORTS_TREE = [                    # include/oscar_tree.h
+    "oscar_suggest_splits_tree_int4", "oscar_tree_attention_int4", "oscar_sample", "oscar_tree_accept",
 ]
 
 
@@ -140,6 +143,16 @@ def lib():
     L.oscar_evict_int4.argtypes = [P(LayoutC), P(Int4PoolC), vp, P(Int4PoolC), vp, i32, i32, vp, vp, vp, vp, vp, vp,
                                    i32, vp]
     L.oscar_evict_int4.restype = st
+    L.oscar_suggest_splits_tree_int4.argtypes = [P(LayoutC), i32, i32, i32, i32]
+    L.oscar_suggest_splits_tree_int4.restype = i32
+    L.oscar_tree_attention_int4.argtypes = [P(LayoutC), vp, i32, vp, vp, i32, i32, P(Bf16PoolC), vp, P(Int4PoolC), vp, i32, vp,
+                                            vp, i32, ctypes.c_float, P(PartialsC), vp, vp, vp]
+    L.oscar_tree_attention_int4.restype = st
+    L.oscar_sample.argtypes = [vp, i32, i64, i32, i32, vp, vp, vp, vp, vp, vp, vp]
+    L.oscar_sample.restype = st
+    L.oscar_tree_accept.argtypes = [P(LayoutC), vp, vp, vp, i32, vp, i32, vp, i32, vp, vp, vp, i32, vp, P(Bf16PoolC), i32, vp,
+                                    i32, vp]
+    L.oscar_tree_accept.restype = st
     L.oscar_set_launch_overlap.argtypes = [i32]
     L.oscar_set_launch_overlap.restype = st
     L.oscar_get_launch_overlap.argtypes = []
@@ -503,6 +516,41 @@ def oscar_evict_int4(layout: Layout, src: Int4Pool, src_page_table: torch.Tensor
     dst_page_table, their old positions to kept [batch, Hkv, at least max(keep)] (int32)."""
     _native().evict_int4(layout, src, src_page_table, dst, dst_page_table, seq_len, hist_end, keep, mass,
                          mass_out, kept, stream)
+
+
+# ---- speculative decoding: trees of drafted tokens (checked natively, as above)
+
+def oscar_suggest_splits_tree_int4(layout: Layout, batch: int, max_nodes: int, max_hist_tokens: int, sm_count: int) -> int:
+    return int(lib().oscar_suggest_splits_tree_int4(ctypes.byref(layout.c()), batch, max_nodes, max_hist_tokens, sm_count))
+
+
+def oscar_tree_attention_int4(layout: Layout, q: torch.Tensor, node_begin: torch.Tensor, mask: Optional[torch.Tensor],
+                              max_nodes: int, bf16_pool: Bf16Pool, bf16_page_table: torch.Tensor, int4_pool: Int4Pool,
+                              int4_page_table: torch.Tensor, seq_len: torch.Tensor, hist_end: torch.Tensor, sm_scale: float,
+                              partials: Partials, out: torch.Tensor, lse: Optional[torch.Tensor] = None, stream=None):
+    """Attention of the nodes q [n, Hq, D] (request b's: node_begin[b] .. node_begin[b + 1] - 1) over [BF16 sink | INT4
+    history | BF16 recent] and the nodes that mask (int32 [n, words], or None: a chain) lets each see, whose rows lie at
+    seq_len + their index.  partials: of n rows."""
+    _native().tree_attention_int4(layout, q, node_begin, mask, max_nodes, bf16_pool, bf16_page_table, int4_pool,
+                                  int4_page_table, seq_len, hist_end, sm_scale, partials, out, lse, stream)
+
+
+def oscar_sample(logits: torch.Tensor, temperature: torch.Tensor, u: torch.Tensor, tokens: torch.Tensor,
+                 top_k: Optional[torch.Tensor] = None, top_p: Optional[torch.Tensor] = None,
+                 min_p: Optional[torch.Tensor] = None, stream=None):
+    """A token per row of logits [rows, vocab] (fp32, bf16 or fp16; rows possibly strided) to tokens (int32 [rows]) by
+    temperature (0: the largest logit), top-k, top-p, min-p and the uniform numbers u, all [rows]."""
+    _native().sample(logits, temperature, u, tokens, top_k, top_p, min_p, stream)
+
+
+def oscar_tree_accept(layout: Layout, target: torch.Tensor, draft: torch.Tensor, parents: torch.Tensor,
+                      node_begin: torch.Tensor, max_nodes: int, seq_len: torch.Tensor, accepted: torch.Tensor,
+                      path: torch.Tensor, tokens: torch.Tensor, new_len: Optional[torch.Tensor] = None, pools=(),
+                      page_table: Optional[torch.Tensor] = None, stream=None):
+    """The path of drafted tokens that the sampled ones confirm (accepted [batch], path and tokens [batch, at least
+    max_nodes], filled up with -1), and its rows of every pool moved to the positions from seq_len on."""
+    _native().tree_accept(layout, target, draft, parents, node_begin, max_nodes, seq_len, accepted, path, tokens, new_len,
+                          pools, page_table, stream)
 
 
 def oscar_get_device_status(stream=None) -> int:

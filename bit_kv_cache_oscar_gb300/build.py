@@ -57,7 +57,7 @@ def _stamp(path: str, text: str) -> str:
 def build(verbose: bool = False, extra: list | None = None) -> str:
     os.makedirs(BUILD, exist_ok=True)
     headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
-    public = [os.path.join(ROOT, "include", f) for f in ("oscar.h", "oscar_int4.h")]
+    public = [os.path.join(ROOT, "include", f) for f in ("oscar.h", "oscar_int4.h", "oscar_tree.h")]
     headers += public
     flags = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden",
                     "-I", os.path.join(ROOT, "include"), "--expt-relaxed-constexpr",

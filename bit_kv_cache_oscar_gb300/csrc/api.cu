@@ -1,5 +1,6 @@
 // C ABI of liboscar.so: argument validation, the device status word, dispatch
-// to the kernels.  Declarations and contracts: include/oscar.h, include/oscar_int4.h.
+// to the kernels.  Declarations and contracts: include/oscar.h, include/oscar_int4.h,
+// include/oscar_tree.h.
 
 #include <atomic>
 #include <cmath>
@@ -11,6 +12,7 @@
 
 #include "int4.cuh"
 #include "oscar_internal.cuh"
+#include "tree.cuh"
 
 namespace {
 
@@ -122,6 +124,14 @@ oscar_status_t check_tables(const oscar_layout_t *L, int32_t max_pages, int32_t 
     if (max_pages < 1) return fail(OSCAR_ERR_INVALID_ARG, "max_pages_per_req %d < 1", max_pages);
     if ((long long)max_pages * L->page_size > 2147483647LL - 64)
         return fail(OSCAR_ERR_INVALID_ARG, "max_pages_per_req %d: positions pass int32", max_pages);
+    return OSCAR_OK;
+}
+
+// Node rows of a call on trees of drafted tokens.
+oscar_status_t check_nodes(int32_t n, int32_t max_nodes) {
+    if (n < 0 || n > 65535 * 256) return fail(OSCAR_ERR_INVALID_ARG, "n %d outside 0..%d", n, 65535 * 256);
+    if (max_nodes < 1 || max_nodes > OSCAR_TREE_MAX_NODES)
+        return fail(OSCAR_ERR_INVALID_ARG, "max_nodes %d outside 1..%d", max_nodes, OSCAR_TREE_MAX_NODES);
     return OSCAR_OK;
 }
 
@@ -620,6 +630,84 @@ oscar_status_t oscar_evict_int4(const oscar_layout_t *layout, const oscar_int4_p
                                            max_pages_per_req, batch, seq_len, hist_end, keep, mass, mass_out, kept,
                                            kept_stride, status_ptr(), (cudaStream_t)stream),
                        "oscar_evict_int4 launch");
+}
+
+int32_t oscar_suggest_splits_tree_int4(const oscar_layout_t *L, int32_t batch, int32_t max_nodes, int32_t max_hist_tokens,
+                                       int32_t sm_count) {
+    if (!L || L->n_kv_heads <= 0 || L->gqa <= 0 || batch <= 0 || max_nodes <= 0 || max_hist_tokens <= 0 || sm_count <= 0) return 1;
+    return oscar::suggest_splits_tree(*L, batch, max_nodes, max_hist_tokens, sm_count);
+}
+
+oscar_status_t oscar_tree_attention_int4(const oscar_layout_t *layout, const uint16_t *q, int32_t n, const int32_t *node_begin,
+                                         const int32_t *mask, int32_t mask_words, int32_t max_nodes,
+                                         const oscar_bf16_pool_t *bf16_pool, const int32_t *bf16_page_table,
+                                         const oscar_int4_pool_t *int4_pool, const int32_t *int4_page_table,
+                                         int32_t max_pages_per_req, const int32_t *seq_len, const int32_t *hist_end,
+                                         int32_t batch, float sm_scale, const oscar_partials_t *partials, uint16_t *out,
+                                         float *lse, void *stream) {
+    TRY(check_layout(layout));
+    TRY(check_bf16_pool(bf16_pool));
+    TRY(check_int4_pool(layout, int4_pool));
+    TRY(check_partials(partials));
+    TRY(check_tables(layout, max_pages_per_req, batch));
+    TRY(check_nodes(n, max_nodes));
+    if (batch == 0 || n == 0) return OSCAR_OK;
+    if (!q || !node_begin || !bf16_page_table || !int4_page_table || !seq_len || !hist_end || !out)
+        return fail(OSCAR_ERR_INVALID_ARG, "NULL argument");
+    if (!aligned16(q)) return fail(OSCAR_ERR_INVALID_ARG, "q not 16-byte aligned");
+    if (reinterpret_cast<uintptr_t>(out) & 7u) return fail(OSCAR_ERR_INVALID_ARG, "out not 8-byte aligned");
+    if (mask && (mask_words < 1 || 32LL * mask_words < max_nodes))
+        return fail(OSCAR_ERR_INVALID_ARG, "mask_words %d: fewer bits than max_nodes %d", mask_words, max_nodes);
+    const oscar::Attn4Input in{q, bf16_view(bf16_pool), bf16_page_table, int4_view(int4_pool), int4_page_table,
+                               max_pages_per_req, seq_len, hist_end, sm_scale};
+    return cuda_status(oscar::launch_tree_attention(*layout, in, {node_begin, n, max_nodes}, mask, mask_words, batch,
+                                                    part_view(partials), out, lse, status_ptr(), (cudaStream_t)stream),
+                       "oscar_tree_attention_int4 launch");
+}
+
+oscar_status_t oscar_sample(const void *logits, int32_t dtype, int64_t stride, int32_t rows, int32_t vocab,
+                            const float *temperature, const int32_t *top_k, const float *top_p, const float *min_p,
+                            const float *u, int32_t *tokens, void *stream) {
+    if (dtype != OSCAR_DTYPE_F32 && dtype != OSCAR_DTYPE_BF16 && dtype != OSCAR_DTYPE_F16)
+        return fail(OSCAR_ERR_UNSUPPORTED, "dtype %d: fp32, bf16 or fp16 logits", dtype);
+    if (rows < 0 || rows > 65535) return fail(OSCAR_ERR_INVALID_ARG, "rows %d outside 0..65535", rows);
+    if (vocab < 1 || vocab > OSCAR_SAMPLE_MAX_VOCAB)
+        return fail(OSCAR_ERR_INVALID_ARG, "vocab %d outside 1..%d", vocab, OSCAR_SAMPLE_MAX_VOCAB);
+    if (rows == 0) return OSCAR_OK;
+    if (rows > 1 && stride < vocab) return fail(OSCAR_ERR_INVALID_ARG, "stride below vocab");
+    if (!logits || !temperature || !u || !tokens) return fail(OSCAR_ERR_INVALID_ARG, "NULL argument");
+    if (reinterpret_cast<uintptr_t>(logits) % (dtype == OSCAR_DTYPE_F32 ? 4 : 2))
+        return fail(OSCAR_ERR_INVALID_ARG, "logits not aligned to their type");
+    return cuda_status(oscar::launch_sample({logits, dtype, stride, rows, vocab, temperature, top_k, top_p, min_p, u}, tokens,
+                                            (cudaStream_t)stream),
+                       "oscar_sample launch");
+}
+
+oscar_status_t oscar_tree_accept(const oscar_layout_t *layout, const int32_t *target, const int32_t *draft,
+                                 const int32_t *parents, int32_t n, const int32_t *node_begin, int32_t max_nodes,
+                                 const int32_t *seq_len, int32_t batch, int32_t *accepted, int32_t *path, int32_t *tokens,
+                                 int32_t path_stride, int32_t *new_len, const oscar_bf16_pool_t *pools, int32_t n_pools,
+                                 const int32_t *page_table, int32_t max_pages_per_req, void *stream) {
+    TRY(check_layout(layout));
+    TRY(check_nodes(n, max_nodes));
+    if (n_pools < 0 || n_pools > 4096) return fail(OSCAR_ERR_INVALID_ARG, "n_pools %d outside 0..4096", n_pools);
+    if (n_pools > 0) {
+        if (!pools || !page_table) return fail(OSCAR_ERR_INVALID_ARG, "NULL pools or page table");
+        TRY(check_tables(layout, max_pages_per_req, batch));
+        for (int32_t i = 0; i < n_pools; ++i) TRY(check_bf16_pool(pools + i));
+    }
+    if (batch < 0 || batch > 65535) return fail(OSCAR_ERR_INVALID_ARG, "batch %d outside 0..65535", batch);
+    if (path_stride < max_nodes)
+        return fail(OSCAR_ERR_INVALID_ARG, "path_stride %d below max_nodes %d", path_stride, max_nodes);
+    if (batch == 0) return OSCAR_OK;
+    if ((n > 0 && (!target || !draft || !parents)) || !node_begin || !seq_len || !accepted || !path || !tokens)
+        return fail(OSCAR_ERR_INVALID_ARG, "NULL argument");
+    if (new_len && new_len < seq_len + batch && seq_len < new_len + batch)
+        return fail(OSCAR_ERR_INVALID_ARG, "new_len and seq_len overlap");
+    return cuda_status(oscar::launch_tree_accept(*layout, {target, draft, parents, seq_len}, {node_begin, n, max_nodes}, batch,
+                                                 {accepted, path, tokens, new_len, path_stride}, pools, n_pools, page_table,
+                                                 max_pages_per_req, status_ptr(), (cudaStream_t)stream),
+                       "oscar_tree_accept launch");
 }
 
 oscar_status_t oscar_get_device_status(int32_t *status_bits, void *stream) {

@@ -1,0 +1,700 @@
+// Attention of a tree of drafted tokens over an INT4 history with BF16 sink and recent rows: tiles of 16 query rows
+// (node, query head of one kv head) on mma.sync, the BF16 rows with the nodes' mask, and the merge of the splits.
+//
+// As for one token (attn_int4.cuh), with a row's codes n, scale s and zero z per channel group, a logit is
+// sm (s sum_c q_c n_c + z sum_c q_c), and the products meet the codes as f16 subnormals.  Here the 16 query rows are the A
+// operand of m16n8k16 and eight keys the B operand, so that a pair of logit accumulators is the A operand of the value product
+// as it lies (no movement between lanes), and a code is unpacked once for 16 rows.  The value product is
+//   sum_t p_t v_t = sum_t (p_t s_t) (n_t - 8) + sum_t p_t (z_t + 8 s_t)
+// with centred codes, normal f16 numbers at one operation more a pair: uncentred the two sums cancel most of each other, which
+// would ask for p s in two parts and for sums that are not truncated (the accumulators of mma.sync are).  p s is one f16
+// number, 2^-12 relative, under a power of two per row that follows the largest p s so far.
+//
+// A CTA takes (split, 16 query rows, kv head, request); each of its 8 warps takes every 8th block of 32 tokens through a ring
+// of bulk tensor copies of its own, and they join at the end.  Slot S of the partials is the BF16 rows': the last CTA of a
+// row tile, whose warps take 16 positions at a time straight from global memory.
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "merge_math.cuh"
+#include "tma.cuh"
+#include "tree_args.cuh"
+
+namespace oscar {
+namespace {
+
+constexpr int kW = 8;                            // warps of a CTA
+constexpr int kTile = 16;                        // query rows of a CTA
+constexpr uint32_t kM0 = 0x000F000Fu, kM1 = 0x00F000F0u;
+constexpr int kResRow = kHeadDim + 4;
+constexpr float kNone = -1e30f;                  // running maximum before the first token
+constexpr float kSlack = 8.f;                    // logits (base 2) may pass the running maximum by this
+constexpr int kPShift = 8;                       // a new scaling brings the largest p·s into [2^8, 2^9); near 2^15 another is due
+constexpr float kPMost = 0x1p110f;
+
+template <int NG>
+struct Ring {
+    static constexpr int bytes = 4096 + kBlock4 * NG * 8;
+    static constexpr int stride = (bytes + 511) & ~511;
+    static constexpr int n = 3;
+    static constexpr int total = kW * n * stride;
+};
+
+__device__ __forceinline__ float lo16(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi16(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ uint32_t pack_h2(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ uint32_t pack_b2(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
+    uint32_t d;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    return d;
+}
+__device__ __forceinline__ void tma_rows(uint32_t dst, const void *tmap, int row, uint32_t bar, uint64_t pol) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint "
+        "[%0], [%1, {%2, %3}], [%4], %5;"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(0), "r"(row), "r"(bar), "l"(pol)
+        : "memory");
+}
+// Over the four lanes of a row.
+__device__ __forceinline__ float row_max(float x) {
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+    return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+}
+__device__ __forceinline__ float row_sum(float x) {
+    x += __shfl_xor_sync(0xffffffffu, x, 1);
+    return x + __shfl_xor_sync(0xffffffffu, x, 2);
+}
+// Codes of nibbles 0 (low) or 1 (high) of a word's two halves, less 8: (1024 + n) - 1032, (1024 + 16 n) / 16 - 72.
+__device__ __forceinline__ uint32_t centred_low(uint32_t w) {
+    uint32_t d;
+    asm("{\n.reg .b32 t;\nlop3.b32 t, %1, 0x000F000F, 0x64006400, 0xEA;\nadd.f16x2 %0, t, %2;\n}" : "=r"(d) : "r"(w), "r"(0xE408E408u));
+    return d;
+}
+__device__ __forceinline__ uint32_t centred_high(uint32_t w) {
+    uint32_t d;
+    asm("{\n.reg .b32 t;\nlop3.b32 t, %1, 0x00F000F0, 0x64006400, 0xEA;\nfma.rn.f16x2 %0, t, %2, %3;\n}"
+        : "=r"(d) : "r"(w), "r"(0x2C002C00u), "r"(0xD480D480u));
+    return d;
+}
+// The power of two that brings x > 0, 2^e <= x < 2^(e + 1), to 2^kPShift.
+__device__ __forceinline__ float scaling(float x) {
+    const int e = max((int)(__float_as_uint(x) >> 23) - 127, kPShift - 110);
+    return __uint_as_float((uint32_t)(kPShift - e + 127) << 23);
+}
+
+// What a warp holds of its 16 rows: lane (g, t) has rows g and g + 8 (index r); out[c][i][2 r + e] is channel
+// 32 c + 8 t + 4 e + i of row g + 8 r.
+struct Rows {
+    float m[2], l[2], z[4][2], out[4][4][4];
+};
+
+__device__ __forceinline__ void clear(Rows &x) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        x.m[r] = kNone;
+        x.l[r] = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x.z[k][r] = 0.f;
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x.out[c][i][e] = 0.f;
+}
+
+// Channels 32 i + 8 t .. + 7 of the lane's query rows g + 8 r.
+struct Query {
+    uint4 w[2][4];
+    __device__ __forceinline__ Query(const TreeArgs &a, const TreeRequest &rq, int h, int row0, int rows, int lane) {
+        const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int row = g + 8 * r;
+            const uint16_t *src = a.q + (row < rows ? tree_row(a, rq, h, row0 + row) * kHeadDim : 0) + 8 * t;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[r][i] = row < rows ? *reinterpret_cast<const uint4 *>(src + 32 * i) : make_uint4(0, 0, 0, 0);
+        }
+    }
+};
+
+// ---- the BF16 rows ---------------------------------------------------------------------------------
+// Positions [0, min(sink, T)), [max(hist_end, those), T) and the nodes' [T, T + n), in tiles of 16.
+__device__ __forceinline__ void window_warp(const TreeArgs &a, const TreeRequest &rq, int b, int h, int row0, int rows, int warp, int lane, Rows &x) {
+    const int g = lane >> 2, t = lane & 3, sh = a.page_shift, T = rq.T, end = T + rq.n;
+    const int n0 = min(a.sink, T), lo1 = max(rq.he, n0), sink_tiles = (n0 + 15) / 16, rec0 = lo1 / 16;
+    const int tiles = sink_tiles + (end + 15) / 16 - rec0;
+    const Query q(a, rq, h, row0, rows, lane);
+    int node[2];                                     // of the lane's rows
+#pragma unroll
+    for (int r = 0; r < 2; ++r) node[r] = (row0 + min(g + 8 * r, rows - 1)) / a.G;
+#pragma unroll 1
+    for (int k = warp; k < tiles; k += kW) {
+        const bool in_sink = k < sink_tiles;
+        const int p0 = (in_sink ? k : rec0 + k - sink_tiles) * 16, lo = in_sink ? 0 : lo1, hi = in_sink ? n0 : end;
+        const int page = a.bpt[(size_t)b * a.max_pages + (p0 >> sh)];
+        if ((uint32_t)page >= (uint32_t)a.bf.n_pages) {
+            if (lane == 0) flag_status(a.status, OSCAR_DEV_BAD_BF16_PAGE);
+            continue;
+        }
+        // lane (g, t): channels 32 i + 8 t .. + 7 of tokens g and g + 8
+        uint4 kk[2][4], vv[2][4];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int p = p0 + g + 8 * u;
+            const bool in = p >= lo && p < hi;
+            const size_t at = ((((size_t)page << sh) + (p & ((1 << sh) - 1))) * a.n_kv + h) * kHeadDim + 8 * t;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                kk[u][i] = in ? *reinterpret_cast<const uint4 *>(a.bf.k + at + 32 * i) : make_uint4(0, 0, 0, 0);
+                vv[u][i] = in ? *reinterpret_cast<const uint4 *>(a.bf.v + at + 32 * i) : make_uint4(0, 0, 0, 0);
+            }
+        }
+        float s[2][4];                               // [keys 8 u + 2 t + e][2 r + e]
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            s[u][0] = s[u][1] = s[u][2] = s[u][3] = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                mma16816_bf16(s[u], q.w[0][i].x, q.w[1][i].x, q.w[0][i].y, q.w[1][i].y, kk[u][i].x, kk[u][i].y);
+                mma16816_bf16(s[u], q.w[0][i].z, q.w[1][i].z, q.w[0][i].w, q.w[1][i].w, kk[u][i].z, kk[u][i].w);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int p = p0 + 8 * u + 2 * t + (e & 1), r = e >> 1;
+                bool sees = p >= lo && p < hi;
+                if (sees && p >= T) {
+                    const int j = p - T;
+                    sees = a.mask ? (a.mask[(size_t)(rq.first + node[r]) * a.mask_words + (j >> 5)] >> (j & 31)) & 1 : j <= node[r];
+                }
+                s[u][e] = sees ? s[u][e] * a.scale2 : -INFINITY;
+            }
+        // infinities and NaN among the values: rows that do not see them must not meet them in a product
+        bool odd = false;
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t w[4] = {vv[u][i].x, vv[u][i].y, vv[u][i].z, vv[u][i].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) odd |= (w[e] & 0x7f80u) == 0x7f80u || (w[e] & 0x7f800000u) == 0x7f800000u;
+            }
+        odd = __any_sync(0xffffffffu, odd);
+        float al[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const float m = fmaxf(x.m[r], row_max(fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]))));
+            al[r] = ex2_approx(x.m[r] - m);
+            x.m[r] = m;
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) s[u][2 * r + e] = ex2_approx(s[u][2 * r + e] - m);
+            x.l[r] = fmaf(x.l[r], al[r], (s[0][2 * r] + s[0][2 * r + 1]) + (s[1][2 * r] + s[1][2 * r + 1]));
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x.out[c][i][e] *= al[e >> 1];
+        if (odd) {
+            // one key at a time, only where it has weight
+#pragma unroll 1
+            for (int key = 0; key < 16; ++key) {
+                const int u = key >> 3, from = (lane & ~3) | ((key & 7) >> 1), p = p0 + key;
+                if (p < lo || p >= hi) continue;
+                float pr[2];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float first = __shfl_sync(0xffffffffu, u ? s[1][2 * r] : s[0][2 * r], from);
+                    const float second = __shfl_sync(0xffffffffu, u ? s[1][2 * r + 1] : s[0][2 * r + 1], from);
+                    pr[r] = key & 1 ? second : first;
+                }
+                const uint16_t *v = a.bf.v + ((((size_t)page << sh) + (p & ((1 << sh) - 1))) * a.n_kv + h) * kHeadDim + 8 * t;
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (pr[e >> 1] != 0.f) x.out[c][i][e] = fmaf(pr[e >> 1], bf16_to_f32(v[32 * c + 4 * (e & 1) + i]), x.out[c][i][e]);
+            }
+            continue;
+        }
+        uint32_t ph[4], pl[4];                       // A operand: rows g, g + 8 of keys 2 t + e, then of keys 8 + 2 t + e
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const uint32_t hi2 = pack_b2(s[u][2 * r], s[u][2 * r + 1]);
+                ph[2 * u + r] = hi2;
+                pl[2 * u + r] = pack_b2(s[u][2 * r] - lo16(hi2), s[u][2 * r + 1] - hi16(hi2));
+            }
+        // channels 32 c + 4 n + 2 j + e of eight tokens are an 8 x 8 matrix of 16 bits: transposed, the B operand
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const uint32_t sel = e ? 0x7632 : 0x5410;
+                    const uint32_t b0 = movmatrix_trans(__byte_perm(j ? vv[0][c].y : vv[0][c].x, j ? vv[0][c].w : vv[0][c].z, sel));
+                    const uint32_t b1 = movmatrix_trans(__byte_perm(j ? vv[1][c].y : vv[1][c].x, j ? vv[1][c].w : vv[1][c].z, sel));
+                    mma16816_bf16(x.out[c][2 * j + e], pl[0], pl[1], pl[2], pl[3], b0, b1);
+                    mma16816_bf16(x.out[c][2 * j + e], ph[0], ph[1], ph[2], ph[3], b0, b1);
+                }
+    }
+}
+
+// ---- the history -----------------------------------------------------------------------------------
+template <int NG>
+__device__ __forceinline__ void history_warp(const TreeArgs &a, const CUtensorMap *tmk, const CUtensorMap *tmv, uint8_t *ring, uint32_t bars,
+                                             const TreeRequest &rq, int b, int h, int row0, int rows, int split, int warp, int lane, Rows &x) {
+    using R = Ring<NG>;
+    const int t = lane & 3, sh = a.page_shift, S = a.part.S, he = rq.he;
+    const int first = a.sink / kBlock4, nb = he > a.sink ? (he + kBlock4 - 1) / kBlock4 - first : 0;
+    const int lo = first + (int)((long long)split * nb / S) + warp, hi = first + (int)((long long)(split + 1) * nb / S);
+    const int n = lo < hi ? (hi - lo + kW - 1) / kW : 0;        // blocks lo, lo + kW, ...
+    const int32_t *pt = a.ipt + (size_t)b * a.max_pages;
+    const uint64_t pol = l2_evict_first_policy();
+
+    int pg0 = -1, pg1 = -1;        // lane j: pages of the two 16-token halves of block lo + kW (batch + j)
+    uint32_t ok = 0;               // two bits per stage: halves that were loaded
+    auto issue = [&](int i, int st) {
+        if ((i & 31) == 0) {
+            const int p = (lo + kW * (i + lane)) * kBlock4;
+            pg0 = pg1 = -1;
+            if (i + lane < n) {
+                const bool in0 = p + 16 > a.sink && p < he, in1 = p + kBlock4 > a.sink && p + 16 < he;
+                if (in0) pg0 = pt[p >> sh];
+                if (in1) pg1 = pt[(p + 16) >> sh];
+                if ((in0 && (uint32_t)pg0 >= (uint32_t)a.i4_pages) || (in1 && (uint32_t)pg1 >= (uint32_t)a.i4_pages))
+                    flag_status(a.status, OSCAR_DEV_BAD_INT4_PAGE);
+            }
+        }
+        const int a0 = __shfl_sync(0xffffffffu, pg0, i & 31), a1 = __shfl_sync(0xffffffffu, pg1, i & 31);
+        const bool ok0 = (uint32_t)a0 < (uint32_t)a.i4_pages, ok1 = (uint32_t)a1 < (uint32_t)a.i4_pages;
+        ok = (ok & ~(3u << (2 * st))) | ((ok0 ? 1u : 0u) | (ok1 ? 2u : 0u)) << (2 * st);
+        if (lane == 0) {
+            const int p = (lo + kW * i) * kBlock4;
+            const uint32_t dst = saddr(ring + st * R::stride), bar = bars + 8 * st;
+            // pages of 32 or more: one box of 32 rows; pages of 16: a box a half
+            const int box = sh >= 5 ? kBlock4 : 16;
+            const bool l0 = sh >= 5 ? ok0 || ok1 : ok0, l1 = sh >= 5 ? false : ok1;
+            mbar_arrive_expect_tx(bar, (uint32_t)(l0 + l1) * box * (R::bytes / kBlock4));
+            const int page[2] = {ok0 ? a0 : a1, a1};
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                if (!(half ? l1 : l0)) continue;
+                const int row = ((page[half] * a.n_kv + h) << sh) + ((p + 16 * half) & ((1 << sh) - 1));
+                tma_rows(dst + half * 1024, tmk, row, bar, pol);
+                tma_rows(dst + 2048 + half * 1024, tmv, row, bar, pol);
+                tma_load_1d(dst + 4096 + half * 16 * NG * 8, a.sz + (size_t)row * NG * 4, (uint32_t)box * NG * 8, bar, pol);
+            }
+        }
+    };
+    for (int i = 0; i < R::n && i < n; ++i) issue(i, i);
+
+    // A operand of the logits: channels 32 i + 8 t + e of chunk i, the odd nibbles' against 1/16 of the query; fac undoes the
+    // scalings, qz is the zero's factor, per row and group.
+    uint32_t aq[4][2][4];
+    float fac[2], qz[NG][2];
+    {
+        const Query q(a, rq, h, row0, rows, lane);
+        float mul[2], qs[2][NG];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            float mx = 0.f;
+#pragma unroll
+            for (int k = 0; k < NG; ++k) qs[r][k] = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t w[4] = {q.w[r][i].x, q.w[r][i].y, q.w[r][i].z, q.w[r][i].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    mx = fmaxf(mx, fmaxf(fabsf(lo16(w[e])), fabsf(hi16(w[e]))));
+                    qs[r][i * NG / 4] += lo16(w[e]) + hi16(w[e]);
+                }
+            }
+            mx = row_max(mx);
+            const int ex = min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 117);      // |q| < 2^(ex + 1)
+            mul[r] = __uint_as_float((uint32_t)(14 - ex + 127) << 23);
+            fac[r] = a.scale2 * __uint_as_float((uint32_t)(10 + ex + 127) << 23);              // 2^24 / mul
+#pragma unroll
+            for (int k = 0; k < NG; ++k) qz[k][r] = row_sum(qs[r][k]) * a.scale2;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const uint4 w = q.w[r][i];
+                const float m0 = mul[r], m1 = mul[r] * 0.0625f;
+                aq[i][0][r] = pack_h2(lo16(w.x) * m0, lo16(w.z) * m0);
+                aq[i][0][2 + r] = pack_h2(hi16(w.x) * m1, hi16(w.z) * m1);
+                aq[i][1][r] = pack_h2(lo16(w.y) * m0, lo16(w.w) * m0);
+                aq[i][1][2 + r] = pack_h2(hi16(w.y) * m1, hi16(w.w) * m1);
+            }
+    }
+    float vinv[2] = {kPMost, kPMost};                // what the rows' p·s are multiplied by, powers of two
+    for (int i = 0, st = 0, phase = 0; i < n; ++i) {
+        if (!mbar_wait(bars + 8 * st, phase)) {
+            if (lane == 0) flag_status(a.status, OSCAR_DEV_WAIT_TIMEOUT);
+            // the copies still under way land before this memory is used again
+            for (int k = i + 1; k < i + R::n && k < n; ++k) mbar_wait(bars + 8 * (k % R::n), (k / R::n) & 1);
+            break;
+        }
+        const uint8_t *stage = ring + st * R::stride;
+        const uint32_t sb = saddr(stage);
+        const int p0 = (lo + kW * i) * kBlock4;
+        const uint32_t okb = (ok >> (2 * st)) & 3u;
+        const bool full = okb == 3u && p0 >= a.sink && p0 + kBlock4 <= he;
+
+        float s[4][4];                               // [8 keys][2 r + e]: key 8 u + 2 t + e of row g + 8 r
+        uint32_t vw[4][2][NG];                       // value scale | zero of keys 8 u + 2 t + e
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int row = 8 * u + (lane & 7);
+            uint32_t w[4];
+            ldmatrix_x4(sb + row * 64 + (((lane >> 3) ^ ((row >> 1) & 3)) << 4), w[0], w[1], w[2], w[3]);
+            float d[NG][4];
+#pragma unroll
+            for (int k = 0; k < NG; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) d[k][e] = 0.f;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const uint32_t y = w[c], y8 = y >> 8;
+                float(&dd)[4] = d[c * NG / 4];
+                mma16816_nv(dd, aq[c][0][0], aq[c][0][1], aq[c][0][2], aq[c][0][3], y & kM0, y & kM1);
+                mma16816_nv(dd, aq[c][1][0], aq[c][1][1], aq[c][1][2], aq[c][1][3], y8 & kM0, y8 & kM1);
+            }
+            const uint2 *rec = reinterpret_cast<const uint2 *>(stage + 4096) + (8 * u + 2 * t) * NG;
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int k = 0; k < NG; ++k) {
+                    const uint2 z = rec[e * NG + k];
+                    const float ks = lo16(z.x), kz = hi16(z.x);
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        // sum over groups of ks d fac + kz qz
+                        const float y = fmaf(ks * d[k][2 * r + e], fac[r], kz * qz[k][r]);
+                        s[u][2 * r + e] = k ? s[u][2 * r + e] + y : y;
+                    }
+                    vw[u][e][k] = z.y;
+                }
+        }
+        if (!full) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int p = p0 + 8 * u + 2 * t + e;
+                    if (p < a.sink || p >= he || !((okb >> (u >> 1)) & 1u)) {
+                        s[u][e] = s[u][2 + e] = -INFINITY;
+#pragma unroll
+                        for (int k = 0; k < NG; ++k) vw[u][e][k] = 0u;
+                    }
+                }
+        }
+        // Raise the running maximum when a block passes it, change the scaling when a p·s might pass f16's range: looked at only
+        // where the lane's largest logit with its largest scale would, together or not.
+        float vmax = 0.f;
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int k = 0; k < NG; ++k) vmax = fmaxf(vmax, lo16(vw[u][e][k]));
+        float top[2];
+        bool raise = false;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            top[r] = fmaxf(fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1])),
+                           fmaxf(fmaxf(s[2][2 * r], s[2][2 * r + 1]), fmaxf(s[3][2 * r], s[3][2 * r + 1])));
+            const float over = top[r] - x.m[r];
+            raise |= over > kSlack || ex2_approx(over) * vinv[r] * vmax > 0x1p15f;
+        }
+        if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const float m = fmaxf(x.m[r], row_max(top[r])), al = ex2_approx(x.m[r] - m);
+                // what was summed shrinks by al, so the scaling may grow by as much (by 2^100 at most)
+                const float up = __uint_as_float((uint32_t)(__float2int_rn(fminf(m - x.m[r], 100.f)) + 127) << 23), old = vinv[r];
+                x.m[r] = m;
+                x.l[r] *= al;
+#pragma unroll
+                for (int k = 0; k < NG; ++k) x.z[k][r] *= al;
+                float y = 0.f;
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+#pragma unroll
+                        for (int k = 0; k < NG; ++k) y = fmaxf(y, ex2_approx(s[u][2 * r + e] - m) * lo16(vw[u][e][k]));
+                y = row_max(y);
+                vinv[r] = fminf(old * up, kPMost);
+                if (y * vinv[r] > 0x1p13f) vinv[r] = scaling(y);
+                const float f = al * (vinv[r] / old);
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) x.out[c][j][2 * r + e] *= f;
+            }
+        }
+        float z4[NG][2];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float zc[NG];                        // zero of the centred codes
+#pragma unroll
+                for (int k = 0; k < NG; ++k) zc[k] = fmaf(8.f, lo16(vw[u][e][k]), hi16(vw[u][e][k]));
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float p = ex2_approx(s[u][2 * r + e] - x.m[r]);
+                    x.l[r] += p;
+#pragma unroll
+                    for (int k = 0; k < NG; ++k) z4[k][r] = u + e ? fmaf(p, zc[k], z4[k][r]) : p * zc[k];
+                    s[u][2 * r + e] = p * vinv[r];
+                }
+            }
+#pragma unroll
+        for (int k = 0; k < NG; ++k)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) x.z[k][r] += z4[k][r];
+        uint32_t ap[2][4], vc[2][4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            if (c % 2 == 0)
+#pragma unroll
+                for (int tl = 0; tl < 2; ++tl) {
+                    const int row = tl * 16 + (lane & 15);
+                    ldmatrix_x4_trans(sb + 2048 + row * 64 + (((c + (lane >> 4)) ^ ((row >> 1) & 3)) << 4), vc[tl][0], vc[tl][1], vc[tl][2],
+                                      vc[tl][3]);
+                }
+            const int k = c * NG / 4;
+            if (c * NG % 4 == 0)                     // a new group
+#pragma unroll
+                for (int tl = 0; tl < 2; ++tl)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) {
+                        const int u = 2 * tl + (v >> 1), r = v & 1;
+                        ap[tl][v] = pack_h2(s[u][2 * r] * lo16(vw[u][0][k]), s[u][2 * r + 1] * lo16(vw[u][1][k]));
+                    }
+#pragma unroll
+            for (int tl = 0; tl < 2; ++tl) {
+                const uint32_t y0 = vc[tl][2 * (c & 1)], y1 = vc[tl][2 * (c & 1) + 1], z0 = y0 >> 8, z1 = y1 >> 8;
+                mma16816_nv(x.out[c][0], ap[tl][0], ap[tl][1], ap[tl][2], ap[tl][3], centred_low(y0), centred_low(y1));
+                mma16816_nv(x.out[c][1], ap[tl][0], ap[tl][1], ap[tl][2], ap[tl][3], centred_high(y0), centred_high(y1));
+                mma16816_nv(x.out[c][2], ap[tl][0], ap[tl][1], ap[tl][2], ap[tl][3], centred_low(z0), centred_low(z1));
+                mma16816_nv(x.out[c][3], ap[tl][0], ap[tl][1], ap[tl][2], ap[tl][3], centred_high(z0), centred_high(z1));
+            }
+        }
+        __syncwarp();
+        if (i + R::n < n) issue(i + R::n, st);
+        if (++st == R::n) {
+            st = 0;
+            phase ^= 1;
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        const float up = 1.f / vinv[r];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) x.out[c][j][2 * r + e] *= up;
+#pragma unroll
+        for (int k = 0; k < NG; ++k) {
+            const float z = row_sum(x.z[k][r]);
+#pragma unroll
+            for (int c = k * 4 / NG; c < (k + 1) * 4 / NG; ++c)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) x.out[c][j][2 * r + e] += z;
+        }
+    }
+}
+
+// grid ((S + 1) x row tiles, Hkv, batch), the row tiles of a split next to each other: they read the same history
+template <int NG>
+__global__ void __launch_bounds__(kW * 32, 1)
+    tree_kernel(TreeArgs a, int tiles, const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
+    using R = Ring<NG>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t bars[kW * R::n];
+    __shared__ float wf[kW * kTile], wM[kTile];
+    uint8_t *smem = smem_raw + ((1024u - (saddr(smem_raw) & 1023u)) & 1023u);
+    const int slot = blockIdx.x / tiles, row0 = blockIdx.x % tiles * kTile, h = blockIdx.y, b = blockIdx.z, S = a.part.S;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (lane == 0)
+        for (int i = 0; i < R::n; ++i) mbar_init(saddr(&bars[warp * R::n + i]), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    __syncwarp();
+    pdl_wait();
+    const TreeRequest rq(a, b);
+    const int rows = min(kTile, rq.n * a.G - row0);
+    if (rows <= 0) return;
+    Rows x;
+    clear(x);
+    if (slot == S)
+        window_warp(a, rq, b, h, row0, rows, warp, lane, x);
+    else
+        history_warp<NG>(a, &tmk, &tmv, smem + warp * R::n * R::stride, saddr(&bars[warp * R::n]), rq, b, h, row0, rows, slot, warp, lane, x);
+    __syncthreads();                                 // every warp is done with its ring: results take its place
+    float *wm = reinterpret_cast<float *>(smem), *wl = wm + kW * kTile, *wa = wl + kW * kTile + warp * kTile * kResRow;
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        const int row = g + 8 * r;
+        const float l = row_sum(x.l[r]);
+        if (t == 0) {
+            wm[warp * kTile + row] = l > 0.f || l != l ? x.m[r] : -INFINITY;
+            wl[warp * kTile + row] = l;
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                *reinterpret_cast<float4 *>(wa + row * kResRow + 32 * c + 8 * t + 4 * e) =
+                    make_float4(x.out[c][0][2 * r + e], x.out[c][1][2 * r + e], x.out[c][2][2 * r + e], x.out[c][3][2 * r + e]);
+    }
+    __syncthreads();
+    // every warp's weight 2^(m - M) once, then the sums
+    if (threadIdx.x < kW * kTile) {
+        const int row = threadIdx.x % kTile;
+        float M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kW; ++w) M = fmaxf(M, wm[w * kTile + row]);
+        wf[threadIdx.x] = wm[threadIdx.x] != -INFINITY ? exp2f(wm[threadIdx.x] - M) : 0.f;
+        if (threadIdx.x < kTile) wM[row] = M;
+    }
+    __syncthreads();
+    const float *sum = wl + kW * kTile;
+    for (int e = threadIdx.x; e < rows * kHeadDim; e += kW * 32) {
+        const int row = e / kHeadDim, d = e % kHeadDim;
+        float L = 0.f, A = 0.f;
+#pragma unroll
+        for (int w = 0; w < kW; ++w) {
+            const float f = wf[w * kTile + row], y = sum[(w * kTile + row) * kResRow + d];
+            L = f != 0.f ? fmaf(wl[w * kTile + row], f, L) : L;
+            A = f != 0.f ? fmaf(y, f, A) : A;
+        }
+        const size_t at = tree_row(a, rq, h, row0 + row) * (S + 1) + slot;
+        a.part.acc[at * kHeadDim + d] = A;
+        if (d == 0) {
+            a.part.m[at] = wM[row];
+            a.part.l[at] = L;
+        }
+    }
+}
+
+// A warp takes a (node row, query head): its slots in ascending order, four channels a lane, eight slots on their way.
+__global__ void __launch_bounds__(128) tree_merge_kernel(TreeArgs a) {
+    pdl_wait();
+    const TreeRequest rq(a, blockIdx.y);
+    const int Hq = a.n_kv * a.G, lane = threadIdx.x & 31, S1 = a.part.S + 1;
+    const int item = blockIdx.x * 4 + (threadIdx.x >> 5);
+    if (item >= rq.n * Hq) return;
+    const size_t orow = (size_t)rq.first * Hq + item, row0 = orow * S1;
+    const float4 *acc = reinterpret_cast<const float4 *>(a.part.acc + row0 * kHeadDim) + lane;
+    float M = -INFINITY;
+    for (int i = lane; i < S1; i += 32) M = fmaxf(M, a.part.m[row0 + i]);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float L = 0.f;
+    float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s0 = 0; s0 < S1; s0 += 32) {
+        const bool in = s0 + lane < S1;
+        const float li = in ? a.part.l[row0 + s0 + lane] : 0.f, mi = in ? a.part.m[row0 + s0 + lane] : -INFINITY;
+        const float wi = mi != -INFINITY ? exp2_taylor(__fsub_rn(mi, M)) : 0.f;
+        for (int i0 = 0; i0 < 32 && s0 + i0 < S1; i0 += 8) {
+            float4 y[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (s0 + i0 + i < S1) y[i] = __ldcg(acc + (size_t)(s0 + i0 + i) * (kHeadDim / 4));
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float l = __shfl_sync(0xffffffffu, li, (i0 + i) & 31), w = __shfl_sync(0xffffffffu, wi, (i0 + i) & 31);
+                if (s0 + i0 + i < S1 && w != 0.f) {
+                    L = __fmaf_rn(l, w, L);
+                    A = make_float4(__fmaf_rn(y[i].x, w, A.x), __fmaf_rn(y[i].y, w, A.y), __fmaf_rn(y[i].z, w, A.z), __fmaf_rn(y[i].w, w, A.w));
+                }
+            }
+        }
+    }
+    const bool on = L > 0.f || L != L;
+    const float o0 = on ? __fdiv_rn(A.x, L) : 0.f, o1 = on ? __fdiv_rn(A.y, L) : 0.f, o2 = on ? __fdiv_rn(A.z, L) : 0.f,
+                o3 = on ? __fdiv_rn(A.w, L) : 0.f;
+    *reinterpret_cast<uint2 *>(a.o + orow * kHeadDim + 4 * lane) = make_uint2(pack_b2(o0, o1), pack_b2(o2, o3));
+    if (a.lse && lane == 0) a.lse[orow] = on ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+}
+
+bool rows_tensor_map(CUtensorMap *tm, const uint8_t *base, long long rows, int box_rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {kRow4, (cuuint64_t)rows}, strides[1] = {kRow4};
+    const cuuint32_t box[2] = {kRow4, (cuuint32_t)box_rows}, estr[2] = {1, 1};
+    return fn(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int NG>
+cudaError_t launch_rows(const TreeArgs &a, int tiles, const CUtensorMap &tmk, const CUtensorMap &tmv, int batch, cudaStream_t st) {
+    const int join = (2 * kW * kTile + kW * kTile * kResRow) * 4, smem = std::max(Ring<NG>::total, join) + 1024;
+    auto kern = tree_kernel<NG>;
+    if (cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void *>(kern), smem)) return e;
+    return launch_ahead(kern, dim3((a.part.S + 1) * tiles, a.n_kv, batch), kW * 32, smem, st, a, tiles, tmk, tmv);
+}
+
+}  // namespace
+
+int suggest_splits_tree(const oscar_layout_t &L, int batch, int max_nodes, int max_hist, int sm_count) {
+    const long long tiles = (max_nodes * (long long)L.gqa + kTile - 1) / kTile, units = (long long)batch * L.n_kv_heads * tiles;
+    long long want = std::max(1LL, sm_count / units);
+    want = std::min(want, (max_hist + 511LL) / 512);
+    return (int)std::max(1LL, std::min(want, 1024LL));
+}
+
+cudaError_t launch_tree_attention(const oscar_layout_t &L, const Attn4Input &in, const TreeInput &t, const int32_t *mask, int mask_words,
+                                  int batch, PartialsView part, uint16_t *out, float *lse, int32_t *status, cudaStream_t st) {
+    TreeArgs a{in.q, t, mask, mask_words, in.bf, in.bpt, in.i4.scale_zero, in.i4.n_pages, in.ipt, in.max_pages, page_shift(L), L.n_kv_heads, L.gqa,
+               L.sink, in.seq_len, in.hist_end, in.sm_scale * kLog2e, part, out, lse, status};
+    CUtensorMap tmk, tmv;
+    const long long rows = (long long)in.i4.n_pages * L.n_kv_heads * L.page_size;
+    const int box = L.page_size < kBlock4 ? L.page_size : kBlock4;
+    if (!rows_tensor_map(&tmk, in.i4.codes_k, rows, box) || !rows_tensor_map(&tmv, in.i4.codes_v, rows, box)) return cudaErrorInvalidValue;
+    const int tiles = (t.max_nodes * L.gqa + kTile - 1) / kTile;
+    cudaError_t e;
+    switch (L.group) {
+        case 32: e = launch_rows<4>(a, tiles, tmk, tmv, batch, st); break;
+        case 64: e = launch_rows<2>(a, tiles, tmk, tmv, batch, st); break;
+        default: e = launch_rows<1>(a, tiles, tmk, tmv, batch, st); break;
+    }
+    if (e) return e;
+    return launch_ahead(tree_merge_kernel, dim3((t.max_nodes * L.n_kv_heads * L.gqa + 3) / 4, batch), 128, 0, st, a);
+}
+
+}  // namespace oscar

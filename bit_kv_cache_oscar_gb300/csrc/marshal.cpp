@@ -1,4 +1,4 @@
-// The Python side of the INT4 entry points: every argument's type, shape and device checked, addresses,
+// The Python side of the INT4 and speculative decoding entry points: every argument's type, shape and device checked, addresses,
 // strides and the current stream passed on to liboscar.so: the one that the binding loaded, whose entry points
 // connect() looks up, since a library found by name or path could be another copy of the package.
 //
@@ -17,8 +17,9 @@
 #include <exception>
 #include <initializer_list>
 #include <string>
+#include <vector>
 
-#include "oscar_int4.h"
+#include "oscar_tree.h"
 
 namespace {
 
@@ -27,6 +28,7 @@ PyObject *g_error = nullptr;                 // OscarError
 // liboscar.so's entry points (connect)
 #define ENTRY_POINTS(X) \
     X(oscar_append_kv) X(oscar_demote_int4) X(oscar_promote_int4) X(oscar_decode_attention_int4) X(oscar_attention_mass_int4) X(oscar_evict_int4) \
+    X(oscar_tree_attention_int4) X(oscar_sample) X(oscar_tree_accept) \
     X(oscar_last_error_string)
 struct {
 #define X(f) decltype(&::f) f;
@@ -54,6 +56,7 @@ const char *dtype_text(at::ScalarType t) {
         case at::kFloat: return "torch.float32";
         case at::kInt: return "torch.int32";
         case at::kByte: return "torch.uint8";
+        case at::kHalf: return "torch.float16";
         default: return c10::toString(t);
     }
 }
@@ -337,6 +340,88 @@ void evict_int4(PyObject *const *a) {
     c.done(unlocked(g_lib.oscar_evict_int4, L, &src, spt, &dst, dpt, c.pages32(max_pages), c.pages32(batch), T, he, keep, mass, out, kept, c.pages32(stride), st));
 }
 
+// layout, q, node_begin, mask, max_nodes, bf16_pool, bf16_page_table, int4_pool, int4_page_table, seq_len, hist_end, sm_scale,
+// partials, out, lse, stream
+void tree_attention_int4(PyObject *const *a) {
+    const oscar_layout_t layout_ = layout(a[0]), *L = &layout_;
+    const Call c("oscar_tree_attention_int4");
+    int64_t batch, max_pages, words = 0;
+    c.table(a[8], &batch, &max_pages);
+    const int64_t Hq = (int64_t)L->n_kv_heads * L->gqa;
+    const at::Tensor &qt = c.tensor("q", a[1]);
+    const int64_t n = qt.dim() ? qt.size(0) : 0;
+    const uint16_t *q = c.at<uint16_t>("q", a[1], at::kBFloat16, {n, Hq, 128});
+    const int32_t *begin = c.ints("node_begin", a[2], batch + 1);
+    if (a[3] != Py_None) {
+        const at::Tensor &m = c.tensor("mask", a[3]);
+        words = m.dim() ? m.size(m.dim() - 1) : 0;
+    }
+    const int32_t *mask = c.at<int32_t>("mask", a[3], at::kInt, {n, words}), nodes = whole(a[4]);
+    const oscar_bf16_pool_t bf = c.bf16(L, a[5]);
+    const int32_t *bpt = c.pages("bf16_page_table", a[6], batch, max_pages);
+    const oscar_int4_pool_t i4 = c.int4(L, a[7]);
+    const int32_t *ipt = c.pages("int4_page_table", a[8], batch, max_pages), *T = c.ints("seq_len", a[9], batch), *he = c.ints("hist_end", a[10], batch);
+    const float scale = (float)real(a[11]);
+    const Attr m(a[12], s_m), l(a[12], s_l), acc(a[12], s_acc), ns(a[12], s_n_splits);
+    const int32_t S = whole(ns.o);
+    const int64_t S1 = (int64_t)S + 1;
+    const oscar_partials_t part{c.at<float>("partials m", m.o, at::kFloat, {n, Hq, S1}), c.at<float>("partials l", l.o, at::kFloat, {n, Hq, S1}),
+                                c.at<float>("partials acc", acc.o, at::kFloat, {n, Hq, S1, 128}), S};
+    uint16_t *out = c.at<uint16_t>("out", a[13], at::kBFloat16, {n, Hq, 128});
+    float *lse = c.at<float>("lse", a[14], at::kFloat, {n, Hq});
+    void *st = c.stream(a[15]);
+    c.done(unlocked(g_lib.oscar_tree_attention_int4, L, q, c.pages32(n), begin, mask, c.pages32(words), nodes, &bf, bpt, &i4, ipt, c.pages32(max_pages), T, he,
+                    c.pages32(batch), scale, &part, out, lse, st));
+}
+
+// logits, temperature, u, tokens, top_k, top_p, min_p, stream
+void sample(PyObject *const *a) {
+    const Call c("oscar_sample");
+    const at::Tensor &x = c.tensor("logits", a[0]);
+    if (x.dim() != 2) refuse(c.name + ": logits must be [rows, vocab]");
+    const int64_t rows = x.size(0), vocab = x.size(1);
+    const at::ScalarType t = x.scalar_type();
+    if (t != at::kFloat && t != at::kBFloat16 && t != at::kHalf)
+        refuse(c.name + ": logits must be torch.float32, torch.bfloat16 or torch.float16, not " + dtype_text(t));
+    c.check("logits", x, t, {rows, vocab});
+    if (rows && vocab > 1 && x.stride(1) != 1) refuse(c.name + ": a row's logits must lie together");
+    const int64_t stride = rows > 1 ? x.stride(0) : vocab;
+    const int32_t dtype = t == at::kFloat ? OSCAR_DTYPE_F32 : t == at::kHalf ? OSCAR_DTYPE_F16 : OSCAR_DTYPE_BF16;
+    const float *temp = c.at<float>("temperature", a[1], at::kFloat, {rows}), *u = c.at<float>("u", a[2], at::kFloat, {rows});
+    int32_t *tokens = c.at<int32_t>("tokens", a[3], at::kInt, {rows});
+    const int32_t *k = c.ints("top_k", a[4], rows);
+    const float *p = c.at<float>("top_p", a[5], at::kFloat, {rows}), *m = c.at<float>("min_p", a[6], at::kFloat, {rows});
+    const void *logits = x.data_ptr();
+    void *st = c.stream(a[7]);
+    c.done(unlocked(g_lib.oscar_sample, logits, dtype, stride, c.pages32(rows), c.pages32(vocab), temp, k, p, m, u, tokens, st));
+}
+
+// layout, target, draft, parents, node_begin, max_nodes, seq_len, accepted, path, tokens, new_len, pools, page_table, stream
+void tree_accept(PyObject *const *a) {
+    const oscar_layout_t layout_ = layout(a[0]), *L = &layout_;
+    const Call c("oscar_tree_accept");
+    const at::Tensor &t = c.tensor("target", a[1]), &len = c.tensor("seq_len", a[6]), &way = c.tensor("path", a[8]);
+    const int64_t n = t.dim() ? t.size(0) : 0, batch = len.dim() ? len.size(0) : 0, stride = way.dim() ? way.size(way.dim() - 1) : 0;
+    const int32_t *target = c.ints("target", a[1], n), *draft = c.ints("draft", a[2], n), *parents = c.ints("parents", a[3], n);
+    const int32_t *begin = c.ints("node_begin", a[4], batch + 1), nodes = whole(a[5]), *T = c.ints("seq_len", a[6], batch);
+    int32_t *accepted = c.at<int32_t>("accepted", a[7], at::kInt, {batch}), *path = c.at<int32_t>("path", a[8], at::kInt, {batch, stride});
+    int32_t *tokens = c.at<int32_t>("tokens", a[9], at::kInt, {batch, stride}), *new_len = c.at<int32_t>("new_len", a[10], at::kInt, {batch});
+    struct Held {
+        PyObject *o;
+        ~Held() { Py_XDECREF(o); }
+    } all{PySequence_Tuple(a[11])};
+    if (!all.o) throw Refused();
+    std::vector<oscar_bf16_pool_t> pools;
+    for (Py_ssize_t i = 0; i < PyTuple_GET_SIZE(all.o); ++i) pools.push_back(c.bf16(L, PyTuple_GET_ITEM(all.o, i)));
+    const oscar_bf16_pool_t *pool = pools.data();
+    int64_t tables = batch, max_pages = 0;
+    if (a[12] != Py_None) c.table(a[12], &tables, &max_pages);
+    const int32_t *pt = c.pages("page_table", a[12], batch, max_pages);
+    void *st = c.stream(a[13]);
+    c.done(unlocked(g_lib.oscar_tree_accept, L, target, draft, parents, c.pages32(n), begin, nodes, T, c.pages32(batch), accepted, path, tokens, c.pages32(stride),
+                    new_len, pool, c.pages32((int64_t)pools.size()), pt, c.pages32(max_pages), st));
+}
+
 // Python entry: a fixed number of positional arguments; no C++ exception leaves it.
 template <void (*F)(PyObject *const *), int N>
 PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
@@ -368,7 +453,7 @@ PyObject *connect(PyObject *, PyObject *const *args, Py_ssize_t n) {
 
 #define ENTRY(f, n) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<f, n>)), METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {ENTRY(append_kv, 17), ENTRY(demote_int4, 10), ENTRY(promote_int4, 8), ENTRY(decode_attention_int4, 15),
-                           ENTRY(attention_mass_int4, 12), ENTRY(evict_int4, 12), 
+                           ENTRY(attention_mass_int4, 12), ENTRY(evict_int4, 12), ENTRY(tree_attention_int4, 16), ENTRY(sample, 8), ENTRY(tree_accept, 14),
                            {"connect", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&connect)), METH_FASTCALL, nullptr}, {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_marshal", "Argument checks of the INT4 entry points.", -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -1,0 +1,52 @@
+// What the tree attention kernels take, shared by them and the merge.
+#pragma once
+
+#include <cuda.h>
+
+#include "ptx.cuh"
+#include "tree.cuh"
+
+namespace oscar {
+
+constexpr int kBlock4 = 32;                      // tokens of one box of the INT4 pool
+
+struct TreeArgs {
+    const uint16_t *q;
+    TreeInput t;
+    const int32_t *mask;
+    int mask_words;
+    Bf16PoolView bf;
+    const int32_t *bpt;
+    const uint16_t *sz;
+    int i4_pages;
+    const int32_t *ipt;
+    int max_pages, page_shift, n_kv, G, sink;
+    const int32_t *seq_len, *hist_end;
+    float scale2;
+    PartialsView part;                           // rows are (node row, query head)
+    uint16_t *o;
+    float *lse;
+    int32_t *status;
+};
+
+// A request's lengths and nodes as every kernel of the call reads them; n = 0: it is skipped.
+struct TreeRequest {
+    int first, n, T, he;
+    __device__ __forceinline__ TreeRequest(const TreeArgs &a, int b) {
+        n = read_nodes(a.t, b, a.status, first);
+        T = he = 0;
+        if (n == 0) return;
+        read_lengths(a.seq_len, a.hist_end, b, a.sink, a.max_pages << a.page_shift, a.status, T, he);
+        if (T + n > a.max_pages << a.page_shift) {
+            if (threadIdx.x == 0) flag_status(a.status, OSCAR_DEV_BAD_LENGTH);
+            n = 0;
+        }
+    }
+};
+
+// Row index of (node row, query head) in out, lse and, times S + 1, in the partials.
+__device__ __forceinline__ size_t tree_row(const TreeArgs &a, const TreeRequest &r, int h, int row) {
+    return ((size_t)(r.first + row / a.G) * a.n_kv + h) * a.G + row % a.G;
+}
+
+}  // namespace oscar
