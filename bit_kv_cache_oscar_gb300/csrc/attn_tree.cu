@@ -537,25 +537,31 @@ __device__ __forceinline__ void history_warp(const TreeArgs &a, const CUtensorMa
     }
 }
 
-// grid ((S + 1) x row tiles, Hkv, batch), the row tiles of a split next to each other: they read the same history
+// grid (slots x row tiles, Hkv, batch), slots slot0 .. S, the row tiles of a slot next to each other: they read the same rows.
+// slot0 = S (the BF16 rows alone): launched behind tree_tc_kernel, which starts it once what comes before both is done; it
+// reads none of that one's results, but does not end before it.
 template <int NG>
 __global__ void __launch_bounds__(kW * 32, 1)
-    tree_kernel(TreeArgs a, int tiles, const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
+    tree_kernel(TreeArgs a, int tiles, int slot0, const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
     using R = Ring<NG>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t bars[kW * R::n];
     __shared__ float wf[kW * kTile], wM[kTile];
     uint8_t *smem = smem_raw + ((1024u - (saddr(smem_raw) & 1023u)) & 1023u);
-    const int slot = blockIdx.x / tiles, row0 = blockIdx.x % tiles * kTile, h = blockIdx.y, b = blockIdx.z, S = a.part.S;
+    const int slot = slot0 + blockIdx.x / tiles, row0 = blockIdx.x % tiles * kTile, h = blockIdx.y, b = blockIdx.z, S = a.part.S;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (lane == 0)
         for (int i = 0; i < R::n; ++i) mbar_init(saddr(&bars[warp * R::n + i]), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     __syncwarp();
-    pdl_wait();
+    const bool behind = slot0 == S;
+    if (!behind) pdl_wait();
     const TreeRequest rq(a, b);
     const int rows = min(kTile, rq.n * a.G - row0);
-    if (rows <= 0) return;
+    if (rows <= 0) {
+        if (behind) pdl_wait();
+        return;
+    }
     Rows x;
     clear(x);
     if (slot == S)
@@ -608,6 +614,7 @@ __global__ void __launch_bounds__(kW * 32, 1)
             a.part.l[at] = L;
         }
     }
+    if (behind) pdl_wait();
 }
 
 // A warp takes a (node row, query head): its slots in ascending order, four channels a lane, eight slots on their way.
@@ -662,36 +669,44 @@ bool rows_tensor_map(CUtensorMap *tm, const uint8_t *base, long long rows, int b
 }
 
 template <int NG>
-cudaError_t launch_rows(const TreeArgs &a, int tiles, const CUtensorMap &tmk, const CUtensorMap &tmv, int batch, cudaStream_t st) {
+cudaError_t launch_rows(const TreeArgs &a, int tiles, int slot0, const CUtensorMap &tmk, const CUtensorMap &tmv, int batch, cudaStream_t st) {
     const int join = (2 * kW * kTile + kW * kTile * kResRow) * 4, smem = std::max(Ring<NG>::total, join) + 1024;
     auto kern = tree_kernel<NG>;
     if (cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void *>(kern), smem)) return e;
-    return launch_ahead(kern, dim3((a.part.S + 1) * tiles, a.n_kv, batch), kW * 32, smem, st, a, tiles, tmk, tmv);
+    return launch_ahead(kern, dim3((a.part.S + 1 - slot0) * tiles, a.n_kv, batch), kW * 32, smem, st, a, tiles, slot0, tmk, tmv);
 }
 
 }  // namespace
 
+// Rows of 16 on mma.sync up to 32 query rows a kv head, of 128 on tcgen05 from there on.
+static bool on_tcgen05(const oscar_layout_t &L, int max_nodes) { return L.group == 128 && max_nodes * L.gqa > 16; }
+
 int suggest_splits_tree(const oscar_layout_t &L, int batch, int max_nodes, int max_hist, int sm_count) {
-    const long long tiles = (max_nodes * (long long)L.gqa + kTile - 1) / kTile, units = (long long)batch * L.n_kv_heads * tiles;
-    long long want = std::max(1LL, sm_count / units);
+    const long long rows = max_nodes * (long long)L.gqa, tile = on_tcgen05(L, max_nodes) ? 128 : kTile;
+    const long long units = (long long)batch * L.n_kv_heads * ((rows + tile - 1) / tile);
+    long long want = std::max(1LL, (sm_count - 8) / units);
     want = std::min(want, (max_hist + 511LL) / 512);
     return (int)std::max(1LL, std::min(want, 1024LL));
 }
 
 cudaError_t launch_tree_attention(const oscar_layout_t &L, const Attn4Input &in, const TreeInput &t, const int32_t *mask, int mask_words,
                                   int batch, PartialsView part, uint16_t *out, float *lse, int32_t *status, cudaStream_t st) {
-    TreeArgs a{in.q, t, mask, mask_words, in.bf, in.bpt, in.i4.scale_zero, in.i4.n_pages, in.ipt, in.max_pages, page_shift(L), L.n_kv_heads, L.gqa,
+    TreeArgs a{in.q, t, mask, mask_words, in.bf, in.bpt, in.i4.codes_k, in.i4.codes_v, in.i4.scale_zero, in.i4.n_pages, in.ipt, in.max_pages, page_shift(L), L.n_kv_heads, L.gqa,
                L.sink, in.seq_len, in.hist_end, in.sm_scale * kLog2e, part, out, lse, status};
     CUtensorMap tmk, tmv;
     const long long rows = (long long)in.i4.n_pages * L.n_kv_heads * L.page_size;
     const int box = L.page_size < kBlock4 ? L.page_size : kBlock4;
     if (!rows_tensor_map(&tmk, in.i4.codes_k, rows, box) || !rows_tensor_map(&tmv, in.i4.codes_v, rows, box)) return cudaErrorInvalidValue;
     const int tiles = (t.max_nodes * L.gqa + kTile - 1) / kTile;
+    const bool tc = on_tcgen05(L, t.max_nodes);
+    if (tc)
+        if (cudaError_t e = launch_tree_history_tc(a, t.max_nodes * L.gqa, batch, st)) return e;
+    const int slot0 = tc ? part.S : 0;
     cudaError_t e;
     switch (L.group) {
-        case 32: e = launch_rows<4>(a, tiles, tmk, tmv, batch, st); break;
-        case 64: e = launch_rows<2>(a, tiles, tmk, tmv, batch, st); break;
-        default: e = launch_rows<1>(a, tiles, tmk, tmv, batch, st); break;
+        case 32: e = launch_rows<4>(a, tiles, slot0, tmk, tmv, batch, st); break;
+        case 64: e = launch_rows<2>(a, tiles, slot0, tmk, tmv, batch, st); break;
+        default: e = launch_rows<1>(a, tiles, slot0, tmk, tmv, batch, st); break;
     }
     if (e) return e;
     return launch_ahead(tree_merge_kernel, dim3((t.max_nodes * L.n_kv_heads * L.gqa + 3) / 4, batch), 128, 0, st, a);

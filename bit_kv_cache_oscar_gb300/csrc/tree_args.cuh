@@ -17,6 +17,7 @@ struct TreeArgs {
     int mask_words;
     Bf16PoolView bf;
     const int32_t *bpt;
+    const uint8_t *codes_k, *codes_v;
     const uint16_t *sz;
     int i4_pages;
     const int32_t *ipt;
@@ -48,5 +49,9 @@ struct TreeRequest {
 __device__ __forceinline__ size_t tree_row(const TreeArgs &a, const TreeRequest &r, int h, int row) {
     return ((size_t)(r.first + row / a.G) * a.n_kv + h) * a.G + row % a.G;
 }
+
+// The history's slots on the 5th-generation tensor cores (group 128), 128 query rows of a kv head at a time.  The kernel lets its
+// successor in the stream start before it ends: tree_kernel alone may be launched after it, which waits for it at its end.
+cudaError_t launch_tree_history_tc(const TreeArgs &a, int max_rows, int batch, cudaStream_t st);
 
 }  // namespace oscar
