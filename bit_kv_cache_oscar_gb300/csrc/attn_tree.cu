@@ -685,6 +685,7 @@ int suggest_splits_tree(const oscar_layout_t &L, int batch, int max_nodes, int m
     const long long rows = max_nodes * (long long)L.gqa, tile = on_tcgen05(L, max_nodes) ? 128 : kTile;
     const long long units = (long long)batch * L.n_kv_heads * ((rows + tile - 1) / tile);
     long long want = std::max(1LL, (sm_count - 8) / units);
+    if (max_hist > want * 16384) want = std::max(want, std::min(max_hist / 8192LL, 12LL * sm_count / units));
     want = std::min(want, (max_hist + 511LL) / 512);
     return (int)std::max(1LL, std::min(want, 1024LL));
 }

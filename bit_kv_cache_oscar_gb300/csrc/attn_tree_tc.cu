@@ -2,12 +2,11 @@
 // tensor cores: the history's slots of the partials for 128 query rows of a kv head at a time, group 128.
 //
 // Per 128 positions, with f16 operands and fp32 sums in tensor memory (tcgen05, M128 N128 K16, eight steps each):
-//   D[row][t] = sum_c Q'[row][c] n_t,c           the query rows by the codes as subnormals n 2^-24 (odd nibbles: 16 n)
+//   D[row][t] = sum_c Q'[row][c] n_t,c           the query rows (tensor memory) by the codes as subnormals n 2^-24 (odd nibbles: 16 n)
 //   e = f s_t D + z_t zq_row - M_row,  p = 2^e   f undoes the scalings, zq = sm sum_c q_c, M the row's reference
 //   O[row][c] += sum_t (p s'_t) (n'_t,c - 8),  l += p,  zs += p (z'_t + 8 s'_t)
-// A product p s' is one f16 number, 2^-12 relative; M is raised whenever one passes 2^15 (then brought to about 2^8) or p passes
-// 2^100, so that the largest p s' so far, not the largest p, sits near the top of f16's range.  M moves in whole steps: what was
-// formed under the old one is brought to the new one exactly.  Codes are centred for the reason given
+// A product p s' is one f16 number, 2^-12 relative; M is raised whenever one passes 2^15 (then brought to 2^8) or p passes 2^110,
+// so that the largest p s' so far, not the largest p, sits near the top of f16's range.  Codes are centred for the reason given
 // in attn_tree.cu.  Both operands of codes lie in shared memory as they come, a position's channels together: K-major for the
 // logits, MN-major for the values, so both are unpacked the same way.
 //
@@ -15,10 +14,9 @@
 // the positions; its p s' elsewhere are zeros.  So all softmax warps work however few rows there are, and the copies' results are
 // joined like splits.
 //
-// One CTA an SM: warps 0-3 softmax of the even tiles, 4-7 of the odd ones (a warp a lane quarter), 8-11 unpack keys, 12-15 values,
-// 16 copies, 17 issues the products.  The two groups of softmax warps have references, sums and O of their own, joined at the end,
-// so that nothing but the tensor cores passes from one tile to the next.  Two buffers of unpacked codes; p s' takes the place of
-// its logits.
+// One CTA an SM: warps 0-7 softmax (two per lane quarter, half of the positions each, under one reference), 8-11 unpack keys,
+// 12-15 values, 16 copies, 17 issues the products; logits of a tile are formed while the softmax of the tile before runs.  Two
+// buffers of unpacked codes and of logits; p s' takes the place of its logits.
 
 #include <cuda_fp16.h>
 
@@ -29,7 +27,7 @@ namespace {
 
 constexpr int kT = 128;                          // positions of a tile
 constexpr int kR = 128;                          // query rows of a CTA
-constexpr int kStages = 2;
+constexpr int kStages = 3;
 constexpr int kSoftWarps = 8, kUnpackWarps = 4;  // (unpack: of keys, and of values)
 constexpr int kThreads = 32 * (kSoftWarps + 2 * kUnpackWarps + 2);
 constexpr int kSzBuffers = 4;
@@ -37,16 +35,17 @@ constexpr int kOperand = kT * kHeadDim * 2;      // 32 KB
 constexpr int kHalf = kOperand / 2;              // its channels 0..63
 constexpr int kStageCodes = kT * kRow4;          // 8 KB
 constexpr int kStageBytes = 2 * kStageCodes + kT * 8;
-constexpr int kOffK = 0, kOffV = 2 * kOperand, kOffQ = 4 * kOperand, kOffStage = 5 * kOperand;
+constexpr int kOffK = 0, kOffV = 2 * kOperand, kOffStage = 4 * kOperand;
 constexpr int kOffSz = kOffStage + kStages * kStageBytes;          // [buffers][2][64] float4
 constexpr int kSzBytes = 2 * kT / 2 * 16;
 constexpr int kOffMeta = kOffSz + kSzBuffers * kSzBytes;           // barriers, piece masks, TMEM address
-constexpr int kSmem = kOffMeta + 512 + 1024;
+constexpr int kOffPair = kOffMeta + 512;         // [4 quarters][2][32] float2
+constexpr int kSmem = kOffPair + 4 * 2 * 32 * 8 + 1024;
 constexpr int kResRow = kHeadDim + 4;
-constexpr uint32_t kColS = 0, kColO = 256;      // [2][128] each
+constexpr uint32_t kColS = 0, kColO = 256, kColQ = 384;
 constexpr float kNoRef = -1e30f;
-constexpr float kMostP = 0x1p100f;              // of the sum of 32 p
-constexpr float kNewW = 8.f, kNewP = 80.f;       // a new reference brings p s' to 2^8 at most, p to 2^80
+constexpr float kMostW = 0x1p15f, kMostP = 0x1p110f;
+constexpr float kNewW = 8.f, kNewP = 100.f;      // a new reference brings p s' to 2^8 at most, p to 2^100
 constexpr uint32_t kIdesc = (1u << 4) | ((uint32_t)(kT >> 3) << 17) | ((uint32_t)(kR >> 4) << 24);      // f16, f16, fp32
 constexpr uint32_t kIdescMN = kIdesc | (1u << 16);                                                      // B MN-major
 constexpr uint32_t kM0 = 0x000F000Fu, kM1 = 0x00F000F0u;
@@ -61,7 +60,7 @@ __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity) {
 struct Meta {
     uint64_t full[kStages], empty[kStages], kready[2], vready[2], kfree[2], vfree[2], szready[kSzBuffers], szfree[kSzBuffers], sfull[2], pready[2], pvdone;
     uint32_t ok[kStages];                        // pieces of 16 positions that were copied
-    uint32_t masked[kSzBuffers], valid[kSzBuffers][4];               // of the tile whose scales are there: some position is unusable; bits of usable ones
+    alignas(8) uint32_t valid[kSzBuffers][4], masked[kSzBuffers];    // of the tile whose scales are there: bits of usable positions; some are not
     float max_q;
     uint32_t tmem;
 };
@@ -80,22 +79,32 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
         ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                 : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
-                 ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
-}
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
           "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t *r) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                 ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+// The two softmax warps of a lane quarter.
+__device__ __forceinline__ void pair_sync(int quarter) { asm volatile("bar.sync %0, 64;" ::"r"(quarter + 1) : "memory"); }
+__device__ __forceinline__ bool pair_any(int quarter, bool x) {
+    uint32_t r;
+    asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, %2, 64, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+                 : "=r"(r)
+                 : "r"((uint32_t)x), "r"(quarter + 1)
+                 : "memory");
+    return r != 0;
 }
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r) {
     asm volatile(
@@ -171,149 +180,168 @@ struct RowState {
     float zq, M, l, zs;
 };
 
-// 32 positions of a tile: logits from D in r, p s' packed in w, the sums of p and p z in l and zs; true where the row's reference
-// is too low.  sk: f s | z of the keys, sv: s' | z' + 8 s' of the values, two positions each.
-template <bool FULL>
-__device__ __forceinline__ bool chunk_softmax(const RowState &st, const float4 *sk, const float4 *sv, const uint32_t (&r)[32], uint32_t valid,
-                                              uint32_t (&w)[16], float &l, float &zs) {
+// The logits (less the reference), base 2, of two positions: D in d0, d1, the constants of pair j at sk.
+__device__ __forceinline__ f2 shifted_logits(const float4 *sk, int j, uint32_t d0, uint32_t d1, f2 zq2, f2 m2) {
+    const float4 c = sk[j];
+    return fma2(pair(c.x, c.y), pair(__uint_as_float(d0), __uint_as_float(d1)), fma2(pair(c.z, c.w), zq2, m2));
+}
+
+// A warp's part of a tile, NU x 16 positions: tS the first one's logits, sk: f s | z of the keys, sv: s' | z' + 8 s' of the values
+// (two positions each), valid: the bits of usable positions.
+template <int NU>
+struct Unit {
+    uint32_t tS;
+    const float4 *sk, *sv;
+    uint64_t valid;
+};
+
+// p s' packed in w, the sums in l and zs; true where a reference is due.
+template <int NU, bool FULL>
+__device__ __forceinline__ bool tile_softmax(const RowState &st, const Unit<NU> &x, uint32_t (&w)[NU * 8], float &l, float &zs) {
     const f2 zq2 = pair(st.zq, st.zq), m2 = pair(-st.M, -st.M);
     f2 l2[2] = {0ull, 0ull}, z2[2] = {0ull, 0ull};
     __half2 most = __half2half2(__ushort_as_half(0));
+    uint32_t r[2][16];
+    tmem_ld16(x.tS, r[0]);
+    tmem_ld_wait();
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-        const float4 c = sk[j], cv = sv[j];
-        float e0, e1, w0, w1;
-        unpair(fma2(pair(c.x, c.y), pair(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), fma2(pair(c.z, c.w), zq2, m2)), e0, e1);
-        if (!FULL) {
-            if (!((valid >> (2 * j)) & 1)) e0 = -INFINITY;
-            if (!((valid >> (2 * j + 1)) & 1)) e1 = -INFINITY;
+    for (int u = 0; u < NU; ++u) {
+        if (u + 1 < NU) tmem_ld16(x.tS + 16 * (u + 1), r[(u + 1) & 1]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            float e0, e1, w0, w1;
+            unpair(shifted_logits(x.sk, 8 * u + j, r[u & 1][2 * j], r[u & 1][2 * j + 1], zq2, m2), e0, e1);
+            if (!FULL) {
+                if (!((x.valid >> (16 * u + 2 * j)) & 1)) e0 = -INFINITY;
+                if (!((x.valid >> (16 * u + 2 * j + 1)) & 1)) e1 = -INFINITY;
+            }
+            const f2 p = pair(ex2_approx(e0), ex2_approx(e1));
+            const float4 cv = x.sv[8 * u + j];
+            l2[j & 1] = add2(l2[j & 1], p);
+            z2[j & 1] = fma2(p, pair(cv.z, cv.w), z2[j & 1]);
+            unpair(mul2(p, pair(cv.x, cv.y)), w0, w1);
+            const __half2 h = __floats2half2_rn(w0, w1);
+            most = __hmax2(most, h);
+            w[8 * u + j] = *reinterpret_cast<const uint32_t *>(&h);
         }
-        const f2 p = pair(ex2_approx(e0), ex2_approx(e1));
-        l2[j & 1] = add2(l2[j & 1], p);
-        z2[j & 1] = fma2(p, pair(cv.z, cv.w), z2[j & 1]);
-        unpair(mul2(p, pair(cv.x, cv.y)), w0, w1);
-        const __half2 h = __floats2half2_rn(w0, w1);
-        most = __hmax2(most, h);
-        w[j] = *reinterpret_cast<const uint32_t *>(&h);
+        if (u + 1 < NU) tmem_ld_wait();
     }
     float a, b;
     unpair(add2(l2[0], l2[1]), a, b);
     l = a + b;
     unpair(add2(z2[0], z2[1]), a, b);
     zs = a + b;
-    return fmaxf(__low2float(most), __high2float(most)) >= 32768.f || l >= kMostP;
+    return fmaxf(__low2float(most), __high2float(most)) >= kMostW || l >= kMostP;
 }
 
-// A reference that serves 32 positions too, for the rows of the warp that need one, and what was formed under the old one brought
-// to it: the sums, O (has_o; this tile's logits were issued behind the product that last wrote it) and this tile's `done` chunks
-// of p s' before.  Rare, and kept out of the loop's registers: the logits are read again at tL.
-__device__ __noinline__ RowState new_reference(RowState st, uint32_t tL, uint32_t tO, bool has_o, uint32_t tP, int done, const float4 *sk,
-                                               const float4 *sv, uint32_t valid) {
+// New references for the rows of the pair of warps that need one, and what was summed under the old ones brought to them: each
+// warp takes half of O's columns.
+template <int NU>
+__device__ __forceinline__ void new_reference(RowState &st, const Unit<NU> &x, uint32_t tO, bool has_o, int quarter, int half, int lane,
+                                              float2 *pairs) {
     float top = -INFINITY, topw = -INFINITY;     // largest logit, largest logit + log2 s'
     const f2 zq2 = pair(st.zq, st.zq);
 #pragma unroll 1
-    for (int u = 0; u < 4; ++u) {
+    for (int u = 0; u < 2 * NU; ++u) {
         uint32_t r[8];
-        tmem_ld8(tL + 8 * u, r);
+        tmem_ld8(x.tS + 8 * u, r);
         tmem_ld_wait();
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const float4 c = sk[4 * u + j], cv = sv[4 * u + j];
             float e[2];
-            unpair(fma2(pair(c.x, c.y), pair(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), mul2(pair(c.z, c.w), zq2)), e[0], e[1]);
+            unpair(shifted_logits(x.sk, 4 * u + j, r[2 * j], r[2 * j + 1], zq2, 0ull), e[0], e[1]);
+            const float4 cv = x.sv[4 * u + j];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                if (!((valid >> (8 * u + 2 * j + k)) & 1)) continue;
+                if (!((x.valid >> (8 * u + 2 * j + k)) & 1)) continue;
                 top = fmaxf(top, e[k]);
                 topw = fmaxf(topw, e[k] + __log2f(k ? cv.y : cv.x));
             }
         }
     }
-    const float M = st.M;
-    // kept where it will do, within what the positions are checked for less a margin for rounding
-    if (topw - M >= 14.9f || top - M >= 94.f) {
-        const float want = ceilf(fmaxf(topw - kNewW, top - kNewP));
-        st.M = M == kNoRef ? want : fmaxf(M, want);
-    }
-    const int down = __float2int_rn(M - st.M);                   // (whole, or far below)
-    const float f = down < -126 ? 0.f : __uint_as_float((uint32_t)(down + 127) << 23);
+    pairs[(quarter * 2 + half) * 32 + lane] = make_float2(top, topw);
+    pair_sync(quarter);
+    const float2 other = pairs[(quarter * 2 + (half ^ 1)) * 32 + lane];
+    top = fmaxf(top, other.x);
+    topw = fmaxf(topw, other.y);
+    float M = st.M;
+    // kept where it will do: 2^(topw - M) and 2^(top - M) within the limits the tile is checked for, with a margin for rounding
+    if (topw - M >= 14.9f || top - M >= 102.f) M = fmaxf(M, fmaxf(topw - kNewW, top - kNewP));
+    const float f = ex2_approx(st.M - M);
+    st.M = M;
     st.l *= f;
     st.zs *= f;
-    if (has_o)
+    if (!has_o) return;
 #pragma unroll 1
-        for (int k = 0; k < 16; ++k) {
-            uint32_t o[8];
-            tmem_ld8(tO + 8 * k, o);
-            tmem_ld_wait();
-#pragma unroll
-            for (int j = 0; j < 8; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-            tmem_st8(tO + 8 * k, o);
-        }
-    const __half2 fh = __float2half2_rn(f);
-#pragma unroll 1
-    for (int k = 0; k < 2 * done; ++k) {
-        uint32_t o[8];
-        tmem_ld8(tP + 8 * k, o);
+    for (int c = 0; c < 8; ++c) {
+        uint32_t r[8];
+        tmem_ld8(tO + 64 * half + 8 * c, r);
         tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const __half2 h = __hmul2(*reinterpret_cast<const __half2 *>(&o[j]), fh);
-            o[j] = *reinterpret_cast<const uint32_t *>(&h);
-        }
-        tmem_st8(tP + 8 * k, o);
+        for (int j = 0; j < 8; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * f);
+        tmem_st8(tO + 64 * half + 8 * c, r);
     }
     tmem_st_wait();
-    return st;
 }
 
 template <int REP>
 __device__ __forceinline__ void softmax_loop(const TreeArgs &a, const Tiles &ti, Meta &mt, uint8_t *sm, uint32_t tmem, int warp, int lane,
                                              RowState &st) {
-    constexpr int NCH = 4 / REP;                 // chunks of 32 positions
-    const int quarter = warp & 3, group = warp >> 2;
-    const int first = REP == 1 ? 0 : REP == 2 ? 2 * (quarter >> 1) : quarter;          // this copy's first chunk
-    const uint32_t lanes = (uint32_t)(32 * quarter) << 16, tS = tmem + kColS + 128 * group + lanes, tO = tmem + kColO + 128 * group + lanes;
-    for (int i = group; i < ti.n; i += 2) {
-        const int z = i % kSzBuffers;
-        if (!wait_for(saddr(&mt.sfull[group]), (i >> 1) & 1) || !wait_for(saddr(&mt.szready[z]), (i / kSzBuffers) & 1)) {
+    constexpr int NU = 4 / REP;                  // units of 16 positions
+    const int quarter = warp & 3, half = warp >> 2;
+    const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
+    const int copy = REP == 1 ? 0 : REP == 2 ? quarter >> 1 : quarter;
+    const int first = (2 * copy + half) * NU;    // this warp's first unit
+    float2 *pairs = reinterpret_cast<float2 *>(sm + kOffPair);
+    bool gone = false;
+    for (int i = 0; i < ti.n; ++i) {
+        const int b = i & 1, z = i % kSzBuffers;
+        const uint32_t ph = (i >> 1) & 1;
+        // a warp whose wait ran out waits no more, but goes on: its partner's barriers count it
+        if (!gone && !(wait_for(saddr(&mt.sfull[b]), ph) && wait_for(saddr(&mt.szready[z]), (i / kSzBuffers) & 1))) {
             if (lane == 0) flag_status(a.status, OSCAR_DEV_WAIT_TIMEOUT);
-            return;
+            gone = true;
         }
         tc_fence_after();
-        const float4 *sk = reinterpret_cast<const float4 *>(sm + kOffSz + z * kSzBytes) + 16 * first, *sv = sk + kT / 2;
+        Unit<NU> x;
+        const uint32_t tS = tmem + kColS + b * 128 + lanes;
+        x.tS = tS + 16 * first;
+        x.sk = reinterpret_cast<const float4 *>(sm + kOffSz + z * kSzBytes) + 8 * first;
+        x.sv = x.sk + kT / 2;
         const bool full = !mt.masked[z];
-#pragma unroll
-        for (int c = 0; c < NCH; ++c) {
-            uint32_t r[32], w[16];
-            float l, zs;
-            const uint32_t valid = full ? ~0u : mt.valid[z][first + c];
-            for (int again = 0; again < 3; ++again) {          // (once, or twice where a reference was due)
-                tmem_ld32(tS + 32 * (first + c), r);
-                tmem_ld_wait();
-                const bool due = full ? chunk_softmax<true>(st, sk + 16 * c, sv + 16 * c, r, valid, w, l, zs)
-                                      : chunk_softmax<false>(st, sk + 16 * c, sv + 16 * c, r, valid, w, l, zs);
-                if (!__any_sync(0xffffffffu, due)) break;
-                st = new_reference(st, tS + 32 * (first + c), tO, i >= 2, tS + 16 * first, c, sk + 16 * c, sv + 16 * c, valid);
+        x.valid = ~0ull;
+        if (!full) x.valid = *reinterpret_cast<const uint64_t *>(&mt.valid[z][2 * (first >> 2)]) >> (16 * (first & 3));
+        uint32_t w[NU * 8];
+        float l, zs;
+        auto form = [&] { return full ? tile_softmax<NU, true>(st, x, w, l, zs) : tile_softmax<NU, false>(st, x, w, l, zs); };
+        if (pair_any(quarter, form())) {
+            if (!gone && i > 0 && !wait_for(saddr(&mt.pvdone), (i - 1) & 1)) {
+                if (lane == 0) flag_status(a.status, OSCAR_DEV_WAIT_TIMEOUT);
+                gone = true;
             }
-            st.l += l;
-            st.zs += zs;
-            // p s' in the place of logits that were read: chunk k at columns 16 k .. + 15
-            tmem_st16(tS + 16 * (first + c), w);
+            tc_fence_after();
+            new_reference<NU>(st, x, tmem + kColO + lanes, i > 0, quarter, half, lane, pairs);
+            form();
+            pair_sync(quarter);                  // both are done with the logits
         }
+        st.l += l;
+        st.zs += zs;
+        // p s' in the logits' place, zeros where other copies of the row have theirs
+#pragma unroll
+        for (int u = 0; u < NU; ++u) tmem_st8(tS + 8 * (first + u), &w[8 * u]);
         if (REP > 1) {
-            // zeros where other copies of the row have theirs
-            uint32_t none[16];
+            uint32_t none[8];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) none[j] = 0u;
+            for (int j = 0; j < 8; ++j) none[j] = 0u;
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-                if (c / NCH * NCH != first) tmem_st16(tS + 16 * c, none);
+            for (int u = 0; u < 8; ++u)
+                if (u / (2 * NU) != copy && (u & 1) == half) tmem_st8(tS + 8 * u, none);
         }
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-            mbar_arrive(saddr(&mt.pready[group]));
+            mbar_arrive(saddr(&mt.pready[b]));
             mbar_arrive(saddr(&mt.szfree[z]));
         }
     }
@@ -420,7 +448,7 @@ __device__ __forceinline__ void copy_loop(const TreeArgs &a, const Tiles &ti, Me
 __device__ __forceinline__ void product_loop(const TreeArgs &a, const Tiles &ti, Meta &mt, uint32_t sb, uint32_t tmem) {
     uint32_t elected;
     asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(elected));
-    const uint64_t dq = sw128_kmajor_desc(sb + kOffQ), dk = sw128_kmajor_desc(sb + kOffK), dv = mn_desc(sb + kOffV);
+    const uint64_t dk = sw128_kmajor_desc(sb + kOffK), dv = mn_desc(sb + kOffV);
     auto values = [&](int j) {                   // O += p s' . codes of tile j
         const int b = j & 1;
         const uint32_t ph = (j >> 1) & 1;
@@ -428,12 +456,12 @@ __device__ __forceinline__ void product_loop(const TreeArgs &a, const Tiles &ti,
         tc_fence_after();
         if (elected) {
             const uint64_t d = dv + (uint64_t)(b * (kOperand >> 4));
-            const uint32_t p = tmem + kColS + b * 128, o = tmem + kColO + b * 128;
-            mma_ts(o, p, d, kIdescMN, j >= 2);
+            const uint32_t p = tmem + kColS + b * 128, o = tmem + kColO;
+            mma_ts(o, p, d, kIdescMN, j != 0);
 #pragma unroll
             for (int kk = 1; kk < kT / 16; ++kk) mma_ts(o, p + 8 * kk, d + (2048 >> 4) * kk, kIdescMN, 1);
             tc_commit(saddr(&mt.vfree[b]));
-            if (j == ti.n - 1) tc_commit(saddr(&mt.pvdone));
+            tc_commit(saddr(&mt.pvdone));
         }
         __syncwarp();
         return true;
@@ -445,12 +473,9 @@ __device__ __forceinline__ void product_loop(const TreeArgs &a, const Tiles &ti,
         tc_fence_after();
         if (elected) {
             const uint64_t d = dk + (uint64_t)(b * (kOperand >> 4));
-            const uint32_t s = tmem + kColS + b * 128;
+            const uint32_t s = tmem + kColS + b * 128, q = tmem + kColQ;
 #pragma unroll
-            for (int kk = 0; kk < kHeadDim / 16; ++kk) {
-                const uint32_t at = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
-                tc_mma_bf16(s, dq + at, d + at, kIdesc, kk != 0);
-            }
+            for (int kk = 0; kk < kHeadDim / 16; ++kk) mma_ts(s, q + 8 * kk, d + (((kk >> 2) * kHalf + (kk & 3) * 32) >> 4), kIdesc, kk != 0);
             tc_commit(saddr(&mt.kfree[b]));
             tc_commit(saddr(&mt.sfull[b]));
         }
@@ -484,11 +509,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(TreeArgs a, int bl
             mbar_init(saddr(&mt.kfree[i]), 1);
             mbar_init(saddr(&mt.vfree[i]), 1);
             mbar_init(saddr(&mt.sfull[i]), 1);
-            mbar_init(saddr(&mt.pready[i]), kSoftWarps / 2);
+            mbar_init(saddr(&mt.pready[i]), kSoftWarps);
         }
         for (int i = 0; i < kSzBuffers; ++i) {
             mbar_init(saddr(&mt.szready[i]), kUnpackWarps);
-            mbar_init(saddr(&mt.szfree[i]), kSoftWarps / 2);
+            mbar_init(saddr(&mt.szfree[i]), kSoftWarps);
         }
         mbar_init(saddr(&mt.pvdone), 1);
         mt.max_q = 0.f;
@@ -507,55 +532,51 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(TreeArgs a, int bl
     RowState st{0.f, kNoRef, 0.f, 0.f};
     float fac = 0.f;
     if (rows > 0 && ti.n > 0) {
-        // the query rows as f16 under one scaling, copies and all, in the order of the unpacked codes, odd nibbles' channels by 1/16:
-        // a warp takes 8 rows of the operand at a time, four lanes (32 channels each) a row
-        const int q = lane & 3;
-        float mx = 0.f;
-        for (int r = 8 * warp + (lane >> 2); r < rows; r += 8 * (kThreads / 32)) {
-            const uint4 *src = reinterpret_cast<const uint4 *>(a.q + tree_row(a, rq, h, row0 + r) * kHeadDim + 32 * q);
+        // the lane's query row, and the largest finite element of all rows: they share a scaling
+        const int row = (32 * (warp & 3) + lane) % pad;
+        const bool on = row < rows;
+        const uint4 *src = reinterpret_cast<const uint4 *>(a.q + (on ? tree_row(a, rq, h, row0 + row) * kHeadDim : 0));
+        float mx = 0.f, sum = 0.f;
+        if (warp < kSoftWarps) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint4 x = src[i];
-                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {    // (a row's infinities are its own matter)
-                    const float x0 = fabsf(lo16(w[e])), x1 = fabsf(hi16(w[e]));
-                    mx = fmaxf(mx, fmaxf(x0 < INFINITY ? x0 : 0.f, x1 < INFINITY ? x1 : 0.f));
-                }
-            }
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        if (lane == 0) atomicMax(reinterpret_cast<int *>(&mt.max_q), __float_as_int(mx));          // (not negative)
-        __syncthreads();
-        mx = mt.max_q;
-        const int ex = min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 117);                 // |q| < 2^(ex + 1)
-        const float m0 = __uint_as_float((uint32_t)(14 - ex + 127) << 23), m1 = m0 * 0.0625f;
-        fac = a.scale2 * __uint_as_float((uint32_t)(10 + ex + 127) << 23);                          // 2^24 / m0
-        float *zq = reinterpret_cast<float *>(sm + kOffSz);                                          // (before its first use)
-        for (int m = 8 * warp + (lane >> 2); m < kR; m += 8 * (kThreads / 32)) {
-            const int row = m % pad;
-            const bool on = row < rows;
-            const uint4 *src = reinterpret_cast<const uint4 *>(a.q + (on ? tree_row(a, rq, h, row0 + row) * kHeadDim + 32 * q : 0));
-            float sum = 0.f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < kHeadDim / 8; ++i) {
                 const uint4 x = on ? src[i] : make_uint4(0, 0, 0, 0);
                 const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) sum += lo16(w[e]) + hi16(w[e]);
-                const int chunk = 4 * q + i;
-                *reinterpret_cast<uint4 *>(sm + kOffQ + (chunk >> 3) * kHalf + (m >> 3) * 1024 + (m & 7) * 128 + (((chunk & 7) ^ (m & 7)) << 4)) =
-                    make_uint4(pack_h2(lo16(x.x) * m0, lo16(x.z) * m0), pack_h2(hi16(x.x) * m1, hi16(x.z) * m1), pack_h2(lo16(x.y) * m0, lo16(x.w) * m0),
-                               pack_h2(hi16(x.y) * m1, hi16(x.w) * m1));
+                for (int e = 0; e < 4; ++e) {
+                    const float x0 = fabsf(lo16(w[e])), x1 = fabsf(hi16(w[e]));
+                    mx = fmaxf(mx, fmaxf(x0 < INFINITY ? x0 : 0.f, x1 < INFINITY ? x1 : 0.f));
+                    sum += lo16(w[e]) + hi16(w[e]);
+                }
             }
-            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-            if (q == 0) zq[m] = sum * a.scale2;
+            st.zq = a.scale2 * sum;
+#pragma unroll
+            for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            if (lane == 0) atomicMax(reinterpret_cast<int *>(&mt.max_q), __float_as_int(mx));       // (not negative)
         }
-        fence_proxy_async_smem();
         __syncthreads();
-        if (warp < kSoftWarps) st.zq = zq[32 * (warp & 3) + lane];
+        mx = mt.max_q;
+        const int ex = min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 117);                  // |q| < 2^(ex + 1)
+        const float m0 = __uint_as_float((uint32_t)(14 - ex + 127) << 23), m1 = m0 * 0.0625f;
+        fac = a.scale2 * __uint_as_float((uint32_t)(10 + ex + 127) << 23);                           // 2^24 / m0
+        // as f16, in the order of the unpacked codes, odd nibbles' channels by 1/16
+        if (warp < kSoftWarps) {
+#pragma unroll
+        for (int ii = 0; ii < 2; ++ii) {         // each warp of a quarter one half
+            const int i = 2 * (warp >> 2) + ii;
+            uint32_t w[16];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint4 x = on ? src[4 * i + k] : make_uint4(0, 0, 0, 0);
+                w[4 * k + 0] = pack_h2(lo16(x.x) * m0, lo16(x.z) * m0);
+                w[4 * k + 1] = pack_h2(hi16(x.x) * m1, hi16(x.z) * m1);
+                w[4 * k + 2] = pack_h2(lo16(x.y) * m0, lo16(x.w) * m0);
+                w[4 * k + 3] = pack_h2(hi16(x.y) * m1, hi16(x.w) * m1);
+            }
+            tmem_st16(tmem + kColQ + ((uint32_t)(32 * (warp & 3)) << 16) + 16 * i, w);
+        }
+        tmem_st_wait();
+        }
     }
     tc_fence_before();
     __syncthreads();
@@ -565,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(TreeArgs a, int bl
             if (rep == 4) softmax_loop<4>(a, ti, mt, sm, tmem, warp, lane, st);
             else if (rep == 2) softmax_loop<2>(a, ti, mt, sm, tmem, warp, lane, st);
             else softmax_loop<1>(a, ti, mt, sm, tmem, warp, lane, st);
-            if (!wait_for(saddr(&mt.pvdone), 0) && lane == 0) flag_status(a.status, OSCAR_DEV_WAIT_TIMEOUT);
+            if (!wait_for(saddr(&mt.pvdone), (ti.n - 1) & 1) && lane == 0) flag_status(a.status, OSCAR_DEV_WAIT_TIMEOUT);
             tc_fence_after();
         } else if (warp < kSoftWarps + kUnpackWarps) {
             unpack_loop<false>(a, ti, mt, sm, threadIdx.x - 32 * kSoftWarps, lane, fac);
@@ -579,23 +600,28 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(TreeArgs a, int bl
     }
     __syncwarp();
     __syncthreads();                             // every product is done: results take the operands' place
-    float *res = reinterpret_cast<float *>(sm), *rm = res + 2 * kR * kResRow, *rl = rm + 2 * kR;
+    float *res = reinterpret_cast<float *>(sm), *rm = res + kR * kResRow, *rl = rm + kR, *rz = rl + 2 * kR;
+    const int half = warp >> 2, at = 32 * (warp & 3) + lane;
     if (warp < kSoftWarps && rows > 0) {
-        const int group = warp >> 2, at = 128 * group + 32 * (warp & 3) + lane;
-        rm[at] = st.l > 0.f || st.l != st.l ? st.M : -INFINITY;
-        rl[at] = st.l;
-        if (ti.n > group)
+        rl[half * kR + at] = st.l;
+        rz[half * kR + at] = st.zs;
+    }
+    __syncthreads();
+    if (warp < kSoftWarps && rows > 0) {
+        const float l = rl[at] + rl[kR + at], zs = rz[at] + rz[kR + at];
+        if (half == 0) rm[at] = l > 0.f || l != l ? st.M : -INFINITY;
+        if (ti.n > 0)
 #pragma unroll 1
-            for (int c = 0; c < 8; ++c) {
-                uint32_t r[16];
-                tmem_ld16(tmem + kColO + 128 * group + ((uint32_t)(32 * (warp & 3)) << 16) + 16 * c, r);
+            for (int c = 2 * half; c < 2 * half + 2; ++c) {
+                uint32_t r[32];
+                tmem_ld32(tmem + kColO + ((uint32_t)(32 * (warp & 3)) << 16) + 32 * c, r);
                 tmem_ld_wait();
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {    // a code word's columns are its channels 0 4 1 5 2 6 3 7
+                for (int k = 0; k < 4; ++k) {    // a code word's columns are its channels 0 4 1 5 2 6 3 7
                     float x[8];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) x[(j >> 1) + 4 * (j & 1)] = __uint_as_float(r[8 * k + j]) + st.zs;
-                    float *to = res + at * kResRow + 16 * c + 8 * k;
+                    for (int j = 0; j < 8; ++j) x[(j >> 1) + 4 * (j & 1)] = __uint_as_float(r[8 * k + j]) + zs;
+                    float *to = res + at * kResRow + 32 * c + 8 * k;
                     *reinterpret_cast<float4 *>(to) = make_float4(x[0], x[1], x[2], x[3]);
                     *reinterpret_cast<float4 *>(to + 4) = make_float4(x[4], x[5], x[6], x[7]);
                 }
@@ -603,17 +629,18 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(TreeArgs a, int bl
     }
     tc_fence_before();
     __syncthreads();
-    // a row's copies and groups joined, a warp a row
+    // a row's copies joined, a warp a row
     for (int row = warp; row < rows; row += kThreads / 32) {
         float M = -INFINITY;
-        for (int k = row; k < 2 * kR; k += pad) M = fmaxf(M, rm[k]);
+        for (int k = 0; k < rep; ++k) M = fmaxf(M, rm[row + k * pad]);
         float L = 0.f;
         float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int k = row; k < 2 * kR; k += pad) {
-            const float f = rm[k] != -INFINITY ? exp2f(rm[k] - M) : 0.f;
+        for (int k = 0; k < rep; ++k) {
+            const int from = row + k * pad;
+            const float f = rm[from] != -INFINITY ? exp2f(rm[from] - M) : 0.f;
             if (f == 0.f) continue;
-            const float4 x = *reinterpret_cast<const float4 *>(res + k * kResRow + 4 * lane);
-            L = fmaf(rl[k], f, L);
+            const float4 x = *reinterpret_cast<const float4 *>(res + from * kResRow + 4 * lane);
+            L = fmaf(rl[from] + rl[kR + from], f, L);
             A = make_float4(fmaf(x.x, f, A.x), fmaf(x.y, f, A.y), fmaf(x.z, f, A.z), fmaf(x.w, f, A.w));
         }
         const size_t to = tree_row(a, rq, h, row0 + row) * (S + 1) + slot;
