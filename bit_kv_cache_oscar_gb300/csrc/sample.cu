@@ -10,10 +10,11 @@
 // numbers have no order, so neither the number of CTAs nor atomics change a token, and are exact enough that u meets the same
 // token as in 64-bit arithmetic (a sum in fp32, 2^-24 off, would miss for one row in a hundred over a large vocabulary).
 //
-// A cluster of 1 to 8 CTAs takes a row and holds it in shared memory, so a row is read once.  A search goes through bins: first
-// 2,048 equal steps of y, whose order is the logits' order, then, within the bin that the target falls into, equal steps of the
-// logits' bits until a bin is one value.  The entries of that first bin are gathered into a list, which the later levels read
-// (unless they are too many: then the row again).  Weights in a bin are summed by 32-bit atomics on three parts of 15 bits.
+// A cluster of 1 to 8 CTAs takes a row and holds it in shared memory, so a row is read once.  The filters' search goes through
+// bins: 2,048 equal steps of y, whose order is the logits' order, counted (top-k) or weighed (top-p alone) by atomics; all entries up
+// to the bin that the target falls into go to the first CTA, which sorts them, cuts the order by every filter, sorts what is left by
+// index and draws.  Entries that are too many for that (flat rows, large top-k) take more levels of bins instead, within the bin
+// equal steps of the logits' bits until a bin is one value.  Weights in a bin are summed by 32-bit atomics on three parts of 15 bits.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -30,9 +31,20 @@ constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kBins = 2048;                          // 4 a thread
 constexpr float kDeep = 44.5f;                       // y from here on: weight zero
 constexpr float kBinScale = kBins / kDeep;
-constexpr int kList = 1024;                          // entries of a CTA's list
+constexpr int kList = 2048;                          // entries that one CTA sorts
+constexpr int kKeys = 1024;                          // entries of a CTA's list for the further levels
 constexpr int kUnit = 44;                            // weights in units of 2^-44
 constexpr int kLimb = 15;
+
+// 2^31 2^(-j / 256), each within 2^-21 of a unit before its rounding.
+struct Table {
+    uint32_t t[256];
+    constexpr Table() : t() {
+        double x = 2147483648.0;
+        for (int j = 0; j < 256; ++j, x *= 0.99729605608547012625765991384792) t[j] = (uint32_t)(x + 0.5);
+    }
+};
+__device__ constexpr Table kTable{};
 
 struct SampleArgs {
     SampleInput in;
@@ -81,11 +93,10 @@ struct Row {
     __device__ __forceinline__ float depth(float x) const { return x == top ? 0.f : __fmul_rn(__fsub_rn(top, x), ch); }
     __device__ __forceinline__ bool kept(float x, int i) const { return x > v || (x == v && i <= I); }
     __device__ __forceinline__ uint64_t weight(float x) const {
-        if (x == top) return 1ull << kUnit;
         const float d = __fsub_rn(top, x), bb = __fsub_rn(d, top);
         const float dl = __fsub_rn(__fsub_rn(top, __fsub_rn(d, bb)), __fadd_rn(x, bb));      // what d lacks, exactly
         const float y = __fmul_rn(d, ch);
-        if (!(y < kDeep)) return 0;                  // NaN among them: infinite d, or no d and an infinite temperature's 0
+        if (!(y < kDeep)) return x == top ? 1ull << kUnit : 0;       // NaN among them: infinities less themselves or by 0
         const float yl = __fmaf_rn(dl, ch, __fmaf_rn(d, cl, __fmaf_rn(d, ch, -y)));
         const float t = __fmaf_rn(y, 256.f, 12582912.f);
         const int k = __float_as_int(t) - 0x4B400000;
@@ -98,9 +109,15 @@ struct Row {
 };
 
 struct Shared {
-    uint32_t hist[4][kBins];                         // counts, weights' three parts
+    union {
+        uint32_t hist[4][kBins];                     // counts, weights' three parts
+        struct {
+            uint64_t list[kList], weight[kList];     // entries to sort; their weights
+        };
+        uint64_t steps[kWarps][32];                  // sums of each warp's steps through its vectors
+    };
     uint32_t table[256];
-    uint32_t list_key[kList];
+    uint32_t list_key[kKeys];
     uint64_t warp_sum[kWarps];                       // read by the cluster
     uint64_t scan[kWarps];
     float warp_top[kWarps];
@@ -108,8 +125,15 @@ struct Shared {
     uint32_t n_list, key_min, key_max;               // read by the cluster
     int pick_index;
     uint32_t bin;
-    uint64_t before;
+    uint64_t before, total;
+    // the row's arguments
+    float temp, ch, cl;
+    int top_k, min_mode;                             // min_p: 0 off, 1 top + min_off, 2 the largest logit, 3 one token
+    uint64_t p64, u64;
+    bool top_p;
+    double min_off;
 };
+constexpr int kSharedBytes = (sizeof(Shared) + 15) / 16 * 16;
 
 // A value of another CTA of the cluster.
 template <typename T>
@@ -176,18 +200,27 @@ struct Part {
 
     // The lowest index at which the running sum of f in index order reaches the target that goal(total) gives, kept within
     // 1 .. total; -1 where the total is 0.  All threads of all CTAs return it.
-    template <typename F, typename G>
-    __device__ __forceinline__ int pick(Shared &s, F f, G goal) const {
+    // LAST: the thread that finds it writes it to *token instead, and nobody else learns it (a total of 0 writes nothing).
+    template <bool LAST, typename F, typename G>
+    __device__ __forceinline__ int pick(Shared &s, F f, G goal, int32_t *token = nullptr) const {
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
         const int lo = (int)((long long)nv * warp / kWarps), hi = (int)((long long)nv * (warp + 1) / kWarps);
         uint64_t sum = 0;
-        for (int j = lo + lane; j < hi; j += 32) {
-            const uint4 x = vec[j];
-            const int i0 = begin - skip + j * VE;
+        int step = 0;
+        for (int j0 = lo; j0 < hi; j0 += 32, ++step) {
+            const int j = j0 + lane;
+            uint64_t mine = 0;
+            if (j < hi) {
+                const uint4 x = vec[j];
+                const int i0 = begin - skip + j * VE;
 #pragma unroll
-            for (int e = 0; e < VE; ++e) sum += f(T::get(x, e), i0 + e);
+                for (int e = 0; e < VE; ++e) mine += f(T::get(x, e), i0 + e);
+            }
+            if (__any_sync(0xffffffffu, mine != 0)) mine = warp_sum64(mine);
+            if (lane == 0) s.steps[warp][step] = mine;
+            sum += mine;
         }
-        sum = warp_sum64(sum);
+        __syncwarp();
         if (lane == 0) s.warp_sum[warp] = sum;
         if (threadIdx.x == 0) s.pick_index = -1;
         cluster_join();
@@ -203,33 +236,31 @@ struct Part {
         uint64_t target = goal(total);
         target = target < 1 ? 1 : target > total ? total : target;
         if (total > 0 && before < target && target <= before + sum) {        // one warp of the cluster
-            for (int j0 = lo; j0 < hi; j0 += 32) {
-                const int j = j0 + lane;
-                uint4 x = make_uint4(0, 0, 0, 0);
-                if (j < hi) x = vec[j];
-                const int i0 = begin - skip + j * VE;
-                uint64_t mine = 0;
+            const uint64_t mine = lane < step ? s.steps[warp][lane] : 0, upto = before + warp_scan64(mine, lane);
+            const int at = __ffs(__ballot_sync(0xffffffffu, upto >= target)) - 1;
+            before = __shfl_sync(0xffffffffu, upto - mine, at);
+            const int j = lo + 32 * at + lane, i0 = begin - skip + j * VE;
+            uint4 x = make_uint4(0, 0, 0, 0);
+            uint64_t w = 0;
+            if (j < hi) {
+                x = vec[j];
 #pragma unroll
-                for (int e = 0; e < VE; ++e) mine += j < hi ? f(T::get(x, e), i0 + e) : 0;
-                if (!__any_sync(0xffffffffu, mine > 0)) continue;
-                const uint64_t upto = before + warp_scan64(mine, lane);
-                const unsigned reached = __ballot_sync(0xffffffffu, upto >= target);
-                if (reached) {
-                    if (lane == __ffs(reached) - 1) {
-                        uint64_t at = upto - mine;
-                        int found = -1;
+                for (int e = 0; e < VE; ++e) w += f(T::get(x, e), i0 + e);
+            }
+            uint64_t to = before + warp_scan64(w, lane);
+            if (lane == __ffs(__ballot_sync(0xffffffffu, to >= target)) - 1) {
+                to -= w;
+                int found = -1;
 #pragma unroll
-                        for (int e = 0; e < VE; ++e) {
-                            at += f(T::get(x, e), i0 + e);
-                            if (found < 0 && at >= target) found = i0 + e;
-                        }
-                        s.pick_index = found;
-                    }
-                    break;
+                for (int e = 0; e < VE; ++e) {
+                    to += f(T::get(x, e), i0 + e);
+                    if (found < 0 && to >= target) found = i0 + e;
                 }
-                before = __shfl_sync(0xffffffffu, upto, 31);
+                if (LAST) *token = found;
+                else s.pick_index = found;
             }
         }
+        if (LAST) return total > 0;
         cluster_join();
         int found = -1;
         for (int k = 0; k < C; ++k) found = max(found, peer(&s.pick_index, k));
@@ -239,7 +270,8 @@ struct Part {
 
     // The bins of this search level, filled by every CTA: finds the first one up to which base and the weights reach the
     // target that goal(total) gives, and leaves it in s.bin with the weight before it in s.before.  False: no bin does.
-    template <bool MASS, typename G>
+    // LEAST: the bins of y hold counts, taken for the least weight that so many entries there can have.
+    template <bool MASS, bool LEAST = false, typename G>
     __device__ __forceinline__ bool find_bin(Shared &s, uint64_t base, G goal) const {
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b0 = threadIdx.x * 4;
         cluster_join();
@@ -262,6 +294,9 @@ struct Part {
                 w[3] += h.w;
             }
         }
+        if (LEAST)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] *= (uint64_t)(ex2_approx(kUnit - (b0 + i + 1) * (1.f / kBinScale)) * 0.999f);
         const uint64_t mine = w[0] + w[1] + w[2] + w[3];
         const uint64_t upto = warp_scan64(mine, lane);
         if (lane == 31) s.scan[warp] = upto;
@@ -274,6 +309,7 @@ struct Part {
             total += x;
         }
         const uint64_t target = goal(total);
+        if (threadIdx.x == 0) s.total = total;
         before += upto - mine;
         if (before < target && target <= before + mine) {
 #pragma unroll
@@ -289,26 +325,25 @@ struct Part {
         return s.bin < kBins;
     }
 
+    template <bool MASS>
     __device__ __forceinline__ void clear(Shared &s) const {
         uint4 *h = reinterpret_cast<uint4 *>(s.hist);
-        for (int i = threadIdx.x; i < 4 * kBins / 4; i += kThreads) h[i] = make_uint4(0, 0, 0, 0);
+        for (int i = threadIdx.x; i < (MASS ? 4 : 1) * kBins / 4; i += kThreads) h[i] = make_uint4(0, 0, 0, 0);
         __syncthreads();
     }
     template <bool MASS>
     static __device__ __forceinline__ void add(Shared &s, int bin, uint64_t w) {
+        atomicAdd(&s.hist[0][bin], 1u);
         if (MASS) {
             atomicAdd(&s.hist[1][bin], (uint32_t)w & ((1u << kLimb) - 1));
             atomicAdd(&s.hist[2][bin], (uint32_t)(w >> kLimb) & ((1u << kLimb) - 1));
             atomicAdd(&s.hist[3][bin], (uint32_t)(w >> (2 * kLimb)));
-        } else {
-            atomicAdd(&s.hist[0][bin], 1u);
         }
     }
-
-    // Narrows what is kept to the shortest prefix whose weight (1 a token, or w) reaches the target.
-    template <bool MASS, typename G>
-    __device__ __forceinline__ void cut(Shared &s, Row &row, G goal) const {
-        clear(s);
+    // The bins of y.
+    template <bool MASS>
+    __device__ __forceinline__ void depths(Shared &s, const Row &row) const {
+        clear<MASS>(s);
         each([&](float x, int i) {
             const float y = row.depth(x);
             if (y < kDeep && row.kept(x, i)) {
@@ -316,6 +351,12 @@ struct Part {
                 if (w) add<MASS>(s, min((int)(y * kBinScale), kBins - 1), w);
             }
         });
+    }
+
+    // Narrows what is kept to the shortest prefix whose weight (1 a token, or w) reaches the target.
+    template <bool MASS, typename G>
+    __device__ __forceinline__ void cut(Shared &s, Row &row, G goal) const {
+        depths<MASS>(s, row);
         uint64_t target = 0;
         if (!find_bin<MASS>(s, 0, [&](uint64_t total) { return target = goal(total); })) return;
         const int bin = s.bin;
@@ -338,7 +379,7 @@ struct Part {
             lo = min(lo, k);
             hi = max(hi, k);
             const uint32_t at = atomicAdd(&s.n_list, 1u);
-            if (at < kList) s.list_key[at] = k;
+            if (at < kKeys) s.list_key[at] = k;
         });
         __syncwarp();
         lo = __reduce_min_sync(0xffffffffu, lo);
@@ -357,11 +398,11 @@ struct Part {
         const uint32_t n = s.n_list;
         for (;;) {
             const int shift = hi > lo ? max(0, 32 - __clz(hi - lo) - 11) : 0;          // (hi - lo) >> shift < 2048
-            clear(s);
+            clear<MASS>(s);
             auto count = [&](uint32_t k) {
                 if (k >= lo && k <= hi) add<MASS>(s, (k - lo) >> shift, MASS ? row.weight(key_value(k)) : 1);
             };
-            if (n <= kList)
+            if (n <= kKeys)
                 for (uint32_t i = threadIdx.x; i < n; i += kThreads) count(s.list_key[i]);
             else
                 each([&](float x, int i) {
@@ -376,22 +417,132 @@ struct Part {
         // one value left: the first ties of it
         const float v = key_value(lo);
         const uint64_t each_w = MASS ? row.weight(v) : 1, ties = (target - before + each_w - 1) / each_w;
-        row.I = pick(s, [&](float x, int i) -> uint64_t { return x == v && row.kept(x, i); }, [&](uint64_t) { return ties; });
+        row.I = pick<false>(s, [&](float x, int i) -> uint64_t { return x == v && row.kept(x, i); }, [&](uint64_t) { return ties; });
         row.v = v;
     }
 };
 
+// The n entries of s.list (falling key | index) sorted upwards, the places behind them up to the next power of two filled up.
+__device__ __forceinline__ void sort_list(Shared &s, int n) {
+    int size = 2;
+    while (size < n) size *= 2;
+    for (int i = n + threadIdx.x; i < size; i += kThreads) s.list[i] = ~0ull;
+    __syncthreads();
+    for (int k = 2; k <= size; k *= 2)
+        for (int j = k / 2; j > 0; j /= 2) {
+            for (int i = threadIdx.x; i < size / 2; i += kThreads) {
+                const int x = 2 * i - (i & (j - 1)), y = x + j;
+                const uint64_t u = s.list[x], v = s.list[y];
+                if ((u > v) == ((x & k) == 0)) {
+                    s.list[x] = v;
+                    s.list[y] = u;
+                }
+            }
+            if (j > 32 || size > 2 * kThreads) __syncthreads();
+            else if (j > 1) __syncwarp();            // the next step's pairs of a warp are its own
+            else __syncthreads();
+        }
+}
+
+// Inclusive sums of four values a thread over the CTA, in thread order.
+__device__ __forceinline__ void block_scan(Shared &s, uint64_t (&x)[4]) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    x[1] += x[0];
+    x[2] += x[1];
+    x[3] += x[2];
+    uint64_t before = warp_scan64(x[3], lane);
+    if (lane == 31) s.scan[warp] = before;
+    before -= x[3];
+    __syncthreads();
+    for (int k = 0; k < warp; ++k) before += s.scan[k];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] += before;
+    __syncthreads();
+}
+
+// The draw from a row's first n entries, unsorted in s.list, by one CTA: total is what top-p is of, where the list does not hold it
+// all (0: the first k entries' weight).
+__device__ __forceinline__ int draw_list(Shared &s, const Row &row, int n, int k, uint64_t total) {
+    static_assert(kList == 4 * kThreads, "four entries a thread");
+    const int first = 4 * threadIdx.x;
+    sort_list(s, n);
+    int keep = min(n, k);
+    uint64_t sum[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        sum[e] = first + e < keep ? row.weight(key_value((uint32_t)(s.list[first + e] >> 32))) : 0;
+        s.weight[first + e] = sum[e];
+    }
+    block_scan(s, sum);
+    if (threadIdx.x == kThreads - 1 && total == 0) s.total = sum[3];
+    if (threadIdx.x == 0) s.n_list = keep;
+    __syncthreads();
+    if (s.top_p) {
+        const uint64_t z = total ? total : s.total;
+        uint64_t target = __umul64hi(z, s.p64) + (z * s.p64 != 0);
+        if (target < 1) target = 1;
+        uint64_t before = sum[0] - s.weight[first];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (before < target && sum[e] >= target) atomicMin(&s.n_list, (uint32_t)(first + e + 1));
+            before = sum[e];
+        }
+    }
+    // min-p: behind the entry before the first that is too small (row.v: the least logit)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (first + e > 0 && first + e < keep && (s.min_mode == 3 || key_value((uint32_t)(s.list[first + e] >> 32)) < row.v))
+            atomicMin(&s.n_list, (uint32_t)(first + e));
+    __syncthreads();
+    keep = s.n_list;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (first + e == keep - 1) s.before = __umul64hi(sum[e], s.u64) + 1;
+    // by index, with the place that holds the weight
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (first + e < keep) s.list[first + e] = (s.list[first + e] << 32) | (uint32_t)(first + e);
+    __syncthreads();
+    sort_list(s, keep);
+    const uint64_t target = s.before;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum[e] = first + e < keep ? s.weight[(uint32_t)s.list[first + e]] : 0;
+    const uint64_t own = sum[0];
+    block_scan(s, sum);
+    uint64_t before = sum[0] - own;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if (before < target && sum[e] >= target) s.pick_index = (int)(s.list[first + e] >> 32);
+        before = sum[e];
+    }
+    __syncthreads();
+    return s.pick_index;
+}
+
 template <int TYPE>
-__global__ void __launch_bounds__(kThreads) sample_kernel(SampleArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a) {
     using T = Type<TYPE>;
     using raw = typename T::raw;
     constexpr int VE = Part<TYPE>::VE;
     extern __shared__ __align__(16) uint8_t smem[];
     Shared &s = *reinterpret_cast<Shared *>(smem);
-    uint4 *data = reinterpret_cast<uint4 *>(smem + ((sizeof(Shared) + 15) & ~size_t(15)));
+    uint4 *data = reinterpret_cast<uint4 *>(smem + kSharedBytes);
     const int C = gridDim.x, rank = blockIdx.x, r = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (threadIdx.x < 256) s.table[threadIdx.x] = threadIdx.x ? (uint32_t)__double2ull_rn(exp2(31.0 - threadIdx.x / 256.0)) : 0x80000000u;
+    if (threadIdx.x < 256) s.table[threadIdx.x] = kTable.t[threadIdx.x];
     pdl_wait();
+    if (threadIdx.x == kThreads - 1) {               // the row's arguments: 64-bit operations are few on this GPU
+        const float temp = a.in.temperature[r], p = a.in.top_p ? a.in.top_p[r] : 1.f, mp = a.in.min_p ? a.in.min_p[r] : 0.f;
+        const double c = fmin(1.4426950408889634 / (double)temp, 0x1p120);
+        s.temp = temp;
+        s.ch = (float)c;
+        s.cl = (float)(c - (double)s.ch);
+        s.top_k = a.in.top_k ? a.in.top_k[r] : 0;
+        s.top_p = p < 1.f;
+        s.p64 = (uint64_t)((double)fmaxf(p, 0.f) * 0x1p64);
+        s.u64 = (uint64_t)((double)fminf(fmaxf(a.in.u[r], 0.f), 0x1.fffffep-1f) * 0x1p64);
+        s.min_mode = mp > 1.f ? 3 : mp == 1.f ? 2 : mp > 0.f ? 1 : 0;
+        s.min_off = s.min_mode == 1 ? (double)temp * log((double)mp) : 0.0;
+    }
     const int begin = min(a.in.vocab, rank * a.per), n = min(a.in.vocab, begin + a.per) - begin;
     const raw *src = static_cast<const raw *>(a.in.logits) + (size_t)r * a.in.stride + begin;
     const int skip = (int)((reinterpret_cast<uintptr_t>(src) & 15) / sizeof(raw));
@@ -446,51 +597,106 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleArgs a) {
     cluster_join();
     top = -INFINITY;
     for (int k = 0; k < C; ++k) top = fmaxf(top, peer(&s.top, k));
-    const float temp = a.in.temperature[r];
-    int token = -1;
-    if (top > -INFINITY) {
-        auto first_of_top = [&] { return part.pick(s, [&](float x, int) -> uint64_t { return x == top; }, [](uint64_t) -> uint64_t { return 1; }); };
-        if (!(temp > 0.f)) {
-            token = first_of_top();
-        } else {
-            Row row;
-            const double c = fmin(1.4426950408889634 / (double)temp, 0x1p120);
-            row.top = top;
-            row.ch = (float)c;
-            row.cl = (float)(c - (double)row.ch);
-            row.v = -INFINITY;
-            row.I = 0x7fffffff;
-            row.table = s.table;
-            const int k = a.in.top_k ? a.in.top_k[r] : 0;
-            if (k > 0 && k < a.in.vocab) part.template cut<false>(s, row, [&](uint64_t) -> uint64_t { return k; });
-            const float p = a.in.top_p ? a.in.top_p[r] : 1.f;
-            if (p < 1.f) {
-                // the least whole number that is at least p of the total
-                const uint64_t p64 = (uint64_t)((double)fmaxf(p, 0.f) * 0x1p64);
-                part.template cut<true>(s, row, [&](uint64_t total) -> uint64_t {
-                    const uint64_t t = __umul64hi(total, p64) + (total * p64 != 0);
-                    return t < 1 ? 1 : t;
+    const float temp = s.temp;
+    int32_t *token = a.tokens + r;
+    if (!(top > -INFINITY)) {
+        if (rank == 0 && threadIdx.x == 0) *token = -1;
+    } else if (!(temp > 0.f)) {
+        part.template pick<true>(s, [&](float x, int) -> uint64_t { return x == top; }, [](uint64_t) -> uint64_t { return 1; }, token);
+    } else {
+        Row row{top, s.ch, s.cl, -INFINITY, 0x7fffffff, s.table};
+        float least = -INFINITY;                     // min-p's, for the sorted list
+        if (s.min_mode) least = s.min_mode >= 2 || top == INFINITY ? top : __double2float_ru((double)top + s.min_off);
+        // the bin up to which a filter may keep tokens
+        bool cut = false, by_count = false;
+        if (s.top_k > 0 && s.top_k < a.in.vocab) {
+            part.template depths<false>(s, row);
+            const uint64_t k = s.top_k;
+            cut = by_count = part.template find_bin<false>(s, 0, [&](uint64_t) { return k; });
+        }
+        uint64_t weighed = 0;
+        if (!cut && s.top_p) {
+            // top-p alone: all weights summed, entries counted by depth, and the bin by which so many surely reach p of the sum
+            part.template clear<false>(s);
+            uint64_t sum = 0;
+            part.each([&](float x, int) {
+                const float y = row.depth(x);
+                if (!(y < kDeep)) return;
+                sum += row.weight(x);
+                part.template add<false>(s, min((int)(y * kBinScale), kBins - 1), 1);
+            });
+            __syncwarp();
+            sum = warp_sum64(sum);
+            if (lane == 0) s.warp_sum[warp] = sum;
+            cluster_join();
+            for (int k = lane; k < C * kWarps; k += 32) weighed += peer(&s.warp_sum[k % kWarps], k / kWarps);
+            weighed = warp_sum64(weighed);
+            const uint64_t t = __umul64hi(weighed, s.p64) + (weighed * s.p64 != 0);
+            cut = true;
+            if (!part.template find_bin<false, true>(s, 0, [&](uint64_t) { return t; })) {
+                if (threadIdx.x == 0) s.bin = kBins - 1;
+                __syncthreads();
+            }
+        }
+        uint32_t n = 0, at = 0;
+        if (cut) {
+            // this CTA's entries up to that bin, and where they go
+            const uint32_t bin = s.bin;
+            uint32_t mine = 0;
+            for (uint32_t i = threadIdx.x; i <= bin; i += kThreads) mine += s.hist[0][i];
+            mine = __reduce_add_sync(0xffffffffu, mine);
+            if (threadIdx.x == 0) s.n_list = 0;
+            __syncthreads();
+            if (lane == 0) atomicAdd(&s.n_list, mine);
+            cluster_join();
+            for (int k = 0; k < C; ++k) {
+                const uint32_t m = peer(&s.n_list, k);
+                if (k < rank) at += m;
+                n += m;
+            }
+            if (threadIdx.x == 0) s.key_min = at;
+            cluster_join();                          // (the counts and bins are read)
+            if (n <= kList) {
+                uint32_t list;
+                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(list) : "r"(saddr(s.list)), "r"(0));
+                part.each([&](float x, int i) {
+                    const float y = row.depth(x);
+                    if (!(y < kDeep) || min((int)(y * kBinScale), kBins - 1) > (int)bin) return;
+                    const uint32_t to = atomicAdd(&s.key_min, 1u);
+                    if (to < kList)
+                        asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(list + 8 * to), "l"((uint64_t)falling_key(x) << 32 | (uint32_t)i) : "memory");
                 });
             }
-            const float mp = a.in.min_p ? a.in.min_p[r] : 0.f;
-            if (mp > 1.f) {                              // no weight is that large: the first token of the order
-                row.I = first_of_top();
-                row.v = top;
-            } else if (mp > 0.f) {
-                const double least = mp == 1.f || top == INFINITY ? (double)top : (double)top + (double)temp * log((double)mp);
-                const float v = __double2float_ru(least);
-                if (v > row.v) {
-                    row.v = v;
-                    row.I = 0x7fffffff;
-                }
-            }
-            const float u = fminf(fmaxf(a.in.u[r], 0.f), 0x1.fffffep-1f);
-            const uint64_t u64 = (uint64_t)((double)u * 0x1p64);
-            token = part.pick(s, [&](float x, int i) -> uint64_t { return row.kept(x, i) ? row.weight(x) : 0; },
-                              [&](uint64_t total) -> uint64_t { return __umul64hi(total, u64) + 1; });
         }
+        if (cut && n <= kList) {
+            cluster_join();                          // the list is complete
+            if (rank == 0) {
+                row.v = least;
+                const int t = draw_list(s, row, n, by_count ? s.top_k : n, by_count ? 0 : weighed);
+                if (threadIdx.x == 0) *token = t;
+            }
+            return;                                  // nothing of another CTA is read from here on
+        }
+        // the row as it is, narrowed filter by filter
+        if (by_count) {
+            const uint64_t k = s.top_k;
+            part.template cut<false>(s, row, [&](uint64_t) { return k; });
+        }
+        if (s.top_p)
+            part.template cut<true>(s, row, [&](uint64_t total) -> uint64_t {
+                const uint64_t t = __umul64hi(total, s.p64) + (total * s.p64 != 0);
+                return t < 1 ? 1 : t;
+            });
+        if (s.min_mode == 3) {                       // no weight is that large: the first token of the order
+            row.I = part.template pick<false>(s, [&](float x, int) -> uint64_t { return x == top; }, [](uint64_t) -> uint64_t { return 1; });
+            row.v = top;
+        } else if (least > row.v) {
+            row.v = least;
+            row.I = 0x7fffffff;
+        }
+        part.template pick<true>(s, [&](float x, int i) -> uint64_t { return row.kept(x, i) ? row.weight(x) : 0; },
+                                 [&](uint64_t total) -> uint64_t { return __umul64hi(total, s.u64) + 1; }, token);
     }
-    if (rank == 0 && threadIdx.x == 0) a.tokens[r] = token;
     cluster_join();                                      // no CTA ends while another reads its memory
 }
 
@@ -518,15 +724,14 @@ cudaError_t launch_type(const SampleArgs &a, int C, int smem, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_sample(const SampleInput &in, int32_t *tokens, cudaStream_t st) {
-    // CTAs a row: as many as leave room for two on an SM, and more (8 at most) while the rows leave SMs idle and a CTA
-    // has 2,048 tokens or more
-    const int size = in.dtype == OSCAR_DTYPE_F32 ? 4 : 2;
-    const int room = 112 * 1024 - (int)sizeof(Shared) - 64;
+    // CTAs a row: as many as leave room for two on an SM (115,712 bytes each), and more (8 at most) while the rows leave SMs idle
+    // and a CTA has 2,048 tokens or more
+    const int size = in.dtype == OSCAR_DTYPE_F32 ? 4 : 2, room = 115712 - kSharedBytes - 48;
     int C = 1;
     while (C < 8 && (in.vocab + C - 1) / C * size > room) C *= 2;
     while (C < 8 && (long long)in.rows * C * 2 <= 304 && in.vocab / (2 * C) >= 2048) C *= 2;
     SampleArgs a{in, (in.vocab + C - 1) / C, tokens};
-    const int smem = (int)((sizeof(Shared) + 15) & ~size_t(15)) + ((a.per + 2 * (16 / size)) * size + 15) / 16 * 16;
+    const int smem = kSharedBytes + ((a.per + 2 * (16 / size)) * size + 15) / 16 * 16;
     switch (in.dtype) {
         case OSCAR_DTYPE_F32: return launch_type<OSCAR_DTYPE_F32>(a, C, smem, st);
         case OSCAR_DTYPE_BF16: return launch_type<OSCAR_DTYPE_BF16>(a, C, smem, st);
