@@ -11,10 +11,12 @@
 // token as in 64-bit arithmetic (a sum in fp32, 2^-24 off, would miss for one row in a hundred over a large vocabulary).
 //
 // A cluster of 1 to 8 CTAs takes a row and holds it in shared memory, so a row is read once.  The filters' search goes through
-// bins: 2,048 equal steps of y, whose order is the logits' order, counted (top-k) or weighed (top-p alone) by atomics; all entries up
-// to the bin that the target falls into go to the first CTA, which sorts them, cuts the order by every filter, sorts what is left by
-// index and draws.  Entries that are too many for that (flat rows, large top-k) take more levels of bins instead, within the bin
-// equal steps of the logits' bits until a bin is one value.  Weights in a bin are summed by 32-bit atomics on three parts of 15 bits.
+// bins: 2,048 equal steps of y, whose order is the logits' order, counted by atomics.  For top-k the counts give the bin that the
+// target falls into; for top-p, with the sum of all weights, the few bins that it can fall into (a bin's weights differ by 1.5 %).
+// Where no more than 2,048 entries lie up to there, they go to the first CTA, which sorts them, cuts the order by every filter, sorts
+// what is left by index and draws.  Where that many lie in those bins alone, it sorts these and says where the cut is, and the draw
+// goes through the row.  Where more do (flat rows), further levels of bins follow, within a bin equal steps of the logits' bits, until
+// a bin is one value; weights in a bin are then summed by 32-bit atomics on three parts of 15 bits.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -124,8 +126,10 @@ struct Shared {
     float top;                                       // of this CTA, read by the cluster
     uint32_t n_list, key_min, key_max;               // read by the cluster
     int pick_index;
-    uint32_t bin;
+    uint32_t bin, bin_from;
     uint64_t before, total;
+    float cut_v;                                     // of the first CTA, read by the cluster
+    int cut_i;
     // the row's arguments
     float temp, ch, cl;
     int top_k, min_mode;                             // min_p: 0 off, 1 top + min_off, 2 the largest logit, 3 one token
@@ -176,6 +180,63 @@ __device__ __forceinline__ uint64_t warp_scan64(uint64_t x, int lane) {         
 __device__ __forceinline__ void cluster_join() {
     __syncwarp();
     cluster_sync_all();
+}
+
+// The n entries of s.list (falling key | index) sorted upwards, the places behind them up to the next power of two filled up.
+__device__ __forceinline__ void sort_list(Shared &s, int n) {
+    int size = 2;
+    while (size < n) size *= 2;
+    for (int i = n + threadIdx.x; i < size; i += kThreads) s.list[i] = ~0ull;
+    __syncthreads();
+    for (int k = 2; k <= size; k *= 2)
+        for (int j = k / 2; j > 0; j /= 2) {
+            for (int i = threadIdx.x; i < size / 2; i += kThreads) {
+                const int x = 2 * i - (i & (j - 1)), y = x + j;
+                const uint64_t u = s.list[x], v = s.list[y];
+                if ((u > v) == ((x & k) == 0)) {
+                    s.list[x] = v;
+                    s.list[y] = u;
+                }
+            }
+            if (j > 32 || size > 2 * kThreads) __syncthreads();
+            else if (j > 1) __syncwarp();            // the next step's pairs of a warp are its own
+            else __syncthreads();
+        }
+}
+
+// Inclusive sums of four values a thread over the CTA, in thread order.
+__device__ __forceinline__ void block_scan(Shared &s, uint64_t (&x)[4]) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    x[1] += x[0];
+    x[2] += x[1];
+    x[3] += x[2];
+    uint64_t before = warp_scan64(x[3], lane);
+    if (lane == 31) s.scan[warp] = before;
+    before -= x[3];
+    __syncthreads();
+    for (int k = 0; k < warp; ++k) before += s.scan[k];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] += before;
+    __syncthreads();
+}
+
+// Where the prefix of a row's order that reaches the target ends, among the n entries unsorted in s.list, before which there is
+// weight `base` (of 1 an entry, or w): the entry's value and index.
+template <bool MASS>
+__device__ __forceinline__ void cut_list(Shared &s, const Row &row, int n, uint64_t base, uint64_t target) {
+    const int first = 4 * threadIdx.x;
+    sort_list(s, n);
+    uint64_t sum[4], w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum[e] = w[e] = first + e >= n ? 0 : MASS ? row.weight(key_value((uint32_t)(s.list[first + e] >> 32))) : 1;
+    block_scan(s, sum);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (base + sum[e] - w[e] < target && (base + sum[e] >= target || first + e == n - 1)) {       // (the last one reaches it)
+            s.cut_v = key_value((uint32_t)(s.list[first + e] >> 32));
+            s.cut_i = (int)(uint32_t)s.list[first + e];
+        }
+    __syncthreads();
 }
 
 // The part of the row that this CTA holds: whole vectors, element e of vector j with index begin - skip + j VE + e; the
@@ -270,7 +331,8 @@ struct Part {
 
     // The bins of this search level, filled by every CTA: finds the first one up to which base and the weights reach the
     // target that goal(total) gives, and leaves it in s.bin with the weight before it in s.before.  False: no bin does.
-    // LEAST: the bins of y hold counts, taken for the least weight that so many entries there can have.
+    // LEAST: the bins of y hold counts, taken for the least weight that so many entries there can have; s.bin is a bin by which the
+    // true weights have reached the target, s.bin_from the first by which they can have.
     template <bool MASS, bool LEAST = false, typename G>
     __device__ __forceinline__ bool find_bin(Shared &s, uint64_t base, G goal) const {
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b0 = threadIdx.x * 4;
@@ -300,7 +362,7 @@ struct Part {
         const uint64_t mine = w[0] + w[1] + w[2] + w[3];
         const uint64_t upto = warp_scan64(mine, lane);
         if (lane == 31) s.scan[warp] = upto;
-        if (threadIdx.x == 0) s.bin = kBins;
+        if (threadIdx.x == 0) s.bin = s.bin_from = kBins;
         __syncthreads();
         uint64_t before = base, total = 0;
         for (int k = 0; k < kWarps; ++k) {
@@ -311,13 +373,16 @@ struct Part {
         const uint64_t target = goal(total);
         if (threadIdx.x == 0) s.total = total;
         before += upto - mine;
-        if (before < target && target <= before + mine) {
+        // what 2^(1 / kBinScale) and the roundings leave of the target
+        const uint64_t low = LEAST ? max(1ull, (unsigned long long)__umul64hi(target, (uint64_t)(0.98 * 0x1p63) << 1)) : target;
+        if (before < target && low <= before + mine) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 if (before < target && target <= before + w[i]) {
                     s.bin = b0 + i;
                     s.before = before;
                 }
+                if (LEAST && before < low && low <= before + w[i]) s.bin_from = b0 + i;
                 before += w[i];
             }
         }
@@ -351,6 +416,111 @@ struct Part {
                 if (w) add<MASS>(s, min((int)(y * kBinScale), kBins - 1), w);
             }
         });
+    }
+
+    // The entries of the bins from .. to that row keeps, of all CTAs, to the first CTA's list; at: where this one's begin.
+    __device__ __forceinline__ void gather(Shared &s, const Row &row, uint32_t from, uint32_t to, uint32_t at) const {
+        if (threadIdx.x == 0) s.key_min = at;
+        cluster_join();                              // (the bins are read; their memory becomes the list)
+        uint32_t list;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(list) : "r"(saddr(s.list)), "r"(0));
+        each([&](float x, int i) {
+            const float y = row.depth(x);
+            const uint32_t bin = min((int)(y * kBinScale), kBins - 1);
+            if (!(y < kDeep) || bin < from || bin > to || !row.kept(x, i)) return;
+            const uint32_t place = atomicAdd(&s.key_min, 1u);
+            if (place < kList)
+                asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(list + 8 * place), "l"((uint64_t)falling_key(x) << 32 | (uint32_t)i) : "memory");
+        });
+        cluster_join();                              // the list is complete
+    }
+
+    // Entries counted in the bins from .. to: of all CTAs, and of those before this one.
+    __device__ __forceinline__ uint32_t entries(Shared &s, uint32_t from, uint32_t to, uint32_t &before) const {
+        uint32_t mine = 0;
+        for (uint32_t i = from + threadIdx.x; i <= to; i += kThreads) mine += s.hist[0][i];
+        mine = __reduce_add_sync(0xffffffffu, mine);
+        if (threadIdx.x == 0) s.n_list = 0;
+        __syncthreads();
+        if ((threadIdx.x & 31) == 0) atomicAdd(&s.n_list, mine);
+        cluster_join();
+        uint32_t n = 0;
+        before = 0;
+        for (int k = 0; k < C; ++k) {
+            const uint32_t m = peer(&s.n_list, k);
+            if (k < rank) before += m;
+            n += m;
+        }
+        cluster_join();
+        return n;
+    }
+
+    // The sum over the cluster of a value a thread.
+    __device__ __forceinline__ uint64_t cluster_sum(Shared &s, uint64_t x) const {
+        const int lane = threadIdx.x & 31;
+        __syncwarp();
+        x = warp_sum64(x);
+        if (lane == 0) s.warp_sum[threadIdx.x >> 5] = x;
+        cluster_join();
+        x = 0;
+        for (int k = lane; k < C * kWarps; k += 32) x += peer(&s.warp_sum[k % kWarps], k / kWarps);
+        x = warp_sum64(x);
+        cluster_join();
+        return x;
+    }
+
+    // Narrows what is kept by top-k (MASS false, k tokens) or top-p (s.p64 of the kept weight).  With whole: returns how many
+    // entries the first CTA's list holds, if all that can be kept are there (nothing is narrowed then); else 0.  weighed: the kept
+    // weight (top-p).
+    template <bool MASS>
+    __device__ __forceinline__ uint32_t narrow(Shared &s, Row &row, uint64_t k, bool whole, uint64_t &weighed) const {
+        clear<false>(s);
+        uint64_t sum = 0;
+        each([&](float x, int i) {
+            const float y = row.depth(x);
+            if (!(y < kDeep) || !row.kept(x, i)) return;
+            if (MASS) sum += row.weight(x);
+            add<false>(s, min((int)(y * kBinScale), kBins - 1), 1);
+        });
+        uint64_t target = k;
+        if (MASS) {
+            weighed = cluster_sum(s, sum);
+            target = __umul64hi(weighed, s.p64) + (weighed * s.p64 != 0);
+            if (target < 1) target = 1;
+        }
+        const bool found = find_bin<false, MASS>(s, 0, [&](uint64_t) { return target; });
+        if (!MASS && !found) return 0;               // fewer than k have weight: all stay
+        const uint32_t to = found ? s.bin : kBins - 1, from = !MASS ? to : min(s.bin_from, to);
+        uint64_t base = MASS ? 0 : s.before;
+        uint32_t at, n;
+        if (whole) {
+            n = entries(s, 0, to, at);
+            if (n <= kList) {
+                gather(s, row, 0, to, at);
+                return n;
+            }
+        }
+        n = entries(s, from, to, at);
+        if (n > kList) {
+            cut<MASS>(s, row, [&](uint64_t) { return target; });
+            return 0;
+        }
+        if (MASS) {
+            // the weight above those bins
+            sum = 0;
+            each([&](float x, int i) {
+                const float y = row.depth(x);
+                if (y < kDeep && (uint32_t)min((int)(y * kBinScale), kBins - 1) < from && row.kept(x, i)) sum += row.weight(x);
+            });
+            base = cluster_sum(s, sum);
+        }
+        gather(s, row, from, to, at);
+        if (rank == 0) cut_list<MASS>(s, row, n, base, target);
+        cluster_join();
+        row.v = peer(&s.cut_v, 0);
+        row.I = peer(&s.cut_i, 0);
+        cluster_join();
+        return 0;
     }
 
     // Narrows what is kept to the shortest prefix whose weight (1 a token, or w) reaches the target.
@@ -421,44 +591,6 @@ struct Part {
         row.v = v;
     }
 };
-
-// The n entries of s.list (falling key | index) sorted upwards, the places behind them up to the next power of two filled up.
-__device__ __forceinline__ void sort_list(Shared &s, int n) {
-    int size = 2;
-    while (size < n) size *= 2;
-    for (int i = n + threadIdx.x; i < size; i += kThreads) s.list[i] = ~0ull;
-    __syncthreads();
-    for (int k = 2; k <= size; k *= 2)
-        for (int j = k / 2; j > 0; j /= 2) {
-            for (int i = threadIdx.x; i < size / 2; i += kThreads) {
-                const int x = 2 * i - (i & (j - 1)), y = x + j;
-                const uint64_t u = s.list[x], v = s.list[y];
-                if ((u > v) == ((x & k) == 0)) {
-                    s.list[x] = v;
-                    s.list[y] = u;
-                }
-            }
-            if (j > 32 || size > 2 * kThreads) __syncthreads();
-            else if (j > 1) __syncwarp();            // the next step's pairs of a warp are its own
-            else __syncthreads();
-        }
-}
-
-// Inclusive sums of four values a thread over the CTA, in thread order.
-__device__ __forceinline__ void block_scan(Shared &s, uint64_t (&x)[4]) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    x[1] += x[0];
-    x[2] += x[1];
-    x[3] += x[2];
-    uint64_t before = warp_scan64(x[3], lane);
-    if (lane == 31) s.scan[warp] = before;
-    before -= x[3];
-    __syncthreads();
-    for (int k = 0; k < warp; ++k) before += s.scan[k];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] += before;
-    __syncthreads();
-}
 
 // The draw from a row's first n entries, unsorted in s.list, by one CTA: total is what top-p is of, where the list does not hold it
 // all (0: the first k entries' weight).
@@ -607,86 +739,19 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a) {
         Row row{top, s.ch, s.cl, -INFINITY, 0x7fffffff, s.table};
         float least = -INFINITY;                     // min-p's, for the sorted list
         if (s.min_mode) least = s.min_mode >= 2 || top == INFINITY ? top : __double2float_ru((double)top + s.min_off);
-        // the bin up to which a filter may keep tokens
-        bool cut = false, by_count = false;
-        if (s.top_k > 0 && s.top_k < a.in.vocab) {
-            part.template depths<false>(s, row);
-            const uint64_t k = s.top_k;
-            cut = by_count = part.template find_bin<false>(s, 0, [&](uint64_t) { return k; });
-        }
+        const bool by_count = s.top_k > 0 && s.top_k < a.in.vocab;
         uint64_t weighed = 0;
-        if (!cut && s.top_p) {
-            // top-p alone: all weights summed, entries counted by depth, and the bin by which so many surely reach p of the sum
-            part.template clear<false>(s);
-            uint64_t sum = 0;
-            part.each([&](float x, int) {
-                const float y = row.depth(x);
-                if (!(y < kDeep)) return;
-                sum += row.weight(x);
-                part.template add<false>(s, min((int)(y * kBinScale), kBins - 1), 1);
-            });
-            __syncwarp();
-            sum = warp_sum64(sum);
-            if (lane == 0) s.warp_sum[warp] = sum;
-            cluster_join();
-            for (int k = lane; k < C * kWarps; k += 32) weighed += peer(&s.warp_sum[k % kWarps], k / kWarps);
-            weighed = warp_sum64(weighed);
-            const uint64_t t = __umul64hi(weighed, s.p64) + (weighed * s.p64 != 0);
-            cut = true;
-            if (!part.template find_bin<false, true>(s, 0, [&](uint64_t) { return t; })) {
-                if (threadIdx.x == 0) s.bin = kBins - 1;
-                __syncthreads();
-            }
-        }
-        uint32_t n = 0, at = 0;
-        if (cut) {
-            // this CTA's entries up to that bin, and where they go
-            const uint32_t bin = s.bin;
-            uint32_t mine = 0;
-            for (uint32_t i = threadIdx.x; i <= bin; i += kThreads) mine += s.hist[0][i];
-            mine = __reduce_add_sync(0xffffffffu, mine);
-            if (threadIdx.x == 0) s.n_list = 0;
-            __syncthreads();
-            if (lane == 0) atomicAdd(&s.n_list, mine);
-            cluster_join();
-            for (int k = 0; k < C; ++k) {
-                const uint32_t m = peer(&s.n_list, k);
-                if (k < rank) at += m;
-                n += m;
-            }
-            if (threadIdx.x == 0) s.key_min = at;
-            cluster_join();                          // (the counts and bins are read)
-            if (n <= kList) {
-                uint32_t list;
-                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(list) : "r"(saddr(s.list)), "r"(0));
-                part.each([&](float x, int i) {
-                    const float y = row.depth(x);
-                    if (!(y < kDeep) || min((int)(y * kBinScale), kBins - 1) > (int)bin) return;
-                    const uint32_t to = atomicAdd(&s.key_min, 1u);
-                    if (to < kList)
-                        asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(list + 8 * to), "l"((uint64_t)falling_key(x) << 32 | (uint32_t)i) : "memory");
-                });
-            }
-        }
-        if (cut && n <= kList) {
-            cluster_join();                          // the list is complete
+        uint32_t n = 0;
+        if (by_count) n = part.template narrow<false>(s, row, s.top_k, true, weighed);
+        if (!n && s.top_p) n = part.template narrow<true>(s, row, 0, !by_count, weighed);
+        if (n) {
             if (rank == 0) {
                 row.v = least;
-                const int t = draw_list(s, row, n, by_count ? s.top_k : n, by_count ? 0 : weighed);
+                const int t = draw_list(s, row, n, by_count ? s.top_k : n, weighed);
                 if (threadIdx.x == 0) *token = t;
             }
             return;                                  // nothing of another CTA is read from here on
         }
-        // the row as it is, narrowed filter by filter
-        if (by_count) {
-            const uint64_t k = s.top_k;
-            part.template cut<false>(s, row, [&](uint64_t) { return k; });
-        }
-        if (s.top_p)
-            part.template cut<true>(s, row, [&](uint64_t total) -> uint64_t {
-                const uint64_t t = __umul64hi(total, s.p64) + (total * s.p64 != 0);
-                return t < 1 ? 1 : t;
-            });
         if (s.min_mode == 3) {                       // no weight is that large: the first token of the order
             row.I = part.template pick<false>(s, [&](float x, int) -> uint64_t { return x == top; }, [](uint64_t) -> uint64_t { return 1; });
             row.v = top;
