@@ -674,7 +674,7 @@ oscar_status_t oscar_sample(const void *logits, int32_t dtype, int64_t stride, i
     if (vocab < 1 || vocab > OSCAR_SAMPLE_MAX_VOCAB)
         return fail(OSCAR_ERR_INVALID_ARG, "vocab %d outside 1..%d", vocab, OSCAR_SAMPLE_MAX_VOCAB);
     if (rows == 0) return OSCAR_OK;
-    if (rows > 1 && stride < vocab) return fail(OSCAR_ERR_INVALID_ARG, "stride below vocab");
+    if (rows > 1 && stride != 0 && stride < vocab) return fail(OSCAR_ERR_INVALID_ARG, "stride neither 0 nor vocab and more");
     if (!logits || !temperature || !u || !tokens) return fail(OSCAR_ERR_INVALID_ARG, "NULL argument");
     if (reinterpret_cast<uintptr_t>(logits) % (dtype == OSCAR_DTYPE_F32 ? 4 : 2))
         return fail(OSCAR_ERR_INVALID_ARG, "logits not aligned to their type");

@@ -12,7 +12,8 @@
 //
 // A CTA takes (split, 16 query rows, kv head, request); each of its 8 warps takes every 8th block of 32 tokens through a ring
 // of bulk tensor copies of its own, and they join at the end.  Slot S of the partials is the BF16 rows': the last CTA of a
-// row tile, whose warps take 16 positions at a time straight from global memory.
+// row tile, whose warps take 16 positions at a time straight from global memory.  With one split, a CTA takes both, one after the
+// other, and writes the result: no partials, no merge.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -39,7 +40,7 @@ template <int NG>
 struct Ring {
     static constexpr int bytes = 4096 + kBlock4 * NG * 8;
     static constexpr int stride = (bytes + 511) & ~511;
-    static constexpr int n = 3;
+    static constexpr int n = NG == 4 ? 2 : 3;                    // as many as leave room for two CTAs on an SM
     static constexpr int total = kW * n * stride;
 };
 
@@ -114,28 +115,27 @@ __device__ __forceinline__ void clear(Rows &x) {
             for (int e = 0; e < 4; ++e) x.out[c][i][e] = 0.f;
 }
 
-// Channels 32 i + 8 t .. + 7 of the lane's query rows g + 8 r.
-struct Query {
-    uint4 w[2][4];
-    __device__ __forceinline__ Query(const TreeArgs &a, const TreeRequest &rq, int h, int row0, int rows, int lane) {
-        const int g = lane >> 2, t = lane & 3;
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int row = g + 8 * r;
-            const uint16_t *src = a.q + (row < rows ? tree_row(a, rq, h, row0 + row) * kHeadDim : 0) + 8 * t;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w[r][i] = row < rows ? *reinterpret_cast<const uint4 *>(src + 32 * i) : make_uint4(0, 0, 0, 0);
-        }
-    }
-};
+// Channels 32 i + 8 t .. + 7 of query row g + 8 r of the tile, t = lane % 4.
+__device__ __forceinline__ uint4 query_piece(const TreeArgs &a, const TreeRequest &rq, int h, int row0, int rows, int r, int i, int lane) {
+    const int row = (lane >> 2) + 8 * r;
+    if (row >= rows) return make_uint4(0, 0, 0, 0);
+    return *reinterpret_cast<const uint4 *>(a.q + tree_row(a, rq, h, row0 + row) * kHeadDim + 32 * i + 8 * (lane & 3));
+}
 
 // ---- the BF16 rows ---------------------------------------------------------------------------------
 // Positions [0, min(sink, T)), [max(hist_end, those), T) and the nodes' [T, T + n), in tiles of 16.
-__device__ __forceinline__ void window_warp(const TreeArgs &a, const TreeRequest &rq, int b, int h, int row0, int rows, int warp, int lane, Rows &x) {
+__device__ __forceinline__ void window_warp(const TreeArgs &a, const TreeRequest &rq, int b, int h, int row0, int rows, uint4 *frag, int warp, int lane,
+                                            Rows &x) {
     const int g = lane >> 2, t = lane & 3, sh = a.page_shift, T = rq.T, end = T + rq.n;
     const int n0 = min(a.sink, T), lo1 = max(rq.he, n0), sink_tiles = (n0 + 15) / 16, rec0 = lo1 / 16;
     const int tiles = sink_tiles + (end + 15) / 16 - rec0;
-    const Query q(a, rq, h, row0, rows, lane);
+    // the A operand of the logits, as it lies, for all warps: fragment 2 i + e of lane l at 32 (2 i + e) + l
+    for (int k = warp; k < 4; k += kW) {
+        const uint4 x = query_piece(a, rq, h, row0, rows, 0, k, lane), y = query_piece(a, rq, h, row0, rows, 1, k, lane);
+        frag[64 * k + lane] = make_uint4(x.x, y.x, x.y, y.y);
+        frag[64 * k + 32 + lane] = make_uint4(x.z, y.z, x.w, y.w);
+    }
+    __syncthreads();
     int node[2];                                     // of the lane's rows
 #pragma unroll
     for (int r = 0; r < 2; ++r) node[r] = (row0 + min(g + 8 * r, rows - 1)) / a.G;
@@ -149,26 +149,24 @@ __device__ __forceinline__ void window_warp(const TreeArgs &a, const TreeRequest
             continue;
         }
         // lane (g, t): channels 32 i + 8 t .. + 7 of tokens g and g + 8
-        uint4 kk[2][4], vv[2][4];
+        const bool in0 = p0 + g >= lo && p0 + g < hi, in1 = p0 + g + 8 >= lo && p0 + g + 8 < hi;
+        const size_t at = ((((size_t)page << sh) + ((p0 + g) & ((1 << sh) - 1))) * a.n_kv + h) * kHeadDim + 8 * t, far = (size_t)8 * a.n_kv * kHeadDim;
+        uint4 kk[2][4];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int p = p0 + g + 8 * u;
-            const bool in = p >= lo && p < hi;
-            const size_t at = ((((size_t)page << sh) + (p & ((1 << sh) - 1))) * a.n_kv + h) * kHeadDim + 8 * t;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                kk[u][i] = in ? *reinterpret_cast<const uint4 *>(a.bf.k + at + 32 * i) : make_uint4(0, 0, 0, 0);
-                vv[u][i] = in ? *reinterpret_cast<const uint4 *>(a.bf.v + at + 32 * i) : make_uint4(0, 0, 0, 0);
-            }
+        for (int i = 0; i < 4; ++i) {
+            kk[0][i] = in0 ? *reinterpret_cast<const uint4 *>(a.bf.k + at + 32 * i) : make_uint4(0, 0, 0, 0);
+            kk[1][i] = in1 ? *reinterpret_cast<const uint4 *>(a.bf.k + at + far + 32 * i) : make_uint4(0, 0, 0, 0);
         }
         float s[2][4];                               // [keys 8 u + 2 t + e][2 r + e]
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            s[u][0] = s[u][1] = s[u][2] = s[u][3] = 0.f;
+        for (int u = 0; u < 2; ++u) s[u][0] = s[u][1] = s[u][2] = s[u][3] = 0.f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                mma16816_bf16(s[u], q.w[0][i].x, q.w[1][i].x, q.w[0][i].y, q.w[1][i].y, kk[u][i].x, kk[u][i].y);
-                mma16816_bf16(s[u], q.w[0][i].z, q.w[1][i].z, q.w[0][i].w, q.w[1][i].w, kk[u][i].z, kk[u][i].w);
+        for (int i = 0; i < 4; ++i) {
+            const uint4 x = frag[64 * i + lane], y = frag[64 * i + 32 + lane];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                mma16816_bf16(s[u], x.x, x.y, x.z, x.w, kk[u][i].x, kk[u][i].y);
+                mma16816_bf16(s[u], y.x, y.y, y.z, y.w, kk[u][i].z, kk[u][i].w);
             }
         }
 #pragma unroll
@@ -183,17 +181,6 @@ __device__ __forceinline__ void window_warp(const TreeArgs &a, const TreeRequest
                 }
                 s[u][e] = sees ? s[u][e] * a.scale2 : -INFINITY;
             }
-        // infinities and NaN among the values: rows that do not see them must not meet them in a product
-        bool odd = false;
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t w[4] = {vv[u][i].x, vv[u][i].y, vv[u][i].z, vv[u][i].w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) odd |= (w[e] & 0x7f80u) == 0x7f80u || (w[e] & 0x7f800000u) == 0x7f800000u;
-            }
-        odd = __any_sync(0xffffffffu, odd);
         float al[2];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
@@ -206,36 +193,6 @@ __device__ __forceinline__ void window_warp(const TreeArgs &a, const TreeRequest
                 for (int e = 0; e < 2; ++e) s[u][2 * r + e] = ex2_approx(s[u][2 * r + e] - m);
             x.l[r] = fmaf(x.l[r], al[r], (s[0][2 * r] + s[0][2 * r + 1]) + (s[1][2 * r] + s[1][2 * r + 1]));
         }
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x.out[c][i][e] *= al[e >> 1];
-        if (odd) {
-            // one key at a time, only where it has weight
-#pragma unroll 1
-            for (int key = 0; key < 16; ++key) {
-                const int u = key >> 3, from = (lane & ~3) | ((key & 7) >> 1), p = p0 + key;
-                if (p < lo || p >= hi) continue;
-                float pr[2];
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const float first = __shfl_sync(0xffffffffu, u ? s[1][2 * r] : s[0][2 * r], from);
-                    const float second = __shfl_sync(0xffffffffu, u ? s[1][2 * r + 1] : s[0][2 * r + 1], from);
-                    pr[r] = key & 1 ? second : first;
-                }
-                const uint16_t *v = a.bf.v + ((((size_t)page << sh) + (p & ((1 << sh) - 1))) * a.n_kv + h) * kHeadDim + 8 * t;
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (pr[e >> 1] != 0.f) x.out[c][i][e] = fmaf(pr[e >> 1], bf16_to_f32(v[32 * c + 4 * (e & 1) + i]), x.out[c][i][e]);
-            }
-            continue;
-        }
         uint32_t ph[4], pl[4];                       // A operand: rows g, g + 8 of keys 2 t + e, then of keys 8 + 2 t + e
 #pragma unroll
         for (int u = 0; u < 2; ++u)
@@ -245,26 +202,60 @@ __device__ __forceinline__ void window_warp(const TreeArgs &a, const TreeRequest
                 ph[2 * u + r] = hi2;
                 pl[2 * u + r] = pack_b2(s[u][2 * r] - lo16(hi2), s[u][2 * r + 1] - hi16(hi2));
             }
-        // channels 32 c + 4 n + 2 j + e of eight tokens are an 8 x 8 matrix of 16 bits: transposed, the B operand
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int c = 0; c < 4; ++c) {
+            const uint4 v0 = in0 ? *reinterpret_cast<const uint4 *>(a.bf.v + at + 32 * c) : make_uint4(0, 0, 0, 0);
+            const uint4 v1 = in1 ? *reinterpret_cast<const uint4 *>(a.bf.v + at + far + 32 * c) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x.out[c][i][e] *= al[e >> 1];
+            // infinities and NaN among the values: rows that do not see them must not meet them in a product
+            const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+            bool odd = false;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) odd |= (w[e] & 0x7f80u) == 0x7f80u || (w[e] & 0x7f800000u) == 0x7f800000u;
+            if (__any_sync(0xffffffffu, odd)) {
+                // one key at a time, only where it has weight
+#pragma unroll 1
+                for (int key = 0; key < 16; ++key) {
+                    const int u = key >> 3, from = (lane & ~3) | ((key & 7) >> 1), p = p0 + key;
+                    if (p < lo || p >= hi) continue;
+                    float pr[2];
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const float first = __shfl_sync(0xffffffffu, u ? s[1][2 * r] : s[0][2 * r], from);
+                        const float second = __shfl_sync(0xffffffffu, u ? s[1][2 * r + 1] : s[0][2 * r + 1], from);
+                        pr[r] = key & 1 ? second : first;
+                    }
+                    const uint16_t *v = a.bf.v + ((((size_t)page << sh) + (p & ((1 << sh) - 1))) * a.n_kv + h) * kHeadDim + 8 * t + 32 * c;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (pr[e >> 1] != 0.f) x.out[c][i][e] = fmaf(pr[e >> 1], bf16_to_f32(v[4 * (e & 1) + i]), x.out[c][i][e]);
+                }
+                continue;
+            }
+            // channels 32 c + 4 n + 2 j + e of eight tokens are an 8 x 8 matrix of 16 bits: transposed, the B operand
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const uint32_t sel = e ? 0x7632 : 0x5410;
-                    const uint32_t b0 = movmatrix_trans(__byte_perm(j ? vv[0][c].y : vv[0][c].x, j ? vv[0][c].w : vv[0][c].z, sel));
-                    const uint32_t b1 = movmatrix_trans(__byte_perm(j ? vv[1][c].y : vv[1][c].x, j ? vv[1][c].w : vv[1][c].z, sel));
+                    const uint32_t b0 = movmatrix_trans(__byte_perm(j ? v0.y : v0.x, j ? v0.w : v0.z, sel));
+                    const uint32_t b1 = movmatrix_trans(__byte_perm(j ? v1.y : v1.x, j ? v1.w : v1.z, sel));
                     mma16816_bf16(x.out[c][2 * j + e], pl[0], pl[1], pl[2], pl[3], b0, b1);
                     mma16816_bf16(x.out[c][2 * j + e], ph[0], ph[1], ph[2], ph[3], b0, b1);
                 }
+        }
     }
 }
 
 // ---- the history -----------------------------------------------------------------------------------
 template <int NG>
 __device__ __forceinline__ void history_warp(const TreeArgs &a, const CUtensorMap *tmk, const CUtensorMap *tmv, uint8_t *ring, uint32_t bars,
-                                             const TreeRequest &rq, int b, int h, int row0, int rows, int split, int warp, int lane, Rows &x) {
+                                             const TreeRequest &rq, int b, int h, int row0, int rows, int split, uint4 *frag, int warp, int lane, Rows &x) {
     using R = Ring<NG>;
     const int t = lane & 3, sh = a.page_shift, S = a.part.S, he = rq.he;
     const int first = a.sink / kBlock4, nb = he > a.sink ? (he + kBlock4 - 1) / kBlock4 - first : 0;
@@ -310,12 +301,10 @@ __device__ __forceinline__ void history_warp(const TreeArgs &a, const CUtensorMa
     };
     for (int i = 0; i < R::n && i < n; ++i) issue(i, i);
 
-    // A operand of the logits: channels 32 i + 8 t + e of chunk i, the odd nibbles' against 1/16 of the query; fac undoes the
-    // scalings, qz is the zero's factor, per row and group.
-    uint32_t aq[4][2][4];
+    // A operand of the logits, for all warps (fragment 2 i + e of lane l at 32 (2 i + e) + l): channels 32 i + 8 t .. of chunk i,
+    // the odd nibbles' against 1/16 of the query; fac undoes the scalings, qz is the zero's factor, per row and group.
     float fac[2], qz[NG][2];
     {
-        const Query q(a, rq, h, row0, rows, lane);
         float mul[2], qs[2][NG];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
@@ -324,7 +313,8 @@ __device__ __forceinline__ void history_warp(const TreeArgs &a, const CUtensorMa
             for (int k = 0; k < NG; ++k) qs[r][k] = 0.f;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const uint32_t w[4] = {q.w[r][i].x, q.w[r][i].y, q.w[r][i].z, q.w[r][i].w};
+                const uint4 q = query_piece(a, rq, h, row0, rows, r, i, lane);
+                const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     mx = fmaxf(mx, fmaxf(fabsf(lo16(w[e])), fabsf(hi16(w[e]))));
@@ -338,18 +328,22 @@ __device__ __forceinline__ void history_warp(const TreeArgs &a, const CUtensorMa
 #pragma unroll
             for (int k = 0; k < NG; ++k) qz[k][r] = row_sum(qs[r][k]) * a.scale2;
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = warp; i < 4; i += kW) {
+            uint32_t f[2][4];
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                const uint4 w = q.w[r][i];
+                const uint4 w = query_piece(a, rq, h, row0, rows, r, i, lane);
                 const float m0 = mul[r], m1 = mul[r] * 0.0625f;
-                aq[i][0][r] = pack_h2(lo16(w.x) * m0, lo16(w.z) * m0);
-                aq[i][0][2 + r] = pack_h2(hi16(w.x) * m1, hi16(w.z) * m1);
-                aq[i][1][r] = pack_h2(lo16(w.y) * m0, lo16(w.w) * m0);
-                aq[i][1][2 + r] = pack_h2(hi16(w.y) * m1, hi16(w.w) * m1);
+                f[0][r] = pack_h2(lo16(w.x) * m0, lo16(w.z) * m0);
+                f[0][2 + r] = pack_h2(hi16(w.x) * m1, hi16(w.z) * m1);
+                f[1][r] = pack_h2(lo16(w.y) * m0, lo16(w.w) * m0);
+                f[1][2 + r] = pack_h2(hi16(w.y) * m1, hi16(w.w) * m1);
             }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) frag[64 * i + 32 * e + lane] = make_uint4(f[e][0], f[e][1], f[e][2], f[e][3]);
+        }
     }
+    __syncthreads();
     float vinv[2] = {kPMost, kPMost};                // what the rows' p·s are multiplied by, powers of two
     for (int i = 0, st = 0, phase = 0; i < n; ++i) {
         if (!mbar_wait(bars + 8 * st, phase)) {
@@ -364,41 +358,49 @@ __device__ __forceinline__ void history_warp(const TreeArgs &a, const CUtensorMa
         const uint32_t okb = (ok >> (2 * st)) & 3u;
         const bool full = okb == 3u && p0 >= a.sink && p0 + kBlock4 <= he;
 
-        float s[4][4];                               // [8 keys][2 r + e]: key 8 u + 2 t + e of row g + 8 r
-        uint32_t vw[4][2][NG];                       // value scale | zero of keys 8 u + 2 t + e
+        // [8 keys][2 r + e]: logit of key 8 u + 2 t + e and row g + 8 r
+        float s[4][4];
+        const uint2 *const rec = reinterpret_cast<const uint2 *>(stage + 4096) + 2 * t * NG;        // records of key 8 u + 2 t + e: (8 u + e) NG + k
+        {
+            uint32_t w[4][4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int row = 8 * u + (lane & 7);
-            uint32_t w[4];
-            ldmatrix_x4(sb + row * 64 + (((lane >> 3) ^ ((row >> 1) & 3)) << 4), w[0], w[1], w[2], w[3]);
-            float d[NG][4];
-#pragma unroll
-            for (int k = 0; k < NG; ++k)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) d[k][e] = 0.f;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const uint32_t y = w[c], y8 = y >> 8;
-                float(&dd)[4] = d[c * NG / 4];
-                mma16816_nv(dd, aq[c][0][0], aq[c][0][1], aq[c][0][2], aq[c][0][3], y & kM0, y & kM1);
-                mma16816_nv(dd, aq[c][1][0], aq[c][1][1], aq[c][1][2], aq[c][1][3], y8 & kM0, y8 & kM1);
+            for (int u = 0; u < 4; ++u) {
+                const int row = 8 * u + (lane & 7);
+                ldmatrix_x4(sb + row * 64 + (((lane >> 3) ^ ((row >> 1) & 3)) << 4), w[u][0], w[u][1], w[u][2], w[u][3]);
             }
-            const uint2 *rec = reinterpret_cast<const uint2 *>(stage + 4096) + (8 * u + 2 * t) * NG;
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
+            for (int k = 0; k < NG; ++k) {
+                float d[4][4];
 #pragma unroll
-                for (int k = 0; k < NG; ++k) {
-                    const uint2 z = rec[e * NG + k];
-                    const float ks = lo16(z.x), kz = hi16(z.x);
+                for (int u = 0; u < 4; ++u)
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        // sum over groups of ks d fac + kz qz
-                        const float y = fmaf(ks * d[k][2 * r + e], fac[r], kz * qz[k][r]);
-                        s[u][2 * r + e] = k ? s[u][2 * r + e] + y : y;
+                    for (int e = 0; e < 4; ++e) d[u][e] = 0.f;
+#pragma unroll
+                for (int c = 4 * k / NG; c < 4 * (k + 1) / NG; ++c) {
+                    const uint4 x0 = frag[64 * c + lane], x1 = frag[64 * c + 32 + lane];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const uint32_t y = w[u][c], y8 = y >> 8;
+                        mma16816_nv(d[u], x0.x, x0.y, x0.z, x0.w, y & kM0, y & kM1);
+                        mma16816_nv(d[u], x1.x, x1.y, x1.z, x1.w, y8 & kM0, y8 & kM1);
                     }
-                    vw[u][e][k] = z.y;
                 }
+                // sum over groups of ks d fac + kz qz
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t z = rec[(8 * u + e) * NG + k].x;
+                        const float ks = lo16(z), kz = hi16(z);
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            const float y = fmaf(ks * d[u][2 * r + e], fac[r], kz * qz[k][r]);
+                            s[u][2 * r + e] = k ? s[u][2 * r + e] + y : y;
+                        }
+                    }
+            }
         }
+        uint32_t usable = 0xffu;                     // bit 2 u + e
         if (!full) {
 #pragma unroll
             for (int u = 0; u < 4; ++u)
@@ -407,11 +409,15 @@ __device__ __forceinline__ void history_warp(const TreeArgs &a, const CUtensorMa
                     const int p = p0 + 8 * u + 2 * t + e;
                     if (p < a.sink || p >= he || !((okb >> (u >> 1)) & 1u)) {
                         s[u][e] = s[u][2 + e] = -INFINITY;
-#pragma unroll
-                        for (int k = 0; k < NG; ++k) vw[u][e][k] = 0u;
+                        usable &= ~(1u << (2 * u + e));
                     }
                 }
         }
+        // value scale | zero of key 8 u + 2 t + e, group k; nothing where there is no such key
+        auto value_record = [&](int u, int e, int k) {
+            const uint32_t z = rec[(8 * u + e) * NG + k].y;
+            return full || ((usable >> (2 * u + e)) & 1) ? z : 0u;
+        };
         // Raise the running maximum when a block passes it, change the scaling when a p·s might pass f16's range: looked at only
         // where the lane's largest logit with its largest scale would, together or not.
         float vmax = 0.f;
@@ -420,7 +426,7 @@ __device__ __forceinline__ void history_warp(const TreeArgs &a, const CUtensorMa
 #pragma unroll
             for (int e = 0; e < 2; ++e)
 #pragma unroll
-                for (int k = 0; k < NG; ++k) vmax = fmaxf(vmax, lo16(vw[u][e][k]));
+                for (int k = 0; k < NG; ++k) vmax = fmaxf(vmax, lo16(value_record(u, e, k)));
         float top[2];
         bool raise = false;
 #pragma unroll
@@ -446,7 +452,7 @@ __device__ __forceinline__ void history_warp(const TreeArgs &a, const CUtensorMa
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
 #pragma unroll
-                        for (int k = 0; k < NG; ++k) y = fmaxf(y, ex2_approx(s[u][2 * r + e] - m) * lo16(vw[u][e][k]));
+                        for (int k = 0; k < NG; ++k) y = fmaxf(y, ex2_approx(s[u][2 * r + e] - m) * lo16(value_record(u, e, k)));
                 y = row_max(y);
                 vinv[r] = fminf(old * up, kPMost);
                 if (y * vinv[r] > 0x1p13f) vinv[r] = scaling(y);
@@ -466,7 +472,10 @@ __device__ __forceinline__ void history_warp(const TreeArgs &a, const CUtensorMa
             for (int e = 0; e < 2; ++e) {
                 float zc[NG];                        // zero of the centred codes
 #pragma unroll
-                for (int k = 0; k < NG; ++k) zc[k] = fmaf(8.f, lo16(vw[u][e][k]), hi16(vw[u][e][k]));
+                for (int k = 0; k < NG; ++k) {
+                    const uint32_t z = value_record(u, e, k);
+                    zc[k] = fmaf(8.f, lo16(z), hi16(z));
+                }
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     const float p = ex2_approx(s[u][2 * r + e] - x.m[r]);
@@ -497,7 +506,7 @@ __device__ __forceinline__ void history_warp(const TreeArgs &a, const CUtensorMa
 #pragma unroll
                     for (int v = 0; v < 4; ++v) {
                         const int u = 2 * tl + (v >> 1), r = v & 1;
-                        ap[tl][v] = pack_h2(s[u][2 * r] * lo16(vw[u][0][k]), s[u][2 * r + 1] * lo16(vw[u][1][k]));
+                        ap[tl][v] = pack_h2(s[u][2 * r] * lo16(value_record(u, 0, k)), s[u][2 * r + 1] * lo16(value_record(u, 1, k)));
                     }
 #pragma unroll
             for (int tl = 0; tl < 2; ++tl) {
@@ -537,24 +546,25 @@ __device__ __forceinline__ void history_warp(const TreeArgs &a, const CUtensorMa
     }
 }
 
-// grid (slots x row tiles, Hkv, batch), slots slot0 .. S, the row tiles of a slot next to each other: they read the same rows.
+// grid (slots x row tiles, Hkv, batch), slots slot0 .. S, the row tiles of a slot next to each other: they read the same rows; S = 1
+// and slot0 = 0: the row tiles, all of it by one CTA each.
 // slot0 = S (the BF16 rows alone): launched behind tree_tc_kernel, which starts it once what comes before both is done; it
 // reads none of that one's results, but does not end before it.
 template <int NG>
-__global__ void __launch_bounds__(kW * 32, 1)
+__global__ void __launch_bounds__(kW * 32, NG == 1 ? 2 : 1)
     tree_kernel(TreeArgs a, int tiles, int slot0, const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
     using R = Ring<NG>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t bars[kW * R::n];
-    __shared__ float wf[kW * kTile], wM[kTile];
-    uint8_t *smem = smem_raw + ((1024u - (saddr(smem_raw) & 1023u)) & 1023u);
+    uint8_t *smem = smem_raw + ((512u - (saddr(smem_raw) & 511u)) & 511u);          // the swizzle pattern repeats every 512 bytes
+    uint4 *frag = reinterpret_cast<uint4 *>(smem + R::total);
     const int slot = slot0 + blockIdx.x / tiles, row0 = blockIdx.x % tiles * kTile, h = blockIdx.y, b = blockIdx.z, S = a.part.S;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (lane == 0)
         for (int i = 0; i < R::n; ++i) mbar_init(saddr(&bars[warp * R::n + i]), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     __syncwarp();
-    const bool behind = slot0 == S;
+    const bool behind = slot0 == S, whole = S == 1 && !behind;
     if (!behind) pdl_wait();
     const TreeRequest rq(a, b);
     const int rows = min(kTile, rq.n * a.G - row0);
@@ -564,10 +574,10 @@ __global__ void __launch_bounds__(kW * 32, 1)
     }
     Rows x;
     clear(x);
-    if (slot == S)
-        window_warp(a, rq, b, h, row0, rows, warp, lane, x);
-    else
-        history_warp<NG>(a, &tmk, &tmv, smem + warp * R::n * R::stride, saddr(&bars[warp * R::n]), rq, b, h, row0, rows, slot, warp, lane, x);
+    if (slot < S)
+        history_warp<NG>(a, &tmk, &tmv, smem + warp * R::n * R::stride, saddr(&bars[warp * R::n]), rq, b, h, row0, rows, slot, frag, warp, lane, x);
+    if (whole) __syncthreads();                      // frag is read
+    if (slot == S || whole) window_warp(a, rq, b, h, row0, rows, frag, warp, lane, x);
     __syncthreads();                                 // every warp is done with its ring: results take its place
     float *wm = reinterpret_cast<float *>(smem), *wl = wm + kW * kTile, *wa = wl + kW * kTile + warp * kTile * kResRow;
     const int g = lane >> 2, t = lane & 3;
@@ -588,6 +598,8 @@ __global__ void __launch_bounds__(kW * 32, 1)
     }
     __syncthreads();
     // every warp's weight 2^(m - M) once, then the sums
+    const float *sum = wl + kW * kTile;
+    float *wf = wl + kW * kTile + kW * kTile * kResRow, *wM = wf + kW * kTile;
     if (threadIdx.x < kW * kTile) {
         const int row = threadIdx.x % kTile;
         float M = -INFINITY;
@@ -597,7 +609,6 @@ __global__ void __launch_bounds__(kW * 32, 1)
         if (threadIdx.x < kTile) wM[row] = M;
     }
     __syncthreads();
-    const float *sum = wl + kW * kTile;
     for (int e = threadIdx.x; e < rows * kHeadDim; e += kW * 32) {
         const int row = e / kHeadDim, d = e % kHeadDim;
         float L = 0.f, A = 0.f;
@@ -607,7 +618,13 @@ __global__ void __launch_bounds__(kW * 32, 1)
             L = f != 0.f ? fmaf(wl[w * kTile + row], f, L) : L;
             A = f != 0.f ? fmaf(y, f, A) : A;
         }
-        const size_t at = tree_row(a, rq, h, row0 + row) * (S + 1) + slot;
+        const size_t orow = tree_row(a, rq, h, row0 + row), at = orow * (S + 1) + slot;
+        if (whole) {
+            const bool on = L > 0.f || L != L;
+            a.o[orow * kHeadDim + d] = f32_to_bf16_rn(on ? __fdiv_rn(A, L) : 0.f);
+            if (a.lse && d == 0) a.lse[orow] = on ? (wM[row] + log2f(L)) * 0.6931471805599453f : -INFINITY;
+            continue;
+        }
         a.part.acc[at * kHeadDim + d] = A;
         if (d == 0) {
             a.part.m[at] = wM[row];
@@ -670,21 +687,32 @@ bool rows_tensor_map(CUtensorMap *tm, const uint8_t *base, long long rows, int b
 
 template <int NG>
 cudaError_t launch_rows(const TreeArgs &a, int tiles, int slot0, const CUtensorMap &tmk, const CUtensorMap &tmv, int batch, cudaStream_t st) {
-    const int join = (2 * kW * kTile + kW * kTile * kResRow) * 4, smem = std::max(Ring<NG>::total, join) + 1024;
+    const int join = (3 * kW * kTile + kTile + kW * kTile * kResRow) * 4, smem = std::max(Ring<NG>::total + 4096, join) + 512;
     auto kern = tree_kernel<NG>;
     if (cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void *>(kern), smem)) return e;
-    return launch_ahead(kern, dim3((a.part.S + 1 - slot0) * tiles, a.n_kv, batch), kW * 32, smem, st, a, tiles, slot0, tmk, tmv);
+    return launch_ahead(kern, dim3((a.part.S == 1 && slot0 == 0 ? 1 : a.part.S + 1 - slot0) * tiles, a.n_kv, batch), kW * 32, smem, st, a, tiles, slot0, tmk, tmv);
 }
 
 }  // namespace
 
-// Rows of 16 on mma.sync up to 32 query rows a kv head, of 128 on tcgen05 from there on.
-static bool on_tcgen05(const oscar_layout_t &L, int max_nodes) { return L.group == 128 && max_nodes * L.gqa > 16; }
+// Which kernel takes the history: 128 query rows a CTA on tcgen05 (group 128), or 16 on mma.sync.  The former takes 8.2 ns a tile
+// of 128 positions and 128 rows, the whole GPU, the latter 5.2 ns for 16 rows, and the former's launches cost 7 us more.  With 8 kv
+// heads, tcgen05 and mma.sync, us: 32 rows, 1 x 100K 63 and 76, 64 x 4K 236 and 258, 1 x 4K 22 and 16; 64 rows, 16 ragged of 100K 735
+// and 1,050, 1 x 4K 25.5 and 19.6.
+static bool on_tcgen05(const oscar_layout_t &L, int batch, int max_nodes, long long tokens) {
+    const long long rows = (long long)max_nodes * L.gqa, tiles = (long long)batch * L.n_kv_heads * (tokens / 128 + 1);
+    return L.group == 128 && rows > 16 && tiles * (52 * ((rows + 15) / 16) - 82 * ((rows + 127) / 128)) > 70000;
+}
 
+// On tcgen05: one CTA an SM in one wave that leaves some SMs to the BF16 rows, or, where splits would pass 16K positions, splits of 8K,
+// which finish evenly (16 ragged of 100K, 64 rows: 858 us with one split, 735) and keep long sums short.  On mma.sync: one wave of two
+// CTAs an SM (one for groups of 32 and 64), the BF16 rows' among them; one split where that leaves less than two, splits of 8K where
+// they would be long (4 rows a kv head, 16 ragged of 100K: 979, 477, 438, 433 and 459 us with 1, 4, 8, 12 and 24).
 int suggest_splits_tree(const oscar_layout_t &L, int batch, int max_nodes, int max_hist, int sm_count) {
-    const long long rows = max_nodes * (long long)L.gqa, tile = on_tcgen05(L, max_nodes) ? 128 : kTile;
+    const bool tc = on_tcgen05(L, batch, max_nodes, max_hist);
+    const long long rows = max_nodes * (long long)L.gqa, tile = tc ? 128 : kTile;
     const long long units = (long long)batch * L.n_kv_heads * ((rows + tile - 1) / tile);
-    long long want = std::max(1LL, (sm_count - 8) / units);
+    long long want = std::max(1LL, tc ? (sm_count - 8) / units : (L.group == 128 ? 2LL : 1LL) * sm_count / units - 1);
     if (max_hist > want * 16384) want = std::max(want, std::min(max_hist / 8192LL, 12LL * sm_count / units));
     want = std::min(want, (max_hist + 511LL) / 512);
     return (int)std::max(1LL, std::min(want, 1024LL));
@@ -699,7 +727,7 @@ cudaError_t launch_tree_attention(const oscar_layout_t &L, const Attn4Input &in,
     const int box = L.page_size < kBlock4 ? L.page_size : kBlock4;
     if (!rows_tensor_map(&tmk, in.i4.codes_k, rows, box) || !rows_tensor_map(&tmv, in.i4.codes_v, rows, box)) return cudaErrorInvalidValue;
     const int tiles = (t.max_nodes * L.gqa + kTile - 1) / kTile;
-    const bool tc = on_tcgen05(L, t.max_nodes);
+    const bool tc = on_tcgen05(L, batch, t.max_nodes, (long long)in.max_pages * L.page_size);
     if (tc)
         if (cudaError_t e = launch_tree_history_tc(a, t.max_nodes * L.gqa, batch, st)) return e;
     const int slot0 = tc ? part.S : 0;
@@ -709,7 +737,7 @@ cudaError_t launch_tree_attention(const oscar_layout_t &L, const Attn4Input &in,
         case 64: e = launch_rows<2>(a, tiles, slot0, tmk, tmv, batch, st); break;
         default: e = launch_rows<1>(a, tiles, slot0, tmk, tmv, batch, st); break;
     }
-    if (e) return e;
+    if (e || (part.S == 1 && !tc)) return e;
     return launch_ahead(tree_merge_kernel, dim3((t.max_nodes * L.n_kv_heads * L.gqa + 3) / 4, batch), 128, 0, st, a);
 }
 

@@ -84,8 +84,8 @@ OSCAR_API oscar_status_t oscar_tree_attention_int4(const oscar_layout_t *layout,
  *   min_p  the tokens with w_i >= min_p                             (off: NULL, or a value <= 0 or NaN)
  * and one at least.  The token is the kept one of lowest index i for which the w of the kept tokens up to and
  * including i sum to more than u times their total.
- *   logits       [rows][vocab] of the given type, row r at logits + r·stride (elements; stride >= vocab); any
- *                alignment of the type.  -inf: never drawn.  NaN counts as -inf.  Where the largest logit is
+ *   logits       [rows][vocab] of the given type, row r at logits + r·stride (elements; stride >= vocab, or 0: one
+ *                row for all); any alignment of the type.  -inf: never drawn.  NaN counts as -inf.  Where the largest logit is
  *                +inf, the tokens that have it share the weight alone.
  *   temperature  fp32 [rows]; 0 (or less, or NaN): the largest logit's lowest index, the filters and u are not
  *                read; +inf: every finite logit weighs the same.
