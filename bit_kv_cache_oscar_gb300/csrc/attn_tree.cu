@@ -8,10 +8,12 @@
 //   sum_t p_t v_t = sum_t (p_t s_t) (n_t - 8) + sum_t p_t (z_t + 8 s_t)
 // with centred codes, normal f16 numbers at one operation more a pair: uncentred the two sums cancel most of each other, which
 // would ask for p s in two parts and for sums that are not truncated (the accumulators of mma.sync are).  p s is one f16
-// number, 2^-12 relative, under a power of two per row that follows the largest p s so far.
+// number, 2^-11 relative.  p = 2^(logit - M) with a reference M per row that is raised, in whole steps, whenever a p s passes 2^15
+// (then brought to about 2^8) or p passes 2^100: the largest p s so far, not the largest p, sits near the top of f16's range.
 //
-// A CTA takes (split, 16 query rows, kv head, request); each of its 8 warps takes every 8th block of 32 tokens through a ring
-// of bulk tensor copies of its own, and they join at the end.  Slot S of the partials is the BF16 rows': the last CTA of a
+// A CTA takes (split, 16 query rows, kv head, request); each of its W warps takes every W-th block of 32 tokens through a ring
+// of bulk tensor copies of its own, and they join at the end.  W is 12 where the launch has about a CTA an SM, else 8, two CTAs
+// an SM (group 128; smaller groups need the registers of one).  Slot S of the partials is the BF16 rows': the last CTA of a
 // row tile, whose warps take 16 positions at a time straight from global memory.  With one split, a CTA takes both, one after the
 // other, and writes the result: no partials, no merge.
 
@@ -27,21 +29,20 @@
 namespace oscar {
 namespace {
 
-constexpr int kW = 8;                            // warps of a CTA
 constexpr int kTile = 16;                        // query rows of a CTA
+constexpr int kWide = 160;                       // CTAs of a launch up to which each gets an SM
 constexpr uint32_t kM0 = 0x000F000Fu, kM1 = 0x00F000F0u;
 constexpr int kResRow = kHeadDim + 4;
-constexpr float kNone = -1e30f;                  // running maximum before the first token
-constexpr float kSlack = 8.f;                    // logits (base 2) may pass the running maximum by this
-constexpr int kPShift = 8;                       // a new scaling brings the largest p·s into [2^8, 2^9); near 2^15 another is due
-constexpr float kPMost = 0x1p110f;
+constexpr float kNone = -1e30f;                  // reference before the first token
+constexpr float kMostP = 0x1p100f;               // of the sum of a lane's p in a block
+constexpr float kNewW = 8.f, kNewP = 80.f;       // a new reference brings p·s to 2^8 at most, p to 2^80
 
-template <int NG>
+template <int NG, int W>
 struct Ring {
     static constexpr int bytes = 4096 + kBlock4 * NG * 8;
     static constexpr int stride = (bytes + 511) & ~511;
     static constexpr int n = NG == 4 ? 2 : 3;                    // as many as leave room for two CTAs on an SM
-    static constexpr int total = kW * n * stride;
+    static constexpr int total = W * n * stride;
 };
 
 __device__ __forceinline__ float lo16(uint32_t w) { return __uint_as_float(w << 16); }
@@ -50,6 +51,7 @@ __device__ __forceinline__ uint32_t pack_h2(float a, float b) {
     const __half2 h = __floats2half2_rn(a, b);
     return *reinterpret_cast<const uint32_t *>(&h);
 }
+__device__ __forceinline__ __nv_bfloat162 as_bf2(uint32_t w) { return *reinterpret_cast<const __nv_bfloat162 *>(&w); }
 __device__ __forceinline__ uint32_t pack_b2(float a, float b) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t *>(&h);
@@ -87,12 +89,6 @@ __device__ __forceinline__ uint32_t centred_high(uint32_t w) {
         : "=r"(d) : "r"(w), "r"(0x2C002C00u), "r"(0xD480D480u));
     return d;
 }
-// The power of two that brings x > 0, 2^e <= x < 2^(e + 1), to 2^kPShift.
-__device__ __forceinline__ float scaling(float x) {
-    const int e = max((int)(__float_as_uint(x) >> 23) - 127, kPShift - 110);
-    return __uint_as_float((uint32_t)(kPShift - e + 127) << 23);
-}
-
 // What a warp holds of its 16 rows: lane (g, t) has rows g and g + 8 (index r); out[c][i][2 r + e] is channel
 // 32 c + 8 t + 4 e + i of row g + 8 r.
 struct Rows {
@@ -124,13 +120,14 @@ __device__ __forceinline__ uint4 query_piece(const TreeArgs &a, const TreeReques
 
 // ---- the BF16 rows ---------------------------------------------------------------------------------
 // Positions [0, min(sink, T)), [max(hist_end, those), T) and the nodes' [T, T + n), in tiles of 16.
+template <int W>
 __device__ __forceinline__ void window_warp(const TreeArgs &a, const TreeRequest &rq, int b, int h, int row0, int rows, uint4 *frag, int warp, int lane,
                                             Rows &x) {
     const int g = lane >> 2, t = lane & 3, sh = a.page_shift, T = rq.T, end = T + rq.n;
     const int n0 = min(a.sink, T), lo1 = max(rq.he, n0), sink_tiles = (n0 + 15) / 16, rec0 = lo1 / 16;
     const int tiles = sink_tiles + (end + 15) / 16 - rec0;
     // the A operand of the logits, as it lies, for all warps: fragment 2 i + e of lane l at 32 (2 i + e) + l
-    for (int k = warp; k < 4; k += kW) {
+    for (int k = warp; k < 4; k += W) {
         const uint4 x = query_piece(a, rq, h, row0, rows, 0, k, lane), y = query_piece(a, rq, h, row0, rows, 1, k, lane);
         frag[64 * k + lane] = make_uint4(x.x, y.x, x.y, y.y);
         frag[64 * k + 32 + lane] = make_uint4(x.z, y.z, x.w, y.w);
@@ -140,7 +137,7 @@ __device__ __forceinline__ void window_warp(const TreeArgs &a, const TreeRequest
 #pragma unroll
     for (int r = 0; r < 2; ++r) node[r] = (row0 + min(g + 8 * r, rows - 1)) / a.G;
 #pragma unroll 1
-    for (int k = warp; k < tiles; k += kW) {
+    for (int k = warp; k < tiles; k += W) {
         const bool in_sink = k < sink_tiles;
         const int p0 = (in_sink ? k : rec0 + k - sink_tiles) * 16, lo = in_sink ? 0 : lo1, hi = in_sink ? n0 : end;
         const int page = a.bpt[(size_t)b * a.max_pages + (p0 >> sh)];
@@ -253,22 +250,22 @@ __device__ __forceinline__ void window_warp(const TreeArgs &a, const TreeRequest
 }
 
 // ---- the history -----------------------------------------------------------------------------------
-template <int NG>
+template <int NG, int W>
 __device__ __forceinline__ void history_warp(const TreeArgs &a, const CUtensorMap *tmk, const CUtensorMap *tmv, uint8_t *ring, uint32_t bars,
                                              const TreeRequest &rq, int b, int h, int row0, int rows, int split, uint4 *frag, int warp, int lane, Rows &x) {
-    using R = Ring<NG>;
+    using R = Ring<NG, W>;
     const int t = lane & 3, sh = a.page_shift, S = a.part.S, he = rq.he;
     const int first = a.sink / kBlock4, nb = he > a.sink ? (he + kBlock4 - 1) / kBlock4 - first : 0;
     const int lo = first + (int)((long long)split * nb / S) + warp, hi = first + (int)((long long)(split + 1) * nb / S);
-    const int n = lo < hi ? (hi - lo + kW - 1) / kW : 0;        // blocks lo, lo + kW, ...
+    const int n = lo < hi ? (hi - lo + W - 1) / W : 0;        // blocks lo, lo + W, ...
     const int32_t *pt = a.ipt + (size_t)b * a.max_pages;
     const uint64_t pol = l2_evict_first_policy();
 
-    int pg0 = -1, pg1 = -1;        // lane j: pages of the two 16-token halves of block lo + kW (batch + j)
+    int pg0 = -1, pg1 = -1;        // lane j: pages of the two 16-token halves of block lo + W (batch + j)
     uint32_t ok = 0;               // two bits per stage: halves that were loaded
     auto issue = [&](int i, int st) {
         if ((i & 31) == 0) {
-            const int p = (lo + kW * (i + lane)) * kBlock4;
+            const int p = (lo + W * (i + lane)) * kBlock4;
             pg0 = pg1 = -1;
             if (i + lane < n) {
                 const bool in0 = p + 16 > a.sink && p < he, in1 = p + kBlock4 > a.sink && p + 16 < he;
@@ -282,7 +279,7 @@ __device__ __forceinline__ void history_warp(const TreeArgs &a, const CUtensorMa
         const bool ok0 = (uint32_t)a0 < (uint32_t)a.i4_pages, ok1 = (uint32_t)a1 < (uint32_t)a.i4_pages;
         ok = (ok & ~(3u << (2 * st))) | ((ok0 ? 1u : 0u) | (ok1 ? 2u : 0u)) << (2 * st);
         if (lane == 0) {
-            const int p = (lo + kW * i) * kBlock4;
+            const int p = (lo + W * i) * kBlock4;
             const uint32_t dst = saddr(ring + st * R::stride), bar = bars + 8 * st;
             // pages of 32 or more: one box of 32 rows; pages of 16: a box a half
             const int box = sh >= 5 ? kBlock4 : 16;
@@ -302,7 +299,7 @@ __device__ __forceinline__ void history_warp(const TreeArgs &a, const CUtensorMa
     for (int i = 0; i < R::n && i < n; ++i) issue(i, i);
 
     // A operand of the logits, for all warps (fragment 2 i + e of lane l at 32 (2 i + e) + l): channels 32 i + 8 t .. of chunk i,
-    // the odd nibbles' against 1/16 of the query; fac undoes the scalings, qz is the zero's factor, per row and group.
+    // the odd nibbles' against 1/16 of the query; fac undoes the scalings, qz is the zero's factor before it, per row and group.
     float fac[2], qz[NG][2];
     {
         float mul[2], qs[2][NG];
@@ -326,9 +323,9 @@ __device__ __forceinline__ void history_warp(const TreeArgs &a, const CUtensorMa
             mul[r] = __uint_as_float((uint32_t)(14 - ex + 127) << 23);
             fac[r] = a.scale2 * __uint_as_float((uint32_t)(10 + ex + 127) << 23);              // 2^24 / mul
 #pragma unroll
-            for (int k = 0; k < NG; ++k) qz[k][r] = row_sum(qs[r][k]) * a.scale2;
+            for (int k = 0; k < NG; ++k) qz[k][r] = row_sum(qs[r][k]) * (mul[r] * 0x1p-24f);   // (fac's units)
         }
-        for (int i = warp; i < 4; i += kW) {
+        for (int i = warp; i < 4; i += W) {
             uint32_t f[2][4];
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
@@ -344,7 +341,6 @@ __device__ __forceinline__ void history_warp(const TreeArgs &a, const CUtensorMa
         }
     }
     __syncthreads();
-    float vinv[2] = {kPMost, kPMost};                // what the rows' p·s are multiplied by, powers of two
     for (int i = 0, st = 0, phase = 0; i < n; ++i) {
         if (!mbar_wait(bars + 8 * st, phase)) {
             if (lane == 0) flag_status(a.status, OSCAR_DEV_WAIT_TIMEOUT);
@@ -354,13 +350,12 @@ __device__ __forceinline__ void history_warp(const TreeArgs &a, const CUtensorMa
         }
         const uint8_t *stage = ring + st * R::stride;
         const uint32_t sb = saddr(stage);
-        const int p0 = (lo + kW * i) * kBlock4;
+        const int p0 = (lo + W * i) * kBlock4;
         const uint32_t okb = (ok >> (2 * st)) & 3u;
         const bool full = okb == 3u && p0 >= a.sink && p0 + kBlock4 <= he;
 
-        // [8 keys][2 r + e]: logit of key 8 u + 2 t + e and row g + 8 r
-        float s[4][4];
-        const uint2 *const rec = reinterpret_cast<const uint2 *>(stage + 4096) + 2 * t * NG;        // records of key 8 u + 2 t + e: (8 u + e) NG + k
+        f2 s[4][2];                                  // keys 8 u + 2 t, + 1 of row g + 8 r: the logits before fac
+        uint32_t vw[4][2][NG];                       // value scale | zero of those keys
         {
             uint32_t w[4][4];
 #pragma unroll
@@ -385,19 +380,20 @@ __device__ __forceinline__ void history_warp(const TreeArgs &a, const CUtensorMa
                         mma16816_nv(d[u], x1.x, x1.y, x1.z, x1.w, y8 & kM0, y8 & kM1);
                     }
                 }
-                // sum over groups of ks d fac + kz qz
+                // sum over groups of ks d + kz qz
 #pragma unroll
-                for (int u = 0; u < 4; ++u)
+                for (int u = 0; u < 4; ++u) {
+                    const uint2 *rec = reinterpret_cast<const uint2 *>(stage + 4096) + (8 * u + 2 * t) * NG + k;
+                    const uint2 z0 = rec[0], z1 = rec[NG];
+                    vw[u][0][k] = z0.y;
+                    vw[u][1][k] = z1.y;
+                    const f2 ks = pair(lo16(z0.x), lo16(z1.x)), kz = pair(hi16(z0.x), hi16(z1.x));
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const uint32_t z = rec[(8 * u + e) * NG + k].x;
-                        const float ks = lo16(z), kz = hi16(z);
-#pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            const float y = fmaf(ks * d[u][2 * r + e], fac[r], kz * qz[k][r]);
-                            s[u][2 * r + e] = k ? s[u][2 * r + e] + y : y;
-                        }
+                    for (int r = 0; r < 2; ++r) {
+                        const f2 qk = pair(qz[k][r], qz[k][r]);
+                        s[u][r] = fma2(ks, pair(d[u][2 * r], d[u][2 * r + 1]), k ? fma2(kz, qk, s[u][r]) : mul2(kz, qk));
                     }
+                }
             }
         }
         uint32_t usable = 0xffu;                     // bit 2 u + e
@@ -408,87 +404,105 @@ __device__ __forceinline__ void history_warp(const TreeArgs &a, const CUtensorMa
                 for (int e = 0; e < 2; ++e) {
                     const int p = p0 + 8 * u + 2 * t + e;
                     if (p < a.sink || p >= he || !((okb >> (u >> 1)) & 1u)) {
-                        s[u][e] = s[u][2 + e] = -INFINITY;
                         usable &= ~(1u << (2 * u + e));
+#pragma unroll
+                        for (int k = 0; k < NG; ++k) vw[u][e][k] = 0u;
                     }
                 }
         }
-        // value scale | zero of key 8 u + 2 t + e, group k; nothing where there is no such key
-        auto value_record = [&](int u, int e, int k) {
-            const uint32_t z = rec[(8 * u + e) * NG + k].y;
-            return full || ((usable >> (2 * u + e)) & 1) ? z : 0u;
-        };
-        // Raise the running maximum when a block passes it, change the scaling when a p·s might pass f16's range: looked at only
-        // where the lane's largest logit with its largest scale would, together or not.
-        float vmax = 0.f;
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-#pragma unroll
-                for (int k = 0; k < NG; ++k) vmax = fmaxf(vmax, lo16(value_record(u, e, k)));
-        float top[2];
-        bool raise = false;
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            top[r] = fmaxf(fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1])),
-                           fmaxf(fmaxf(s[2][2 * r], s[2][2 * r + 1]), fmaxf(s[3][2 * r], s[3][2 * r + 1])));
-            const float over = top[r] - x.m[r];
-            raise |= over > kSlack || ex2_approx(over) * vinv[r] * vmax > 0x1p15f;
-        }
-        if (__any_sync(0xffffffffu, raise)) {
+        f2 p[4][2];                                  // 2^(logit - M)
+        float l[2];
+        for (int again = 0;; ++again) {              // once, or twice where a reference was due
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                const float m = fmaxf(x.m[r], row_max(top[r])), al = ex2_approx(x.m[r] - m);
-                // what was summed shrinks by al, so the scaling may grow by as much (by 2^100 at most)
-                const float up = __uint_as_float((uint32_t)(__float2int_rn(fminf(m - x.m[r], 100.f)) + 127) << 23), old = vinv[r];
-                x.m[r] = m;
-                x.l[r] *= al;
+                const f2 fr = pair(fac[r], fac[r]), mr = pair(-x.m[r], -x.m[r]);
+                f2 l2 = 0ull;
 #pragma unroll
-                for (int k = 0; k < NG; ++k) x.z[k][r] *= al;
-                float y = 0.f;
+                for (int u = 0; u < 4; ++u) {
+                    float e0, e1;
+                    unpair(fma2(s[u][r], fr, mr), e0, e1);
+                    if (!full) {
+                        if (!((usable >> (2 * u)) & 1)) e0 = -INFINITY;
+                        if (!((usable >> (2 * u + 1)) & 1)) e1 = -INFINITY;
+                    }
+                    p[u][r] = pair(ex2_approx(e0), ex2_approx(e1));
+                    l2 = add2(l2, p[u][r]);
+                }
+                float l0, l1;
+                unpair(l2, l0, l1);
+                l[r] = l0 + l1;
+            }
+            // looked at closer where the rows' sums with the largest of the lane's scales would pass f16's range, together or not
+            __nv_bfloat162 v2 = as_bf2(vw[0][0][0]);
 #pragma unroll
-                for (int u = 0; u < 4; ++u)
+            for (int u = 0; u < 4; ++u)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e)
+                for (int e = 0; e < 2; ++e)
 #pragma unroll
-                        for (int k = 0; k < NG; ++k) y = fmaxf(y, ex2_approx(s[u][2 * r + e] - m) * lo16(value_record(u, e, k)));
-                y = row_max(y);
-                vinv[r] = fminf(old * up, kPMost);
-                if (y * vinv[r] > 0x1p13f) vinv[r] = scaling(y);
-                const float f = al * (vinv[r] / old);
+                    for (int k = 0; k < NG; ++k) v2 = __hmax2(v2, as_bf2(vw[u][e][k]));        // scales in the low halves
+            const float both = fmaxf(l[0], l[1]);
+            if (!__any_sync(0xffffffffu, both * __low2float(v2) >= 0x1p15f || both >= kMostP) || again) break;
+#pragma unroll 1
+            for (int r = 0; r < 2; ++r) {
+                float top = -INFINITY, topw = -INFINITY;                   // largest logit, largest logit + log2 s
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
+                for (int u = 0; u < 4; ++u) {
+                    float e[2];
+                    unpair(mul2(r ? s[u][1] : s[u][0], pair(r ? fac[1] : fac[0], r ? fac[1] : fac[0])), e[0], e[1]);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
+                    for (int j = 0; j < 2; ++j) {
+                        if (!((usable >> (2 * u + j)) & 1)) continue;
+                        top = fmaxf(top, e[j]);
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) x.out[c][j][2 * r + e] *= f;
+                        for (int k = 0; k < NG; ++k) topw = fmaxf(topw, e[j] + __log2f(lo16(vw[u][j][k])));
+                    }
+                }
+                top = row_max(top);
+                topw = row_max(topw);
+                const float M = r ? x.m[1] : x.m[0];
+                float to = M;
+                // kept where it will do: the check above is for sums of eight and scales apart
+                if (topw - M >= 11.9f || top - M >= 90.f) {
+                    const float want = ceilf(fmaxf(topw - kNewW, top - kNewP));
+                    to = M == kNone ? want : fmaxf(M, want);
+                }
+                const int down = __float2int_rn(M - to);                   // (whole, or far below)
+                const float f = down < -126 ? 0.f : __uint_as_float((uint32_t)(down + 127) << 23);
+                if (r) x.m[1] = to;
+                else x.m[0] = to;
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const float fq = q == r ? f : 1.f;
+                    x.l[q] *= fq;
+#pragma unroll
+                    for (int k = 0; k < NG; ++k) x.z[k][q] *= fq;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) x.out[c][j][2 * q + e] *= fq;
+                }
             }
         }
-        float z4[NG][2];
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
+        for (int r = 0; r < 2; ++r) x.l[r] += l[r];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float zc[NG];                        // zero of the centred codes
+        for (int k = 0; k < NG; ++k) {
+            f2 z2[2] = {0ull, 0ull};
 #pragma unroll
-                for (int k = 0; k < NG; ++k) {
-                    const uint32_t z = value_record(u, e, k);
-                    zc[k] = fmaf(8.f, lo16(z), hi16(z));
-                }
+            for (int u = 0; u < 4; ++u) {            // zero of the centred codes
+                const f2 vs = pair(lo16(vw[u][0][k]), lo16(vw[u][1][k])), zc = fma2(pair(8.f, 8.f), vs, pair(hi16(vw[u][0][k]), hi16(vw[u][1][k])));
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const float p = ex2_approx(s[u][2 * r + e] - x.m[r]);
-                    x.l[r] += p;
-#pragma unroll
-                    for (int k = 0; k < NG; ++k) z4[k][r] = u + e ? fmaf(p, zc[k], z4[k][r]) : p * zc[k];
-                    s[u][2 * r + e] = p * vinv[r];
-                }
+                for (int r = 0; r < 2; ++r) z2[r] = fma2(p[u][r], zc, z2[r]);
             }
 #pragma unroll
-        for (int k = 0; k < NG; ++k)
-#pragma unroll
-            for (int r = 0; r < 2; ++r) x.z[k][r] += z4[k][r];
+            for (int r = 0; r < 2; ++r) {
+                float z0, z1;
+                unpair(z2[r], z0, z1);
+                x.z[k][r] += z0 + z1;
+            }
+        }
         uint32_t ap[2][4], vc[2][4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -506,7 +520,9 @@ __device__ __forceinline__ void history_warp(const TreeArgs &a, const CUtensorMa
 #pragma unroll
                     for (int v = 0; v < 4; ++v) {
                         const int u = 2 * tl + (v >> 1), r = v & 1;
-                        ap[tl][v] = pack_h2(s[u][2 * r] * lo16(value_record(u, 0, k)), s[u][2 * r + 1] * lo16(value_record(u, 1, k)));
+                        float w0, w1;
+                        unpair(mul2(p[u][r], pair(lo16(vw[u][0][k]), lo16(vw[u][1][k]))), w0, w1);
+                        ap[tl][v] = pack_h2(w0, w1);
                     }
 #pragma unroll
             for (int tl = 0; tl < 2; ++tl) {
@@ -526,13 +542,6 @@ __device__ __forceinline__ void history_warp(const TreeArgs &a, const CUtensorMa
     }
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-        const float up = 1.f / vinv[r];
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) x.out[c][j][2 * r + e] *= up;
 #pragma unroll
         for (int k = 0; k < NG; ++k) {
             const float z = row_sum(x.z[k][r]);
@@ -550,12 +559,12 @@ __device__ __forceinline__ void history_warp(const TreeArgs &a, const CUtensorMa
 // and slot0 = 0: the row tiles, all of it by one CTA each.
 // slot0 = S (the BF16 rows alone): launched behind tree_tc_kernel, which starts it once what comes before both is done; it
 // reads none of that one's results, but does not end before it.
-template <int NG>
-__global__ void __launch_bounds__(kW * 32, NG == 1 ? 2 : 1)
+template <int NG, int W>
+__global__ void __launch_bounds__(W * 32, NG == 1 && W == 8 ? 2 : 1)
     tree_kernel(TreeArgs a, int tiles, int slot0, const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
-    using R = Ring<NG>;
+    using R = Ring<NG, W>;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t bars[kW * R::n];
+    __shared__ uint64_t bars[W * R::n];
     uint8_t *smem = smem_raw + ((512u - (saddr(smem_raw) & 511u)) & 511u);          // the swizzle pattern repeats every 512 bytes
     uint4 *frag = reinterpret_cast<uint4 *>(smem + R::total);
     const int slot = slot0 + blockIdx.x / tiles, row0 = blockIdx.x % tiles * kTile, h = blockIdx.y, b = blockIdx.z, S = a.part.S;
@@ -575,11 +584,11 @@ __global__ void __launch_bounds__(kW * 32, NG == 1 ? 2 : 1)
     Rows x;
     clear(x);
     if (slot < S)
-        history_warp<NG>(a, &tmk, &tmv, smem + warp * R::n * R::stride, saddr(&bars[warp * R::n]), rq, b, h, row0, rows, slot, frag, warp, lane, x);
+        history_warp<NG, W>(a, &tmk, &tmv, smem + warp * R::n * R::stride, saddr(&bars[warp * R::n]), rq, b, h, row0, rows, slot, frag, warp, lane, x);
     if (whole) __syncthreads();                      // frag is read
-    if (slot == S || whole) window_warp(a, rq, b, h, row0, rows, frag, warp, lane, x);
+    if (slot == S || whole) window_warp<W>(a, rq, b, h, row0, rows, frag, warp, lane, x);
     __syncthreads();                                 // every warp is done with its ring: results take its place
-    float *wm = reinterpret_cast<float *>(smem), *wl = wm + kW * kTile, *wa = wl + kW * kTile + warp * kTile * kResRow;
+    float *wm = reinterpret_cast<float *>(smem), *wl = wm + W * kTile, *wa = wl + W * kTile + warp * kTile * kResRow;
     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
@@ -598,22 +607,22 @@ __global__ void __launch_bounds__(kW * 32, NG == 1 ? 2 : 1)
     }
     __syncthreads();
     // every warp's weight 2^(m - M) once, then the sums
-    const float *sum = wl + kW * kTile;
-    float *wf = wl + kW * kTile + kW * kTile * kResRow, *wM = wf + kW * kTile;
-    if (threadIdx.x < kW * kTile) {
+    const float *sum = wl + W * kTile;
+    float *wf = wl + W * kTile + W * kTile * kResRow, *wM = wf + W * kTile;
+    if (threadIdx.x < W * kTile) {
         const int row = threadIdx.x % kTile;
         float M = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kW; ++w) M = fmaxf(M, wm[w * kTile + row]);
+        for (int w = 0; w < W; ++w) M = fmaxf(M, wm[w * kTile + row]);
         wf[threadIdx.x] = wm[threadIdx.x] != -INFINITY ? exp2f(wm[threadIdx.x] - M) : 0.f;
         if (threadIdx.x < kTile) wM[row] = M;
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < rows * kHeadDim; e += kW * 32) {
+    for (int e = threadIdx.x; e < rows * kHeadDim; e += W * 32) {
         const int row = e / kHeadDim, d = e % kHeadDim;
         float L = 0.f, A = 0.f;
 #pragma unroll
-        for (int w = 0; w < kW; ++w) {
+        for (int w = 0; w < W; ++w) {
             const float f = wf[w * kTile + row], y = sum[(w * kTile + row) * kResRow + d];
             L = f != 0.f ? fmaf(wl[w * kTile + row], f, L) : L;
             A = f != 0.f ? fmaf(y, f, A) : A;
@@ -685,12 +694,12 @@ bool rows_tensor_map(CUtensorMap *tm, const uint8_t *base, long long rows, int b
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int NG>
+template <int NG, int W>
 cudaError_t launch_rows(const TreeArgs &a, int tiles, int slot0, const CUtensorMap &tmk, const CUtensorMap &tmv, int batch, cudaStream_t st) {
-    const int join = (3 * kW * kTile + kTile + kW * kTile * kResRow) * 4, smem = std::max(Ring<NG>::total + 4096, join) + 512;
-    auto kern = tree_kernel<NG>;
+    const int join = (3 * W * kTile + kTile + W * kTile * kResRow) * 4, smem = std::max(Ring<NG, W>::total + 4096, join) + 512;
+    auto kern = tree_kernel<NG, W>;
     if (cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void *>(kern), smem)) return e;
-    return launch_ahead(kern, dim3((a.part.S == 1 && slot0 == 0 ? 1 : a.part.S + 1 - slot0) * tiles, a.n_kv, batch), kW * 32, smem, st, a, tiles, slot0, tmk, tmv);
+    return launch_ahead(kern, dim3((a.part.S == 1 && slot0 == 0 ? 1 : a.part.S + 1 - slot0) * tiles, a.n_kv, batch), W * 32, smem, st, a, tiles, slot0, tmk, tmv);
 }
 
 }  // namespace
@@ -705,15 +714,18 @@ static bool on_tcgen05(const oscar_layout_t &L, int batch, int max_nodes, long l
 }
 
 // On tcgen05: one CTA an SM in one wave that leaves some SMs to the BF16 rows, or, where splits would pass 16K positions, splits of 8K,
-// which finish evenly (16 ragged of 100K, 64 rows: 858 us with one split, 735) and keep long sums short.  On mma.sync: one wave of two
-// CTAs an SM (one for groups of 32 and 64), the BF16 rows' among them; one split where that leaves less than two, splits of 8K where
-// they would be long (4 rows a kv head, 16 ragged of 100K: 979, 477, 438, 433 and 459 us with 1, 4, 8, 12 and 24).
+// which finish evenly (16 ragged of 100K, 64 rows: 858 us with one split, 735) and keep long sums short.  On mma.sync: one wave, the
+// BF16 rows' CTAs among it, of 12 warps and one CTA an SM where that leaves three splits, else (and for groups of 32 and 64) of 8
+// warps, two CTAs an SM (one); splits of 8K where they would pass 32K.  4 rows a kv head, us, 12 and 8 warps: 1 x 100K 43.6 and 48.6
+// (18 and 37 splits), 64 x 4K 136 and 127 (one split), 8 x 8K 41 and 42 (2 and 3), 16 ragged of 100K 425 and 433 (8 and 12).
 int suggest_splits_tree(const oscar_layout_t &L, int batch, int max_nodes, int max_hist, int sm_count) {
     const bool tc = on_tcgen05(L, batch, max_nodes, max_hist);
     const long long rows = max_nodes * (long long)L.gqa, tile = tc ? 128 : kTile;
     const long long units = (long long)batch * L.n_kv_heads * ((rows + tile - 1) / tile);
-    long long want = std::max(1LL, tc ? (sm_count - 8) / units : (L.group == 128 ? 2LL : 1LL) * sm_count / units - 1);
-    if (max_hist > want * 16384) want = std::max(want, std::min(max_hist / 8192LL, 12LL * sm_count / units));
+    long long want = tc ? (sm_count - 8) / units : sm_count / units - 1;
+    if (!tc && want < 3 && L.group == 128) want = 2LL * sm_count / units - 1;
+    want = std::max(want, 1LL);
+    if (max_hist > want * (tc ? 16384 : 32768)) want = std::max(want, std::min(max_hist / 8192LL, 12LL * sm_count / units));
     want = std::min(want, (max_hist + 511LL) / 512);
     return (int)std::max(1LL, std::min(want, 1024LL));
 }
@@ -731,11 +743,12 @@ cudaError_t launch_tree_attention(const oscar_layout_t &L, const Attn4Input &in,
     if (tc)
         if (cudaError_t e = launch_tree_history_tc(a, t.max_nodes * L.gqa, batch, st)) return e;
     const int slot0 = tc ? part.S : 0;
+    const bool wide = !tc && (long long)(part.S + 1) * tiles * L.n_kv_heads * batch <= kWide;
     cudaError_t e;
     switch (L.group) {
-        case 32: e = launch_rows<4>(a, tiles, slot0, tmk, tmv, batch, st); break;
-        case 64: e = launch_rows<2>(a, tiles, slot0, tmk, tmv, batch, st); break;
-        default: e = launch_rows<1>(a, tiles, slot0, tmk, tmv, batch, st); break;
+        case 32: e = launch_rows<4, 8>(a, tiles, slot0, tmk, tmv, batch, st); break;
+        case 64: e = launch_rows<2, 8>(a, tiles, slot0, tmk, tmv, batch, st); break;
+        default: e = wide ? launch_rows<1, 12>(a, tiles, slot0, tmk, tmv, batch, st) : launch_rows<1, 8>(a, tiles, slot0, tmk, tmv, batch, st);
     }
     if (e || (part.S == 1 && !tc)) return e;
     return launch_ahead(tree_merge_kernel, dim3((t.max_nodes * L.n_kv_heads * L.gqa + 3) / 4, batch), 128, 0, st, a);
