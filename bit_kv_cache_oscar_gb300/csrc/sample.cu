@@ -23,6 +23,7 @@
 
 #include <cstring>
 
+#include "pairs.cuh"
 #include "ptx.cuh"
 #include "tree.cuh"
 
@@ -94,19 +95,36 @@ struct Row {
     const uint32_t *table;                           // 2^31 2^(-j / 256)
     __device__ __forceinline__ float depth(float x) const { return x == top ? 0.f : __fmul_rn(__fsub_rn(top, x), ch); }
     __device__ __forceinline__ bool kept(float x, int i) const { return x > v || (x == v && i <= I); }
+    // Weights of two logits.
+    __device__ __forceinline__ void weights(float xa, float xb, uint64_t &wa, uint64_t &wb) const {
+        const f2 minus = pair(-1.f, -1.f), x = pair(xa, xb), t = pair(top, top), magic = pair(12582912.f, 12582912.f);
+        const f2 d = fma2(x, minus, t), bb = add2(d, pair(-top, -top));
+        // what d lacks, exactly: (top - (d - bb)) - (x + bb)
+        const f2 dl = fma2(add2(x, bb), minus, fma2(fma2(bb, minus, d), minus, t));
+        const f2 c = pair(ch, ch), ny = mul2(d, pair(-ch, -ch));                              // -y, and what it lacks
+        const f2 yl = fma2(dl, c, fma2(d, pair(cl, cl), fma2(d, c, ny)));
+        const f2 kt = fma2(ny, pair(-256.f, -256.f), magic);
+        // -r; 2^-r - 1 = -a + a^2/2 - a^3/6 with a = r ln 2; the next term is below 2^-42
+        const f2 nr = fma2(yl, minus, fma2(add2(kt, pair(-12582912.f, -12582912.f)), pair(0x1p-8f, 0x1p-8f), ny));
+        const f2 p = mul2(nr, fma2(nr, fma2(nr, pair(0.0555041087f, 0.0555041087f), pair(0.240226507f, 0.240226507f)), pair(0.693147181f, 0.693147181f)));
+        const f2 q = fma2(p, pair(0x1p31f, 0x1p31f), magic);
+        float na, nb, ka, kb, qa, qb;
+        unpair(ny, na, nb);
+        unpair(kt, ka, kb);
+        unpair(q, qa, qb);
+        auto whole = [&](float xx, float n, float k, float m) -> uint64_t {
+            // NaN among the depths: infinities less themselves or by 0
+            if (!(n > -kDeep)) return xx == top ? 1ull << kUnit : 0;
+            const uint32_t kb = __float_as_uint(k);                        // 0x4B400000 + k
+            return ((uint64_t)table[kb & 255] * (__float_as_uint(m) + (0x80000000u - 0x4B400000u))) >> (62 - kUnit + ((kb >> 8) & 63));
+        };
+        wa = whole(xa, na, ka, qa);
+        wb = whole(xb, nb, kb, qb);
+    }
     __device__ __forceinline__ uint64_t weight(float x) const {
-        const float d = __fsub_rn(top, x), bb = __fsub_rn(d, top);
-        const float dl = __fsub_rn(__fsub_rn(top, __fsub_rn(d, bb)), __fadd_rn(x, bb));      // what d lacks, exactly
-        const float y = __fmul_rn(d, ch);
-        if (!(y < kDeep)) return x == top ? 1ull << kUnit : 0;       // NaN among them: infinities less themselves or by 0
-        const float yl = __fmaf_rn(dl, ch, __fmaf_rn(d, cl, __fmaf_rn(d, ch, -y)));
-        const float t = __fmaf_rn(y, 256.f, 12582912.f);
-        const int k = __float_as_int(t) - 0x4B400000;
-        const float r = __fadd_rn(__fmaf_rn(__fsub_rn(t, 12582912.f), -0x1p-8f, y), yl);
-        // 2^-r - 1 = -a + a^2/2 - a^3/6 with a = r ln 2; the next term is below 2^-42
-        const float p = __fmul_rn(r, __fmaf_rn(r, __fmaf_rn(r, -0.0555041087f, 0.240226507f), -0.693147181f));
-        const uint32_t up = 0x80000000u + (uint32_t)(__float_as_int(__fmaf_rn(p, 0x1p31f, 12582912.f)) - 0x4B400000);
-        return ((uint64_t)table[k & 255] * up) >> (62 - kUnit + (k >> 8));
+        uint64_t a, b;
+        weights(x, x, a, b);
+        return a;
     }
 };
 
@@ -259,11 +277,41 @@ struct Part {
         }
     }
 
+    // The weight of those of a vector's entries that on(x, i) holds for.
+    template <bool ALL, typename F>
+    __device__ __forceinline__ uint64_t weigh(const Row &row, const uint4 &x, int i0, F on) const {
+        uint32_t use = 0;
+        if (!ALL) {
+#pragma unroll
+            for (int e = 0; e < VE; ++e) use |= (uint32_t)on(T::get(x, e), i0 + e) << e;
+            if (!use) return 0;
+        }
+        uint64_t sum = 0;
+#pragma unroll
+        for (int e = 0; e < VE; e += 2) {
+            uint64_t wa, wb;
+            row.weights(T::get(x, e), T::get(x, e + 1), wa, wb);
+            if (ALL || ((use >> e) & 1)) sum += wa;
+            if (ALL || ((use >> e) & 2)) sum += wb;
+        }
+        return sum;
+    }
+
     // The lowest index at which the running sum of f in index order reaches the target that goal(total) gives, kept within
     // 1 .. total; -1 where the total is 0.  All threads of all CTAs return it.
     // LAST: the thread that finds it writes it to *token instead, and nobody else learns it (a total of 0 writes nothing).
+    // fv: the sum of f over a vector.
     template <bool LAST, typename F, typename G>
     __device__ __forceinline__ int pick(Shared &s, F f, G goal, int32_t *token = nullptr) const {
+        return pick_by<LAST>(s, f, [&](const uint4 &x, int i0) {
+            uint64_t sum = 0;
+#pragma unroll
+            for (int e = 0; e < VE; ++e) sum += f(T::get(x, e), i0 + e);
+            return sum;
+        }, goal, token);
+    }
+    template <bool LAST, typename F, typename V, typename G>
+    __device__ __forceinline__ int pick_by(Shared &s, F f, V fv, G goal, int32_t *token) const {
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
         const int lo = (int)((long long)nv * warp / kWarps), hi = (int)((long long)nv * (warp + 1) / kWarps);
         uint64_t sum = 0;
@@ -272,10 +320,7 @@ struct Part {
             const int j = j0 + lane;
             uint64_t mine = 0;
             if (j < hi) {
-                const uint4 x = vec[j];
-                const int i0 = begin - skip + j * VE;
-#pragma unroll
-                for (int e = 0; e < VE; ++e) mine += f(T::get(x, e), i0 + e);
+                mine = fv(vec[j], begin - skip + j * VE);
             }
             if (__any_sync(0xffffffffu, mine != 0)) mine = warp_sum64(mine);
             if (lane == 0) s.steps[warp][step] = mine;
@@ -305,8 +350,7 @@ struct Part {
             uint64_t w = 0;
             if (j < hi) {
                 x = vec[j];
-#pragma unroll
-                for (int e = 0; e < VE; ++e) w += f(T::get(x, e), i0 + e);
+                w = fv(x, i0);
             }
             uint64_t to = before + warp_scan64(w, lane);
             if (lane == __ffs(__ballot_sync(0xffffffffu, to >= target)) - 1) {
@@ -476,12 +520,17 @@ struct Part {
     __device__ __forceinline__ uint32_t narrow(Shared &s, Row &row, uint64_t k, bool whole, uint64_t &weighed) const {
         clear<false>(s);
         uint64_t sum = 0;
-        each([&](float x, int i) {
-            const float y = row.depth(x);
-            if (!(y < kDeep) || !row.kept(x, i)) return;
-            if (MASS) sum += row.weight(x);
-            add<false>(s, min((int)(y * kBinScale), kBins - 1), 1);
-        });
+        const bool all = row.v == -INFINITY;
+        for (int j = threadIdx.x; j < nv; j += kThreads) {
+            const uint4 x = vec[j];
+            const int i0 = begin - skip + j * VE;
+#pragma unroll
+            for (int e = 0; e < VE; ++e) {
+                const float xe = T::get(x, e), y = row.depth(xe);
+                if (y < kDeep && (all || row.kept(xe, i0 + e))) add<false>(s, min((int)(y * kBinScale), kBins - 1), 1);
+            }
+            if (MASS) sum += all ? weigh<true>(row, x, i0, [](float, int) { return true; }) : weigh<false>(row, x, i0, [&](float xe, int i) { return row.kept(xe, i); });
+        }
         uint64_t target = k;
         if (MASS) {
             weighed = cluster_sum(s, sum);
@@ -508,10 +557,11 @@ struct Part {
         if (MASS) {
             // the weight above those bins
             sum = 0;
-            each([&](float x, int i) {
-                const float y = row.depth(x);
-                if (y < kDeep && (uint32_t)min((int)(y * kBinScale), kBins - 1) < from && row.kept(x, i)) sum += row.weight(x);
-            });
+            for (int j = threadIdx.x; j < nv; j += kThreads)
+                sum += weigh<false>(row, vec[j], begin - skip + j * VE, [&](float x, int i) {
+                    const float y = row.depth(x);
+                    return y < kDeep && (uint32_t)min((int)(y * kBinScale), kBins - 1) < from && (all || row.kept(x, i));
+                });
             base = cluster_sum(s, sum);
         }
         gather(s, row, from, to, at);
@@ -759,8 +809,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a) {
             row.v = least;
             row.I = 0x7fffffff;
         }
-        part.template pick<true>(s, [&](float x, int i) -> uint64_t { return row.kept(x, i) ? row.weight(x) : 0; },
-                                 [&](uint64_t total) -> uint64_t { return __umul64hi(total, s.u64) + 1; }, token);
+        const bool all = row.v == -INFINITY;
+        part.template pick_by<true>(
+            s, [&](float x, int i) -> uint64_t { return row.kept(x, i) ? row.weight(x) : 0; },
+            [&](const uint4 &x, int i0) {
+                auto kept = [&](float xe, int i) { return row.kept(xe, i); };
+                return all ? part.template weigh<true>(row, x, i0, kept) : part.template weigh<false>(row, x, i0, kept);
+            },
+            [&](uint64_t total) -> uint64_t { return __umul64hi(total, s.u64) + 1; }, token);
     }
     cluster_join();                                      // no CTA ends while another reads its memory
 }

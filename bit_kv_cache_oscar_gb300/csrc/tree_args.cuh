@@ -3,6 +3,7 @@
 
 #include <cuda.h>
 
+#include "pairs.cuh"
 #include "ptx.cuh"
 #include "tree.cuh"
 
@@ -44,30 +45,6 @@ struct TreeRequest {
         }
     }
 };
-
-// Pairs of floats for packed arithmetic.
-using f2 = unsigned long long;                   // two floats, the lower index in the lower half
-__device__ __forceinline__ f2 pair(float a, float b) {
-    f2 d;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
-    return d;
-}
-__device__ __forceinline__ void unpair(f2 x, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x)); }
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-    f2 d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
-    f2 d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ f2 add2(f2 a, f2 b) {
-    f2 d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
 
 // Row index of (node row, query head) in out, lse and, times S + 1, in the partials.
 __device__ __forceinline__ size_t tree_row(const TreeArgs &a, const TreeRequest &r, int h, int row) {
