@@ -11,8 +11,8 @@
 // token as in 64-bit arithmetic (a sum in fp32, 2^-24 off, would miss for one row in a hundred over a large vocabulary).
 //
 // A cluster of 1 to 8 CTAs takes a row and holds it in shared memory, so a row is read once.  The filters' search goes through
-// bins: 2,048 equal steps of y, whose order is the logits' order, counted by atomics.  For top-k the counts give the bin that the
-// target falls into; for top-p, with the sum of all weights, the few bins that it can fall into (a bin's weights differ by 1.5 %).
+// bins: 4,096 equal steps of y, whose order is the logits' order, counted by atomics.  For top-k the counts give the bin that the
+// target falls into; for top-p, with the sum of all weights, the few bins that it can fall into (a bin's weights differ by 0.8 %).
 // Where no more than 2,048 entries lie up to there, they go to the first CTA, which sorts them, cuts the order by every filter, sorts
 // what is left by index and draws.  Where that many lie in those bins alone, it sorts these and says where the cut is, and the draw
 // goes through the row.  Where more do (flat rows), further levels of bins follow, within a bin equal steps of the logits' bits, until
@@ -31,9 +31,12 @@ namespace oscar {
 namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kBins = 2048;                          // 4 a thread
 constexpr float kDeep = 44.5f;                       // y from here on: weight zero
-constexpr float kBinScale = kBins / kDeep;
+// Bins of counts, and of weights.
+template <bool MASS> constexpr int kBins = MASS ? 2048 : 4096;
+template <bool MASS> constexpr float kBinScale = kBins<MASS> / kDeep;
+template <bool MASS>
+__device__ __forceinline__ uint32_t bin_of(float y) { return (uint32_t)min((int)(y * kBinScale<MASS>), kBins<MASS> - 1); }
 constexpr int kList = 2048;                          // entries that one CTA sorts
 constexpr int kKeys = 1024;                          // entries of a CTA's list for the further levels
 constexpr int kUnit = 44;                            // weights in units of 2^-44
@@ -130,7 +133,8 @@ struct Row {
 
 struct Shared {
     union {
-        uint32_t hist[4][kBins];                     // counts, weights' three parts
+        uint32_t count[kBins<false>];
+        uint32_t mass[3][kBins<true>];               // weights' three parts
         struct {
             uint64_t list[kList], weight[kList];     // entries to sort; their weights
         };
@@ -145,7 +149,7 @@ struct Shared {
     uint32_t n_list, key_min, key_max;               // read by the cluster
     int pick_index;
     uint32_t bin, bin_from;
-    uint64_t before, total;
+    uint64_t before, total, slice;
     float cut_v;                                     // of the first CTA, read by the cluster
     int cut_i;
     // the row's arguments
@@ -174,14 +178,6 @@ __device__ __forceinline__ T peer(const T *p, int rank) {
         return v;
     }
 }
-__device__ __forceinline__ uint4 peer4(const uint32_t *p, int rank) {
-    uint32_t r;
-    uint4 v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr(p)), "r"(rank));
-    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(r) : "memory");
-    return v;
-}
-
 __device__ __forceinline__ uint64_t warp_sum64(uint64_t x) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
@@ -374,54 +370,52 @@ struct Part {
     }
 
     // The bins of this search level, filled by every CTA: finds the first one up to which base and the weights reach the
-    // target that goal(total) gives, and leaves it in s.bin with the weight before it in s.before.  False: no bin does.
-    // LEAST: the bins of y hold counts, taken for the least weight that so many entries there can have; s.bin is a bin by which the
-    // true weights have reached the target, s.bin_from the first by which they can have.
+    // target that goal(total) gives, and the weight before it.  False: no bin does.
+    // LEAST: the bins of y hold counts, taken for the least weight that so many entries there can have; bin is one by which the
+    // true weights have reached the target, from the first by which they can have.
+    struct Found {
+        uint32_t bin, from;
+        uint64_t before;
+    };
     template <bool MASS, bool LEAST = false, typename G>
-    __device__ __forceinline__ bool find_bin(Shared &s, uint64_t base, G goal) const {
-        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b0 = threadIdx.x * 4;
+    __device__ __forceinline__ bool find_bin(Shared &s, uint64_t base, G goal, Found &found) const {
+        // each CTA sums a slice of the bins over the cluster, up to N of them a thread
+        constexpr int N = kBins<MASS> / kThreads;
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, slice = kBins<MASS> / C, per = (slice + kThreads - 1) / kThreads;
+        const int b0 = rank * slice + threadIdx.x * per;
+        const bool on = (int)threadIdx.x * per < slice;
         cluster_join();
-        uint64_t w[4] = {0, 0, 0, 0};
-        for (int k = 0; k < C; ++k) {
-            if (MASS) {
+        uint64_t w[N], mine = 0;
 #pragma unroll
-                for (int l = 0; l < 3; ++l) {
-                    const uint4 h = peer4(&s.hist[1 + l][b0], k);
-                    w[0] += (uint64_t)h.x << (kLimb * l);
-                    w[1] += (uint64_t)h.y << (kLimb * l);
-                    w[2] += (uint64_t)h.z << (kLimb * l);
-                    w[3] += (uint64_t)h.w << (kLimb * l);
-                }
-            } else {
-                const uint4 h = peer4(&s.hist[0][b0], k);
-                w[0] += h.x;
-                w[1] += h.y;
-                w[2] += h.z;
-                w[3] += h.w;
-            }
+        for (int i = 0; i < N; ++i) {
+            w[i] = 0;
+            if (!on || i >= per) continue;
+            for (int k = 0; k < C; ++k)
+#pragma unroll
+                for (int l = 0; l < (MASS ? 3 : 1); ++l) w[i] += (uint64_t)peer(MASS ? &s.mass[l][b0 + i] : &s.count[b0 + i], k) << (kLimb * l);
+            if (LEAST) w[i] *= (uint64_t)(ex2_approx(kUnit - (b0 + i + 1) * (1.f / kBinScale<MASS>)) * 0.999f);
+            mine += w[i];
         }
-        if (LEAST)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] *= (uint64_t)(ex2_approx(kUnit - (b0 + i + 1) * (1.f / kBinScale)) * 0.999f);
-        const uint64_t mine = w[0] + w[1] + w[2] + w[3];
         const uint64_t upto = warp_scan64(mine, lane);
         if (lane == 31) s.scan[warp] = upto;
-        if (threadIdx.x == 0) s.bin = s.bin_from = kBins;
+        if (threadIdx.x == 0) s.bin = s.bin_from = kBins<MASS>;
         __syncthreads();
-        uint64_t before = base, total = 0;
-        for (int k = 0; k < kWarps; ++k) {
-            const uint64_t x = s.scan[k];
-            if (k < warp) before += x;
+        uint64_t before = base + upto - mine;
+        for (int k = 0; k < warp; ++k) before += s.scan[k];
+        if (threadIdx.x == kThreads - 1) s.slice = before + mine - base;
+        cluster_join();
+        uint64_t total = 0;
+        for (int k = 0; k < C; ++k) {
+            const uint64_t x = peer(&s.slice, k);
+            if (k < rank) before += x;
             total += x;
         }
         const uint64_t target = goal(total);
-        if (threadIdx.x == 0) s.total = total;
-        before += upto - mine;
-        // what 2^(1 / kBinScale) and the roundings leave of the target
-        const uint64_t low = LEAST ? max(1ull, (unsigned long long)__umul64hi(target, (uint64_t)(0.98 * 0x1p63) << 1)) : target;
+        // what 2^(1 / kBinScale), 1.0076, and the roundings leave of the target
+        const uint64_t low = LEAST ? max(1ull, (unsigned long long)__umul64hi(target, (uint64_t)(0.99 * 0x1p63) << 1)) : target;
         if (before < target && low <= before + mine) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < N; ++i) {
                 if (before < target && target <= before + w[i]) {
                     s.bin = b0 + i;
                     s.before = before;
@@ -430,23 +424,35 @@ struct Part {
                 before += w[i];
             }
         }
-        cluster_join();                              // found, and the bins read by all
-        return s.bin < kBins;
+        cluster_join();
+        uint32_t bin = kBins<MASS>, from = kBins<MASS>;
+        uint64_t at = 0;
+        for (int k = 0; k < C; ++k) {
+            const uint32_t x = peer(&s.bin, k);
+            if (x < bin) {
+                bin = x;
+                at = peer(&s.before, k);
+            }
+            if (LEAST) from = min(from, peer(&s.bin_from, k));
+        }
+        found = Found{bin, from, at};
+        return bin < kBins<MASS>;
     }
 
     template <bool MASS>
     __device__ __forceinline__ void clear(Shared &s) const {
-        uint4 *h = reinterpret_cast<uint4 *>(s.hist);
-        for (int i = threadIdx.x; i < (MASS ? 4 : 1) * kBins / 4; i += kThreads) h[i] = make_uint4(0, 0, 0, 0);
+        uint4 *h = reinterpret_cast<uint4 *>(s.count);
+        for (int i = threadIdx.x; i < (MASS ? 3 : 1) * kBins<MASS> / 4; i += kThreads) h[i] = make_uint4(0, 0, 0, 0);
         __syncthreads();
     }
     template <bool MASS>
     static __device__ __forceinline__ void add(Shared &s, int bin, uint64_t w) {
-        atomicAdd(&s.hist[0][bin], 1u);
         if (MASS) {
-            atomicAdd(&s.hist[1][bin], (uint32_t)w & ((1u << kLimb) - 1));
-            atomicAdd(&s.hist[2][bin], (uint32_t)(w >> kLimb) & ((1u << kLimb) - 1));
-            atomicAdd(&s.hist[3][bin], (uint32_t)(w >> (2 * kLimb)));
+            atomicAdd(&s.mass[0][bin], (uint32_t)w & ((1u << kLimb) - 1));
+            atomicAdd(&s.mass[1][bin], (uint32_t)(w >> kLimb) & ((1u << kLimb) - 1));
+            atomicAdd(&s.mass[2][bin], (uint32_t)(w >> (2 * kLimb)));
+        } else {
+            atomicAdd(&s.count[bin], 1u);
         }
     }
     // The bins of y.
@@ -457,7 +463,7 @@ struct Part {
             const float y = row.depth(x);
             if (y < kDeep && row.kept(x, i)) {
                 const uint64_t w = MASS ? row.weight(x) : 1;
-                if (w) add<MASS>(s, min((int)(y * kBinScale), kBins - 1), w);
+                if (w) add<MASS>(s, bin_of<MASS>(y), w);
             }
         });
     }
@@ -470,7 +476,7 @@ struct Part {
         asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(list) : "r"(saddr(s.list)), "r"(0));
         each([&](float x, int i) {
             const float y = row.depth(x);
-            const uint32_t bin = min((int)(y * kBinScale), kBins - 1);
+            const uint32_t bin = bin_of<false>(y);
             if (!(y < kDeep) || bin < from || bin > to || !row.kept(x, i)) return;
             const uint32_t place = atomicAdd(&s.key_min, 1u);
             if (place < kList)
@@ -482,7 +488,7 @@ struct Part {
     // Entries counted in the bins from .. to: of all CTAs, and of those before this one.
     __device__ __forceinline__ uint32_t entries(Shared &s, uint32_t from, uint32_t to, uint32_t &before) const {
         uint32_t mine = 0;
-        for (uint32_t i = from + threadIdx.x; i <= to; i += kThreads) mine += s.hist[0][i];
+        for (uint32_t i = from + threadIdx.x; i <= to; i += kThreads) mine += s.count[i];
         mine = __reduce_add_sync(0xffffffffu, mine);
         if (threadIdx.x == 0) s.n_list = 0;
         __syncthreads();
@@ -527,7 +533,7 @@ struct Part {
 #pragma unroll
             for (int e = 0; e < VE; ++e) {
                 const float xe = T::get(x, e), y = row.depth(xe);
-                if (y < kDeep && (all || row.kept(xe, i0 + e))) add<false>(s, min((int)(y * kBinScale), kBins - 1), 1);
+                if (y < kDeep && (all || row.kept(xe, i0 + e))) add<false>(s, bin_of<false>(y), 1);
             }
             if (MASS) sum += all ? weigh<true>(row, x, i0, [](float, int) { return true; }) : weigh<false>(row, x, i0, [&](float xe, int i) { return row.kept(xe, i); });
         }
@@ -537,10 +543,11 @@ struct Part {
             target = __umul64hi(weighed, s.p64) + (weighed * s.p64 != 0);
             if (target < 1) target = 1;
         }
-        const bool found = find_bin<false, MASS>(s, 0, [&](uint64_t) { return target; });
+        Found f;
+        const bool found = find_bin<false, MASS>(s, 0, [&](uint64_t) { return target; }, f);
         if (!MASS && !found) return 0;               // fewer than k have weight: all stay
-        const uint32_t to = found ? s.bin : kBins - 1, from = !MASS ? to : min(s.bin_from, to);
-        uint64_t base = MASS ? 0 : s.before;
+        const uint32_t to = found ? f.bin : kBins<false> - 1, from = !MASS ? to : min(f.from, to);
+        uint64_t base = MASS ? 0 : f.before;
         uint32_t at, n;
         if (whole) {
             n = entries(s, 0, to, at);
@@ -560,7 +567,7 @@ struct Part {
             for (int j = threadIdx.x; j < nv; j += kThreads)
                 sum += weigh<false>(row, vec[j], begin - skip + j * VE, [&](float x, int i) {
                     const float y = row.depth(x);
-                    return y < kDeep && (uint32_t)min((int)(y * kBinScale), kBins - 1) < from && (all || row.kept(x, i));
+                    return y < kDeep && bin_of<false>(y) < from && (all || row.kept(x, i));
                 });
             base = cluster_sum(s, sum);
         }
@@ -578,12 +585,13 @@ struct Part {
     __device__ __forceinline__ void cut(Shared &s, Row &row, G goal) const {
         depths<MASS>(s, row);
         uint64_t target = 0;
-        if (!find_bin<MASS>(s, 0, [&](uint64_t total) { return target = goal(total); })) return;
-        const int bin = s.bin;
-        uint64_t before = s.before;
+        Found f;
+        if (!find_bin<MASS>(s, 0, [&](uint64_t total) { return target = goal(total); }, f)) return;
+        const uint32_t bin = f.bin;
+        uint64_t before = f.before;
         auto in_bin = [&](float x, int i) {
             const float y = row.depth(x);
-            return y < kDeep && min((int)(y * kBinScale), kBins - 1) == bin && row.kept(x, i);
+            return y < kDeep && bin_of<MASS>(y) == bin && row.kept(x, i);
         };
         // the bin's entries and the range of their keys
         if (threadIdx.x == 0) {
@@ -628,9 +636,9 @@ struct Part {
                 each([&](float x, int i) {
                     if (in_bin(x, i)) count(falling_key(x));
                 });
-            if (!find_bin<MASS>(s, before, [&](uint64_t) { return target; })) return;         // (the bin's sum reaches it: does not happen)
-            before = s.before;
-            lo += s.bin << shift;
+            if (!find_bin<MASS>(s, before, [&](uint64_t) { return target; }, f)) return;      // (the bin's sum reaches it: does not happen)
+            before = f.before;
+            lo += f.bin << shift;
             if (!shift) break;
             hi = min(hi, lo + ((1u << shift) - 1));
         }
