@@ -5,7 +5,7 @@
 //   D[row][t] = sum_c Q'[row][c] n_t,c           the query rows (tensor memory) by the codes as subnormals n 2^-24 (odd nibbles: 16 n)
 //   e = f s_t D + z_t zq_row - M_row,  p = 2^e   f undoes the scalings, zq = sm sum_c q_c, M the row's reference
 //   O[row][c] += sum_t (p s'_t) (n'_t,c - 8),  l += p,  zs += p (z'_t + 8 s'_t)
-// A product p s' is one f16 number, 2^-12 relative; M is raised whenever one passes 2^15 (then brought to 2^8) or p passes 2^110,
+// A product p s' is one f16 number, 2^-11 relative; M is raised whenever one passes 2^15 (then brought to 2^8) or p passes 2^110,
 // so that the largest p s' so far, not the largest p, sits near the top of f16's range.  Codes are centred for the reason given
 // in attn_tree.cu.  Both operands of codes lie in shared memory as they come, a position's channels together: K-major for the
 // logits, MN-major for the values, so both are unpacked the same way.

@@ -147,6 +147,7 @@ struct Shared {
     float warp_top[kWarps];
     float top;                                       // of this CTA, read by the cluster
     uint32_t n_list, key_min, key_max;               // read by the cluster
+    uint32_t n_some, n_all, cursor;
     int pick_index;
     uint32_t bin, bin_from;
     uint64_t before, total, slice;
@@ -468,60 +469,60 @@ struct Part {
         });
     }
 
-    // The entries of the bins from .. to that row keeps, of all CTAs, to the first CTA's list; at: where this one's begin.
+    // Entries counted in the bins from .. to and 0 .. to of this CTA, for the cluster to read behind the next barrier.
+    __device__ __forceinline__ void count_entries(Shared &s, uint32_t from, uint32_t to) const {
+        uint32_t some = 0, all = 0;
+        for (uint32_t i = threadIdx.x; i <= to; i += kThreads) {
+            const uint32_t n = s.count[i];
+            all += n;
+            if (i >= from) some += n;
+        }
+        some = __reduce_add_sync(0xffffffffu, some);
+        all = __reduce_add_sync(0xffffffffu, all);
+        if (threadIdx.x == 0) s.n_some = s.n_all = 0;
+        __syncthreads();
+        if ((threadIdx.x & 31) == 0) {
+            atomicAdd(&s.n_some, some);
+            atomicAdd(&s.n_all, all);
+        }
+    }
+
+    // The entries of the bins from .. to that row keeps, of all CTAs, to the first CTA's list; at: where this one's begin.  Every CTA
+    // is done with its bins: their memory becomes the list.
     __device__ __forceinline__ void gather(Shared &s, const Row &row, uint32_t from, uint32_t to, uint32_t at) const {
-        if (threadIdx.x == 0) s.key_min = at;
-        cluster_join();                              // (the bins are read; their memory becomes the list)
+        if (threadIdx.x == 0) s.cursor = at;
+        __syncthreads();
         uint32_t list;
         asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(list) : "r"(saddr(s.list)), "r"(0));
         each([&](float x, int i) {
             const float y = row.depth(x);
             const uint32_t bin = bin_of<false>(y);
             if (!(y < kDeep) || bin < from || bin > to || !row.kept(x, i)) return;
-            const uint32_t place = atomicAdd(&s.key_min, 1u);
+            const uint32_t here = __activemask(), lane = threadIdx.x & 31, first = __ffs(here) - 1;
+            uint32_t place = 0;
+            if (lane == first) place = atomicAdd(&s.cursor, (uint32_t)__popc(here));
+            place = __shfl_sync(here, place, first) + __popc(here & ((1u << lane) - 1));
             if (place < kList)
                 asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(list + 8 * place), "l"((uint64_t)falling_key(x) << 32 | (uint32_t)i) : "memory");
         });
         cluster_join();                              // the list is complete
     }
 
-    // Entries counted in the bins from .. to: of all CTAs, and of those before this one.
-    __device__ __forceinline__ uint32_t entries(Shared &s, uint32_t from, uint32_t to, uint32_t &before) const {
-        uint32_t mine = 0;
-        for (uint32_t i = from + threadIdx.x; i <= to; i += kThreads) mine += s.count[i];
-        mine = __reduce_add_sync(0xffffffffu, mine);
-        if (threadIdx.x == 0) s.n_list = 0;
-        __syncthreads();
-        if ((threadIdx.x & 31) == 0) atomicAdd(&s.n_list, mine);
-        cluster_join();
-        uint32_t n = 0;
-        before = 0;
-        for (int k = 0; k < C; ++k) {
-            const uint32_t m = peer(&s.n_list, k);
-            if (k < rank) before += m;
-            n += m;
-        }
-        cluster_join();
-        return n;
-    }
-
-    // The sum over the cluster of a value a thread.
-    __device__ __forceinline__ uint64_t cluster_sum(Shared &s, uint64_t x) const {
-        const int lane = threadIdx.x & 31;
+    // A value a thread, summed by warps, for the cluster to read behind the next barrier; and the sum over the cluster.
+    static __device__ __forceinline__ void publish(Shared &s, uint64_t x) {
         __syncwarp();
         x = warp_sum64(x);
-        if (lane == 0) s.warp_sum[threadIdx.x >> 5] = x;
-        cluster_join();
-        x = 0;
-        for (int k = lane; k < C * kWarps; k += 32) x += peer(&s.warp_sum[k % kWarps], k / kWarps);
-        x = warp_sum64(x);
-        cluster_join();
-        return x;
+        if ((threadIdx.x & 31) == 0) s.warp_sum[threadIdx.x >> 5] = x;
+    }
+    __device__ __forceinline__ uint64_t published(Shared &s) const {
+        uint64_t x = 0;
+        for (int k = threadIdx.x & 31; k < C * kWarps; k += 32) x += peer(&s.warp_sum[k % kWarps], k / kWarps);
+        return warp_sum64(x);
     }
 
     // Narrows what is kept by top-k (MASS false, k tokens) or top-p (s.p64 of the kept weight).  With whole: returns how many
     // entries the first CTA's list holds, if all that can be kept are there (nothing is narrowed then); else 0.  weighed: the kept
-    // weight (top-p).
+    // weight (top-p).  (What a CTA publishes is not written again before all have passed another barrier.)
     template <bool MASS>
     __device__ __forceinline__ uint32_t narrow(Shared &s, Row &row, uint64_t k, bool whole, uint64_t &weighed) const {
         clear<false>(s);
@@ -537,27 +538,36 @@ struct Part {
             }
             if (MASS) sum += all ? weigh<true>(row, x, i0, [](float, int) { return true; }) : weigh<false>(row, x, i0, [&](float xe, int i) { return row.kept(xe, i); });
         }
+        if (MASS) publish(s, sum);
         uint64_t target = k;
-        if (MASS) {
-            weighed = cluster_sum(s, sum);
-            target = __umul64hi(weighed, s.p64) + (weighed * s.p64 != 0);
-            if (target < 1) target = 1;
-        }
         Found f;
-        const bool found = find_bin<false, MASS>(s, 0, [&](uint64_t) { return target; }, f);
+        const bool found = find_bin<false, MASS>(s, 0, [&](uint64_t) {
+            if (MASS) {
+                weighed = published(s);
+                target = __umul64hi(weighed, s.p64) + (weighed * s.p64 != 0);
+                if (target < 1) target = 1;
+            }
+            return target;
+        }, f);
         if (!MASS && !found) return 0;               // fewer than k have weight: all stay
         const uint32_t to = found ? f.bin : kBins<false> - 1, from = !MASS ? to : min(f.from, to);
-        uint64_t base = MASS ? 0 : f.before;
-        uint32_t at, n;
-        if (whole) {
-            n = entries(s, 0, to, at);
-            if (n <= kList) {
-                gather(s, row, 0, to, at);
-                return n;
+        count_entries(s, from, to);
+        cluster_join();
+        uint32_t some = 0, some_at = 0, every = 0, every_at = 0;
+        for (int r = 0; r < C; ++r) {
+            const uint32_t x = peer(&s.n_some, r), y = peer(&s.n_all, r);
+            if (r < rank) {
+                some_at += x;
+                every_at += y;
             }
+            some += x;
+            every += y;
         }
-        n = entries(s, from, to, at);
-        if (n > kList) {
+        if (whole && every <= kList) {
+            gather(s, row, 0, to, every_at);
+            return every;
+        }
+        if (some > kList) {
             cut<MASS>(s, row, [&](uint64_t) { return target; });
             return 0;
         }
@@ -569,14 +579,13 @@ struct Part {
                     const float y = row.depth(x);
                     return y < kDeep && bin_of<false>(y) < from && (all || row.kept(x, i));
                 });
-            base = cluster_sum(s, sum);
+            publish(s, sum);
         }
-        gather(s, row, from, to, at);
-        if (rank == 0) cut_list<MASS>(s, row, n, base, target);
+        gather(s, row, from, to, some_at);
+        if (rank == 0) cut_list<MASS>(s, row, some, MASS ? published(s) : f.before, target);
         cluster_join();
         row.v = peer(&s.cut_v, 0);
         row.I = peer(&s.cut_i, 0);
-        cluster_join();
         return 0;
     }
 

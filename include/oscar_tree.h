@@ -51,9 +51,10 @@ OSCAR_API int32_t oscar_suggest_splits_tree_int4(const oscar_layout_t *layout, i
  * nodes pass the page table, is skipped and flagged (OSCAR_DEV_BAD_LENGTH); rows on a bad page are not seen,
  * and flagged.
  * Query products and softmax sums are fp32 or finer.  Of the history, a probability times its value scale
- * enters the value product as one fp16 number (2^-12 relative) under a scaling that follows the largest one
- * so far, and meets codes less 8; of the BF16 rows a probability enters in two bf16 parts (2^-17).  Query
- * elements below 2^-25 of their head's largest lose low bits.
+ * enters the value product as one fp16 number (2^-11 relative) under a scaling that follows the largest one
+ * so far, and meets codes less 8; of the BF16 rows a probability enters in two bf16 parts (2^-16).  Query
+ * elements below 2^-25 of the largest finite one that shares a scaling with them lose low bits: their head's,
+ * or, on the kernel for many rows, the largest of 128 rows (nodes times query heads of a kv head).
  */
 OSCAR_API oscar_status_t oscar_tree_attention_int4(const oscar_layout_t *layout, const uint16_t *q, int32_t n,
                                                    const int32_t *node_begin, const int32_t *mask,
