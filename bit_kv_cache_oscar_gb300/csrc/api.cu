@@ -656,6 +656,8 @@ oscar_status_t oscar_tree_attention_int4(const oscar_layout_t *layout, const uin
         return fail(OSCAR_ERR_INVALID_ARG, "NULL argument");
     if (!aligned16(q)) return fail(OSCAR_ERR_INVALID_ARG, "q not 16-byte aligned");
     if (reinterpret_cast<uintptr_t>(out) & 7u) return fail(OSCAR_ERR_INVALID_ARG, "out not 8-byte aligned");
+    if ((long long)max_pages_per_req * layout->page_size > 2147483647LL - 1024)
+        return fail(OSCAR_ERR_INVALID_ARG, "max_pages_per_req %d: positions and nodes pass int32", max_pages_per_req);
     if (mask && (mask_words < 1 || 32LL * mask_words < max_nodes))
         return fail(OSCAR_ERR_INVALID_ARG, "mask_words %d: fewer bits than max_nodes %d", mask_words, max_nodes);
     const oscar::Attn4Input in{q, bf16_view(bf16_pool), bf16_page_table, int4_view(int4_pool), int4_page_table,

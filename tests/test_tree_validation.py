@@ -51,7 +51,7 @@ def tree(L, lay=None, q=FAKE, n=3, begin=FAKE, mask=FAKE, words=1, nodes=3, bf=N
 @pytest.mark.parametrize("kw", [
     dict(q=None), dict(q=FAKE + 2), dict(begin=None), dict(n=-1), dict(n=65535 * 256 + 1), dict(nodes=0), dict(nodes=257), dict(words=0), dict(nodes=33),
     dict(words=-1), dict(bpt=None), dict(ipt=None), dict(T=None), dict(he=None), dict(out=None), dict(out=FAKE + 4), dict(max_pages=0),
-    dict(max_pages=2 ** 30), dict(batch=-1), dict(batch=65536), dict(splits=0), dict(splits=1025), dict(bf=ob.Bf16PoolC(None, FAKE, 4)),
+    dict(max_pages=2 ** 30), dict(max_pages=2 ** 25 - 15), dict(batch=-1), dict(batch=65536), dict(splits=0), dict(splits=1025), dict(bf=ob.Bf16PoolC(None, FAKE, 4)),
     dict(bf=ob.Bf16PoolC(FAKE, FAKE, 0)), dict(i4=ob.Int4PoolC(FAKE, FAKE, FAKE + 8, 4)), dict(lay=layout(sink=40))])
 def test_tree_attention_refuses(L, kw):
     assert tree(L, **kw) == INVALID
