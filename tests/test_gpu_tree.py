@@ -266,17 +266,21 @@ def test_captured_and_replayed_on_new_lengths(nodes):
 
 
 def test_streams_of_their_own():
-    """Two calls at once on two streams, with partials of their own; a call on a stream that is not the current one."""
+    """Two calls at once on two streams, with partials and outputs of their own, made before and kept until both are done; a call on
+    a stream that is not the current one."""
     a, b = (make([2000, 700], [n, n], seed=20 + n).upload() for n in (3, 20))
     wa, wb = a.run(), b.run()
+    rounds = range(10)
+    sets = [[(torch.empty_like(w[0]), torch.empty_like(w[1]), ob.Partials.empty(c.L, c.n, 3)) for _ in rounds] for c, w in ((a, wa), (b, wb))]
+    wa, wb = a.run(3), b.run(3)
     torch.cuda.synchronize()
     s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
-    got = []
-    for _ in range(10):
-        got.append((a.run(stream=s1), b.run(stream=s2)))
+    for i in rounds:
+        a.run(3, *sets[0][i], stream=s1)
+        b.run(3, *sets[1][i], stream=s2)
     torch.cuda.synchronize()
-    for x, y in got:
-        assert torch.equal(x[0], wa[0]) and torch.equal(y[0], wb[0]) and torch.equal(y[1], wb[1])
+    for got, want in zip(sets, (wa, wb)):
+        assert all(torch.equal(o, want[0]) and torch.equal(l, want[1]) for o, l, _ in got)
 
 
 def test_what_the_call_before_wrote_is_read():
