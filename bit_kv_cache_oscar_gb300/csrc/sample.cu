@@ -149,7 +149,7 @@ struct Shared {
     uint32_t n_list, key_min, key_max;               // read by the cluster
     uint32_t n_some, n_all, cursor;
     int pick_index;
-    uint32_t bin, bin_from;
+    uint32_t bin, bin_from, bin_behind;
     uint64_t before, total, slice;
     float cut_v;                                     // of the first CTA, read by the cluster
     int cut_i;
@@ -373,13 +373,15 @@ struct Part {
     // The bins of this search level, filled by every CTA: finds the first one up to which base and the weights reach the
     // target that goal(total) gives, and the weight before it.  False: no bin does.
     // LEAST: the bins of y hold counts, taken for the least weight that so many entries there can have; bin is one by which the
-    // true weights have reached the target, from the first by which they can have.
+    // true weights have reached the target, from the first by which they can have.  A true sum lies between that and 1 / 0.99 of it
+    // (2^(1 / kBinScale) is 1.0076) and a unit an entry.  Both ends are sought twice, from the sum up to a bin and from the sum behind
+    // it, of which z (the true sum of all) less the target may remain: the latter is the sharper the closer top-p is to 1.
     struct Found {
         uint32_t bin, from;
         uint64_t before;
     };
     template <bool MASS, bool LEAST = false, typename G>
-    __device__ __forceinline__ bool find_bin(Shared &s, uint64_t base, G goal, Found &found) const {
+    __device__ __forceinline__ bool find_bin(Shared &s, uint64_t base, G goal, Found &found, const uint64_t &z = 0) const {
         // each CTA sums a slice of the bins over the cluster, up to N of them a thread
         constexpr int N = kBins<MASS> / kThreads;
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, slice = kBins<MASS> / C, per = (slice + kThreads - 1) / kThreads;
@@ -399,7 +401,7 @@ struct Part {
         }
         const uint64_t upto = warp_scan64(mine, lane);
         if (lane == 31) s.scan[warp] = upto;
-        if (threadIdx.x == 0) s.bin = s.bin_from = kBins<MASS>;
+        if (threadIdx.x == 0) s.bin = s.bin_from = s.bin_behind = kBins<MASS>;
         __syncthreads();
         uint64_t before = base + upto - mine;
         for (int k = 0; k < warp; ++k) before += s.scan[k];
@@ -412,21 +414,31 @@ struct Part {
             total += x;
         }
         const uint64_t target = goal(total);
-        // what 2^(1 / kBinScale), 1.0076, and the roundings leave of the target
-        const uint64_t low = LEAST ? max(1ull, (unsigned long long)__umul64hi(target, (uint64_t)(0.99 * 0x1p63) << 1)) : target;
-        if (before < target && low <= before + mine) {
+        if (LEAST) {
+            constexpr uint64_t kEntries = OSCAR_SAMPLE_MAX_VOCAB;
+            auto share = [&](uint64_t x) { return x > kEntries ? __umul64hi(x - kEntries, (uint64_t)(0.99 * 0x1p63) << 1) : 0; };
+            const uint64_t low = max((unsigned long long)share(target), 1ull), rest = z - target, rest_low = share(rest);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const uint64_t upto_i = before + w[i], behind = total - before, behind_i = total - upto_i;
+                if (before < target && target <= upto_i) atomicMin(&s.bin, (uint32_t)(b0 + i));
+                if (before < low && low <= upto_i) s.bin_from = b0 + i;
+                if (behind > rest_low && behind_i <= rest_low) atomicMin(&s.bin, (uint32_t)(b0 + i));
+                if (behind > rest && behind_i <= rest) s.bin_behind = b0 + i;
+                before = upto_i;
+            }
+        } else if (before < target && target <= before + mine) {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 if (before < target && target <= before + w[i]) {
                     s.bin = b0 + i;
                     s.before = before;
                 }
-                if (LEAST && before < low && low <= before + w[i]) s.bin_from = b0 + i;
                 before += w[i];
             }
         }
         cluster_join();
-        uint32_t bin = kBins<MASS>, from = kBins<MASS>;
+        uint32_t bin = kBins<MASS>, from = kBins<MASS>, behind = kBins<MASS>;
         uint64_t at = 0;
         for (int k = 0; k < C; ++k) {
             const uint32_t x = peer(&s.bin, k);
@@ -434,8 +446,12 @@ struct Part {
                 bin = x;
                 at = peer(&s.before, k);
             }
-            if (LEAST) from = min(from, peer(&s.bin_from, k));
+            if (LEAST) {
+                from = min(from, peer(&s.bin_from, k));
+                behind = min(behind, peer(&s.bin_behind, k));
+            }
         }
+        if (LEAST) from = max(from < kBins<MASS> ? from : 0u, behind < kBins<MASS> ? behind : 0u);
         found = Found{bin, from, at};
         return bin < kBins<MASS>;
     }
@@ -548,7 +564,7 @@ struct Part {
                 if (target < 1) target = 1;
             }
             return target;
-        }, f);
+        }, f, weighed);
         if (!MASS && !found) return 0;               // fewer than k have weight: all stay
         const uint32_t to = found ? f.bin : kBins<false> - 1, from = !MASS ? to : min(f.from, to);
         count_entries(s, from, to);
