@@ -132,7 +132,7 @@ struct Row {
 };
 
 struct Shared {
-    union {
+    union alignas(16) {                              // (cleared 16 bytes at a time)
         uint32_t count[kBins<false>];
         uint32_t mass[3][kBins<true>];               // weights' three parts
         struct {
