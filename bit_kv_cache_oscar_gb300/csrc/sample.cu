@@ -755,8 +755,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a) {
         s.top_p = p < 1.f;
         s.p64 = (uint64_t)((double)fmaxf(p, 0.f) * 0x1p64);
         s.u64 = (uint64_t)((double)fminf(fmaxf(a.in.u[r], 0.f), 0x1.fffffep-1f) * 0x1p64);
-        s.min_mode = mp > 1.f ? 3 : mp == 1.f ? 2 : mp > 0.f ? 1 : 0;
-        s.min_off = s.min_mode == 1 ? (double)temp * log((double)mp) : 0.0;
+        // (an infinite temperature: every finite logit weighs 1, which a min_p up to 1 keeps)
+        s.min_mode = mp > 1.f ? 3 : mp == 1.f && temp < INFINITY ? 2 : mp > 0.f ? 1 : 0;
+        s.min_off = s.min_mode != 1 ? 0.0 : temp < INFINITY ? (double)temp * log((double)mp) : -INFINITY;
     }
     const int begin = min(a.in.vocab, rank * a.per), n = min(a.in.vocab, begin + a.per) - begin;
     const raw *src = static_cast<const raw *>(a.in.logits) + (size_t)r * a.in.stride + begin;
