@@ -595,7 +595,7 @@ __global__ void __launch_bounds__(W * 32, NG == 1 && W == 8 ? 2 : 1)
         const int row = g + 8 * r;
         const float l = row_sum(x.l[r]);
         if (t == 0) {
-            wm[warp * kTile + row] = l > 0.f || l != l ? x.m[r] : -INFINITY;
+            wm[warp * kTile + row] = l > 0.f ? x.m[r] : l != l ? l : -INFINITY;       // (NaN where a logit was: it has to reach the row)
             wl[warp * kTile + row] = l;
         }
 #pragma unroll
@@ -636,7 +636,7 @@ __global__ void __launch_bounds__(W * 32, NG == 1 && W == 8 ? 2 : 1)
         }
         a.part.acc[at * kHeadDim + d] = A;
         if (d == 0) {
-            a.part.m[at] = wM[row];
+            a.part.m[at] = L != L ? L : wM[row];
             a.part.l[at] = L;
         }
     }
@@ -661,7 +661,7 @@ __global__ void __launch_bounds__(128) tree_merge_kernel(TreeArgs a) {
     for (int s0 = 0; s0 < S1; s0 += 32) {
         const bool in = s0 + lane < S1;
         const float li = in ? a.part.l[row0 + s0 + lane] : 0.f, mi = in ? a.part.m[row0 + s0 + lane] : -INFINITY;
-        const float wi = mi != -INFINITY ? exp2_taylor(__fsub_rn(mi, M)) : 0.f;
+        const float wi = mi != mi ? mi : mi != -INFINITY ? exp2_taylor(__fsub_rn(mi, M)) : 0.f;
         for (int i0 = 0; i0 < 32 && s0 + i0 < S1; i0 += 8) {
             float4 y[8];
 #pragma unroll

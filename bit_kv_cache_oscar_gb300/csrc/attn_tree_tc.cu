@@ -587,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(TreeArgs a, int bl
     __syncthreads();
     if (warp < kSoftWarps && rows > 0) {
         const float l = rl[at] + rl[kR + at], zs = rz[at] + rz[kR + at];
-        if (half == 0) rm[at] = l > 0.f || l != l ? st.M : -INFINITY;
+        if (half == 0) rm[at] = l > 0.f ? st.M : l != l ? l : -INFINITY;         // (NaN where a logit was: it has to reach the row)
         if (ti.n > 0)
 #pragma unroll 1
             for (int c = 2 * half; c < 2 * half + 2; ++c) {
@@ -624,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(TreeArgs a, int bl
         const size_t to = tree_row(a, rq, h, row0 + row) * (S + 1) + slot;
         *reinterpret_cast<float4 *>(a.part.acc + to * kHeadDim + 4 * lane) = A;
         if (lane == 0) {
-            a.part.m[to] = M;
+            a.part.m[to] = L != L ? L : M;
             a.part.l[to] = L;
         }
     }
