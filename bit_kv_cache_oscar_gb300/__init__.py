@@ -11,5 +11,5 @@ from .binding import (  # noqa: F401
     oscar_quantize_rotated, oscar_rotate_q, oscar_suggest_splits, oscar_version,
     Int4Pool, oscar_append_kv, oscar_attention_mass_int4, oscar_decode_attention_int4, oscar_demote_int4,
     oscar_evict_int4, oscar_promote_int4, oscar_suggest_splits_int4,
-    oscar_sample, oscar_suggest_splits_tree_int4, oscar_tree_accept, oscar_tree_attention_int4,
+    oscar_sample, oscar_suggest_splits_tree_int4, oscar_tree_accept, oscar_tree_attention_int4, oscar_tree_attention_int4_bounded,
 )

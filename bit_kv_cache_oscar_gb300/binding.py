@@ -64,7 +64,7 @@ EXPORTS_INT4 = [                    # include/oscar_int4.h
     "oscar_decode_attention_int4", "oscar_attention_mass_int4", "oscar_evict_int4",
 ]
 EXPORTS_TREE = [                    # include/oscar_tree.h
-    "oscar_suggest_splits_tree_int4", "oscar_tree_attention_int4", "oscar_sample", "oscar_tree_accept",
+    "oscar_suggest_splits_tree_int4", "oscar_tree_attention_int4", "oscar_tree_attention_int4_bounded", "oscar_sample", "oscar_tree_accept",
 ]
 
 
@@ -148,6 +148,9 @@ def lib():
     L.oscar_tree_attention_int4.argtypes = [P(LayoutC), vp, i32, vp, vp, i32, i32, P(Bf16PoolC), vp, P(Int4PoolC), vp, i32, vp,
                                             vp, i32, ctypes.c_float, P(PartialsC), vp, vp, vp]
     L.oscar_tree_attention_int4.restype = st
+    L.oscar_tree_attention_int4_bounded.argtypes = [P(LayoutC), vp, i32, vp, vp, i32, i32, P(Bf16PoolC), vp, P(Int4PoolC), vp, i32, i32,
+                                                    vp, vp, i32, ctypes.c_float, P(PartialsC), vp, vp, vp]
+    L.oscar_tree_attention_int4_bounded.restype = st
     L.oscar_sample.argtypes = [vp, i32, i64, i32, i32, vp, vp, vp, vp, vp, vp, vp]
     L.oscar_sample.restype = st
     L.oscar_tree_accept.argtypes = [P(LayoutC), vp, vp, vp, i32, vp, i32, vp, i32, vp, vp, vp, i32, vp, P(Bf16PoolC), i32, vp,
@@ -533,6 +536,17 @@ def oscar_tree_attention_int4(layout: Layout, q: torch.Tensor, node_begin: torch
     seq_len + their index.  partials: of n rows."""
     _native().tree_attention_int4(layout, q, node_begin, mask, max_nodes, bf16_pool, bf16_page_table, int4_pool,
                                   int4_page_table, seq_len, hist_end, sm_scale, partials, out, lse, stream)
+
+
+def oscar_tree_attention_int4_bounded(layout: Layout, q: torch.Tensor, node_begin: torch.Tensor, mask: Optional[torch.Tensor],
+                                      max_nodes: int, bf16_pool: Bf16Pool, bf16_page_table: torch.Tensor, int4_pool: Int4Pool,
+                                      int4_page_table: torch.Tensor, max_hist_tokens: int, seq_len: torch.Tensor,
+                                      hist_end: torch.Tensor, sm_scale: float, partials: Partials, out: torch.Tensor,
+                                      lse: Optional[torch.Tensor] = None, stream=None):
+    """The same where histories are known to be shorter than the page tables have room for: max_hist_tokens as given to
+    oscar_suggest_splits_tree_int4, for which the kernel is chosen."""
+    _native().tree_attention_int4_bounded(layout, q, node_begin, mask, max_nodes, bf16_pool, bf16_page_table, int4_pool,
+                                          int4_page_table, seq_len, hist_end, sm_scale, partials, out, lse, stream, max_hist_tokens)
 
 
 def oscar_sample(logits: torch.Tensor, temperature: torch.Tensor, u: torch.Tensor, tokens: torch.Tensor,

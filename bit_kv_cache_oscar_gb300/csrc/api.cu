@@ -2,6 +2,7 @@
 // to the kernels.  Declarations and contracts: include/oscar.h, include/oscar_int4.h,
 // include/oscar_tree.h.
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdarg>
@@ -638,19 +639,21 @@ int32_t oscar_suggest_splits_tree_int4(const oscar_layout_t *L, int32_t batch, i
     return oscar::suggest_splits_tree(*L, batch, max_nodes, max_hist_tokens, sm_count);
 }
 
-oscar_status_t oscar_tree_attention_int4(const oscar_layout_t *layout, const uint16_t *q, int32_t n, const int32_t *node_begin,
-                                         const int32_t *mask, int32_t mask_words, int32_t max_nodes,
-                                         const oscar_bf16_pool_t *bf16_pool, const int32_t *bf16_page_table,
-                                         const oscar_int4_pool_t *int4_pool, const int32_t *int4_page_table,
-                                         int32_t max_pages_per_req, const int32_t *seq_len, const int32_t *hist_end,
-                                         int32_t batch, float sm_scale, const oscar_partials_t *partials, uint16_t *out,
-                                         float *lse, void *stream) {
+oscar_status_t oscar_tree_attention_int4_bounded(const oscar_layout_t *layout, const uint16_t *q, int32_t n,
+                                                 const int32_t *node_begin, const int32_t *mask, int32_t mask_words,
+                                                 int32_t max_nodes, const oscar_bf16_pool_t *bf16_pool,
+                                                 const int32_t *bf16_page_table, const oscar_int4_pool_t *int4_pool,
+                                                 const int32_t *int4_page_table, int32_t max_pages_per_req,
+                                                 int32_t max_hist_tokens, const int32_t *seq_len, const int32_t *hist_end,
+                                                 int32_t batch, float sm_scale, const oscar_partials_t *partials,
+                                                 uint16_t *out, float *lse, void *stream) {
     TRY(check_layout(layout));
     TRY(check_bf16_pool(bf16_pool));
     TRY(check_int4_pool(layout, int4_pool));
     TRY(check_partials(partials));
     TRY(check_tables(layout, max_pages_per_req, batch));
     TRY(check_nodes(n, max_nodes));
+    if (max_hist_tokens < 1) return fail(OSCAR_ERR_INVALID_ARG, "max_hist_tokens %d < 1", max_hist_tokens);
     if (batch == 0 || n == 0) return OSCAR_OK;
     if (!q || !node_begin || !bf16_page_table || !int4_page_table || !seq_len || !hist_end || !out)
         return fail(OSCAR_ERR_INVALID_ARG, "NULL argument");
@@ -662,9 +665,24 @@ oscar_status_t oscar_tree_attention_int4(const oscar_layout_t *layout, const uin
         return fail(OSCAR_ERR_INVALID_ARG, "mask_words %d: fewer bits than max_nodes %d", mask_words, max_nodes);
     const oscar::Attn4Input in{q, bf16_view(bf16_pool), bf16_page_table, int4_view(int4_pool), int4_page_table,
                                max_pages_per_req, seq_len, hist_end, sm_scale};
-    return cuda_status(oscar::launch_tree_attention(*layout, in, {node_begin, n, max_nodes}, mask, mask_words, batch,
-                                                    part_view(partials), out, lse, status_ptr(), (cudaStream_t)stream),
+    return cuda_status(oscar::launch_tree_attention(*layout, in, {node_begin, n, max_nodes}, mask, mask_words, max_hist_tokens,
+                                                    batch, part_view(partials), out, lse, status_ptr(), (cudaStream_t)stream),
                        "oscar_tree_attention_int4 launch");
+}
+
+oscar_status_t oscar_tree_attention_int4(const oscar_layout_t *layout, const uint16_t *q, int32_t n, const int32_t *node_begin,
+                                         const int32_t *mask, int32_t mask_words, int32_t max_nodes,
+                                         const oscar_bf16_pool_t *bf16_pool, const int32_t *bf16_page_table,
+                                         const oscar_int4_pool_t *int4_pool, const int32_t *int4_page_table,
+                                         int32_t max_pages_per_req, const int32_t *seq_len, const int32_t *hist_end,
+                                         int32_t batch, float sm_scale, const oscar_partials_t *partials, uint16_t *out,
+                                         float *lse, void *stream) {
+    // by the page tables' room; a product beyond int32 is refused by the call below
+    const long long room = layout ? (long long)max_pages_per_req * layout->page_size : 0;
+    return oscar_tree_attention_int4_bounded(layout, q, n, node_begin, mask, mask_words, max_nodes, bf16_pool, bf16_page_table,
+                                             int4_pool, int4_page_table, max_pages_per_req,
+                                             (int32_t)std::min(std::max(room, 1LL), 2147483647LL), seq_len, hist_end, batch,
+                                             sm_scale, partials, out, lse, stream);
 }
 
 oscar_status_t oscar_sample(const void *logits, int32_t dtype, int64_t stride, int32_t rows, int32_t vocab,

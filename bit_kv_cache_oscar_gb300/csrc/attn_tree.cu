@@ -708,6 +708,8 @@ cudaError_t launch_rows(const TreeArgs &a, int tiles, int slot0, const CUtensorM
 // of 128 positions and 128 rows, the whole GPU, the latter 5.2 ns for 16 rows, and the former's launches cost 7 us more.  With 8 kv
 // heads, tcgen05 and mma.sync, us: 32 rows, 1 x 100K 63 and 76, 64 x 4K 236 and 258, 1 x 4K 22 and 16; 64 rows, 16 ragged of 100K 735
 // and 1,050, 1 x 4K 25.5 and 19.6.
+// tokens: the longest history's, one number for the splits and for the launch.  By the tables' width instead (128K), 8 nodes: 1 x 4K
+// 22.7 us for 16.0, 1 x 1K 21.0 for 13.8.
 static bool on_tcgen05(const oscar_layout_t &L, int batch, int max_nodes, long long tokens) {
     const long long rows = (long long)max_nodes * L.gqa, tiles = (long long)batch * L.n_kv_heads * (tokens / 128 + 1);
     return L.group == 128 && rows > 16 && tiles * (52 * ((rows + 15) / 16) - 82 * ((rows + 127) / 128)) > 70000;
@@ -731,7 +733,7 @@ int suggest_splits_tree(const oscar_layout_t &L, int batch, int max_nodes, int m
 }
 
 cudaError_t launch_tree_attention(const oscar_layout_t &L, const Attn4Input &in, const TreeInput &t, const int32_t *mask, int mask_words,
-                                  int batch, PartialsView part, uint16_t *out, float *lse, int32_t *status, cudaStream_t st) {
+                                  int max_hist, int batch, PartialsView part, uint16_t *out, float *lse, int32_t *status, cudaStream_t st) {
     TreeArgs a{in.q, t, mask, mask_words, in.bf, in.bpt, in.i4.codes_k, in.i4.codes_v, in.i4.scale_zero, in.i4.n_pages, in.ipt, in.max_pages, page_shift(L), L.n_kv_heads, L.gqa,
                L.sink, in.seq_len, in.hist_end, in.sm_scale * kLog2e, part, out, lse, status};
     CUtensorMap tmk, tmv;
@@ -739,7 +741,7 @@ cudaError_t launch_tree_attention(const oscar_layout_t &L, const Attn4Input &in,
     const int box = L.page_size < kBlock4 ? L.page_size : kBlock4;
     if (!rows_tensor_map(&tmk, in.i4.codes_k, rows, box) || !rows_tensor_map(&tmv, in.i4.codes_v, rows, box)) return cudaErrorInvalidValue;
     const int tiles = (t.max_nodes * L.gqa + kTile - 1) / kTile;
-    const bool tc = on_tcgen05(L, batch, t.max_nodes, (long long)in.max_pages * L.page_size);
+    const bool tc = on_tcgen05(L, batch, t.max_nodes, max_hist);
     if (tc)
         if (cudaError_t e = launch_tree_history_tc(a, t.max_nodes * L.gqa, batch, st)) return e;
     const int slot0 = tc ? part.S : 0;

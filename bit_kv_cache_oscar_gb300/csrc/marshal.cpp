@@ -28,7 +28,7 @@ PyObject *g_error = nullptr;                 // OscarError
 // liboscar.so's entry points (connect)
 #define ENTRY_POINTS(X) \
     X(oscar_append_kv) X(oscar_demote_int4) X(oscar_promote_int4) X(oscar_decode_attention_int4) X(oscar_attention_mass_int4) X(oscar_evict_int4) \
-    X(oscar_tree_attention_int4) X(oscar_sample) X(oscar_tree_accept) \
+    X(oscar_tree_attention_int4) X(oscar_tree_attention_int4_bounded) X(oscar_sample) X(oscar_tree_accept) \
     X(oscar_last_error_string)
 struct {
 #define X(f) decltype(&::f) f;
@@ -341,10 +341,11 @@ void evict_int4(PyObject *const *a) {
 }
 
 // layout, q, node_begin, mask, max_nodes, bf16_pool, bf16_page_table, int4_pool, int4_page_table, seq_len, hist_end, sm_scale,
-// partials, out, lse, stream
-void tree_attention_int4(PyObject *const *a) {
+// partials, out, lse, stream; BOUNDED: and max_hist_tokens
+template <bool BOUNDED>
+void tree_attention(PyObject *const *a) {
     const oscar_layout_t layout_ = layout(a[0]), *L = &layout_;
-    const Call c("oscar_tree_attention_int4");
+    const Call c(BOUNDED ? "oscar_tree_attention_int4_bounded" : "oscar_tree_attention_int4");
     int64_t batch, max_pages, words = 0;
     c.table(a[8], &batch, &max_pages);
     const int64_t Hq = (int64_t)L->n_kv_heads * L->gqa;
@@ -370,9 +371,16 @@ void tree_attention_int4(PyObject *const *a) {
     uint16_t *out = c.at<uint16_t>("out", a[13], at::kBFloat16, {n, Hq, 128});
     float *lse = c.at<float>("lse", a[14], at::kFloat, {n, Hq});
     void *st = c.stream(a[15]);
-    c.done(unlocked(g_lib.oscar_tree_attention_int4, L, q, c.pages32(n), begin, mask, c.pages32(words), nodes, &bf, bpt, &i4, ipt, c.pages32(max_pages), T, he,
-                    c.pages32(batch), scale, &part, out, lse, st));
+    const int32_t n32 = c.pages32(n), words32 = c.pages32(words), pages = c.pages32(max_pages), batch32 = c.pages32(batch);
+    if (BOUNDED)
+        c.done(unlocked(g_lib.oscar_tree_attention_int4_bounded, L, q, n32, begin, mask, words32, nodes, &bf, bpt, &i4, ipt, pages, whole(a[16]), T, he, batch32,
+                        scale, &part, out, lse, st));
+    else
+        c.done(unlocked(g_lib.oscar_tree_attention_int4, L, q, n32, begin, mask, words32, nodes, &bf, bpt, &i4, ipt, pages, T, he, batch32, scale, &part, out,
+                        lse, st));
 }
+void tree_attention_int4(PyObject *const *a) { tree_attention<false>(a); }
+void tree_attention_int4_bounded(PyObject *const *a) { tree_attention<true>(a); }
 
 // logits, temperature, u, tokens, top_k, top_p, min_p, stream
 void sample(PyObject *const *a) {
@@ -453,7 +461,7 @@ PyObject *connect(PyObject *, PyObject *const *args, Py_ssize_t n) {
 
 #define ENTRY(f, n) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<f, n>)), METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {ENTRY(append_kv, 17), ENTRY(demote_int4, 10), ENTRY(promote_int4, 8), ENTRY(decode_attention_int4, 15),
-                           ENTRY(attention_mass_int4, 12), ENTRY(evict_int4, 12), ENTRY(tree_attention_int4, 16), ENTRY(sample, 8), ENTRY(tree_accept, 14),
+                           ENTRY(attention_mass_int4, 12), ENTRY(evict_int4, 12), ENTRY(tree_attention_int4, 16), ENTRY(tree_attention_int4_bounded, 17), ENTRY(sample, 8), ENTRY(tree_accept, 14),
                            {"connect", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&connect)), METH_FASTCALL, nullptr}, {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_marshal", "Argument checks of the INT4 entry points.", -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 

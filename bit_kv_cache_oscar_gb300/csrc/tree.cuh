@@ -23,8 +23,9 @@ __device__ __forceinline__ int read_nodes(const TreeInput &t, int b, int32_t *st
 }
 
 int suggest_splits_tree(const oscar_layout_t &L, int batch, int max_nodes, int max_hist, int sm_count);
+// max_hist: tokens of the longest history, as the splits were suggested for
 cudaError_t launch_tree_attention(const oscar_layout_t &L, const Attn4Input &in, const TreeInput &t, const int32_t *mask, int mask_words,
-                                  int batch, PartialsView part, uint16_t *out, float *lse, int32_t *status, cudaStream_t st);
+                                  int max_hist, int batch, PartialsView part, uint16_t *out, float *lse, int32_t *status, cudaStream_t st);
 
 struct SampleInput {
     const void *logits;

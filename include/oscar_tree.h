@@ -26,8 +26,9 @@ extern "C" {
 
 #define OSCAR_TREE_MAX_NODES 256
 
-/* A history split count for oscar_tree_attention_int4 that fills the GPU (1..1024); max_nodes: nodes of the
- * largest tree. */
+/* A history split count for oscar_tree_attention_int4 and _bounded that fills the GPU (1..1024); max_nodes: nodes
+ * of the largest tree; max_hist_tokens: of the longest history, for which the kernel of the history is chosen too
+ * (oscar_tree_attention_int4_bounded takes the same number). */
 OSCAR_API int32_t oscar_suggest_splits_tree_int4(const oscar_layout_t *layout, int32_t batch, int32_t max_nodes,
                                                  int32_t max_hist_tokens, int32_t sm_count);
 
@@ -66,6 +67,25 @@ OSCAR_API oscar_status_t oscar_tree_attention_int4(const oscar_layout_t *layout,
                                                    const int32_t *seq_len, const int32_t *hist_end, int32_t batch,
                                                    float sm_scale, const oscar_partials_t *partials, uint16_t *out,
                                                    float *lse, void *stream);
+
+/*
+ * The same call for histories of at most max_hist_tokens (1 and more), of which there may be fewer than the page tables
+ * have room for.  Which of two kernels takes the history goes by this bound, in oscar_suggest_splits_tree_int4 as here;
+ * oscar_tree_attention_int4 goes by the page tables' room, max_pages_per_req·page_size.  A table as wide as the longest
+ * request a server admits wants the bound: the kernel for long histories is slower on short ones.  The bound decides
+ * on time and last bits alone: longer histories are met in full.
+ */
+OSCAR_API oscar_status_t oscar_tree_attention_int4_bounded(const oscar_layout_t *layout, const uint16_t *q, int32_t n,
+                                                           const int32_t *node_begin, const int32_t *mask,
+                                                           int32_t mask_words, int32_t max_nodes,
+                                                           const oscar_bf16_pool_t *bf16_pool,
+                                                           const int32_t *bf16_page_table,
+                                                           const oscar_int4_pool_t *int4_pool,
+                                                           const int32_t *int4_page_table, int32_t max_pages_per_req,
+                                                           int32_t max_hist_tokens, const int32_t *seq_len,
+                                                           const int32_t *hist_end, int32_t batch, float sm_scale,
+                                                           const oscar_partials_t *partials, uint16_t *out, float *lse,
+                                                           void *stream);
 
 /* Types of logits. */
 #define OSCAR_DTYPE_F32 0
