@@ -31,7 +31,6 @@ namespace {
 
 constexpr int kTile = 16;                        // query rows of a CTA
 constexpr int kWide = 160;                       // CTAs of a launch up to which each gets an SM
-constexpr uint32_t kM0 = 0x000F000Fu, kM1 = 0x00F000F0u;
 constexpr int kResRow = kHeadDim + 4;
 constexpr float kNone = -1e30f;                  // reference before the first token
 constexpr float kMostP = 0x1p100f;               // of the sum of a lane's p in a block
@@ -45,12 +44,6 @@ struct Ring {
     static constexpr int total = W * n * stride;
 };
 
-__device__ __forceinline__ float lo16(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float hi16(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
-__device__ __forceinline__ uint32_t pack_h2(float a, float b) {
-    const __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
 __device__ __forceinline__ __nv_bfloat162 as_bf2(uint32_t w) { return *reinterpret_cast<const __nv_bfloat162 *>(&w); }
 __device__ __forceinline__ uint32_t pack_b2(float a, float b) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
@@ -76,18 +69,6 @@ __device__ __forceinline__ float row_max(float x) {
 __device__ __forceinline__ float row_sum(float x) {
     x += __shfl_xor_sync(0xffffffffu, x, 1);
     return x + __shfl_xor_sync(0xffffffffu, x, 2);
-}
-// Codes of nibbles 0 (low) or 1 (high) of a word's two halves, less 8: (1024 + n) - 1032, (1024 + 16 n) / 16 - 72.
-__device__ __forceinline__ uint32_t centred_low(uint32_t w) {
-    uint32_t d;
-    asm("{\n.reg .b32 t;\nlop3.b32 t, %1, 0x000F000F, 0x64006400, 0xEA;\nadd.f16x2 %0, t, %2;\n}" : "=r"(d) : "r"(w), "r"(0xE408E408u));
-    return d;
-}
-__device__ __forceinline__ uint32_t centred_high(uint32_t w) {
-    uint32_t d;
-    asm("{\n.reg .b32 t;\nlop3.b32 t, %1, 0x00F000F0, 0x64006400, 0xEA;\nfma.rn.f16x2 %0, t, %2, %3;\n}"
-        : "=r"(d) : "r"(w), "r"(0x2C002C00u), "r"(0xD480D480u));
-    return d;
 }
 // What a warp holds of its 16 rows: lane (g, t) has rows g and g + 8 (index r); out[c][i][2 r + e] is channel
 // 32 c + 8 t + 4 e + i of row g + 8 r.

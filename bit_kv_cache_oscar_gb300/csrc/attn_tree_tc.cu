@@ -48,7 +48,6 @@ constexpr float kMostW = 0x1p15f, kMostP = 0x1p110f;
 constexpr float kNewW = 8.f, kNewP = 100.f;      // a new reference brings p s' to 2^8 at most, p to 2^100
 constexpr uint32_t kIdesc = (1u << 4) | ((uint32_t)(kT >> 3) << 17) | ((uint32_t)(kR >> 4) << 24);      // f16, f16, fp32
 constexpr uint32_t kIdescMN = kIdesc | (1u << 16);                                                      // B MN-major
-constexpr uint32_t kM0 = 0x000F000Fu, kM1 = 0x00F000F0u;
 
 // As mbar_wait, but given up after about a second: roles wait for one another in a chain.
 __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity) {
@@ -113,27 +112,10 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r) {
           "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
-__device__ __forceinline__ uint32_t pack_h2(float a, float b) {
-    const __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-__device__ __forceinline__ float lo16(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float hi16(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 // A code word's operand: channels 0 4 | 1 5 | 2 6 | 3 7 of its eight.
 __device__ __forceinline__ uint4 subnormal(uint32_t w) {
     const uint32_t v = w >> 8;
     return make_uint4(w & kM0, w & kM1, v & kM0, v & kM1);
-}
-__device__ __forceinline__ uint32_t centred_low(uint32_t w) {
-    uint32_t d;
-    asm("{\n.reg .b32 t;\nlop3.b32 t, %1, 0x000F000F, 0x64006400, 0xEA;\nadd.f16x2 %0, t, %2;\n}" : "=r"(d) : "r"(w), "r"(0xE408E408u));
-    return d;
-}
-__device__ __forceinline__ uint32_t centred_high(uint32_t w) {
-    uint32_t d;
-    asm("{\n.reg .b32 t;\nlop3.b32 t, %1, 0x00F000F0, 0x64006400, 0xEA;\nfma.rn.f16x2 %0, t, %2, %3;\n}"
-        : "=r"(d) : "r"(w), "r"(0x2C002C00u), "r"(0xD480D480u));
-    return d;
 }
 __device__ __forceinline__ uint4 centred(uint32_t w) {
     const uint32_t v = w >> 8;

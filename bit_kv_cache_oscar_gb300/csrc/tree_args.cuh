@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cuda_fp16.h>
 
 #include "pairs.cuh"
 #include "ptx.cuh"
@@ -10,6 +11,27 @@
 namespace oscar {
 
 constexpr int kBlock4 = 32;                      // tokens of one box of the INT4 pool
+
+constexpr uint32_t kM0 = 0x000F000Fu, kM1 = 0x00F000F0u;    // nibbles 0 and 1 of a word's two halves
+
+__device__ __forceinline__ float lo16(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi16(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ uint32_t pack_h2(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+// Codes of nibbles 0 (low) or 1 (high) of a word's two halves, less 8: (1024 + n) - 1032, (1024 + 16 n) / 16 - 72.
+__device__ __forceinline__ uint32_t centred_low(uint32_t w) {
+    uint32_t d;
+    asm("{\n.reg .b32 t;\nlop3.b32 t, %1, 0x000F000F, 0x64006400, 0xEA;\nadd.f16x2 %0, t, %2;\n}" : "=r"(d) : "r"(w), "r"(0xE408E408u));
+    return d;
+}
+__device__ __forceinline__ uint32_t centred_high(uint32_t w) {
+    uint32_t d;
+    asm("{\n.reg .b32 t;\nlop3.b32 t, %1, 0x00F000F0, 0x64006400, 0xEA;\nfma.rn.f16x2 %0, t, %2, %3;\n}"
+        : "=r"(d) : "r"(w), "r"(0x2C002C00u), "r"(0xD480D480u));
+    return d;
+}
 
 struct TreeArgs {
     const uint16_t *q;
