@@ -24,15 +24,12 @@
 
 #include "merge_math.cuh"
 #include "tma.cuh"
-#include "tree_args.cuh"
+#include "tree_window.cuh"
 
 namespace oscar {
 namespace {
 
-constexpr int kTile = 16;                        // query rows of a CTA
 constexpr int kWide = 160;                       // CTAs of a launch up to which each gets an SM
-constexpr int kResRow = kHeadDim + 4;
-constexpr float kNone = -1e30f;                  // reference before the first token
 constexpr float kMostP = 0x1p100f;               // of the sum of a lane's p in a block
 constexpr float kNewW = 8.f, kNewP = 80.f;       // a new reference brings p·s to 2^8 at most, p to 2^80
 
@@ -44,190 +41,12 @@ struct Ring {
     static constexpr int total = W * n * stride;
 };
 
-__device__ __forceinline__ __nv_bfloat162 as_bf2(uint32_t w) { return *reinterpret_cast<const __nv_bfloat162 *>(&w); }
-__device__ __forceinline__ uint32_t pack_b2(float a, float b) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
-    uint32_t d;
-    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
-    return d;
-}
 __device__ __forceinline__ void tma_rows(uint32_t dst, const void *tmap, int row, uint32_t bar, uint64_t pol) {
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint "
         "[%0], [%1, {%2, %3}], [%4], %5;"
         ::"r"(dst), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(0), "r"(row), "r"(bar), "l"(pol)
         : "memory");
-}
-// Over the four lanes of a row.
-__device__ __forceinline__ float row_max(float x) {
-    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-    return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-}
-__device__ __forceinline__ float row_sum(float x) {
-    x += __shfl_xor_sync(0xffffffffu, x, 1);
-    return x + __shfl_xor_sync(0xffffffffu, x, 2);
-}
-// What a warp holds of its 16 rows: lane (g, t) has rows g and g + 8 (index r); out[c][i][2 r + e] is channel
-// 32 c + 8 t + 4 e + i of row g + 8 r.
-struct Rows {
-    float m[2], l[2], z[4][2], out[4][4][4];
-};
-
-__device__ __forceinline__ void clear(Rows &x) {
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        x.m[r] = kNone;
-        x.l[r] = 0.f;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) x.z[k][r] = 0.f;
-    }
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x.out[c][i][e] = 0.f;
-}
-
-// Channels 32 i + 8 t .. + 7 of query row g + 8 r of the tile, t = lane % 4.
-__device__ __forceinline__ uint4 query_piece(const TreeArgs &a, const TreeRequest &rq, int h, int row0, int rows, int r, int i, int lane) {
-    const int row = (lane >> 2) + 8 * r;
-    if (row >= rows) return make_uint4(0, 0, 0, 0);
-    return *reinterpret_cast<const uint4 *>(a.q + tree_row(a, rq, h, row0 + row) * kHeadDim + 32 * i + 8 * (lane & 3));
-}
-
-// ---- the BF16 rows ---------------------------------------------------------------------------------
-// Positions [0, min(sink, T)), [max(hist_end, those), T) and the nodes' [T, T + n), in tiles of 16.
-template <int W>
-__device__ __forceinline__ void window_warp(const TreeArgs &a, const TreeRequest &rq, int b, int h, int row0, int rows, uint4 *frag, int warp, int lane,
-                                            Rows &x) {
-    const int g = lane >> 2, t = lane & 3, sh = a.page_shift, T = rq.T, end = T + rq.n;
-    const int n0 = min(a.sink, T), lo1 = max(rq.he, n0), sink_tiles = (n0 + 15) / 16, rec0 = lo1 / 16;
-    const int tiles = sink_tiles + (end + 15) / 16 - rec0;
-    // the A operand of the logits, as it lies, for all warps: fragment 2 i + e of lane l at 32 (2 i + e) + l
-    for (int k = warp; k < 4; k += W) {
-        const uint4 x = query_piece(a, rq, h, row0, rows, 0, k, lane), y = query_piece(a, rq, h, row0, rows, 1, k, lane);
-        frag[64 * k + lane] = make_uint4(x.x, y.x, x.y, y.y);
-        frag[64 * k + 32 + lane] = make_uint4(x.z, y.z, x.w, y.w);
-    }
-    __syncthreads();
-    int node[2];                                     // of the lane's rows
-#pragma unroll
-    for (int r = 0; r < 2; ++r) node[r] = (row0 + min(g + 8 * r, rows - 1)) / a.G;
-#pragma unroll 1
-    for (int k = warp; k < tiles; k += W) {
-        const bool in_sink = k < sink_tiles;
-        const int p0 = (in_sink ? k : rec0 + k - sink_tiles) * 16, lo = in_sink ? 0 : lo1, hi = in_sink ? n0 : end;
-        const int page = a.bpt[(size_t)b * a.max_pages + (p0 >> sh)];
-        if ((uint32_t)page >= (uint32_t)a.bf.n_pages) {
-            if (lane == 0) flag_status(a.status, OSCAR_DEV_BAD_BF16_PAGE);
-            continue;
-        }
-        // lane (g, t): channels 32 i + 8 t .. + 7 of tokens g and g + 8
-        const bool in0 = p0 + g >= lo && p0 + g < hi, in1 = p0 + g + 8 >= lo && p0 + g + 8 < hi;
-        const size_t at = ((((size_t)page << sh) + ((p0 + g) & ((1 << sh) - 1))) * a.n_kv + h) * kHeadDim + 8 * t, far = (size_t)8 * a.n_kv * kHeadDim;
-        uint4 kk[2][4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            kk[0][i] = in0 ? *reinterpret_cast<const uint4 *>(a.bf.k + at + 32 * i) : make_uint4(0, 0, 0, 0);
-            kk[1][i] = in1 ? *reinterpret_cast<const uint4 *>(a.bf.k + at + far + 32 * i) : make_uint4(0, 0, 0, 0);
-        }
-        float s[2][4];                               // [keys 8 u + 2 t + e][2 r + e]
-#pragma unroll
-        for (int u = 0; u < 2; ++u) s[u][0] = s[u][1] = s[u][2] = s[u][3] = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint4 x = frag[64 * i + lane], y = frag[64 * i + 32 + lane];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                mma16816_bf16(s[u], x.x, x.y, x.z, x.w, kk[u][i].x, kk[u][i].y);
-                mma16816_bf16(s[u], y.x, y.y, y.z, y.w, kk[u][i].z, kk[u][i].w);
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int p = p0 + 8 * u + 2 * t + (e & 1), r = e >> 1;
-                bool sees = p >= lo && p < hi;
-                if (sees && p >= T) {
-                    const int j = p - T;
-                    sees = a.mask ? (a.mask[(size_t)(rq.first + node[r]) * a.mask_words + (j >> 5)] >> (j & 31)) & 1 : j <= node[r];
-                }
-                s[u][e] = sees ? s[u][e] * a.scale2 : -INFINITY;
-            }
-        float al[2];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const float m = fmaxf(x.m[r], row_max(fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]))));
-            al[r] = ex2_approx(x.m[r] - m);
-            x.m[r] = m;
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) s[u][2 * r + e] = ex2_approx(s[u][2 * r + e] - m);
-            x.l[r] = fmaf(x.l[r], al[r], (s[0][2 * r] + s[0][2 * r + 1]) + (s[1][2 * r] + s[1][2 * r + 1]));
-        }
-        uint32_t ph[4], pl[4];                       // A operand: rows g, g + 8 of keys 2 t + e, then of keys 8 + 2 t + e
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const uint32_t hi2 = pack_b2(s[u][2 * r], s[u][2 * r + 1]);
-                ph[2 * u + r] = hi2;
-                pl[2 * u + r] = pack_b2(s[u][2 * r] - lo16(hi2), s[u][2 * r + 1] - hi16(hi2));
-            }
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const uint4 v0 = in0 ? *reinterpret_cast<const uint4 *>(a.bf.v + at + 32 * c) : make_uint4(0, 0, 0, 0);
-            const uint4 v1 = in1 ? *reinterpret_cast<const uint4 *>(a.bf.v + at + far + 32 * c) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x.out[c][i][e] *= al[e >> 1];
-            // infinities and NaN among the values: rows that do not see them must not meet them in a product
-            const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-            bool odd = false;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) odd |= (w[e] & 0x7f80u) == 0x7f80u || (w[e] & 0x7f800000u) == 0x7f800000u;
-            if (__any_sync(0xffffffffu, odd)) {
-                // one key at a time, only where it has weight
-#pragma unroll 1
-                for (int key = 0; key < 16; ++key) {
-                    const int u = key >> 3, from = (lane & ~3) | ((key & 7) >> 1), p = p0 + key;
-                    if (p < lo || p >= hi) continue;
-                    float pr[2];
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        const float first = __shfl_sync(0xffffffffu, u ? s[1][2 * r] : s[0][2 * r], from);
-                        const float second = __shfl_sync(0xffffffffu, u ? s[1][2 * r + 1] : s[0][2 * r + 1], from);
-                        pr[r] = key & 1 ? second : first;
-                    }
-                    const uint16_t *v = a.bf.v + ((((size_t)page << sh) + (p & ((1 << sh) - 1))) * a.n_kv + h) * kHeadDim + 8 * t + 32 * c;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (pr[e >> 1] != 0.f) x.out[c][i][e] = fmaf(pr[e >> 1], bf16_to_f32(v[4 * (e & 1) + i]), x.out[c][i][e]);
-                }
-                continue;
-            }
-            // channels 32 c + 4 n + 2 j + e of eight tokens are an 8 x 8 matrix of 16 bits: transposed, the B operand
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const uint32_t sel = e ? 0x7632 : 0x5410;
-                    const uint32_t b0 = movmatrix_trans(__byte_perm(j ? v0.y : v0.x, j ? v0.w : v0.z, sel));
-                    const uint32_t b1 = movmatrix_trans(__byte_perm(j ? v1.y : v1.x, j ? v1.w : v1.z, sel));
-                    mma16816_bf16(x.out[c][2 * j + e], pl[0], pl[1], pl[2], pl[3], b0, b1);
-                    mma16816_bf16(x.out[c][2 * j + e], ph[0], ph[1], ph[2], ph[3], b0, b1);
-                }
-        }
-    }
 }
 
 // ---- the history -----------------------------------------------------------------------------------
@@ -536,92 +355,35 @@ __device__ __forceinline__ void history_warp(const TreeArgs &a, const CUtensorMa
     }
 }
 
-// grid (slots x row tiles, Hkv, batch), slots slot0 .. S, the row tiles of a slot next to each other: they read the same rows; S = 1
-// and slot0 = 0: the row tiles, all of it by one CTA each.
-// slot0 = S (the BF16 rows alone): launched behind tree_tc_kernel, which starts it once what comes before both is done; it
-// reads none of that one's results, but does not end before it.
+// grid (slots x row tiles, Hkv, batch), slots 0 .. S, the row tiles of a slot next to each other: they read the same rows; S = 1:
+// the row tiles, all of it by one CTA each.
 template <int NG, int W>
 __global__ void __launch_bounds__(W * 32, NG == 1 && W == 8 ? 2 : 1)
-    tree_kernel(TreeArgs a, int tiles, int slot0, const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
+    tree_kernel(TreeArgs a, int tiles, const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
     using R = Ring<NG, W>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t bars[W * R::n];
     uint8_t *smem = smem_raw + ((512u - (saddr(smem_raw) & 511u)) & 511u);          // the swizzle pattern repeats every 512 bytes
     uint4 *frag = reinterpret_cast<uint4 *>(smem + R::total);
-    const int slot = slot0 + blockIdx.x / tiles, row0 = blockIdx.x % tiles * kTile, h = blockIdx.y, b = blockIdx.z, S = a.part.S;
+    const int slot = blockIdx.x / tiles, row0 = blockIdx.x % tiles * kTile, h = blockIdx.y, b = blockIdx.z, S = a.part.S;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (lane == 0)
         for (int i = 0; i < R::n; ++i) mbar_init(saddr(&bars[warp * R::n + i]), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     __syncwarp();
-    const bool behind = slot0 == S, whole = S == 1 && !behind;
-    if (!behind) pdl_wait();
+    const bool whole = S == 1;
+    pdl_wait();
     const TreeRequest rq(a, b);
     const int rows = min(kTile, rq.n * a.G - row0);
-    if (rows <= 0) {
-        if (behind) pdl_wait();
-        return;
-    }
+    if (rows <= 0) return;
     Rows x;
     clear(x);
     if (slot < S)
         history_warp<NG, W>(a, &tmk, &tmv, smem + warp * R::n * R::stride, saddr(&bars[warp * R::n]), rq, b, h, row0, rows, slot, frag, warp, lane, x);
     if (whole) __syncthreads();                      // frag is read
-    if (slot == S || whole) window_warp<W>(a, rq, b, h, row0, rows, frag, warp, lane, x);
+    if (slot == S || whole) window_warp<W>(a, rq, b, h, row0, rows, frag, reinterpret_cast<uint4 *>(smem + warp * R::n * R::stride), 0, warp, lane, x);
     __syncthreads();                                 // every warp is done with its ring: results take its place
-    float *wm = reinterpret_cast<float *>(smem), *wl = wm + W * kTile, *wa = wl + W * kTile + warp * kTile * kResRow;
-    const int g = lane >> 2, t = lane & 3;
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        const int row = g + 8 * r;
-        const float l = row_sum(x.l[r]);
-        if (t == 0) {
-            wm[warp * kTile + row] = l > 0.f ? x.m[r] : l != l ? l : -INFINITY;       // (NaN where a logit was: it has to reach the row)
-            wl[warp * kTile + row] = l;
-        }
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-                *reinterpret_cast<float4 *>(wa + row * kResRow + 32 * c + 8 * t + 4 * e) =
-                    make_float4(x.out[c][0][2 * r + e], x.out[c][1][2 * r + e], x.out[c][2][2 * r + e], x.out[c][3][2 * r + e]);
-    }
-    __syncthreads();
-    // every warp's weight 2^(m - M) once, then the sums
-    const float *sum = wl + W * kTile;
-    float *wf = wl + W * kTile + W * kTile * kResRow, *wM = wf + W * kTile;
-    if (threadIdx.x < W * kTile) {
-        const int row = threadIdx.x % kTile;
-        float M = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < W; ++w) M = fmaxf(M, wm[w * kTile + row]);
-        wf[threadIdx.x] = wm[threadIdx.x] != -INFINITY ? exp2f(wm[threadIdx.x] - M) : 0.f;
-        if (threadIdx.x < kTile) wM[row] = M;
-    }
-    __syncthreads();
-    for (int e = threadIdx.x; e < rows * kHeadDim; e += W * 32) {
-        const int row = e / kHeadDim, d = e % kHeadDim;
-        float L = 0.f, A = 0.f;
-#pragma unroll
-        for (int w = 0; w < W; ++w) {
-            const float f = wf[w * kTile + row], y = sum[(w * kTile + row) * kResRow + d];
-            L = f != 0.f ? fmaf(wl[w * kTile + row], f, L) : L;
-            A = f != 0.f ? fmaf(y, f, A) : A;
-        }
-        const size_t orow = tree_row(a, rq, h, row0 + row), at = orow * (S + 1) + slot;
-        if (whole) {
-            const bool on = L > 0.f || L != L;
-            a.o[orow * kHeadDim + d] = f32_to_bf16_rn(on ? __fdiv_rn(A, L) : 0.f);
-            if (a.lse && d == 0) a.lse[orow] = on ? (wM[row] + log2f(L)) * 0.6931471805599453f : -INFINITY;
-            continue;
-        }
-        a.part.acc[at * kHeadDim + d] = A;
-        if (d == 0) {
-            a.part.m[at] = L != L ? L : wM[row];
-            a.part.l[at] = L;
-        }
-    }
-    if (behind) pdl_wait();
+    join_warps<W>(a, rq, h, row0, rows, slot, whole, smem, 0, threadIdx.x, warp, lane, x);
 }
 
 // A warp takes a (node row, query head): its slots in ascending order, four channels a lane, eight slots on their way.
@@ -676,11 +438,11 @@ bool rows_tensor_map(CUtensorMap *tm, const uint8_t *base, long long rows, int b
 }
 
 template <int NG, int W>
-cudaError_t launch_rows(const TreeArgs &a, int tiles, int slot0, const CUtensorMap &tmk, const CUtensorMap &tmv, int batch, cudaStream_t st) {
-    const int join = (3 * W * kTile + kTile + W * kTile * kResRow) * 4, smem = std::max(Ring<NG, W>::total + 4096, join) + 512;
+cudaError_t launch_rows(const TreeArgs &a, int tiles, const CUtensorMap &tmk, const CUtensorMap &tmv, int batch, cudaStream_t st) {
+    const int smem = std::max(Ring<NG, W>::total + 4096, join_bytes<W>()) + 512;
     auto kern = tree_kernel<NG, W>;
     if (cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void *>(kern), smem)) return e;
-    return launch_ahead(kern, dim3((a.part.S == 1 && slot0 == 0 ? 1 : a.part.S + 1 - slot0) * tiles, a.n_kv, batch), W * 32, smem, st, a, tiles, slot0, tmk, tmv);
+    return launch_ahead(kern, dim3((a.part.S == 1 ? 1 : a.part.S + 1) * tiles, a.n_kv, batch), W * 32, smem, st, a, tiles, tmk, tmv);
 }
 
 }  // namespace
@@ -717,23 +479,23 @@ cudaError_t launch_tree_attention(const oscar_layout_t &L, const Attn4Input &in,
                                   int max_hist, int batch, PartialsView part, uint16_t *out, float *lse, int32_t *status, cudaStream_t st) {
     TreeArgs a{in.q, t, mask, mask_words, in.bf, in.bpt, in.i4.codes_k, in.i4.codes_v, in.i4.scale_zero, in.i4.n_pages, in.ipt, in.max_pages, page_shift(L), L.n_kv_heads, L.gqa,
                L.sink, in.seq_len, in.hist_end, in.sm_scale * kLog2e, part, out, lse, status};
-    CUtensorMap tmk, tmv;
-    const long long rows = (long long)in.i4.n_pages * L.n_kv_heads * L.page_size;
-    const int box = L.page_size < kBlock4 ? L.page_size : kBlock4;
-    if (!rows_tensor_map(&tmk, in.i4.codes_k, rows, box) || !rows_tensor_map(&tmv, in.i4.codes_v, rows, box)) return cudaErrorInvalidValue;
     const int tiles = (t.max_nodes * L.gqa + kTile - 1) / kTile;
-    const bool tc = on_tcgen05(L, batch, t.max_nodes, max_hist);
-    if (tc)
-        if (cudaError_t e = launch_tree_history_tc(a, t.max_nodes * L.gqa, batch, st)) return e;
-    const int slot0 = tc ? part.S : 0;
-    const bool wide = !tc && (long long)(part.S + 1) * tiles * L.n_kv_heads * batch <= kWide;
-    cudaError_t e;
-    switch (L.group) {
-        case 32: e = launch_rows<4, 8>(a, tiles, slot0, tmk, tmv, batch, st); break;
-        case 64: e = launch_rows<2, 8>(a, tiles, slot0, tmk, tmv, batch, st); break;
-        default: e = wide ? launch_rows<1, 12>(a, tiles, slot0, tmk, tmv, batch, st) : launch_rows<1, 8>(a, tiles, slot0, tmk, tmv, batch, st);
+    if (on_tcgen05(L, batch, t.max_nodes, max_hist) && tree_tc_fits(a, t.max_nodes * L.gqa, batch)) {
+        if (cudaError_t e = launch_tree_tc(a, t.max_nodes * L.gqa, batch, st)) return e;
+    } else {
+        CUtensorMap tmk, tmv;
+        const long long rows = (long long)in.i4.n_pages * L.n_kv_heads * L.page_size;
+        const int box = L.page_size < kBlock4 ? L.page_size : kBlock4;
+        if (!rows_tensor_map(&tmk, in.i4.codes_k, rows, box) || !rows_tensor_map(&tmv, in.i4.codes_v, rows, box)) return cudaErrorInvalidValue;
+        const bool wide = (long long)(part.S + 1) * tiles * L.n_kv_heads * batch <= kWide;
+        cudaError_t e;
+        switch (L.group) {
+            case 32: e = launch_rows<4, 8>(a, tiles, tmk, tmv, batch, st); break;
+            case 64: e = launch_rows<2, 8>(a, tiles, tmk, tmv, batch, st); break;
+            default: e = wide ? launch_rows<1, 12>(a, tiles, tmk, tmv, batch, st) : launch_rows<1, 8>(a, tiles, tmk, tmv, batch, st);
+        }
+        if (e || part.S == 1) return e;
     }
-    if (e || (part.S == 1 && !tc)) return e;
     return launch_ahead(tree_merge_kernel, dim3((t.max_nodes * L.n_kv_heads * L.gqa + 3) / 4, batch), 128, 0, st, a);
 }
 

@@ -73,8 +73,9 @@ __device__ __forceinline__ size_t tree_row(const TreeArgs &a, const TreeRequest 
     return ((size_t)(r.first + row / a.G) * a.n_kv + h) * a.G + row % a.G;
 }
 
-// The history's slots on the 5th-generation tensor cores (group 128), 128 query rows of a kv head at a time.  The kernel lets its
-// successor in the stream start before it ends: tree_kernel alone may be launched after it, which waits for it at its end.
-cudaError_t launch_tree_history_tc(const TreeArgs &a, int max_rows, int batch, cudaStream_t st);
+// Every slot of the partials with the history on the 5th-generation tensor cores (group 128), 128 query rows of a kv head at a time;
+// where its grid fits.
+bool tree_tc_fits(const TreeArgs &a, int max_rows, int batch);
+cudaError_t launch_tree_tc(const TreeArgs &a, int max_rows, int batch, cudaStream_t st);
 
 }  // namespace oscar
