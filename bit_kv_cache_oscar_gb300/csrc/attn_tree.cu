@@ -145,7 +145,7 @@ __device__ __forceinline__ void history_warp(const TreeArgs &a, const CUtensorMa
         if (!mbar_wait(bars + 8 * st, phase)) {
             if (lane == 0) flag_status(a.status, OSCAR_DEV_WAIT_TIMEOUT);
             // the copies still under way land before this memory is used again
-            for (int k = i + 1; k < i + R::n && k < n; ++k) mbar_wait(bars + 8 * (k % R::n), (k / R::n) & 1);
+            for (int k = i; k < i + R::n && k < n; ++k) mbar_wait(bars + 8 * (k % R::n), (k / R::n) & 1);
             break;
         }
         const uint8_t *stage = ring + st * R::stride;

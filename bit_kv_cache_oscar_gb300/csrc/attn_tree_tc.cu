@@ -62,8 +62,10 @@ struct Meta {
     uint32_t ok[kStages];                        // pieces of 16 positions that were copied
     alignas(8) uint32_t valid[kSzBuffers][4], masked[kSzBuffers];    // of the tile whose scales are there: bits of usable positions; some are not
     float max_q;
-    uint32_t tmem;
+    uint32_t tmem, stuck;                        // stuck: a copy or product may still be under way
 };
+
+static_assert(sizeof(Meta) <= 512, "up to kOffPair");
 
 // Shared-memory descriptor of an MN-major operand in the 128-byte swizzle: 64 elements of 8 k in an atom of 1,024 bytes, the next
 // 8 k `1024` bytes further (stride offset), the next 64 elements kHalf bytes further (leading offset).
@@ -376,6 +378,7 @@ __device__ __forceinline__ void copy_loop(const TreeArgs &a, const Tiles &ti, Me
         return i < ti.n && lane < npc && p + ps > ti.lo && p < ti.hi ? pt[p >> sh] : -2;
     };
     next = page_of(0);
+    int issued = ti.n;
     for (int i = 0; i < ti.n; ++i) {
         const int st = i % kStages, page = next;
         next = page_of(i + 1);
@@ -383,7 +386,8 @@ __device__ __forceinline__ void copy_loop(const TreeArgs &a, const Tiles &ti, Me
         const bool have = page != -2 && (uint32_t)page < (uint32_t)a.i4_pages;
         if (i >= kStages && !wait_for(saddr(&mt.empty[st]), ((i / kStages) & 1) ^ 1)) {
             if (lane == 0) flag_status(a.status, OSCAR_DEV_WAIT_TIMEOUT);
-            return;
+            issued = i;
+            break;
         }
         const uint32_t got = __ballot_sync(0xffffffffu, have);
         const uint32_t bar = saddr(&mt.full[st]);
@@ -403,6 +407,15 @@ __device__ __forceinline__ void copy_loop(const TreeArgs &a, const Tiles &ti, Me
             tma_load_1d(dst + 2 * kStageCodes + lane * ps * 8, a.sz + row * 4, ps * 8, bar, pol);
         }
     }
+    // every copy has landed before the CTA goes on, also where a wait ran out
+    for (int i = max(0, issued - kStages); i < issued; ++i)
+        if (!wait_for(saddr(&mt.full[i % kStages]), (i / kStages) & 1)) {
+            if (lane == 0) {
+                flag_status(a.status, OSCAR_DEV_WAIT_TIMEOUT);
+                mt.stuck = 1;
+            }
+            break;
+        }
 }
 
 // The whole warp waits, one elected lane issues.
@@ -410,6 +423,7 @@ __device__ __forceinline__ void product_loop(const TreeArgs &a, const Tiles &ti,
     uint32_t elected;
     asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(elected));
     const uint64_t dk = sw128_kmajor_desc(sb + kOffK), dv = mn_desc(sb + kOffV);
+    uint32_t last = 0, last_phase = 0;           // the newest commit's barrier: all products so far
     auto values = [&](int j) {                   // O += p s' . codes of tile j
         const int b = j & 1;
         const uint32_t ph = (j >> 1) & 1;
@@ -424,6 +438,8 @@ __device__ __forceinline__ void product_loop(const TreeArgs &a, const Tiles &ti,
             tc_commit(saddr(&mt.vfree[b]));
             tc_commit(saddr(&mt.pvdone));
         }
+        last = saddr(&mt.pvdone);
+        last_phase = j & 1;
         __syncwarp();
         return true;
     };
@@ -440,11 +456,16 @@ __device__ __forceinline__ void product_loop(const TreeArgs &a, const Tiles &ti,
             tc_commit(saddr(&mt.kfree[b]));
             tc_commit(saddr(&mt.sfull[b]));
         }
+        last = saddr(&mt.sfull[b]);
+        last_phase = (i >> 1) & 1;
         __syncwarp();
         if (i > 0) ok = values(i - 1);
     }
     if (ok && ti.n > 0) ok = values(ti.n - 1);
-    if (!ok && elected) flag_status(a.status, OSCAR_DEV_WAIT_TIMEOUT);
+    // every product is done before its operands and tensor memory are given up, also where a wait ran out
+    const bool done = !last || wait_for(last, last_phase);
+    if (elected && !(ok && done)) flag_status(a.status, OSCAR_DEV_WAIT_TIMEOUT);
+    if (elected && !done) mt.stuck = 1;
 }
 
 // Slot S of two tiles of 16 query rows, the BF16 rows: half of the warps a tile.  (A call: inlined it takes registers from the
@@ -506,6 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const TreeArgs a, 
         }
         mbar_init(saddr(&mt.pvdone), 1);
         mt.max_q = 0.f;
+        mt.stuck = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     pdl_wait();
@@ -587,15 +609,16 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const TreeArgs a, 
         }
     }
     __syncwarp();
-    __syncthreads();                             // every product is done: results take the operands' place
+    __syncthreads();                             // every copy and product is done: results take the operands' place
+    const bool write = rows > 0 && !mt.stuck;    // (or one was waited for in vain, and flagged: there are no results)
     float *res = reinterpret_cast<float *>(sm), *rm = res + kR * kResRow, *rl = rm + kR, *rz = rl + 2 * kR;
     const int half = warp >> 2, at = 32 * (warp & 3) + lane;
-    if (warp < kSoftWarps && rows > 0) {
+    if (warp < kSoftWarps && write) {
         rl[half * kR + at] = st.l;
         rz[half * kR + at] = st.zs;
     }
     __syncthreads();
-    if (warp < kSoftWarps && rows > 0) {
+    if (warp < kSoftWarps && write) {
         const float l = rl[at] + rl[kR + at], zs = rz[at] + rz[kR + at];
         if (half == 0) rm[at] = l > 0.f ? st.M : l != l ? l : -INFINITY;         // (NaN where a logit was: it has to reach the row)
         if (ti.n > 0)
@@ -618,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const TreeArgs a, 
     tc_fence_before();
     __syncthreads();
     // a row's copies joined, a warp a row
-    for (int row = warp; row < rows; row += kThreads / 32) {
+    for (int row = write ? warp : rows; row < rows; row += kThreads / 32) {
         float M = -INFINITY;
         for (int k = 0; k < rep; ++k) M = fmaxf(M, rm[row + k * pad]);
         float L = 0.f;
