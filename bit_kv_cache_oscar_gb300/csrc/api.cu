@@ -10,6 +10,8 @@
 #include <cstring>
 #include <mutex>
 #include <string>
+#include <utility>
+#include <vector>
 
 #include "int4.cuh"
 #include "oscar_internal.cuh"
@@ -134,6 +136,37 @@ oscar_status_t check_nodes(int32_t n, int32_t max_nodes) {
     if (max_nodes < 1 || max_nodes > OSCAR_TREE_MAX_NODES)
         return fail(OSCAR_ERR_INVALID_ARG, "max_nodes %d outside 1..%d", max_nodes, OSCAR_TREE_MAX_NODES);
     return OSCAR_OK;
+}
+
+// Pools whose rows one launch moves: no array of one, keys or values, shares memory with another.  Layers made one after another lie
+// in order, keys among themselves and values too, and one pass over both tells (sorting them took 0.6 us of 36 layers' call).
+bool apart(const oscar_bf16_pool_t *pools, int32_t n, uintptr_t page) {
+    using Array = std::pair<uintptr_t, uintptr_t>;
+    const auto range = [&](const uint16_t *p, int32_t i) {
+        return Array{reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + page * pools[i].n_pages};
+    };
+    bool in_order = true;
+    for (int32_t i = 1; i < n && in_order; ++i)
+        in_order = range(pools[i - 1].k, i - 1).second <= range(pools[i].k, i).first && range(pools[i - 1].v, i - 1).second <= range(pools[i].v, i).first;
+    if (in_order) {
+        for (int32_t i = 0, j = 0; i < n && j < n;) {
+            const Array k = range(pools[i].k, i), v = range(pools[j].v, j);
+            if (k.second <= v.first) ++i;
+            else if (v.second <= k.first) ++j;
+            else return false;
+        }
+        return true;
+    }
+    std::vector<Array> arrays;
+    arrays.reserve(2 * (size_t)n);
+    for (int32_t i = 0; i < n; ++i) {
+        arrays.push_back(range(pools[i].k, i));
+        arrays.push_back(range(pools[i].v, i));
+    }
+    std::sort(arrays.begin(), arrays.end());
+    for (size_t i = 1; i < arrays.size(); ++i)
+        if (arrays[i].first < arrays[i - 1].second) return false;
+    return true;
 }
 
 #define TRY(x)                                \
@@ -724,6 +757,8 @@ oscar_status_t oscar_tree_accept(const oscar_layout_t *layout, const int32_t *ta
         return fail(OSCAR_ERR_INVALID_ARG, "NULL argument");
     if (new_len && new_len < seq_len + batch && seq_len < new_len + batch)
         return fail(OSCAR_ERR_INVALID_ARG, "new_len and seq_len overlap");
+    if (!apart(pools, n_pools, (uintptr_t)layout->page_size * layout->n_kv_heads * layout->head_dim * 2))
+        return fail(OSCAR_ERR_INVALID_ARG, "two of the pools' arrays share memory: their rows would be moved twice at once");
     return cuda_status(oscar::launch_tree_accept(*layout, {target, draft, parents, seq_len}, {node_begin, n, max_nodes}, batch,
                                                  {accepted, path, tokens, new_len, path_stride}, pools, n_pools, page_table,
                                                  max_pages_per_req, status_ptr(), (cudaStream_t)stream),

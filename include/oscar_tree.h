@@ -135,7 +135,8 @@ OSCAR_API oscar_status_t oscar_sample(const void *logits, int32_t dtype, int64_t
  *   new_len     int32 [batch] or NULL: seq_len + accepted; not the array seq_len itself.
  *   pools       host array of n_pools BF16 pools (each layer's; 0 and NULL: nothing is moved), of the same
  *               layout and page table [batch][max_pages_per_req].  The rows of path node i, every kv head, move
- *               to position seq_len + i.  No two requests may share the pages of those positions.
+ *               to position seq_len + i.  No two requests may share the pages of those positions.  The arrays of all
+ *               pools, keys and values, lie apart (refused otherwise).
  * A request with no nodes gets accepted = 0.  One with a bad node range, a bad seq_len, or nodes that pass the
  * page table (where pools are given) is skipped and flagged (OSCAR_DEV_BAD_LENGTH): accepted = 0, an empty path,
  * new_len = seq_len.  A row from or to a bad page is not moved, and flagged (OSCAR_DEV_BAD_BF16_PAGE).
