@@ -471,7 +471,7 @@ __device__ __forceinline__ void product_loop(const TreeArgs &a, const Tiles &ti,
 // Slot S of two tiles of 16 query rows, the BF16 rows: half of the warps a tile.  (A call: inlined it takes registers from the
 // history's loops.)
 __device__ __noinline__ void window_cta(const TreeArgs a, uint8_t *sm, int item, int pairs) {
-    constexpr int W = kThreads / 64, bytes = std::max(join_bytes<W>(), W * 4096) + 4096;
+    constexpr int W = kThreads / 64, bytes = std::max(join_bytes<W>(), W * 8192) + 4096;
     static_assert(2 * bytes <= kSmem - 1024, "the fragments, and the values and the join, of both lie in shared memory beside each other");
     const int half = threadIdx.x / (32 * W), warp = threadIdx.x / 32 - W * half, lane = threadIdx.x & 31;
     const int row0 = (2 * (item % pairs) + half) * kTile, h = item / pairs % a.n_kv, b = item / pairs / a.n_kv;
@@ -481,7 +481,7 @@ __device__ __noinline__ void window_cta(const TreeArgs a, uint8_t *sm, int item,
     uint8_t *own = sm + half * bytes;
     Rows x;
     clear(x);
-    window_warp<W, true>(a, rq, b, h, row0, rows, reinterpret_cast<uint4 *>(own + bytes - 4096), reinterpret_cast<uint4 *>(own + warp * 4096),
+    window_warp<W, true>(a, rq, b, h, row0, rows, reinterpret_cast<uint4 *>(own + bytes - 4096), reinterpret_cast<uint4 *>(own + warp * 8192),
                          1 + half, warp, lane, x);
     tile_sync<W, true>(1 + half);                // values are read: results take their place
     join_warps<W, true>(a, rq, h, row0, rows, a.part.S, false, own, 1 + half, 32 * warp + lane, warp, lane, x);

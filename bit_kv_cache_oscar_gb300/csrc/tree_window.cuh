@@ -68,8 +68,8 @@ __device__ __forceinline__ uint4 query_piece(const TreeArgs &a, const TreeReques
 
 // ---- the BF16 rows ---------------------------------------------------------------------------------
 // Positions [0, min(sink, T)), [max(hist_end, those), T) and the nodes' [T, T + n), in tiles of 16.  frag: 4 KB of the W warps' shared
-// memory, stage: 4 KB of this warp's.  A tile's values are on their way while its logits are formed: each lane copies the pieces
-// that it reads itself.
+// memory, stage: 8 KB of this warp's, a tile's values and keys: both are on their way at once, and a lane copies the pieces that it
+// reads itself.  (Keys and values through registers: 64 x 4K, 16 nodes on tcgen05 343 us, so 318; one node on mma.sync 136 and 128.)
 template <int W, bool PART = false>
 __device__ __forceinline__ void window_warp(const TreeArgs &a, const TreeRequest &rq, int b, int h, int row0, int rows, uint4 *frag, uint4 *stage, int barrier,
                                             int warp, int lane, Rows &x) {
@@ -100,16 +100,17 @@ __device__ __forceinline__ void window_warp(const TreeArgs &a, const TreeRequest
         const size_t at = ((((size_t)page << sh) + ((p0 + g) & ((1 << sh) - 1))) * a.n_kv + h) * kHeadDim + 8 * t, far = (size_t)8 * a.n_kv * kHeadDim;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
+            if (in0) cp_async16(saddr(stage + 256 + 64 * c + lane), a.bf.k + at + 32 * c);
+            if (in1) cp_async16(saddr(stage + 288 + 64 * c + lane), a.bf.k + at + far + 32 * c);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
             if (in0) cp_async16(saddr(stage + 64 * c + lane), a.bf.v + at + 32 * c);
             if (in1) cp_async16(saddr(stage + 64 * c + 32 + lane), a.bf.v + at + far + 32 * c);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
-        uint4 kk[2][4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            kk[0][i] = in0 ? *reinterpret_cast<const uint4 *>(a.bf.k + at + 32 * i) : make_uint4(0, 0, 0, 0);
-            kk[1][i] = in1 ? *reinterpret_cast<const uint4 *>(a.bf.k + at + far + 32 * i) : make_uint4(0, 0, 0, 0);
-        }
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
         float s[2][4];                               // [keys 8 u + 2 t + e][2 r + e]
 #pragma unroll
         for (int u = 0; u < 2; ++u) s[u][0] = s[u][1] = s[u][2] = s[u][3] = 0.f;
@@ -118,8 +119,9 @@ __device__ __forceinline__ void window_warp(const TreeArgs &a, const TreeRequest
             const uint4 x = frag[64 * i + lane], y = frag[64 * i + 32 + lane];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                mma16816_bf16(s[u], x.x, x.y, x.z, x.w, kk[u][i].x, kk[u][i].y);
-                mma16816_bf16(s[u], y.x, y.y, y.z, y.w, kk[u][i].z, kk[u][i].w);
+                const uint4 kk = (u ? in1 : in0) ? stage[256 + 32 * u + 64 * i + lane] : make_uint4(0, 0, 0, 0);
+                mma16816_bf16(s[u], x.x, x.y, x.z, x.w, kk.x, kk.y);
+                mma16816_bf16(s[u], y.x, y.y, y.z, y.w, kk.z, kk.w);
             }
         }
 #pragma unroll
@@ -164,11 +166,12 @@ __device__ __forceinline__ void window_warp(const TreeArgs &a, const TreeRequest
 #pragma unroll
                 for (int e = 0; e < 4; ++e) x.out[c][i][e] *= al[e >> 1];
             // infinities and NaN among the values: rows that do not see them must not meet them in a product
+            // (their product with 0 is NaN, all others' a zero of some sign)
             const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-            bool odd = false;
+            __nv_bfloat162 zeros = as_bf2(0u);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) odd |= (w[e] & 0x7f80u) == 0x7f80u || (w[e] & 0x7f800000u) == 0x7f800000u;
-            if (__any_sync(0xffffffffu, odd)) {
+            for (int e = 0; e < 8; ++e) zeros = __hfma2(as_bf2(w[e]), as_bf2(0u), zeros);
+            if (__any_sync(0xffffffffu, (*reinterpret_cast<const uint32_t *>(&zeros) & 0x7fff7fffu) != 0)) {
                 // one key at a time, only where it has weight
 #pragma unroll 1
                 for (int key = 0; key < 16; ++key) {
@@ -245,23 +248,28 @@ __device__ __forceinline__ void join_warps(const TreeArgs &a, const TreeRequest 
         if (tid < kTile) wM[row] = M;
     }
     tile_sync<W, PART>(barrier);
-    for (int e = tid; e < rows * kHeadDim; e += W * 32) {
-        const int row = e / kHeadDim, d = e % kHeadDim;
-        float L = 0.f, A = 0.f;
+    for (int e = tid; e < rows * (kHeadDim / 4); e += W * 32) {
+        const int row = e / (kHeadDim / 4), d = 4 * (e % (kHeadDim / 4));
+        float L = 0.f;
+        float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < W; ++w) {
-            const float f = wf[w * kTile + row], y = sum[(w * kTile + row) * kResRow + d];
-            L = f != 0.f ? fmaf(wl[w * kTile + row], f, L) : L;
-            A = f != 0.f ? fmaf(y, f, A) : A;
+            const float f = wf[w * kTile + row];
+            if (f == 0.f) continue;
+            const float4 y = *reinterpret_cast<const float4 *>(sum + (w * kTile + row) * kResRow + d);
+            L = fmaf(wl[w * kTile + row], f, L);
+            A = make_float4(fmaf(y.x, f, A.x), fmaf(y.y, f, A.y), fmaf(y.z, f, A.z), fmaf(y.w, f, A.w));
         }
         const size_t orow = tree_row(a, rq, h, row0 + row), at = orow * (S + 1) + slot;
         if (whole) {
             const bool on = L > 0.f || L != L;
-            a.o[orow * kHeadDim + d] = f32_to_bf16_rn(on ? __fdiv_rn(A, L) : 0.f);
+            const float o0 = on ? __fdiv_rn(A.x, L) : 0.f, o1 = on ? __fdiv_rn(A.y, L) : 0.f, o2 = on ? __fdiv_rn(A.z, L) : 0.f,
+                        o3 = on ? __fdiv_rn(A.w, L) : 0.f;
+            *reinterpret_cast<uint2 *>(a.o + orow * kHeadDim + d) = make_uint2(pack_b2(o0, o1), pack_b2(o2, o3));
             if (a.lse && d == 0) a.lse[orow] = on ? (wM[row] + log2f(L)) * 0.6931471805599453f : -INFINITY;
             continue;
         }
-        a.part.acc[at * kHeadDim + d] = A;
+        *reinterpret_cast<float4 *>(a.part.acc + at * kHeadDim + d) = A;
         if (d == 0) {
             a.part.m[at] = L != L ? L : wM[row];
             a.part.l[at] = L;
