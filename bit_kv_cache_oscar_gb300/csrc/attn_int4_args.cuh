@@ -7,7 +7,6 @@
 
 namespace oscar {
 
-constexpr int kSms = 152;
 constexpr int kBlock = 32;                       // tokens of one stage
 
 struct Attn4Args {

@@ -29,7 +29,7 @@
 namespace oscar {
 namespace {
 
-constexpr int kWide = 160;                       // CTAs of a launch up to which each gets an SM
+constexpr int kWide = kSms + 8;                  // CTAs of a launch up to which each gets an SM (or nearly)
 constexpr float kMostP = 0x1p100f;               // of the sum of a lane's p in a block
 constexpr float kNewW = 8.f, kNewP = 80.f;       // a new reference brings p·s to 2^8 at most, p to 2^80
 
@@ -448,21 +448,23 @@ cudaError_t launch_rows(const TreeArgs &a, int tiles, const CUtensorMap &tmk, co
 }  // namespace
 
 // Which kernel takes the history: 128 query rows a CTA on tcgen05 (group 128), or 16 on mma.sync.  The former takes 8.2 ns a tile
-// of 128 positions and 128 rows, the whole GPU, the latter 5.2 ns for 16 rows, and the former's launches cost 7 us more.  With 8 kv
-// heads, tcgen05 and mma.sync, us: 32 rows, 1 x 100K 63 and 76, 64 x 4K 236 and 258, 1 x 4K 22 and 16; 64 rows, 16 ragged of 100K 735
-// and 1,050, 1 x 4K 25.5 and 19.6.
-// tokens: the longest history's, one number for the splits and for the launch.  By the tables' width instead (128K), 8 nodes: 1 x 4K
-// 22.7 us for 16.0, 1 x 1K 21.0 for 13.8.
+// of 128 positions and 128 rows, the whole GPU, the latter 5.2 ns for 16 rows; the former's launches cost 7 us more, and its CTAs of
+// the BF16 rows, one an SM, 0.1 us each beyond those that find an SM at once.  With 8 kv heads, tcgen05 and mma.sync, us: 32 rows,
+// 1 x 100K 60 and 71, 1 x 4K 20 and 15, 64 x 4K 224 and 214, 64 x 8K 317 and 366, 128 x 2K 327 and 264; 64 rows, 16 ragged of 100K
+// 735 and 1,069, 1 x 4K 23 and 18, 64 x 4K 319 and 409.
+// tokens: the longest history's, one number for the splits and for the launch.  By the tables' width instead (128K), 8 nodes, 1 x 4K
+// and 1 x 1K took what tcgen05 takes: 20 us for 15, 20 for 13.
 static bool on_tcgen05(const oscar_layout_t &L, int batch, int max_nodes, long long tokens) {
-    const long long rows = (long long)max_nodes * L.gqa, tiles = (long long)batch * L.n_kv_heads * (tokens / 128 + 1);
-    return L.group == 128 && rows > 16 && tiles * (52 * ((rows + 15) / 16) - 82 * ((rows + 127) / 128)) > 70000;
+    const long long rows = (long long)max_nodes * L.gqa, heads = (long long)batch * L.n_kv_heads, tiles = heads * (tokens / 128 + 1);
+    const long long gain = tiles * (52 * ((rows + 15) / 16) - 82 * ((rows + 127) / 128));
+    return L.group == 128 && rows > 16 && gain > 70000 + 1000 * std::max(0LL, heads * ((rows + 31) / 32) - kSms);
 }
 
 // On tcgen05: one CTA an SM in one wave that leaves some SMs to the BF16 rows, or, where splits would pass 16K positions, splits of 8K,
-// which finish evenly (16 ragged of 100K, 64 rows: 858 us with one split, 735) and keep long sums short.  On mma.sync: one wave, the
+// which finish evenly (16 ragged of 100K, 64 rows: 858 us with one split, 735 with 12) and keep long sums short.  On mma.sync: one wave, the
 // BF16 rows' CTAs among it, of 12 warps and one CTA an SM where that leaves three splits, else (and for groups of 32 and 64) of 8
-// warps, two CTAs an SM (one); splits of 8K where they would pass 32K.  4 rows a kv head, us, 12 and 8 warps: 1 x 100K 43.6 and 48.6
-// (18 and 37 splits), 64 x 4K 136 and 127 (one split), 8 x 8K 41 and 42 (2 and 3), 16 ragged of 100K 425 and 433 (8 and 12).
+// warps, two CTAs an SM (one); splits of 8K where they would pass 32K.  4 rows a kv head, us, 12 and 8 warps: 1 x 100K 40 and 50 (18
+// splits), 64 x 4K 125 and 120 (one), 8 x 8K 43 and 42 (3), 16 ragged of 100K 420 and 442 (12).
 int suggest_splits_tree(const oscar_layout_t &L, int batch, int max_nodes, int max_hist, int sm_count) {
     const bool tc = on_tcgen05(L, batch, max_nodes, max_hist);
     const long long rows = max_nodes * (long long)L.gqa, tile = tc ? 128 : kTile;

@@ -8,6 +8,7 @@
 namespace oscar {
 
 constexpr int kRow4 = kHeadDim / 2;                   // bytes of one row's codes
+constexpr int kSms = 152;                             // of the one GPU that this is built for: launch rules count with them
 
 // Launch set up while the kernel before it in the stream still runs: every CTA of `kern` calls pdl_wait()
 // before its first access to memory, so the order of the stream holds as for a plain launch.  The kernels

@@ -42,7 +42,7 @@ constexpr int kKeys = 1024;                          // entries of a CTA's list 
 constexpr int kUnit = 44;                            // weights in units of 2^-44
 constexpr int kLimb = 15;
 
-// 2^31 2^(-j / 256), each within 2^-21 of a unit before its rounding.
+// 2^31 2^(-j / 256), each within 2^-17 of a unit before its rounding (256 products in 64 bits).
 struct Table {
     uint32_t t[256];
     constexpr Table() : t() {
@@ -884,7 +884,7 @@ cudaError_t launch_sample(const SampleInput &in, int32_t *tokens, cudaStream_t s
     const int size = in.dtype == OSCAR_DTYPE_F32 ? 4 : 2, room = 115712 - kSharedBytes - 48;
     int C = 1;
     while (C < 8 && (in.vocab + C - 1) / C * size > room) C *= 2;
-    while (C < 8 && (long long)in.rows * C * 2 <= 304 && in.vocab / (2 * C) >= 2048) C *= 2;
+    while (C < 8 && (long long)in.rows * C * 2 <= 2 * kSms && in.vocab / (2 * C) >= 2048) C *= 2;
     SampleArgs a{in, (in.vocab + C - 1) / C, tokens};
     const int smem = kSharedBytes + ((a.per + 2 * (16 / size)) * size + 15) / 16 * 16;
     switch (in.dtype) {
