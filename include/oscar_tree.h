@@ -48,14 +48,20 @@ OSCAR_API int32_t oscar_suggest_splits_tree_int4(const oscar_layout_t *layout, i
  *   partials    scratch for n rows (oscar_partials_ml_floats(layout, n, S) and so on).
  *   out         bf16 [n][Hq][head_dim], 8-byte aligned; lse (optional) fp32 [n][Hq], natural logarithm.
  * A node that sees nothing (an empty mask row where T = 0) gets out = 0 and lse = -inf.  What a node does not
- * see does not reach its output, infinities and NaN included.  A request with a bad node range, or whose
- * nodes pass the page table, is skipped and flagged (OSCAR_DEV_BAD_LENGTH); rows on a bad page are not seen,
- * and flagged.
+ * see does not reach its output, infinities and NaN included; a NaN among the logits of what it sees makes its output
+ * and lse NaN.  A request with a bad node range, or whose nodes pass the page table, is skipped and flagged
+ * (OSCAR_DEV_BAD_LENGTH); rows on a bad page are not seen, and flagged.  Where node_begin falls, ranges of other
+ * requests may share node rows, whose outputs are then nobody's.
  * Query products and softmax sums are fp32 or finer.  Of the history, a probability times its value scale
  * enters the value product as one fp16 number (2^-11 relative) under a scaling that follows the largest one
- * so far, and meets codes less 8; of the BF16 rows a probability enters in two bf16 parts (2^-16).  Query
- * elements below 2^-25 of the largest finite one that shares a scaling with them lose low bits: their head's,
- * or, on the kernel for many rows, the largest of 128 rows (nodes times query heads of a kv head).
+ * so far, and meets codes less 8; of the BF16 rows a probability enters in two bf16 parts (2^-16).  (The decode
+ * call keeps two fp16 parts.  Before they are rounded to bf16, which takes 1.6·10^-3 of their norm, outputs here are
+ * off by 2 to 3·10^-4 of it.)  The tensor cores
+ * cut a split's running sums off at 2^-23 every 16 positions: splits as suggested are 16K positions long at most, or
+ * 4K a warp, and a count below the suggestion's makes them longer.  Query elements below 2^-25 of the largest finite
+ * one that shares a scaling with them lose low bits: their head's, or, on the kernel for many rows, the largest of 128
+ * rows (nodes times query heads of a kv head); from 2^118 on they count as infinite.  Logits (times log2 e) are expected
+ * within 2^26: beyond, where fp32's last bit is 8 and more, outputs may be infinite or NaN.
  */
 OSCAR_API oscar_status_t oscar_tree_attention_int4(const oscar_layout_t *layout, const uint16_t *q, int32_t n,
                                                    const int32_t *node_begin, const int32_t *mask,
